@@ -292,7 +292,7 @@ def _run_decode(s):
     if own:
         import fp8_w8a8_rollout_gb300 as fp8rl
         if "workspace" not in s:
-            s["workspace"] = fp8rl.attn_decode_workspace(batch, hq, hkv, d)
+            s["workspace"] = fp8rl.attn_decode_workspace(hq, hkv, d)
         out, lse = fp8rl.attn_decode(s["q"], s["k_cache"], s["v_cache"], s["block_table"], s["lens"], s["scales"], page,
                                      workspace=s["workspace"])
         return {"out": out, "lse": lse}
