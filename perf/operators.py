@@ -46,9 +46,9 @@ def _logprob(op, rows, vocab, dtype, topk, temperature, **more):
 def listed():
     return [
         # one decode step's tokens: the call is launch latency
-        _norm(16, 4096, "fp32", name="norm, 16 tokens"),
+        _norm(16, 4096, "fp32", name="norm 16 tokens"),
         # a prefill batch in the power-of-two scale format
-        _norm(8192, 4096, "ue8m0", name="norm, 8192 tokens"),
+        _norm(8192, 4096, "ue8m0", name="norm 8192 tokens"),
         # one short prompt: a few tiles, latency
         _prefill(1, 509, 1, 32, 8, 128, name="prompt of 509"),
         # one long prompt
@@ -62,13 +62,13 @@ def listed():
         # few long answers: the work is along the cache; 8 query heads to a KV head
         _decode(4, 100000, 131071, 5, 32, 4, 128, 64, name="4 long caches"),
         # the sampled tokens of one decode step, with the top 20 for the log
-        _logprob("logprob", 16, 151936, "bf16", 20, 0.7, name="logprob, 16 rows, top 20"),
+        _logprob("logprob", 16, 151936, "bf16", 20, 0.7, name="logprob 16 rows top 20"),
         # the trainer's scoring of a packed batch
-        _logprob("logprob", 4096, 151936, "bf16", 0, 1.0, name="logprob, 4096 rows"),
+        _logprob("logprob", 4096, 151936, "bf16", 0, 1.0, name="logprob 4096 rows"),
         # gradient of a small batch in fp32, odd vocabulary
-        _logprob("logprob_grad", 61, 32001, "fp32", 0, 1.0, name="logprob grad, 61 rows"),
+        _logprob("logprob_grad", 61, 32001, "fp32", 0, 1.0, name="logprob grad 61 rows"),
         # gradient of the packed batch
-        _logprob("logprob_grad", 4096, 151936, "bf16", 0, 1.0, name="logprob grad, 4096 rows"),
+        _logprob("logprob_grad", 4096, 151936, "bf16", 0, 1.0, name="logprob grad 4096 rows"),
     ]
 
 
