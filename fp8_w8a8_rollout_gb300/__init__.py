@@ -31,6 +31,8 @@ __all__ = [
     "fp8rl_gemm_blockscaled_static", "fp8rl_gemm_swiglu_quant", "fp8rl_grouped_gemm_swiglu_quant",
     "gemm_swiglu_quant", "grouped_gemm_swiglu_quant", "quant_gate_up_interleaved",
     "fp8rl_kv_calibrate", "fp8rl_kv_append", "kv_calibrate", "kv_append",
+    "fp8rl_rmsnorm_quant", "rmsnorm_quant", "fp8rl_attn_decode_workspace_size", "fp8rl_attn_decode",
+    "attn_decode_workspace", "attn_decode", "fp8rl_logprob", "fp8rl_logprob_backward", "logprobs", "logprobs_backward",
     "fp8rl_e4m3_encode", "fp8rl_debug_set", "fp8rl_sync_status", "fp8rl_status_string", "fp8rl_version",
     "quant_weight", "quant_weights_batched", "quant_act", "gemm", "grouped_gemm", "HostWeightSync",
     "CanaryError", "canaries_enabled", "check_canaries",
@@ -104,6 +106,12 @@ def load_library(build_if_missing: bool = False):
             "fp8rl_moe_combine": [vp, i64, i64, i64, vp, vp, i64, i64, vp, i64, vp],
             "fp8rl_tis_workspace_size": [i64],
             "fp8rl_tis_weights": [vp, vp, vp, i64, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp],
+            "fp8rl_rmsnorm_quant": [vp, i64, vp, i64, vp, ctypes.c_float, i64, i64, vp, i64, vp, i64, vp, st, vp],
+            "fp8rl_attn_decode_workspace_size": [i64, i64, i64],
+            "fp8rl_attn_decode": [vp, i64, i64, i64, i64, i64, vp, vp, i64, i64, vp, i64, i64, i64, vp, vp,
+                                  ctypes.c_float, vp, i64, vp, vp, ctypes.c_size_t, vp],
+            "fp8rl_logprob": [vp, i32, i64, i64, i64, ctypes.c_float, vp, vp, vp, vp, i64, vp, vp, vp],
+            "fp8rl_logprob_backward": [vp, i32, i64, i64, i64, ctypes.c_float, vp, vp, vp, vp, vp, vp, i64, vp],
             "fp8rl_debug_set": [i32, i64],
             "fp8rl_sync_status": [vp],
             "fp8rl_status_string": [st],
@@ -117,6 +125,7 @@ def load_library(build_if_missing: bool = False):
         lib.fp8rl_moe_plan_workspace_size.restype = ctypes.c_size_t
         lib.fp8rl_host_sync_staging_bytes.restype = ctypes.c_size_t
         lib.fp8rl_tis_workspace_size.restype = ctypes.c_size_t
+        lib.fp8rl_attn_decode_workspace_size.restype = ctypes.c_size_t
         lib.fp8rl_version.restype = i32
         _lib = lib
         return lib
@@ -278,6 +287,42 @@ def fp8rl_tis_weights(d_lp_train, d_lp_rollout, d_mask, n, clip, d_w, d_kl, d_wo
     _ok(load_library().fp8rl_tis_weights(_p(d_lp_train), _p(d_lp_rollout), _p(d_mask), n, clip, _p(d_w),
                                          _p(d_kl), _p(d_workspace), workspace_bytes, _stream(stream)),
         "fp8rl_tis_weights")
+
+
+def fp8rl_rmsnorm_quant(x_bf16, ldx, residual_bf16, ldr, weight_bf16, eps, m, k, h_bf16, ldh, q_e4m3, ldq, x_scale,
+                        fmt=SCALE_FP32, stream=None) -> None:
+    _ok(load_library().fp8rl_rmsnorm_quant(_p(x_bf16), ldx, _p(residual_bf16), ldr, _p(weight_bf16), eps, m, k,
+                                           _p(h_bf16), ldh, _p(q_e4m3), ldq, _p(x_scale), fmt, _stream(stream)),
+        "fp8rl_rmsnorm_quant")
+
+
+def fp8rl_attn_decode_workspace_size(q_heads, kv_heads, head_dim) -> int:
+    return int(load_library().fp8rl_attn_decode_workspace_size(q_heads, kv_heads, head_dim))
+
+
+def fp8rl_attn_decode(q_bf16, ldq, batch, q_heads, kv_heads, head_dim, k_cache, v_cache, ld_cache, num_slots,
+                      d_block_table, ldt, max_blocks, block_size, d_lens, d_scales, softmax_scale, out_bf16, ldo, d_lse,
+                      d_workspace, workspace_bytes, stream=None) -> None:
+    _ok(load_library().fp8rl_attn_decode(_p(q_bf16), ldq, batch, q_heads, kv_heads, head_dim, _p(k_cache), _p(v_cache),
+                                         ld_cache, num_slots, _p(d_block_table), ldt, max_blocks, block_size,
+                                         _p(d_lens), _p(d_scales), softmax_scale, _p(out_bf16), ldo, _p(d_lse),
+                                         _p(d_workspace), workspace_bytes, _stream(stream)),
+        "fp8rl_attn_decode")
+
+
+def fp8rl_logprob(d_logits, logits_fp32, rows, vocab, ld, temperature, d_tokens, d_lp, d_entropy, d_stats, topk,
+                  d_top_ids, d_top_lp, stream=None) -> None:
+    _ok(load_library().fp8rl_logprob(_p(d_logits), logits_fp32, rows, vocab, ld, temperature, _p(d_tokens), _p(d_lp),
+                                     _p(d_entropy), _p(d_stats), topk, _p(d_top_ids), _p(d_top_lp), _stream(stream)),
+        "fp8rl_logprob")
+
+
+def fp8rl_logprob_backward(d_logits, logits_fp32, rows, vocab, ld, temperature, d_tokens, d_stats, d_entropy,
+                           d_grad_lp, d_grad_entropy, d_dlogits, ldd, stream=None) -> None:
+    _ok(load_library().fp8rl_logprob_backward(_p(d_logits), logits_fp32, rows, vocab, ld, temperature, _p(d_tokens),
+                                              _p(d_stats), _p(d_entropy), _p(d_grad_lp), _p(d_grad_entropy),
+                                              _p(d_dlogits), ldd, _stream(stream)),
+        "fp8rl_logprob_backward")
 
 
 def fp8rl_grouped_gemm_blockscaled(xq, x_scale, wq, w_scale, d_offsets, num_experts, rows, n, k,
@@ -653,6 +698,161 @@ def tis_weights(lp_train: torch.Tensor, lp_rollout: torch.Tensor, mask: torch.Te
                                          _out((3,), torch.float64, dev))
     fp8rl_tis_weights(lp_train, lp_rollout, mask, n, clip, w, kl, workspace, workspace.numel(), stream)
     return w, kl
+
+
+def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                  fmt=SCALE_FP32, out=None, stream=None):
+    """(q uint8 [m, k], scale [ceil(k/128), m], h bf16 [m, k]): the RMS norm of
+    h = x + residual times weight, quantised 1x128; h is None without a
+    residual.  `out` is such a triple (its h may be the residual itself)."""
+    _check_cuda(x, weight, residual, *(out or ()))
+    _check_bf16_2d(x, "x")
+    m, k = x.shape
+    if weight.dtype != torch.bfloat16 or weight.shape != (k,) or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous bf16 [k] tensor")
+    if residual is not None:
+        _check_bf16_2d(residual, "residual")
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+    if out is None:
+        q = _out((m, k), torch.uint8, x.device)
+        s = _out(((k + 127) // 128, m), _scale_dtype(fmt), x.device)
+        h = None if residual is None else _out((m, k), torch.bfloat16, x.device)
+    else:
+        q, s, h = out
+        _check_out(q, (m, k), torch.uint8, "q", rows=True)
+        _check_out(s, ((k + 127) // 128, m), _scale_dtype(fmt), "scale")
+        if h is not None:
+            _check_out(h, (m, k), torch.bfloat16, "h", rows=True)
+    fp8rl_rmsnorm_quant(x, _ld(x), residual, _ld(residual), weight, eps, m, k, h, _ld(h), q, _ld(q), s, fmt, stream)
+    return q, s, h
+
+
+def _ld(t: torch.Tensor | None) -> int:
+    """Leading dimension in elements (torch leaves the stride of a single row
+    unspecified: then it is a row's own length); 0 for None."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t[0].numel() if t.shape[0] else 0)
+
+
+def _check_out(t: torch.Tensor, shape, dtype, name: str, rows=False):
+    """A caller's output tensor: its shape and type, contiguous (or, with
+    `rows`, of any row stride)."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
+    if not t.is_contiguous() and not (rows and t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
+        raise ValueError(f"{name} must be contiguous" + (" in its rows" if rows else ""))
+
+
+def _check_heads(t: torch.Tensor, name: str):
+    """bf16 [tokens, heads, d] whose heads lie side by side (a column range of
+    a wider projection output is fine)."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a bf16 [tokens, heads, head_dim] tensor")
+    if (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+
+
+def attn_decode_workspace(q_heads: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """A zero-filled workspace for attn_decode with these heads, any batch."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(device):
+        nbytes = fp8rl_attn_decode_workspace_size(q_heads, kv_heads, head_dim)
+    if nbytes == 0:
+        raise ValueError("q_heads must be a multiple of kv_heads, head_dim 64 or 128")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                lens: torch.Tensor, scales: torch.Tensor, block_size: int, softmax_scale: float | None = None,
+                workspace: torch.Tensor | None = None, out=None, stream=None):
+    """(out bf16 [batch, q_heads, d], lse fp32 [batch, q_heads]): attention of
+    one token per sequence (q [batch, q_heads, d]) over the E4M3 caches
+    ([num_slots, kv_heads * d] uint8, as kv_append writes them), the pages of
+    sequence b in block_table[b] (int32 [batch, max_blocks]), its number of
+    keys in lens[b] (int32).  softmax_scale defaults to d ** -0.5; keep one
+    workspace per stream (attn_decode_workspace) rather than one per call."""
+    _check_cuda(q, k_cache, v_cache, block_table, lens, scales, workspace, *(out or ()))
+    _check_heads(q, "q")
+    batch, hq, d = q.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != torch.uint8 or t.dim() != 2 or t.stride(1) != 1 or t.shape[1] % d:
+            raise ValueError(f"{name} must be a uint8 [num_slots, kv_heads * head_dim] tensor with unit column stride")
+    if k_cache.shape != v_cache.shape or k_cache.stride(0) != v_cache.stride(0):
+        raise ValueError("k_cache and v_cache must have one shape and stride")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch or \
+            (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table must be an int32 [batch, max_blocks] tensor with unit column stride")
+    if lens.dtype != torch.int32 or lens.shape != (batch,) or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous int32 [batch] tensor")
+    if scales.dtype != torch.float32 or scales.numel() < 2 or not scales.is_contiguous():
+        raise ValueError("scales must hold the fp32 K and V scales")
+    hkv = k_cache.shape[1] // d
+    if workspace is None:
+        workspace = attn_decode_workspace(hq, hkv, d, q.device)
+    if out is None:
+        out = (_out((batch, hq, d), torch.bfloat16, q.device), _out((batch, hq), torch.float32, q.device))
+    else:
+        _check_out(out[0], (batch, hq, d), torch.bfloat16, "out")
+        _check_out(out[1], (batch, hq), torch.float32, "lse")
+    fp8rl_attn_decode(q, _ld(q), batch, hq, hkv, d, k_cache, v_cache, _ld(k_cache), k_cache.shape[0],
+                      block_table, _ld(block_table), block_table.shape[1], block_size, lens, scales,
+                      d ** -0.5 if softmax_scale is None else softmax_scale, out[0], hq * d, out[1], workspace,
+                      workspace.numel(), stream)
+    return out
+
+
+def _check_logits(logits: torch.Tensor, tokens: torch.Tensor):
+    if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be a 2-D bf16 or fp32 tensor with unit column stride")
+    if tokens.dtype != torch.int32 or tokens.shape != logits.shape[:1] or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous int32 [rows] tensor")
+
+
+def logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0, topk: int = 0, out=None, stream=None):
+    """(lp fp32 [rows], entropy fp32 [rows], stats fp32 [rows, 2], top_ids
+    int32 [rows, topk], top_lp fp32 [rows, topk]) of logits (bf16 or fp32
+    [rows, vocab]) at a temperature; the last two are None with topk = 0.
+    Rows whose token is outside the vocabulary (-1: padding) give zeros and
+    ids -1.  stats is for logprobs_backward; lp goes to tis_weights."""
+    _check_cuda(logits, tokens, *(out or ()))
+    _check_logits(logits, tokens)
+    rows, vocab = logits.shape
+    dev = logits.device
+    shapes = (((rows,), torch.float32, "lp"), ((rows,), torch.float32, "entropy"), ((rows, 2), torch.float32, "stats")) + \
+        ((((rows, topk), torch.int32, "top_ids"), ((rows, topk), torch.float32, "top_lp")) if topk > 0 else ())
+    if out is None:
+        out = tuple(_out(shape, dtype, dev) for shape, dtype, _ in shapes) + ((None, None) if topk <= 0 else ())
+    else:
+        for t, (shape, dtype, name) in zip(out, shapes):
+            _check_out(t, shape, dtype, name)
+    fp8rl_logprob(logits, int(logits.dtype == torch.float32), rows, vocab, _ld(logits), temperature, tokens, out[0],
+                  out[1], out[2], topk, out[3], out[4], stream)
+    return out
+
+
+def logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: torch.Tensor, entropy: torch.Tensor | None,
+                      grad_lp: torch.Tensor, grad_entropy: torch.Tensor | None = None, temperature: float = 1.0,
+                      out: torch.Tensor | None = None, stream=None):
+    """d logits ([rows, vocab], the logits' type) from the gradients of lp and
+    (optionally) entropy; `out` may be the logits tensor itself."""
+    _check_cuda(logits, tokens, stats, entropy, grad_lp, grad_entropy, out)
+    _check_logits(logits, tokens)
+    rows, vocab = logits.shape
+    _check_out(stats, (rows, 2), torch.float32, "stats")
+    for name, t in (("entropy", entropy), ("grad_lp", grad_lp), ("grad_entropy", grad_entropy)):
+        if t is not None:
+            _check_out(t, (rows,), torch.float32, name)
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs the forward call's entropy")
+    if out is None:
+        out = _out((rows, vocab), logits.dtype, logits.device)
+    else:
+        _check_out(out, (rows, vocab), logits.dtype, "out", rows=True)
+    fp8rl_logprob_backward(logits, int(logits.dtype == torch.float32), rows, vocab, _ld(logits), temperature, tokens,
+                           stats, entropy, grad_lp, grad_entropy, out, _ld(out), stream)
+    return out
 
 
 class HostWeightSync:

@@ -1,0 +1,547 @@
+// attn_decode.cu -- attention of one new token per sequence over the paged
+// E4M3 KV cache that the append writes ("Method steps", step 3: the KV cache
+// is stored in FP8 with one scale per tensor).
+//
+// For sequence b with n cached keys, KV head h and the query heads i that
+// share it: s_ij = softmax_scale * sK * (q_i . k_j), p_ij = exp(s_ij - m_i),
+// out_i = sV * sum_j p_ij v_j / sum_j p_ij, all heads of a group in one pass
+// over the cache (each key and value byte is read once).
+//
+// The cache's codes feed the tensor cores exactly: an E4M3 value is an f16
+// value, so codes are converted, not dequantised, and both scales are applied
+// in fp32 to the scores and to the output.  q is bf16; each head's row is
+// multiplied by a power of two that brings its largest magnitude to [1, 2)
+// and rounded to f16, which holds every bf16 bit of values down to 2^-14 of
+// that largest one (below it, absolute steps of 2^-24 of it).  p lies in
+// [0, 2^8] and is rounded to f16 (11 bits).  Scores, sums, maxima and the
+// output accumulators are fp32.
+//
+// HBM-bound: 2 d bytes per key and KV head, a few operations per byte, so
+// the products run on m16n8k16 tensor instructions with the roles swapped: the
+// 16 rows are keys (scores) or output columns (values), the 8 columns are the
+// query heads of the group, so a group of up to 8 heads costs one instruction
+// and codes go from global memory straight into operand registers.  A lane's 16
+// contiguous bytes of a key row are its operand words of four instructions
+// (the order of the d columns is free as long as q uses the same); for values
+// the bytes of two keys are interleaved by byte permutes.  Scores become the
+// second product's operand by an 8x8 transpose in registers.
+//
+// Work split: sequences, KV heads and 16-key steps form one list of tiles,
+// shared out to the CTAs in equal contiguous ranges, whatever the lengths.  An
+// item (sequence, KV head) that spans CTAs leaves fp32 partials in the
+// workspace; the CTA that arrives last merges them in CTA order, so the
+// result has the same bits on every run.
+#include <algorithm>
+#include <cfloat>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace fp8rl {
+namespace {
+
+constexpr int kAdWarps = 4;
+constexpr int kAdThreads = kAdWarps * 32;
+constexpr int kAdStep = 16;                      // keys a warp takes at a time
+constexpr int kAdTile = kAdStep * kAdWarps;      // keys a CTA takes at a time
+constexpr int kAdMaxBatch = 8192;                // prefix sums held in shared memory
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;                 // a running maximum may lag by this much (base 2): p <= 2^8
+
+struct AdArgs {
+  const uint16_t* q;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const int32_t* table;
+  const int32_t* lens;
+  const float* scales;
+  uint16_t* out;
+  float* lse;  // or null
+  uint32_t* tickets;
+  float* parts;
+  int64_t ldq, ldc, num_slots, ldt, ldo;
+  int32_t batch, hq, hkv, group, sub, page, max_len;
+  float softmax_scale;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// two E4M3 codes (low 16 bits) -> two f16, exactly
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ void store_bf16(uint16_t* p, float v) {
+  asm volatile("{.reg .b16 r;\n\tcvt.rn.bf16.f32 r, %1;\n\tst.global.b16 [%0], r;}" ::"l"(p), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint4 ld_stream16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_stream8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// One step's codes of a warp: 16 keys of one KV head.  Lane (g, t) = (lane /
+// 4, lane % 4): of keys g and g + 8 the K bytes [64 j + 16 t, + 16); of keys
+// 2t, 2t + 1, 2t + 8, 2t + 9 the V bytes [D/8 g, + D/8).
+template <int D>
+struct Codes {
+  uint4 k[2][D / 64];
+  uint32_t v[4][D / 32];
+};
+
+// slots: this lane's key's cache row (-1: masked), lane l < 16 key l of the step
+template <int D>
+__device__ __forceinline__ void load_codes(Codes<D>& c, const AdArgs& a, const uint8_t* kc, const uint8_t* vc, int64_t slot) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t s = __shfl_sync(0xffffffffu, slot, g + 8 * i);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+      c.k[i][j] = s >= 0 ? ld_stream16(kc + s * a.ldc + 64 * j + 16 * t) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t s = __shfl_sync(0xffffffffu, slot, 2 * t + (i & 1) + 8 * (i >> 1));
+    if (D == 128) {
+      const uint4 u = s >= 0 ? ld_stream16(vc + s * a.ldc + 16 * g) : make_uint4(0u, 0u, 0u, 0u);
+      c.v[i][0] = u.x, c.v[i][1] = u.y, c.v[i][2 % (D / 32)] = u.z, c.v[i][3 % (D / 32)] = u.w;
+    } else {
+      const uint2 u = s >= 0 ? ld_stream8(vc + s * a.ldc + 8 * g) : make_uint2(0u, 0u);
+      c.v[i][0] = u.x, c.v[i][1] = u.y;
+    }
+  }
+}
+
+// Shared memory of a CTA
+template <int D, int NT>
+struct AdSmem {
+  float o[kAdWarps][8 * NT][D];  // a warp's accumulators at a segment's end
+  float m[kAdWarps][8 * NT], l[kAdWarps][8 * NT];
+  int32_t last;
+};
+
+// partial of a segment in the workspace: per head D accumulators, then m and l
+template <int D, int NT>
+__host__ __device__ constexpr int64_t part_floats() {
+  return (int64_t)8 * NT * (D + 2);
+}
+
+// D: head size (64 or 128); NT: 8-head columns of a group part (1 or 2)
+template <int D, int NT>
+__global__ void __launch_bounds__(kAdThreads) attn_decode_kernel(const AdArgs a) {
+  extern __shared__ int64_t prefix[];  // batch + 1 running tile counts, then AdSmem
+  __shared__ int64_t warp_sum[kAdWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  AdSmem<D, NT>& sm = *reinterpret_cast<AdSmem<D, NT>*>(prefix + ((a.batch + 2) & ~1));
+  const int heads_sub = a.hkv * a.sub;  // items of a sequence: KV heads times parts of the group
+
+  // running counts of the sequences' tiles (each times heads_sub)
+  {
+    int64_t run = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kAdThreads) {
+      const int b = b0 + tid;
+      const int32_t n = b < a.batch ? min(max(a.lens[b], 0), a.max_len) : 0;
+      int64_t x = (int64_t)((n + kAdTile - 1) / kAdTile) * heads_sub;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      if (lane == 31) warp_sum[warp] = x;
+      __syncthreads();
+      int64_t before = run;
+      for (int w = 0; w < kAdWarps; ++w) {
+        if (w < warp) before += warp_sum[w];
+        run += warp_sum[w];
+      }
+      if (b < a.batch) prefix[b + 1] = before + x;
+      __syncthreads();
+    }
+    if (tid == 0) prefix[0] = 0;
+    __syncthreads();
+  }
+  const int64_t total = prefix[a.batch], cta = blockIdx.x;
+
+  // sequences without keys: zeros, spread over the CTAs
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    if (prefix[b + 1] != prefix[b]) continue;
+    for (int i = tid; i < a.hq * D; i += kAdThreads) a.out[b * a.ldo + i] = 0;
+    if (a.lse)
+      for (int i = tid; i < a.hq; i += kAdThreads) a.lse[(int64_t)b * a.hq + i] = -INFINITY;
+  }
+
+  // no CTA of the first `ctas` has an empty range, so a split item's CTAs are
+  // consecutive and all of them arrive at its ticket
+  const int64_t ctas = min((int64_t)gridDim.x, total);
+  if (cta >= ctas) return;
+  const int64_t w0 = cta * total / ctas, w1 = (cta + 1) * total / ctas;
+  const float sk = a.scales[0], sv = a.scales[1];
+  // the sequence of tile w0: the last b with prefix[b] <= w0
+  int b = 0;
+  {
+    int hi = a.batch;
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (prefix[mid] <= w0) b = mid;
+      else hi = mid;
+    }
+  }
+  int64_t w = w0;
+  bool first_segment = true;
+  while (w < w1) {
+    while (prefix[b + 1] <= w) ++b;
+    const int32_t n = min(a.lens[b], a.max_len);
+    const int64_t tiles = (prefix[b + 1] - prefix[b]) / heads_sub;
+    const int item = (int)((w - prefix[b]) / tiles);  // kv head * sub + part of the group
+    const int64_t item_w0 = prefix[b] + item * tiles, item_w1 = item_w0 + tiles;
+    const int64_t seg_w1 = min(w1, item_w1);
+    const int kvh = item / a.sub, h0 = kvh * a.group + (item % a.sub) * 8 * NT;
+    const int heads = min(8 * NT, (kvh + 1) * a.group - h0);
+    const uint8_t* kc = a.kc + (int64_t)kvh * D;
+    const uint8_t* vc = a.vc + (int64_t)kvh * D;
+    const int32_t* table = a.table + (int64_t)b * a.ldt;
+
+    // the query heads as operand words (column = head): lane (g, t) holds
+    // head g's columns d = 64 j + 16 t + [0, 16)
+    uint32_t qf[NT][D / 64][4][2];
+    float qs[NT][2];  // score scale of this lane's result columns, heads 2t and 2t + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * 8 + g;
+      uint32_t raw[D / 64][8];
+      uint32_t big = 0;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (int64_t)b * a.ldq + (int64_t)(h0 + h) * D + 64 * j + 16 * t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          raw[j][i] = h < heads ? src[i] : 0u;
+          big = max(big, max(raw[j][i] & 0x7FFFu, (raw[j][i] >> 16) & 0x7FFFu));
+        }
+      }
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // 2^-e of the largest magnitude's exponent (its row to [1, 2)); e kept
+      // where 2^-e and 2^e are normal numbers
+      const int e = min(max((int)(big >> 7) - 127, -126), 126);
+      const float down = __int_as_float((127 - e) << 23), up = __int_as_float((127 + e) << 23);
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          qf[nt][j][s][0] = f16x2_rn(bf16_lo(raw[j][2 * s]) * down, bf16_hi(raw[j][2 * s]) * down);
+          qf[nt][j][s][1] = f16x2_rn(bf16_lo(raw[j][2 * s + 1]) * down, bf16_hi(raw[j][2 * s + 1]) * down);
+        }
+      const float f = up * (sk * a.softmax_scale * kLog2e);
+      qs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);      // lane of head 2t
+      qs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);  // lane of head 2t + 1
+    }
+
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+    }
+
+    // this warp's steps: keys [key, key + 16) for key = tile * 64 + warp * 16
+    const int32_t k1 = (int32_t)min((int64_t)n, (seg_w1 - item_w0) * kAdTile);
+    int32_t key = (int32_t)(w - item_w0) * kAdTile + warp * kAdStep;
+    // the cache row of key + lane (lanes 0..15), or -1
+    auto slot_of = [&](int32_t key0) -> int64_t {
+      const int32_t kk = key0 + (lane & 15);
+      if (kk >= k1) return -1;
+      const int32_t pg = kk / a.page;
+      const int64_t blk = table[pg];
+      const int64_t s = blk * a.page + (kk - pg * a.page);
+      return blk >= 0 && s < a.num_slots ? s : -1;
+    };
+    Codes<D> cur;
+    int64_t slot = slot_of(key), next_slot = slot_of(key + kAdTile);
+    if (key < k1) load_codes<D>(cur, a, kc, vc, slot);
+    for (; key < k1; key += kAdTile) {
+      // request the next step's codes before this step's arithmetic
+      Codes<D> nxt;
+      const int64_t after = slot_of(key + 2 * kAdTile);
+      if (key + kAdTile < k1) load_codes<D>(nxt, a, kc, vc, next_slot);
+      const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0);  // bit i < 16: key i counts
+
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const uint32_t r0[4] = {cur.k[0][j].x, cur.k[0][j].y, cur.k[0][j].z, cur.k[0][j].w};
+        const uint32_t r1[4] = {cur.k[1][j].x, cur.k[1][j].y, cur.k[1][j].z, cur.k[1][j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = e4m3x2_to_f16x2(r0[i]), a2 = e4m3x2_to_f16x2_hi(r0[i]);
+          const uint32_t a1 = e4m3x2_to_f16x2(r1[i]), a3 = e4m3x2_to_f16x2_hi(r1[i]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_16816(s[nt], a0, a1, a2, a3, qf[nt][j][i][0], qf[nt][j][i][1]);
+        }
+      }
+      const bool on0 = live >> g & 1u, on1 = live >> (g + 8) & 1u;
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        s[nt][0] = on0 ? s[nt][0] * qs[nt][0] : -INFINITY;
+        s[nt][1] = on0 ? s[nt][1] * qs[nt][1] : -INFINITY;
+        s[nt][2] = on1 ? s[nt][2] * qs[nt][0] : -INFINITY;
+        s[nt][3] = on1 ? s[nt][3] * qs[nt][1] : -INFINITY;
+        const float b0 = fmaxf(s[nt][0], s[nt][2]), b1 = fmaxf(s[nt][1], s[nt][3]);
+        if (__any_sync(0xffffffffu, b0 > m[nt][0] + kRescale || b1 > m[nt][1] + kRescale)) {
+          float big[2] = {b0, b1};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) big[c] = fmaxf(big[c], __shfl_xor_sync(0xffffffffu, big[c], d));
+            const float to = fmaxf(m[nt][c], big[c]);
+            const float f = to == -INFINITY ? 1.0f : ex2(m[nt][c] - to);
+            m[nt][c] = to;
+            l[nt][c] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[nt][i][c] *= f;
+              o[nt][i][c + 2] *= f;
+            }
+          }
+        }
+        const float r0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], r1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+        const float p0 = ex2(s[nt][0] - r0), p1 = ex2(s[nt][1] - r1), p2 = ex2(s[nt][2] - r0), p3 = ex2(s[nt][3] - r1);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        pb[nt][0] = transpose_8x8(f16x2_rn(p0, p1));
+        pb[nt][1] = transpose_8x8(f16x2_rn(p2, p3));
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        // bytes of d and d + 1 of two keys, side by side per d
+        const uint32_t x0 = __byte_perm(cur.v[0][i], cur.v[1][i], 0x5140), x1 = __byte_perm(cur.v[0][i], cur.v[1][i], 0x7362);
+        const uint32_t y0 = __byte_perm(cur.v[2][i], cur.v[3][i], 0x5140), y1 = __byte_perm(cur.v[2][i], cur.v[3][i], 0x7362);
+        const uint32_t a00 = e4m3x2_to_f16x2(x0), a01 = e4m3x2_to_f16x2_hi(x0), a02 = e4m3x2_to_f16x2(y0), a03 = e4m3x2_to_f16x2_hi(y0);
+        const uint32_t a10 = e4m3x2_to_f16x2(x1), a11 = e4m3x2_to_f16x2_hi(x1), a12 = e4m3x2_to_f16x2(y1), a13 = e4m3x2_to_f16x2_hi(y1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16816(o[nt][2 * i], a00, a01, a02, a03, pb[nt][0], pb[nt][1]);
+          mma_16816(o[nt][2 * i + 1], a10, a11, a12, a13, pb[nt][0], pb[nt][1]);
+        }
+      }
+      cur = nxt;
+      slot = next_slot;
+      next_slot = after;
+    }
+
+    // the warps' partials to shared memory; row d = D/8 g + 2 i (+ 1)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int h = nt * 8 + 2 * t + c;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          *reinterpret_cast<float2*>(&sm.o[warp][h][D / 8 * g + 2 * i]) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], d);
+        if (g == 0) {
+          sm.m[warp][h] = m[nt][c];
+          sm.l[warp][h] = l[nt][c];
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = w == item_w0 && seg_w1 == item_w1;
+    float* part = a.parts + (2 * cta + (first_segment ? 0 : 1)) * part_floats<D, NT>();
+    for (int i = tid; i < heads * D; i += kAdThreads) {
+      const int h = i / D, d = i % D;
+      float mm = sm.m[0][h];
+#pragma unroll
+      for (int x = 1; x < kAdWarps; ++x) mm = fmaxf(mm, sm.m[x][h]);
+      const float ref = mm == -INFINITY ? 0.0f : mm;
+      float acc = 0.0f, ll = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kAdWarps; ++x) {
+        const float f = ex2(sm.m[x][h] - ref);
+        acc = fmaf(f, sm.o[x][h][d], acc);
+        ll = fmaf(f, sm.l[x][h], ll);
+      }
+      if (whole) {
+        const float y = ll == 0.0f ? 0.0f : acc * (sv / ll);
+        store_bf16(a.out + b * a.ldo + (int64_t)(h0 + h) * D + d, y);
+        if (a.lse && d == 0) a.lse[(int64_t)b * a.hq + h0 + h] = ll == 0.0f ? -INFINITY : fmaf(mm, kLn2, logf(ll));
+      } else {
+        part[(int64_t)h * D + d] = acc;
+        if (d == 0) {
+          part[8 * NT * D + h] = mm;
+          part[8 * NT * D + 8 * NT + h] = ll;
+        }
+      }
+    }
+    if (!whole) {
+      // CTAs [c0, c1] share this item: the one that holds tile x is
+      // floor(((x + 1) * ctas - 1) / total)
+      const int64_t c0 = ((item_w0 + 1) * ctas - 1) / total, c1 = (item_w1 * ctas - 1) / total;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        // the item's ticket is its first CTA's: a CTA is the first of at most one split item
+        const uint32_t got = atomicAdd(a.tickets + c0, 1u);
+        sm.last = got == (uint32_t)(c1 - c0);
+        if (sm.last) a.tickets[c0] = 0u;  // ready for the next call
+      }
+      __syncthreads();
+      if (sm.last) {
+        __threadfence();
+        for (int i = tid; i < heads * D; i += kAdThreads) {
+          const int h = i / D, d = i % D;
+          float mm = -INFINITY, acc = 0.0f, ll = 0.0f;
+          for (int64_t c = c0; c <= c1; ++c) {
+            // a CTA's first segment went to its slot 0; the item's first CTA
+            // holds it as its first one only if its range starts in the item
+            const bool starts = c * total / ctas >= item_w0;
+            const float* src = a.parts + (2 * c + (c == c0 && !starts ? 1 : 0)) * part_floats<D, NT>();
+            const float pm = __ldcg(src + 8 * NT * D + h), pl = __ldcg(src + 8 * NT * D + 8 * NT + h), po = __ldcg(src + (int64_t)h * D + d);
+            const float to = fmaxf(mm, pm);
+            if (to == -INFINITY) continue;
+            const float f0 = ex2(mm - to), f1 = ex2(pm - to);
+            acc = acc * f0 + po * f1;
+            ll = ll * f0 + pl * f1;
+            mm = to;
+          }
+          const float y = ll == 0.0f ? 0.0f : acc * (sv / ll);
+          store_bf16(a.out + b * a.ldo + (int64_t)(h0 + h) * D + d, y);
+          if (a.lse && d == 0) a.lse[(int64_t)b * a.hq + h0 + h] = ll == 0.0f ? -INFINITY : fmaf(mm, kLn2, logf(ll));
+        }
+      }
+    }
+    __syncthreads();  // sm is free for the next segment
+    first_segment = false;
+    w = seg_w1;
+  }
+}
+
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  return n;
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int kAdCtasPerSm = 3;
+constexpr int64_t kAdMaxLen = (int64_t)1 << 30;  // 32-bit key numbers, two tiles of headroom
+
+int columns(int64_t group) { return group <= 8 ? 1 : 2; }
+
+int64_t ticket_bytes() { return ((int64_t)sm_count() * kAdCtasPerSm * 4 + 255) / 256 * 256; }
+
+template <int D, int NT>
+cudaError_t launch_decode(AdArgs a, void* workspace, cudaStream_t stream) {
+  a.tickets = static_cast<uint32_t*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes());
+  const size_t smem = (size_t)((a.batch + 2) & ~1) * 8 + sizeof(AdSmem<D, NT>);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  attn_decode_kernel<D, NT><<<(unsigned)(sm_count() * kAdCtasPerSm), kAdThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace fp8rl
+
+using namespace fp8rl;
+
+extern "C" FP8RL_API size_t fp8rl_attn_decode_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+  if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128)) return 0;
+  const int64_t part = (int64_t)8 * columns(q_heads / kv_heads) * (head_dim + 2) * 4;
+  return (size_t)(ticket_bytes() + 2 * (int64_t)sm_count() * kAdCtasPerSm * part);
+}
+
+extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t ldq, int64_t batch, int64_t q_heads,
+                                                    int64_t kv_heads, int64_t head_dim, const void* k_cache,
+                                                    const void* v_cache, int64_t ld_cache, int64_t num_slots,
+                                                    const int32_t* d_block_table, int64_t ldt, int64_t max_blocks,
+                                                    int64_t block_size, const int32_t* d_lens, const float* d_scales,
+                                                    float softmax_scale, void* out_bf16, int64_t ldo, float* d_lse,
+                                                    void* d_workspace, size_t workspace_bytes, void* stream) {
+  if (batch < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || num_slots < 0 || max_blocks < 0 || block_size < 1 ||
+      ldt < max_blocks || q_heads % kv_heads != 0 || !(softmax_scale > 0.0f) || !(softmax_scale <= FLT_MAX))
+    return FP8RL_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return FP8RL_ERR_SHAPE;
+  if (q_heads > 65536 || ldq < q_heads * head_dim || ldo < q_heads * head_dim || ld_cache < kv_heads * head_dim)
+    return FP8RL_ERR_INVALID_ARG;
+  if (batch == 0) return FP8RL_OK;
+  if (!q_bf16 || !d_lens || !out_bf16 || !d_scales || !d_workspace) return FP8RL_ERR_INVALID_ARG;
+  if (max_blocks > 0 && (!d_block_table || !k_cache || !v_cache)) return FP8RL_ERR_INVALID_ARG;
+  if (batch > kAdMaxBatch || block_size > kAdMaxLen || max_blocks > kAdMaxLen / block_size) return FP8RL_ERR_SHAPE;
+  if (workspace_bytes < fp8rl_attn_decode_workspace_size(q_heads, kv_heads, head_dim)) return FP8RL_ERR_INVALID_ARG;
+  if (!aligned(q_bf16, 4) || ldq % 2 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) || ld_cache % 16 != 0 ||
+      !aligned(out_bf16, 2) || !aligned(d_block_table, 4) || !aligned(d_lens, 4) || !aligned(d_scales, 4) ||
+      !aligned(d_lse, 4) || !aligned(d_workspace, 16))
+    return FP8RL_ERR_ALIGNMENT;
+  AdArgs a{};
+  a.q = static_cast<const uint16_t*>(q_bf16);
+  a.kc = static_cast<const uint8_t*>(k_cache);
+  a.vc = static_cast<const uint8_t*>(v_cache);
+  a.table = d_block_table;
+  a.lens = d_lens;
+  a.scales = d_scales;
+  a.out = static_cast<uint16_t*>(out_bf16);
+  a.lse = d_lse;
+  a.ldq = ldq, a.ldc = ld_cache, a.num_slots = num_slots, a.ldt = ldt, a.ldo = ldo;
+  a.batch = (int32_t)batch, a.hq = (int32_t)q_heads, a.hkv = (int32_t)kv_heads;
+  a.group = (int32_t)(q_heads / kv_heads);
+  const int nt = columns(a.group);
+  a.sub = (a.group + 8 * nt - 1) / (8 * nt);
+  a.page = (int32_t)block_size;
+  a.max_len = (int32_t)(max_blocks * block_size);
+  a.softmax_scale = softmax_scale;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = head_dim == 128 ? (nt == 1 ? launch_decode<128, 1>(a, d_workspace, cs) : launch_decode<128, 2>(a, d_workspace, cs))
+                                        : (nt == 1 ? launch_decode<64, 1>(a, d_workspace, cs) : launch_decode<64, 2>(a, d_workspace, cs));
+  return e == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
+}

@@ -1,0 +1,588 @@
+// logprob.cu -- log probabilities of given tokens with entropy and top
+// alternatives, and their gradient.
+//
+// Each row of logits x scores one token t at temperature T.  With m = max x,
+// y_j = (x_j - m) / T, e_j = exp(y_j) and S = sum e_j:
+//   log p_j = y_j - ln S,   H = -sum p_j log p_j = ln S - (sum e_j y_j) / S.
+// These are the log-probabilities that the truncated importance sampling
+// weights compare ("Method steps", step 4).
+//
+// Forward: one pass over the row with the running maximum, S and sum e y of a
+// thread's own elements; threads, warps and the CTAs of a cluster meet in a
+// fixed tree, so the result has the same bits on every run.  Few rows are
+// spread over clusters of up to 8 CTAs (partials meet through distributed
+// shared memory: one launch, no workspace).
+//
+// Top alternatives cost no work in that pass.  A thread's running maximum is
+// the largest of its elements, so the k-th largest thread maximum tau is a
+// lower bound of the k-th largest element, and every element that is at least
+// tau lies with a thread whose maximum is at least tau: about k threads (ties
+// aside) of the CTA's 256, whose elements are read a second time and ranked by
+// (value, lower index first) in sorted lists of one key per lane.
+//
+// Backward: dx_j = (g ([j = t] - p_j) - g_H p_j (log p_j + H)) / T from the
+// saved (m, ln S) and H; elementwise, so dx may be x.
+//
+// Both are HBM-bound (one read; one read and one write).
+#include <algorithm>
+#include <cfloat>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace fp8rl {
+namespace {
+
+constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpUnroll = 4;  // 16-byte pieces a thread loads before it uses the first
+constexpr int kMaxTop = 32;   // one key per lane
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kTinyExp2 = -200.0f;  // 2^-200 is 0 in fp32: exponents below it change nothing, and stay finite
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// fmaxf that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// A row's 16-byte pieces, counted from the 16-byte boundary at or below its
+// first element: piece p holds elements [p * N - off, (p + 1) * N - off).
+template <typename In>
+struct Row {
+  static constexpr int N = 16 / sizeof(In);
+  const In* x;
+  int32_t off, vocab, pieces;
+  __device__ __forceinline__ Row(const In* row, int32_t v) : x(row), vocab(v) {
+    off = (int32_t)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(In));
+    pieces = (v + off + N - 1) / N;
+  }
+  __device__ __forceinline__ bool whole(int32_t p) const { return p * N >= off && (p + 1) * N - off <= vocab; }
+  __device__ __forceinline__ uint4 load(int32_t p) const;
+};
+
+constexpr uint32_t kNegInfBf16x2 = 0xFF80FF80u, kNegInfF32 = 0xFF800000u;
+
+// elements outside the row read as -inf
+template <>
+__device__ __forceinline__ uint4 Row<uint16_t>::load(int32_t p) const {
+  if (whole(p)) return __ldg(reinterpret_cast<const uint4*>(x + (p * N - off)));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int32_t j = p * N - off + 2 * i + e;
+      w[i] |= (j >= 0 && j < vocab ? (uint32_t)x[j] : 0xFF80u) << (16 * e);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ uint4 Row<float>::load(int32_t p) const {
+  if (whole(p)) return __ldg(reinterpret_cast<const uint4*>(x + (p * N - off)));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t j = p * N - off + i;
+    w[i] = j >= 0 && j < vocab ? __float_as_uint(x[j]) : kNegInfF32;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename In>
+__device__ __forceinline__ uint4 absent() {
+  const uint32_t w = sizeof(In) == 2 ? kNegInfBf16x2 : kNegInfF32;
+  return make_uint4(w, w, w, w);
+}
+
+template <typename In>
+__device__ __forceinline__ void values(uint4 u, float (&v)[Row<In>::N]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sizeof(In) == 2) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    } else {
+      v[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+
+// the largest value of some pieces (NaN left out)
+template <typename In, int U>
+__device__ __forceinline__ float largest(const uint4 (&u)[U]) {
+  if (sizeof(In) == 2) {
+    uint32_t m = max_bf16x2(max_bf16x2(u[0].x, u[0].y), max_bf16x2(u[0].z, u[0].w));
+#pragma unroll
+    for (int i = 1; i < U; ++i) {
+      m = max_bf16x2(m, max_bf16x2(u[i].x, u[i].y));
+      m = max_bf16x2(m, max_bf16x2(u[i].z, u[i].w));
+    }
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+    m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(u[i].x), __uint_as_float(u[i].y)),
+                       fmaxf(__uint_as_float(u[i].z), __uint_as_float(u[i].w))));
+  return m;
+}
+
+// Running statistics in base 2: with t_j = (x_j - m) log2(e) / T,
+// s = sum 2^t_j and w = sum 2^t_j t_j.  m = -inf: nothing seen.
+struct Stat {
+  float m, s, w;
+};
+
+// the same sums relative to a new maximum: t_j + d, d = (m - to) log2(e) / T
+__device__ __forceinline__ void move_to(Stat& a, float to, float c) {
+  if (a.m == -INFINITY) {
+    a.m = to;  // s and w are 0, or NaN from a NaN element
+    return;
+  }
+  const float d = max_nan((a.m - to) * c, kTinyExp2), f = ex2(d);
+  a.w = f * fmaf(d, a.s, a.w);
+  a.s *= f;
+  a.m = to;
+}
+
+__device__ __forceinline__ Stat merge(Stat a, Stat b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  if (a.m != m) move_to(a, m, c);
+  if (b.m != m) move_to(b, m, c);
+  a.s += b.s;
+  a.w += b.w;
+  return a;
+}
+
+// Keys that order like (value, lower index first): the value's bits as an
+// ordered integer (-0 as 0, NaN below everything) above the complemented index.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return v != v ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+  return o == 0u ? __uint_as_float(0x7FC00000u) : __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ uint64_t key_of(float v, int32_t j) {
+  return (uint64_t)ordered(v) << 32 | (uint32_t)~j;
+}
+
+// The warp's sorted list, lane i its i-th largest key (0: none), takes in
+// every lane's `key` (0: none to offer).  Lanes >= top never count.
+__device__ __forceinline__ void offer(uint64_t& list, uint64_t key, int top) {
+  const int lane = threadIdx.x & 31;
+  for (;;) {
+    const uint64_t worst = __shfl_sync(0xffffffffu, list, top - 1);
+    const uint32_t want = __ballot_sync(0xffffffffu, key > worst);
+    if (!want) return;
+    const int from = __ffs(want) - 1;
+    const uint64_t k = __shfl_sync(0xffffffffu, key, from);
+    const int at = __popc(__ballot_sync(0xffffffffu, list > k));
+    const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
+    if (lane == at) list = k;
+    if (lane > at) list = up;
+    if (lane == from) key = 0;
+  }
+}
+
+struct LpArgs {
+  const void* x;
+  const int32_t* tokens;
+  float* lp;
+  float* entropy;
+  float2* stats;
+  int32_t* top_ids;
+  float* top_lp;
+  int64_t ld;
+  int32_t vocab, top;
+  float temperature;
+};
+
+// grid (cluster, rows), clusters of gridDim.x CTAs: a CTA takes the pieces
+// [rank, rank + 1) * ceil(pieces / cluster) of its row
+template <typename In, bool TOP>
+__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
+  constexpr int N = Row<In>::N, U = kLpUnroll;
+  const int64_t r = blockIdx.y;
+  const int rank = blockIdx.x, ranks = gridDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t t = a.tokens[r];
+  if (t < 0 || t >= a.vocab) {  // no token: the whole cluster leaves
+    if (rank == 0) {
+      if (tid == 0) {
+        a.lp[r] = 0.0f;
+        a.entropy[r] = 0.0f;
+        a.stats[r] = make_float2(0.0f, 0.0f);
+      }
+      if (TOP && tid < a.top) {
+        a.top_ids[r * a.top + tid] = -1;
+        a.top_lp[r * a.top + tid] = 0.0f;
+      }
+    }
+    return;
+  }
+  const In* xr = static_cast<const In*>(a.x) + r * a.ld;
+  const Row<In> row(xr, a.vocab);
+  const int32_t share = (row.pieces + ranks - 1) / ranks;
+  const int32_t p0 = rank * share, p1 = min(row.pieces, p0 + share);
+  const float c = kLog2e / a.temperature;
+
+  Stat st{-INFINITY, 0.0f, 0.0f};
+  for (int32_t p = p0 + tid; p < p1; p += U * kLpThreads) {
+    uint4 u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) u[i] = p + i * kLpThreads < p1 ? row.load(p + i * kLpThreads) : absent<In>();
+    const float big = largest<In>(u);
+    if (big > st.m) move_to(st, big, c);
+    const float m = st.m == -INFINITY ? 0.0f : st.m;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      float v[N];
+      values<In>(u[i], v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float y = max_nan((v[e] - m) * c, kTinyExp2), p2 = ex2(y);
+        st.s += p2;
+        st.w = fmaf(p2, y, st.w);
+      }
+    }
+  }
+  const float mine = st.m;  // the largest of this thread's elements
+
+  __shared__ Stat warp_stat[kLpWarps];
+  __shared__ Stat cta_stat;
+  __shared__ uint64_t lists[kLpWarps][kMaxTop];
+  __shared__ uint64_t cta_list[kMaxTop];
+  __shared__ int16_t cand[kLpThreads];
+  __shared__ int cands;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const Stat o{__shfl_xor_sync(0xffffffffu, st.m, d), __shfl_xor_sync(0xffffffffu, st.s, d),
+                 __shfl_xor_sync(0xffffffffu, st.w, d)};
+    // both lanes of a pair merge in the same order
+    st = (lane & d) ? merge(o, st, c) : merge(st, o, c);
+  }
+  if (lane == 0) warp_stat[warp] = st;
+  if (tid == 0) cands = 0;
+  __syncthreads();
+  if (tid == 0) {
+    for (int i = 1; i < kLpWarps; ++i) st = merge(st, warp_stat[i], c);
+    cta_stat = st;
+  }
+
+  if (TOP) {
+    // tau: the top-th largest thread maximum (0 while fewer threads hold any)
+    const uint32_t own = p0 + tid < p1 ? max(ordered(mine), 1u) : 0u;
+    uint32_t lo = 0u;
+    for (int b = 31; b >= 0; --b) {
+      const uint32_t mid = lo | 1u << b;
+      if (__syncthreads_count(own >= mid) >= a.top) lo = mid;
+    }
+    if (own >= lo && own > 0u) cand[atomicAdd(&cands, 1)] = (int16_t)tid;
+    __syncthreads();
+    // the candidates' pieces, spread over all threads
+    const int32_t each = (p1 - p0 + kLpThreads - 1) / kLpThreads;
+    const int32_t total = cands * each;
+    uint64_t list = 0;
+    for (int32_t f0 = warp * 32; f0 < total; f0 += kLpThreads) {
+      const int32_t f = f0 + lane;
+      const int32_t p = f < total ? p0 + cand[f / each] + (f % each) * kLpThreads : p1;
+      const uint4 u = p < p1 ? row.load(p) : absent<In>();
+      float v[N];
+      values<In>(u, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int32_t j = p * N - row.off + e;
+        const bool in = p < p1 && j >= 0 && j < a.vocab && max(ordered(v[e]), 1u) >= lo;
+        offer(list, in ? key_of(v[e], j) : 0, a.top);
+      }
+    }
+    lists[warp][lane] = lane < a.top ? list : 0;
+    __syncthreads();
+    if (warp == 0) {
+      for (int i = 1; i < kLpWarps; ++i) offer(list, lists[i][lane], a.top);
+      cta_list[lane] = lane < a.top ? list : 0;
+    }
+  }
+
+  if (ranks > 1) ptx::cluster_sync();
+  if (rank == 0 && warp == 0) {
+    __syncwarp();
+    Stat all = cta_stat;
+    uint64_t list = TOP ? cta_list[lane] : 0;
+    for (int i = 1; i < ranks; ++i) {
+      const uint32_t base = ptx::mapa_shared(ptx::smem_u32(&cta_stat), i);
+      const Stat o{__uint_as_float(ptx::ld_dsmem_u32(base)), __uint_as_float(ptx::ld_dsmem_u32(base + 4)),
+                   __uint_as_float(ptx::ld_dsmem_u32(base + 8))};
+      all = merge(all, o, c);
+      if (TOP) {
+        const uint32_t l = ptx::mapa_shared(ptx::smem_u32(&cta_list[lane]), i);
+        offer(list, (uint64_t)ptx::ld_dsmem_u32(l + 4) << 32 | ptx::ld_dsmem_u32(l), a.top);
+      }
+    }
+    // a row of -inf alone: every log-probability -inf, entropy 0
+    const bool none = all.m == -INFINITY && all.s == 0.0f;
+    const float ln_s = logf(all.s);
+    auto log_prob = [&](float v) { return none ? -INFINITY : (v - all.m) / a.temperature - ln_s; };
+    if (lane == 0) {
+      float xt;
+      if (sizeof(In) == 2) xt = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(xr)[t]);
+      else xt = reinterpret_cast<const float*>(xr)[t];
+      a.lp[r] = log_prob(xt);
+      a.entropy[r] = none ? 0.0f : ln_s - kLn2 * (all.w / all.s);
+      a.stats[r] = make_float2(all.m, ln_s);
+    }
+    if (TOP && lane < a.top) {
+      a.top_ids[r * a.top + lane] = (int32_t) ~(uint32_t)list;
+      a.top_lp[r * a.top + lane] = log_prob(from_ordered((uint32_t)(list >> 32)));
+    }
+  }
+  __syncwarp();
+  if (ranks > 1) ptx::cluster_sync();  // rank 0 has read the others' shared memory
+}
+
+// ------------------------------------------------------------------ backward
+
+struct LpGradArgs {
+  const void* x;
+  void* dx;
+  const int32_t* tokens;
+  const float2* stats;
+  const float* entropy;
+  const float* g_lp;
+  const float* g_ent;  // or null
+  int64_t ldx, ldd;
+  int32_t vocab;
+  float temperature;
+};
+
+struct GradRow {
+  float m, c, l2, g, gh, h, inv_t;
+  int32_t t;
+  bool zero;
+};
+
+// dx of element j with value v
+__device__ __forceinline__ float grad_of(const GradRow& q, float v, int32_t j) {
+  const float y = max_nan(fmaf(v - q.m, q.c, -q.l2), kTinyExp2);  // log2 p
+  const float p = ex2(y);
+  float d = -p * fmaf(q.gh, fmaf(y, kLn2, q.h), q.g);
+  if (j == q.t) d += q.g;
+  return d * q.inv_t;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <typename In>
+__device__ __forceinline__ void store1(In* p, float v);
+template <>
+__device__ __forceinline__ void store1<uint16_t>(uint16_t* p, float v) {
+  *p = (uint16_t)bf16x2_rn(v, 0.0f);
+}
+template <>
+__device__ __forceinline__ void store1<float>(float* p, float v) {
+  *p = v;
+}
+
+// grid (slices, rows); dx may be x, so neither is read through the read-only path
+template <typename In>
+__global__ void __launch_bounds__(kLpThreads) logprob_grad_kernel(const LpGradArgs a) {
+  constexpr int N = Row<In>::N, U = kLpUnroll;
+  const int64_t r = blockIdx.y;
+  const In* x = static_cast<const In*>(a.x) + r * a.ldx;
+  In* dx = static_cast<In*>(a.dx) + r * a.ldd;
+  GradRow q;
+  q.t = a.tokens[r];
+  const float2 st = a.stats[r];
+  // no token, or a row of -inf alone (a NaN beside them left its mark in st.y)
+  q.zero = q.t < 0 || q.t >= a.vocab || (st.x == -INFINITY && st.y == -INFINITY);
+  q.m = st.x;
+  q.c = kLog2e / a.temperature;
+  q.l2 = st.y * kLog2e;
+  q.inv_t = 1.0f / a.temperature;
+  q.g = a.g_lp[r];
+  q.gh = a.g_ent ? a.g_ent[r] : 0.0f;
+  q.h = a.g_ent ? a.entropy[r] : 0.0f;
+  const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
+  const int32_t stride = gridDim.x * kLpThreads, first = blockIdx.x * kLpThreads + threadIdx.x;
+  if (!same) {  // rows that start at different places of a 16-byte piece: element by element
+    for (int32_t j = first; j < a.vocab; j += stride) {
+      float v;
+      if (sizeof(In) == 2) v = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(x)[j]);
+      else v = reinterpret_cast<const float*>(x)[j];
+      store1<In>(dx + j, q.zero ? 0.0f : grad_of(q, v, j));
+    }
+    return;
+  }
+  const Row<In> row(x, a.vocab);
+  for (int32_t p = first; p < row.pieces; p += U * stride) {
+    uint4 u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int32_t pi = p + i * stride;
+      if (pi < row.pieces && row.whole(pi)) u[i] = *reinterpret_cast<const uint4*>(x + (pi * N - row.off));
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int32_t pi = p + i * stride, j0 = pi * N - row.off;
+      if (pi >= row.pieces) break;
+      if (row.whole(pi)) {
+        float v[N], d[N];
+        values<In>(u[i], v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) d[e] = q.zero ? 0.0f : grad_of(q, v[e], j0 + e);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = sizeof(In) == 2 ? bf16x2_rn(d[(2 * e) % N], d[(2 * e + 1) % N]) : __float_as_uint(d[e]);
+        __stcs(reinterpret_cast<uint4*>(dx + j0), make_uint4(w[0], w[1], w[2], w[3]));
+      } else {
+        for (int e = 0; e < N; ++e) {
+          const int32_t j = j0 + e;
+          if (j < 0 || j >= a.vocab) continue;
+          float v;
+          if (sizeof(In) == 2) v = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(x)[j]);
+          else v = reinterpret_cast<const float*>(x)[j];
+          store1<In>(dx + j, q.zero ? 0.0f : grad_of(q, v, j));
+        }
+      }
+    }
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  return n;
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int64_t kMaxRows = 65535;             // grid y
+constexpr int64_t kMaxVocab = (int64_t)1 << 30;  // 32-bit element and piece numbers
+
+template <typename In, bool TOP>
+cudaError_t launch_logprob(const LpArgs& a, int64_t rows, cudaStream_t stream) {
+  // Two CTAs per SM keep the memory pipes busy; fewer rows than that are
+  // split over a cluster, down to one load round (four pieces a thread) per CTA.
+  const int64_t want = 2 * (int64_t)sm_count();
+  const int64_t round = (int64_t)kLpThreads * kLpUnroll * Row<In>::N;
+  int cluster = 1;
+  while (cluster < 8 && rows * cluster < want && (int64_t)a.vocab > cluster * round) cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cluster, (unsigned)rows);
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<In, TOP>, a);
+}
+
+}  // namespace
+}  // namespace fp8rl
+
+using namespace fp8rl;
+
+extern "C" FP8RL_API fp8rl_status fp8rl_logprob(const void* d_logits, int32_t logits_fp32, int64_t rows, int64_t vocab,
+                                                int64_t ld, float temperature, const int32_t* d_tokens, float* d_lp,
+                                                float* d_entropy, float* d_stats, int64_t topk, int32_t* d_top_ids,
+                                                float* d_top_lp, void* stream) {
+  if (rows < 0 || vocab < 1 || ld < vocab || topk < 0 || !(temperature > 0.0f) || !(temperature <= FLT_MAX) ||
+      (logits_fp32 != 0 && logits_fp32 != 1))
+    return FP8RL_ERR_INVALID_ARG;
+  if (rows == 0) return FP8RL_OK;
+  if (!d_logits || !d_tokens || !d_lp || !d_entropy || !d_stats) return FP8RL_ERR_INVALID_ARG;
+  if (topk > 0 && (!d_top_ids || !d_top_lp)) return FP8RL_ERR_INVALID_ARG;
+  if (topk > kMaxTop || topk > vocab || vocab > kMaxVocab) return FP8RL_ERR_SHAPE;
+  if (!aligned(d_logits, logits_fp32 ? 4 : 2) || !aligned(d_tokens, 4) || !aligned(d_lp, 4) || !aligned(d_entropy, 4) ||
+      !aligned(d_stats, 8) || !aligned(d_top_ids, 4) || !aligned(d_top_lp, 4))
+    return FP8RL_ERR_ALIGNMENT;
+  const size_t size = logits_fp32 ? 4 : 2;
+  for (int64_t r0 = 0; r0 < rows; r0 += kMaxRows) {
+    const int64_t n = std::min(kMaxRows, rows - r0);
+    LpArgs a{};
+    a.x = static_cast<const char*>(d_logits) + r0 * ld * (int64_t)size;
+    a.tokens = d_tokens + r0;
+    a.lp = d_lp + r0;
+    a.entropy = d_entropy + r0;
+    a.stats = reinterpret_cast<float2*>(d_stats) + r0;
+    a.top_ids = topk ? d_top_ids + r0 * topk : nullptr;
+    a.top_lp = topk ? d_top_lp + r0 * topk : nullptr;
+    a.ld = ld;
+    a.vocab = (int32_t)vocab;
+    a.top = (int32_t)topk;
+    a.temperature = temperature;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = logits_fp32 ? (topk ? launch_logprob<float, true>(a, n, cs) : launch_logprob<float, false>(a, n, cs))
+                                      : (topk ? launch_logprob<uint16_t, true>(a, n, cs) : launch_logprob<uint16_t, false>(a, n, cs));
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return FP8RL_ERR_CUDA;
+    }
+  }
+  return cudaGetLastError() == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
+}
+
+extern "C" FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, int32_t logits_fp32, int64_t rows,
+                                                         int64_t vocab, int64_t ld, float temperature,
+                                                         const int32_t* d_tokens, const float* d_stats,
+                                                         const float* d_entropy, const float* d_grad_lp,
+                                                         const float* d_grad_entropy, void* d_dlogits, int64_t ldd,
+                                                         void* stream) {
+  if (rows < 0 || vocab < 1 || ld < vocab || ldd < vocab || !(temperature > 0.0f) || !(temperature <= FLT_MAX) ||
+      (logits_fp32 != 0 && logits_fp32 != 1))
+    return FP8RL_ERR_INVALID_ARG;
+  if (rows == 0) return FP8RL_OK;
+  if (!d_logits || !d_tokens || !d_stats || !d_grad_lp || !d_dlogits || (d_grad_entropy && !d_entropy))
+    return FP8RL_ERR_INVALID_ARG;
+  if (d_dlogits == d_logits && ldd != ld) return FP8RL_ERR_INVALID_ARG;
+  if (vocab > kMaxVocab) return FP8RL_ERR_SHAPE;
+  const uintptr_t size = logits_fp32 ? 4 : 2;
+  if (!aligned(d_logits, size) || !aligned(d_dlogits, size) || !aligned(d_tokens, 4) || !aligned(d_stats, 8) ||
+      !aligned(d_entropy, 4) || !aligned(d_grad_lp, 4) || !aligned(d_grad_entropy, 4))
+    return FP8RL_ERR_ALIGNMENT;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  for (int64_t r0 = 0; r0 < rows; r0 += kMaxRows) {
+    const int64_t n = std::min(kMaxRows, rows - r0);
+    LpGradArgs a{};
+    a.x = static_cast<const char*>(d_logits) + r0 * ld * (int64_t)size;
+    a.dx = static_cast<char*>(d_dlogits) + r0 * ldd * (int64_t)size;
+    a.tokens = d_tokens + r0;
+    a.stats = reinterpret_cast<const float2*>(d_stats) + r0;
+    a.entropy = d_entropy ? d_entropy + r0 : nullptr;
+    a.g_lp = d_grad_lp + r0;
+    a.g_ent = d_grad_entropy ? d_grad_entropy + r0 : nullptr;
+    a.ldx = ld;
+    a.ldd = ldd;
+    a.vocab = (int32_t)vocab;
+    a.temperature = temperature;
+    // one load round (four pieces a thread) per CTA: elementwise work needs no long-lived CTA
+    const int64_t round = (int64_t)kLpThreads * kLpUnroll * (16 / (int64_t)size);
+    const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(65535, (vocab + round - 1) / round)), (unsigned)n);
+    if (logits_fp32) logprob_grad_kernel<float><<<grid, kLpThreads, 0, cs>>>(a);
+    else logprob_grad_kernel<uint16_t><<<grid, kLpThreads, 0, cs>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
+}

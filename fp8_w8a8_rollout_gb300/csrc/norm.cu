@@ -1,0 +1,233 @@
+// norm.cu -- RMS norm with the residual's addition and an E4M3 output.
+//
+// A decoder's residual branch ends in h = x + residual; the next W8A8 linear
+// reads y = h * rsqrt(mean(h^2) + eps) * weight, quantised per 1x128 group
+// ("Method steps", step 1: activations are quantised dynamically in every
+// forward pass).  Fused, y never exists in bf16: h is the fp32 sum, y stays
+// fp32 and is rounded once, to its E4M3 code ("Where Rounding Happens
+// Matters": round once, at the end of the fused region); only the h that the
+// next residual branch reads is rounded to bf16.
+//
+// HBM-bound: 7 bytes an element with a residual (x, residual, h, the code),
+// 3 without.  A CTA takes one row and holds it in registers (8-column pieces,
+// 16 consecutive lanes to a 128-column group), so each input is read once:
+// all its loads, one CTA-wide sum of squares, then the group maxima by four
+// shuffles.  Threads per row and pieces per thread follow k alone.
+#include <algorithm>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace fp8rl {
+namespace {
+
+constexpr int64_t kNormMaxK = 32768;  // a row's pieces held in registers: 1024 threads x 4 pieces x 8
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* res;     // or null
+  const uint16_t* weight;
+  uint16_t* h;             // or null (may be res or x: each element is read by the thread that writes it)
+  uint8_t* q;
+  void* scale;
+  int64_t ldx, ldr, ldh, ldq, m;
+  int32_t k;
+  float eps;
+  uint32_t* err;
+};
+
+// columns c .. c + 7 of a row; columns at or past k read as zero
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int32_t c, int32_t k) {
+  if (VEC) return c < k ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < k) w[e >> 1] |= (uint32_t)row[c + e] << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8_bf16(uint16_t* row, int32_t c, int32_t k, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = bf16x2_rn(v[2 * i], v[2 * i + 1]);
+  if (VEC) {
+    if (c < k) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < k) row[c + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+__device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
+  v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+  v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+}
+
+// VEC: k and every stride a multiple of 8 elements, every pointer 16-byte
+// aligned (codes 8-byte): whole pieces only
+template <int T, int NP, bool VEC, bool UE8M0>
+__global__ void __launch_bounds__(T) rmsnorm_quant_kernel(const NormArgs a) {
+  // as the activation quantiser: the next kernel may start, and this one
+  // waits for the one before it ahead of its first read or write
+  ptx::grid_dep_launch_dependents();
+  ptx::grid_dep_wait();
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const uint16_t* xr = a.x + row * a.ldx;
+  const uint16_t* rr = a.res ? a.res + row * a.ldr : nullptr;
+  uint4 xv[NP], rv[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int32_t c = (tid + j * T) * 8;
+    xv[j] = load8<VEC>(xr, c, a.k);
+    if (rr) rv[j] = load8<VEC>(rr, c, a.k);
+  }
+  float h[NP][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    unpack8(xv[j], h[j]);
+    if (rr) {
+      float r[8];
+      unpack8(rv[j], r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[j][e] += r[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(h[j][e], h[j][e], ss);
+  }
+  if (a.h) {
+    uint16_t* hr = a.h + row * a.ldh;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) store8_bf16<VEC>(hr, (tid + j * T) * 8, a.k, h[j]);
+  }
+  // the row's sum of squares: a fixed tree, the same bits on every run
+  __shared__ float part[T / 32];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+  if ((tid & 31) == 0) part[tid >> 5] = ss;
+  __syncthreads();
+  ss = part[0];
+#pragma unroll
+  for (int w = 1; w < T / 32; ++w) ss += part[w];
+  const float rms = rsqrtf(ss / (float)a.k + a.eps);
+  uint8_t* qr = a.q + row * a.ldq;
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int32_t c = (tid + j * T) * 8;
+    float w[8];
+    unpack8(load8<VEC>(a.weight, c, a.k), w);
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      h[j][e] = h[j][e] * rms * w[e];
+      amax = fmaxf(amax, fabsf(h[j][e]));
+    }
+    // 16 consecutive lanes hold one 128-column group
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    if (c >= a.k) continue;
+    uint32_t code[2];
+    if (UE8M0) {
+      const int e2 = scale_ue8m0_exponent(amax);
+      const float f = exp2_neg(e2);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        code[i] = e4m3x2(h[j][4 * i] * f, h[j][4 * i + 1] * f) | (e4m3x2(h[j][4 * i + 2] * f, h[j][4 * i + 3] * f) << 16);
+      if ((tid & 15) == 0) static_cast<uint8_t*>(a.scale)[(int64_t)(c / kBlock) * a.m + row] = (uint8_t)(e2 + 127);
+    } else {
+      const float s = scale_fp32(amax), r = __frcp_rn(s);
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = s >= kFastDivMinScale ? div_by_scale(h[j][e], s, r) : __fdiv_rn(h[j][e], s);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) code[i] = e4m3x2(y[4 * i], y[4 * i + 1]) | (e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
+      if ((tid & 15) == 0) static_cast<float*>(a.scale)[(int64_t)(c / kBlock) * a.m + row] = s;
+    }
+    if (VEC) {
+      if (dcheck(c + 8 <= a.k, a.err)) *reinterpret_cast<uint2*>(qr + c) = make_uint2(code[0], code[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < a.k) qr[c + e] = (uint8_t)(code[e >> 2] >> (8 * (e & 3)));
+    }
+  }
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+template <int T, int NP>
+cudaError_t launch_norm(const NormArgs& a, bool vec, bool ue8m0, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.m);
+  cfg.blockDim = dim3(T);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  if (vec)
+    return ue8m0 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, true, true>, a)
+                 : cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, true, false>, a);
+  return ue8m0 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, false, true>, a)
+               : cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, false, false>, a);
+}
+
+}  // namespace
+}  // namespace fp8rl
+
+using namespace fp8rl;
+
+extern "C" FP8RL_API fp8rl_status fp8rl_rmsnorm_quant(const void* x_bf16, int64_t ldx, const void* residual_bf16,
+                                                      int64_t ldr, const void* weight_bf16, float eps, int64_t m,
+                                                      int64_t k, void* h_bf16, int64_t ldh, void* q_e4m3, int64_t ldq,
+                                                      void* x_scale, fp8rl_scale_fmt fmt, void* stream) {
+  if (fmt != FP8RL_SCALE_FP32 && fmt != FP8RL_SCALE_UE8M0) return FP8RL_ERR_INVALID_ARG;
+  if (m < 0 || k < 0 || ldx < k || ldq < k || (residual_bf16 && ldr < k) || (h_bf16 && ldh < k) || !(eps >= 0.0f))
+    return FP8RL_ERR_INVALID_ARG;
+  if (m == 0 || k == 0) return FP8RL_OK;
+  if (!x_bf16 || !weight_bf16 || !q_e4m3 || !x_scale) return FP8RL_ERR_INVALID_ARG;
+  if (k > kNormMaxK || m > INT32_MAX) return FP8RL_ERR_SHAPE;
+  if (!aligned(x_bf16, 2) || !aligned(residual_bf16, 2) || !aligned(weight_bf16, 2) || !aligned(h_bf16, 2))
+    return FP8RL_ERR_ALIGNMENT;
+  if (fmt == FP8RL_SCALE_FP32 && !aligned(x_scale, 4)) return FP8RL_ERR_ALIGNMENT;
+  NormArgs a{};
+  a.x = static_cast<const uint16_t*>(x_bf16);
+  a.res = static_cast<const uint16_t*>(residual_bf16);
+  a.weight = static_cast<const uint16_t*>(weight_bf16);
+  a.h = static_cast<uint16_t*>(h_bf16);
+  a.q = static_cast<uint8_t*>(q_e4m3);
+  a.scale = x_scale;
+  a.ldx = ldx, a.ldr = ldr, a.ldh = ldh, a.ldq = ldq, a.m = m;
+  a.k = (int32_t)k;
+  a.eps = eps;
+  a.err = device_error_word();
+  if (!a.err) return FP8RL_ERR_CUDA;
+  const bool vec = k % 8 == 0 && ldx % 8 == 0 && ldq % 8 == 0 && (!residual_bf16 || ldr % 8 == 0) &&
+                   (!h_bf16 || ldh % 8 == 0) && aligned(x_bf16, 16) && aligned(residual_bf16, 16) &&
+                   aligned(weight_bf16, 16) && aligned(h_bf16, 16) && aligned(q_e4m3, 8);
+  const bool ue = fmt == FP8RL_SCALE_UE8M0;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (k <= 1024) e = launch_norm<128, 1>(a, vec, ue, cs);
+  else if (k <= 2048) e = launch_norm<256, 1>(a, vec, ue, cs);
+  else if (k <= 4096) e = launch_norm<256, 2>(a, vec, ue, cs);
+  else if (k <= 8192) e = launch_norm<512, 2>(a, vec, ue, cs);
+  else if (k <= 16384) e = launch_norm<1024, 2>(a, vec, ue, cs);
+  else e = launch_norm<1024, 4>(a, vec, ue, cs);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return FP8RL_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
+}

@@ -36,7 +36,7 @@
  *   - Calls are asynchronous on `stream` (a cudaStream_t passed as void*;
  *     NULL is the legacy default stream).  Results are ready once the stream
  *     is synchronised.
- *   - Overlapped launches: fp8rl_quant_act_group and the GEMMs at decode
+ *   - Overlapped launches: fp8rl_quant_act_group, fp8rl_rmsnorm_quant and the GEMMs at decode
  *     sizes (dense, m <= 64, and up to 128 for the narrow shapes that debug
  *     key 10 lists; fp8rl_gemm_act_quant at m <= 16) are launched
  *     with programmatic stream serialisation, and let the next kernel of the
@@ -557,6 +557,112 @@ FP8RL_API size_t fp8rl_tis_workspace_size(int64_t n);
 FP8RL_API fp8rl_status fp8rl_tis_weights(const float* d_lp_train, const float* d_lp_rollout, const uint8_t* d_mask,
                                          int64_t n, float clip, float* d_w, double* d_kl, void* d_workspace,
                                          size_t workspace_bytes, void* stream);
+
+/*
+ * RMS norm with the residual's addition, quantised for the next W8A8 linear
+ * ("Method steps", step 1: activations are quantised dynamically in every
+ * forward pass; "Where Rounding Happens Matters": a fused region rounds once).
+ *   h = x + residual                       fp32 (x alone without a residual)
+ *   y = h * rsqrt(mean(h^2) + eps) * weight   fp32, never rounded to bf16
+ *   scale, codes of y as fp8rl_quant_act_group, per 1x128 group
+ *   x_bf16        device, bf16 [m][k], row stride ldx
+ *   residual_bf16 device, bf16 [m][k], row stride ldr; null: none
+ *   weight_bf16   device, bf16 [k]
+ *   h_bf16        device, bf16 [m][k], row stride ldh, out: h rounded once (the next
+ *                 residual); null: not written.  May be residual_bf16 or x_bf16 itself.
+ *   q_e4m3        device, E4M3 [m][k], row stride ldq
+ *   x_scale       device, [ceil(k/128)][m], fp32 or uint8 (fmt)
+ * Rows that are 16-byte aligned (k and the strides multiples of 8) take the
+ * vector path; any layout is accepted.  Launched with programmatic stream
+ * serialisation like fp8rl_quant_act_group (it waits for the kernel before it
+ * ahead of its first read).  m == 0 or k == 0 is a no-op.
+ * Errors: INVALID_ARG (null pointers, negative sizes, short strides, eps < 0 or
+ *         NaN, unknown fmt), SHAPE (k > 32768, m >= 2^31), ALIGNMENT (element
+ *         alignment), CUDA.
+ */
+FP8RL_API fp8rl_status fp8rl_rmsnorm_quant(const void* x_bf16, int64_t ldx, const void* residual_bf16, int64_t ldr,
+                                           const void* weight_bf16, float eps, int64_t m, int64_t k, void* h_bf16,
+                                           int64_t ldh, void* q_e4m3, int64_t ldq, void* x_scale,
+                                           fp8rl_scale_fmt fmt, void* stream);
+
+/*
+ * Attention of one new token per sequence over the paged E4M3 KV cache
+ * ("Method steps", step 3), grouped heads: query head i reads KV head
+ * i / (q_heads / kv_heads).  With n = d_lens[b] cached keys,
+ *   s_j = softmax_scale * d_scales[0] * (q . k_j),  out = d_scales[1] * sum_j softmax(s)_j v_j.
+ *   q_bf16          device, bf16 [batch][q_heads * head_dim], row stride ldq
+ *   k_cache, v_cache device, E4M3 [num_slots][ld_cache] as fp8rl_kv_append writes them;
+ *                   KV head h in columns [h * head_dim, (h + 1) * head_dim)
+ *   d_block_table   device, int32 [batch][max_blocks], row stride ldt: key j of sequence b is in
+ *                   cache row table[b][j / block_size] * block_size + j % block_size
+ *   d_lens          device, int32 [batch]: keys of each sequence, the new token's own among them
+ *                   once it has been appended; clamped to [0, max_blocks * block_size]
+ *   d_scales        device, float [2]: the K and V scales of fp8rl_kv_calibrate
+ *   out_bf16        device, bf16 [batch][q_heads * head_dim], row stride ldo
+ *   d_lse           device, fp32 [batch][q_heads]: ln sum_j exp(s_j); or null
+ *   d_workspace     device scratch of fp8rl_attn_decode_workspace_size() bytes, owned by the
+ *                   caller, 16-byte aligned, zeroed once when it is allocated (every call leaves
+ *                   its counters zero).  One call at a time per workspace.
+ * Codes enter the products exactly; scores, softmax statistics and sums are
+ * fp32, the probabilities are rounded to f16, the output once to bf16.  The
+ * table and the lengths are device data and are not read on the host: a key
+ * whose cache row falls outside [0, num_slots) (a table entry of -1) is left
+ * out, and nothing is read for it.  A sequence without keys gives zeros and
+ * lse = -inf.  Cache rows beyond a sequence's keys are not read.  The same
+ * bits on every run; one launch.
+ * Errors: INVALID_ARG (null pointers, negative sizes, short strides, q_heads not a multiple
+ *         of kv_heads, softmax_scale not positive and finite, workspace too small),
+ *         SHAPE (head_dim other than 64 and 128, batch > 8192, more than 2^30 keys a sequence),
+ *         ALIGNMENT (q 4-byte with an even ldq; caches 16-byte with ld_cache % 16 == 0;
+ *         workspace 16-byte; element alignment), CUDA.
+ */
+FP8RL_API size_t fp8rl_attn_decode_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t ldq, int64_t batch, int64_t q_heads,
+                                         int64_t kv_heads, int64_t head_dim, const void* k_cache, const void* v_cache,
+                                         int64_t ld_cache, int64_t num_slots, const int32_t* d_block_table, int64_t ldt,
+                                         int64_t max_blocks, int64_t block_size, const int32_t* d_lens,
+                                         const float* d_scales, float softmax_scale, void* out_bf16, int64_t ldo,
+                                         float* d_lse, void* d_workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Log probabilities of given tokens with entropy and top alternatives: what
+ * fp8rl_tis_weights compares ("Method steps", step 4), from a row of logits x
+ * at temperature T.  With m = max x and S = sum_j exp((x_j - m) / T),
+ *   log p_j = (x_j - m) / T - ln S,   entropy = -sum_j p_j log p_j.
+ *   d_logits    device, bf16 (logits_fp32 = 0) or fp32 (1) [rows][vocab], row stride ld elements
+ *   d_tokens    device, int32 [rows]; a token outside [0, vocab) (padding) marks a row that is not
+ *               read: its outputs are 0, its alternatives' ids -1
+ *   d_lp, d_entropy  device, fp32 [rows] out
+ *   d_stats     device, fp32 [rows][2] out: m and ln S, for the backward pass
+ *   d_top_ids, d_top_lp  device, int32 / fp32 [rows][topk] out: the topk most likely tokens, most likely
+ *               first, equal logits by the lower id (-0 equals 0); null with topk = 0
+ * Logits of -inf have probability 0.  A row of -inf alone gives lp = -inf and
+ * entropy 0; a row with a NaN or +inf gives NaN (its alternatives are
+ * unspecified).  Sums are fp32 in an order that the sizes and the rows'
+ * place in a 16-byte piece fix: the same bits on every run.  One launch per 65535 rows; no workspace.
+ * Errors: INVALID_ARG (null pointers, negative rows, vocab < 1, ld < vocab, T not positive and
+ *         finite, topk < 0), SHAPE (topk > 32 or > vocab, vocab > 2^30), ALIGNMENT (element
+ *         alignment; d_stats 8-byte), CUDA.
+ */
+FP8RL_API fp8rl_status fp8rl_logprob(const void* d_logits, int32_t logits_fp32, int64_t rows, int64_t vocab, int64_t ld,
+                                     float temperature, const int32_t* d_tokens, float* d_lp, float* d_entropy,
+                                     float* d_stats, int64_t topk, int32_t* d_top_ids, float* d_top_lp, void* stream);
+
+/*
+ * Gradient of fp8rl_logprob with respect to the logits, from g = dL/d lp and
+ * (optionally) gh = dL/d entropy of each row:
+ *   dx_j = (g ([j = t] - p_j) - gh p_j (log p_j + entropy)) / T
+ *   d_stats, d_entropy  device, the forward call's outputs (d_entropy may be null without d_grad_entropy)
+ *   d_grad_lp           device, fp32 [rows]
+ *   d_grad_entropy      device, fp32 [rows], or null
+ *   d_dlogits           device, [rows][vocab] of the logits' type, row stride ldd; may be d_logits
+ *                       itself (with ldd = ld), no other overlap
+ * Rows without a token and rows of -inf alone get zeros.  Errors: as fp8rl_logprob.
+ */
+FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, int32_t logits_fp32, int64_t rows, int64_t vocab,
+                                              int64_t ld, float temperature, const int32_t* d_tokens,
+                                              const float* d_stats, const float* d_entropy, const float* d_grad_lp,
+                                              const float* d_grad_entropy, void* d_dlogits, int64_t ldd, void* stream);
 
 /* Static, NUL-terminated name of a status code. */
 FP8RL_API const char* fp8rl_status_string(fp8rl_status s);
