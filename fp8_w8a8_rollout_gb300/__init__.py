@@ -31,6 +31,7 @@ __all__ = [
     "fp8rl_gemm_blockscaled_static", "fp8rl_gemm_swiglu_quant", "fp8rl_grouped_gemm_swiglu_quant",
     "gemm_swiglu_quant", "grouped_gemm_swiglu_quant", "quant_gate_up_interleaved",
     "fp8rl_kv_calibrate", "fp8rl_kv_append", "kv_calibrate", "kv_append",
+    "fp8rl_attn_prefill_plan_size", "fp8rl_attn_prefill_plan", "fp8rl_attn_prefill", "attn_prefill_plan", "attn_prefill",
     "fp8rl_rmsnorm_quant", "rmsnorm_quant", "fp8rl_attn_decode_workspace_size", "fp8rl_attn_decode",
     "attn_decode_workspace", "attn_decode", "fp8rl_logprob", "fp8rl_logprob_backward", "logprobs", "logprobs_backward",
     "fp8rl_e4m3_encode", "fp8rl_debug_set", "fp8rl_sync_status", "fp8rl_status_string", "fp8rl_version",
@@ -107,6 +108,10 @@ def load_library(build_if_missing: bool = False):
             "fp8rl_tis_workspace_size": [i64],
             "fp8rl_tis_weights": [vp, vp, vp, i64, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp],
             "fp8rl_rmsnorm_quant": [vp, i64, vp, i64, vp, ctypes.c_float, i64, i64, vp, i64, vp, i64, vp, st, vp],
+            "fp8rl_attn_prefill_plan_size": [i64, i64, i64, i64],
+            "fp8rl_attn_prefill_plan": [vp, i64, i64, i64, i64, vp, ctypes.c_size_t, vp],
+            "fp8rl_attn_prefill": [vp, i64, vp, i64, vp, i64, vp, ctypes.c_size_t, i64, i64, i64, i64, i64,
+                                   ctypes.c_float, vp, i64, vp, vp],
             "fp8rl_attn_decode_workspace_size": [i64, i64, i64],
             "fp8rl_attn_decode": [vp, i64, i64, i64, i64, i64, vp, vp, i64, i64, vp, i64, i64, i64, vp, vp,
                                   ctypes.c_float, vp, i64, vp, vp, ctypes.c_size_t, vp],
@@ -125,6 +130,7 @@ def load_library(build_if_missing: bool = False):
         lib.fp8rl_moe_plan_workspace_size.restype = ctypes.c_size_t
         lib.fp8rl_host_sync_staging_bytes.restype = ctypes.c_size_t
         lib.fp8rl_tis_workspace_size.restype = ctypes.c_size_t
+        lib.fp8rl_attn_prefill_plan_size.restype = ctypes.c_size_t
         lib.fp8rl_attn_decode_workspace_size.restype = ctypes.c_size_t
         lib.fp8rl_version.restype = i32
         _lib = lib
@@ -294,6 +300,24 @@ def fp8rl_rmsnorm_quant(x_bf16, ldx, residual_bf16, ldr, weight_bf16, eps, m, k,
     _ok(load_library().fp8rl_rmsnorm_quant(_p(x_bf16), ldx, _p(residual_bf16), ldr, _p(weight_bf16), eps, m, k,
                                            _p(h_bf16), ldh, _p(q_e4m3), ldq, _p(x_scale), fmt, _stream(stream)),
         "fp8rl_rmsnorm_quant")
+
+
+def fp8rl_attn_prefill_plan_size(total_tokens, batch, q_heads, kv_heads) -> int:
+    return int(load_library().fp8rl_attn_prefill_plan_size(total_tokens, batch, q_heads, kv_heads))
+
+
+def fp8rl_attn_prefill_plan(d_cu_seqlens, batch, total_tokens, q_heads, kv_heads, d_plan, plan_bytes, stream=None) -> None:
+    _ok(load_library().fp8rl_attn_prefill_plan(_p(d_cu_seqlens), batch, total_tokens, q_heads, kv_heads, _p(d_plan),
+                                               plan_bytes, _stream(stream)),
+        "fp8rl_attn_prefill_plan")
+
+
+def fp8rl_attn_prefill(q_bf16, ldq, k_bf16, ldk, v_bf16, ldv, d_plan, plan_bytes, batch, total_tokens, q_heads, kv_heads,
+                       head_dim, softmax_scale, out_bf16, ldo, d_lse, stream=None) -> None:
+    _ok(load_library().fp8rl_attn_prefill(_p(q_bf16), ldq, _p(k_bf16), ldk, _p(v_bf16), ldv, _p(d_plan), plan_bytes,
+                                          batch, total_tokens, q_heads, kv_heads, head_dim, softmax_scale, _p(out_bf16),
+                                          ldo, _p(d_lse), _stream(stream)),
+        "fp8rl_attn_prefill")
 
 
 def fp8rl_attn_decode_workspace_size(q_heads, kv_heads, head_dim) -> int:
@@ -752,6 +776,55 @@ def _check_heads(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be a bf16 [tokens, heads, head_dim] tensor")
     if (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
+
+
+class AttnPlan:
+    """The work layout of attn_prefill for one set of packed sequences and
+    heads (attn_prefill_plan): one per step, used by every layer."""
+
+    def __init__(self, data, batch, total_tokens, q_heads, kv_heads):
+        self.data, self.batch, self.total_tokens = data, batch, total_tokens
+        self.q_heads, self.kv_heads = q_heads, kv_heads
+
+
+def attn_prefill_plan(cu_seqlens: torch.Tensor, total_tokens: int, q_heads: int, kv_heads: int, stream=None) -> AttnPlan:
+    """The plan of packed sequences: sequence b is tokens [cu_seqlens[b],
+    cu_seqlens[b + 1]) (device int32 [batch + 1]) of total_tokens."""
+    _check_cuda(cu_seqlens)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 [batch + 1] tensor")
+    batch = cu_seqlens.numel() - 1
+    nbytes = fp8rl_attn_prefill_plan_size(total_tokens, batch, q_heads, kv_heads)
+    if nbytes == 0:
+        raise ValueError("q_heads must be a multiple of kv_heads, at most 2^30 tokens and 2^20 sequences")
+    data = _out((nbytes,), torch.uint8, cu_seqlens.device)
+    fp8rl_attn_prefill_plan(cu_seqlens, batch, total_tokens, q_heads, kv_heads, data, nbytes, stream)
+    return AttnPlan(data, batch, total_tokens, q_heads, kv_heads)
+
+
+def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPlan, softmax_scale: float | None = None,
+                 out=None, stream=None):
+    """(out bf16 [tokens, q_heads, d], lse fp32 [tokens, q_heads]): causal
+    attention over packed prompts (q [tokens, q_heads, d], k and v [tokens,
+    kv_heads, d]; column ranges of one projection's output are fine).
+    softmax_scale defaults to d ** -0.5."""
+    _check_cuda(q, k, v, plan.data, *(out or ()))
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_heads(t, name)
+    tokens, hq, d = q.shape
+    hkv = k.shape[1]
+    if k.shape != (tokens, hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [tokens, kv_heads, head_dim] with q's tokens and head_dim")
+    if (plan.total_tokens, plan.q_heads, plan.kv_heads) != (tokens, hq, hkv):
+        raise ValueError("the plan was made for other sizes")
+    if out is None:
+        out = (_out((tokens, hq, d), torch.bfloat16, q.device), _out((tokens, hq), torch.float32, q.device))
+    else:
+        _check_out(out[0], (tokens, hq, d), torch.bfloat16, "out")
+        _check_out(out[1], (tokens, hq), torch.float32, "lse")
+    fp8rl_attn_prefill(q, _ld(q), k, _ld(k), v, _ld(v), plan.data, plan.data.numel(), plan.batch, tokens, hq, hkv, d,
+                       d ** -0.5 if softmax_scale is None else softmax_scale, out[0], hq * d, out[1], stream)
+    return out
 
 
 def attn_decode_workspace(q_heads: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:

@@ -1,0 +1,706 @@
+// attn_prefill.cu -- causal attention over whole prompts, packed, with grouped
+// heads: the attention between the W8A8 linears of a prefill (queries, keys
+// and values are column ranges of the qkv linear's bf16 output).
+//
+// For sequence position i and the keys j <= i of its sequence:
+//   s_ij = softmax_scale (q_i . k_j),  out_i = sum_j exp(s_ij - m_i) v_j / l_i,
+//   l_i = sum_j exp(s_ij - m_i),       lse_i = m_i + ln l_i.
+//
+// Compute-bound (4 d flop per query-key pair and head): both products run on
+// tcgen05 with fp32 accumulators in TMEM.  One CTA per SM walks work items; an
+// item is two tiles of 128 query rows of one KV head.  A tile's rows are
+// (position, head) pairs: the query heads that share a KV head lie side by
+// side in memory, so a TMA box of `pack` heads x 128 / pack positions fills a
+// tile and one pass over the keys serves all of them (and the diagonal
+// wastes at most a key tile per 128 / pack positions).
+//
+// Roles: a TMA thread streams 128-key tiles of K and V through a ring of five
+// 32 KB stages; an MMA thread issues S = Q K^T (shared memory x shared memory)
+// and O += P V (P from TMEM, V as it lies in memory, d contiguous) for the two
+// tiles in turn, so the tensor cores multiply for one tile while the other's
+// softmax runs; two warpgroups do the softmax, a thread per row, with no
+// exchange between threads: the row's 128 scores to registers, their maximum,
+// exp2, the row sum, and P as bf16 back over the scores' columns.  The running
+// maximum is allowed to lag by 8 (base 2): only when a row grows past that is
+// its O read from TMEM, rescaled and written back, before P is handed over.
+//
+// P is rounded to bf16 because both operands of a tcgen05 f16-kind product
+// have one type and V is bf16; l sums the unrounded fp32 values.  Statistics
+// and accumulators are fp32, the output is rounded once.
+//
+// The plan (one per step, used by every layer) lists the items, longest key
+// range first; CTAs take them in snake order, which evens the causal lengths
+// out.  Every wait is bounded.
+#include <algorithm>
+#include <cfloat>
+#include <mutex>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace fp8rl {
+namespace {
+
+using namespace ptx;
+
+constexpr int kApThreads = 384;     // warps 0-3: roles, 4-7 and 8-11: softmax of tile 0 and 1
+constexpr int kApTile = 128;        // query rows of a tile, keys of a key tile
+constexpr int kApStages = 5;
+constexpr int kApRoleRegs = 64, kApSoftmaxRegs = 216;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;
+constexpr uint64_t kApTimeoutNs = 2000000000ull;
+
+// the plan: a header, then one int4 per item {first token of the sequence,
+// its length, first position of the item, 0}
+struct PlanHeader {
+  int32_t items, span, total, batch;  // span: positions of an item
+};
+
+struct ApArgs {
+  const int4* plan;
+  uint16_t* out;
+  float* lse;  // or null
+  uint32_t* err;
+  int64_t ldo;
+  int32_t capacity, total, hq, hkv, group, pack;
+  float softmax_scale;
+};
+
+template <int D>
+struct ApCfg {
+  static constexpr int kHalves = D / 64;                      // 64-column (128-byte) parts of a row
+  static constexpr uint32_t kHalfBytes = kApTile * 128;       // 16 KB
+  static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
+  static constexpr uint32_t kRing = 2 * kTileBytes;           // byte offset of the key/value stages
+  static constexpr uint32_t kBook = kRing + kApStages * kTileBytes;
+  static constexpr uint32_t kSmem = kBook + 256 + 1024;       // barriers; alignment
+  static constexpr uint32_t kTmemS = 0, kTmemO = 256;         // S of tile x at 128 x, O at 256 + 128 x
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// Instruction descriptor of tcgen05.mma kind::f16: D fp32 (bits 4-5 = 1), A
+// and B bf16 (bits 7-9, 10-12 = 1), A K-major, B K-major or (bit 16) with its
+// N index contiguous, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool b_n_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// Descriptor of a B tile whose N index is contiguous: rows (K index) of 128
+// swizzled bytes = 64 N elements; the next 64 N elements `half` bytes further
+// (leading byte offset), the next 8 rows 1024 bytes further (stride byte offset).
+__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr, uint32_t half) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(half >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[smem] * B[smem], one M x N x 16 bf16 step
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// the same with A in TMEM (row r in lane r, two bf16 per 32-bit column)
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+struct Item {
+  int32_t start, len, pos0;  // sequence's first token, its length, first position
+  int32_t head0, kvh;        // first query head, KV head
+  int32_t n[2];              // key tiles of the two query tiles
+};
+
+// work index w of the snake order, round r: item w / heads, head part w % heads
+__device__ __forceinline__ Item item_of(const ApArgs& a, int64_t w, int32_t parts) {
+  const int4 p = a.plan[1 + w / (a.hkv * parts)];
+  const int32_t hp = (int32_t)(w % (a.hkv * parts));
+  Item it;
+  it.start = p.x;
+  it.len = p.y;
+  it.pos0 = p.z;
+  it.kvh = hp / parts;
+  it.head0 = it.kvh * a.group + (hp % parts) * a.pack;
+  const int32_t span = kApTile / a.pack;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int32_t first = it.pos0 + x * span;
+    it.n[x] = first < it.len ? (min(it.len, first + span) + kApTile - 1) / kApTile : 0;
+  }
+  return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kApThreads, 1)
+    attn_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const ApArgs a) {
+  using C = ApCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(base_ptr + C::kBook);
+  uint64_t* kv_empty = kv_full + kApStages;
+  uint64_t* q_full = kv_empty + kApStages;  // one per tile
+  uint64_t* q_empty = q_full + 2;           // both tiles' scores of an item are done
+  uint64_t* s_full = q_empty + 1;           // scores of a tile in TMEM
+  uint64_t* p_full = s_full + 2;            // P of a tile in TMEM, O rescaled (128 threads)
+  uint64_t* o_full = p_full + 2;            // O of a tile finished
+  uint64_t* drain = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  volatile int* abortv = abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kApStages; ++s) {
+      mbar_init(smem_u32(&kv_full[s]), 1);
+      mbar_init(smem_u32(&kv_empty[s]), 1);
+    }
+    mbar_init(smem_u32(q_empty), 1);
+    mbar_init(smem_u32(drain), 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&q_full[x]), 1);
+      mbar_init(smem_u32(&s_full[x]), 1);
+      mbar_init(smem_u32(&p_full[x]), kApTile);
+      mbar_init(smem_u32(&o_full[x]), 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 2) tmem_alloc(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const PlanHeader head = *reinterpret_cast<const PlanHeader*>(a.plan);
+  const int32_t parts = a.group / a.pack;
+  const bool fits = head.span == 2 * kApTile / a.pack && head.total == a.total && head.items >= 0 && head.items <= a.capacity;
+  if (!fits && threadIdx.x == 0 && a.err) atomicOr(a.err, kErrDeviceCheck);
+  const int64_t work = fits ? (int64_t)head.items * a.hkv * parts : 0;
+  const int64_t grid = gridDim.x;
+  // this CTA's r-th work index, or past the end
+  auto work_of = [&](int64_t r) { return r * grid + ((r & 1) ? grid - 1 - blockIdx.x : blockIdx.x); };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kApRoleRegs));
+    if (warp == 0) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+        uint32_t g = 0, items = 0;
+        uint32_t q_issued[2] = {0, 0};
+        bool alive = true;
+        auto load_kv = [&](const CUtensorMap* map, const Item& it, int32_t j) {
+          const int s = g % kApStages;
+          if (!mbar_wait_bounded(smem_u32(&kv_empty[s]), ((g / kApStages) & 1) ^ 1, abortv, a.err, kApTimeoutNs)) return false;
+          const uint32_t bar = smem_u32(&kv_full[s]);
+          mbar_arrive_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(base + C::kRing + s * C::kTileBytes + h * C::kHalfBytes, map, 64 * h, it.kvh, it.start + j * kApTile, bar);
+          ++g;
+          return true;
+        };
+        for (int64_t r = 0; alive; ++r) {
+          const int64_t w = work_of(r);
+          if (r * grid >= work) break;
+          if (w >= work) continue;
+          const Item it = item_of(a, w, parts);
+          const int32_t n = max(it.n[0], it.n[1]);
+          if (n == 0) continue;
+          if (!mbar_wait_bounded(smem_u32(q_empty), (items & 1) ^ 1, abortv, a.err, kApTimeoutNs)) break;
+          ++items;
+          for (int x = 0; x < 2; ++x) {
+            if (it.n[x] == 0) continue;
+            const uint32_t bar = smem_u32(&q_full[x]);
+            mbar_arrive_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_3d(base + x * C::kTileBytes + h * C::kHalfBytes, &map_q, 64 * h, it.head0,
+                          it.start + it.pos0 + x * (kApTile / a.pack), bar);
+            ++q_issued[x];
+            if (x == 0) alive = load_kv(&map_k, it, 0);  // the first tile's scores need no more than this
+            if (!alive) break;
+          }
+          for (int32_t j = 0; j < n && alive; ++j) {
+            alive = load_kv(&map_v, it, j);
+            if (alive && j + 1 < n) alive = load_kv(&map_k, it, j + 1);
+          }
+        }
+        if (*abortv) {
+          // let the copies still in flight land before shared memory is released
+          for (uint32_t j = g > (uint32_t)kApStages ? g - kApStages : 0; j < g; ++j)
+            mbar_wait_bounded(smem_u32(&kv_full[j % kApStages]), (j / kApStages) & 1, nullptr, nullptr, 10000000ull);
+          for (int x = 0; x < 2; ++x)
+            if (q_issued[x]) mbar_wait_bounded(smem_u32(&q_full[x]), (q_issued[x] - 1) & 1, nullptr, nullptr, 10000000ull);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer (all lanes wait, lane 0 issues)
+      constexpr uint32_t kDescQk = idesc_bf16(kApTile, kApTile, false), kDescPv = idesc_bf16(kApTile, D, true);
+      uint32_t g = 0;                    // stages consumed
+      uint32_t q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
+      bool alive = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), parity, abortv, a.err, kApTimeoutNs)) != 0;
+      };
+      auto scores = [&](int x, uint32_t stage) {  // S_x = Q_x K^T
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_bf16_ss(tmem + C::kTmemS + 128 * x, sw128_kmajor_desc(base + x * C::kTileBytes + (k >> 2) * C::kHalfBytes + (k & 3) * 32),
+                        sw128_kmajor_desc(base + C::kRing + stage * C::kTileBytes + (k >> 2) * C::kHalfBytes + (k & 3) * 32), kDescQk,
+                        k > 0);
+          mma_commit(smem_u32(&s_full[x]));
+        }
+        __syncwarp();
+      };
+      auto values = [&](int x, uint32_t stage, bool first) {  // O_x (+)= P_x V
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < kApTile / 16; ++k)
+            mma_bf16_ts(tmem + C::kTmemO + 128 * x, tmem + C::kTmemS + 128 * x + 8 * k,
+                        sw128_nmajor_desc(base + C::kRing + stage * C::kTileBytes + k * 2048, C::kHalfBytes), kDescPv, !first || k > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (lane == 0) mma_commit(smem_u32(bar));
+        __syncwarp();
+      };
+      for (int64_t r = 0; alive; ++r) {
+        const int64_t w = work_of(r);
+        if (r * grid >= work) break;
+        if (w >= work) continue;
+        const Item it = item_of(a, w, parts);
+        const int32_t n = max(it.n[0], it.n[1]);
+        if (n == 0) continue;
+        uint32_t ks = g % kApStages;
+        alive = wait(&kv_full[ks], (g / kApStages) & 1);
+        ++g;
+        for (int x = 0; x < 2 && alive; ++x) {
+          if (it.n[x] == 0) continue;
+          alive = wait(&q_full[x], q_seen[x] & 1);
+          ++q_seen[x];
+          if (alive) {
+            tc_fence_after();
+            scores(x, ks);
+          }
+        }
+        if (!alive) break;
+        commit(&kv_empty[ks]);
+        if (n == 1) commit(q_empty);
+        for (int32_t j = 0; j < n && alive; ++j) {
+          const uint32_t vs = g % kApStages;
+          alive = wait(&kv_full[vs], (g / kApStages) & 1);
+          ++g;
+          if (!alive) break;
+          const int32_t valid = it.len - j * kApTile;
+          if (valid < kApTile) {
+            // Rows past the sequence's end are another sequence's values, and
+            // a probability of 0 does not cancel a NaN: zero them.
+            const uint32_t v0 = C::kRing + vs * C::kTileBytes;
+            for (int32_t i = valid * 8 + lane; i < kApTile * 8; i += 32)
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+                *reinterpret_cast<uint4*>(base_ptr + v0 + h * C::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_shared();
+            __syncwarp();
+          }
+          const uint32_t kn = g % kApStages;
+          if (j + 1 < n) {
+            alive = wait(&kv_full[kn], (g / kApStages) & 1);
+            ++g;
+            if (!alive) break;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (j < it.n[x]) {
+              alive = alive && wait(&p_full[x], p_seen[x] & 1);
+              ++p_seen[x];
+              if (!alive) break;
+              tc_fence_after();
+              values(x, vs, j == 0);
+              if (j + 1 == it.n[x]) commit(&o_full[x]);
+            }
+            if (x == 1) commit(&kv_empty[vs]);
+            if (j + 1 < it.n[x]) scores(x, kn);
+          }
+          if (!alive) break;
+          if (j + 1 < n) commit(&kv_empty[kn]);
+          if (j + 2 == n) commit(q_empty);  // the item's last scores are issued
+        }
+      }
+      // every product issued so far has finished with shared memory and TMEM
+      commit(drain);
+      mbar_wait_bounded(smem_u32(drain), 0, nullptr, a.err, kApTimeoutNs);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax: thread = row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kApSoftmaxRegs));
+    const int x = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t ts = tmem + lanes + C::kTmemS + 128 * x, to = tmem + lanes + C::kTmemO + 128 * x;
+    const float c = a.softmax_scale * kLog2e;
+    const uint64_t c2 = f32x2(c, c);
+    uint32_t s_seen = 0, o_seen = 0;
+    bool alive = true;
+    for (int64_t r = 0; alive; ++r) {
+      const int64_t w = work_of(r);
+      if (r * grid >= work) break;
+      if (w >= work) continue;
+      const Item it = item_of(a, w, parts);
+      const int32_t n = it.n[x];
+      if (n == 0) continue;
+      const int32_t first = it.pos0 + x * (kApTile / a.pack), pos = first + row / a.pack, head = it.head0 + row % a.pack;
+      float mc = -INFINITY;  // reference maximum times c
+      uint64_t l2 = f32x2(0.0f, 0.0f);
+      for (int32_t j = 0; j < n; ++j) {
+        alive = mbar_wait_bounded(smem_u32(&s_full[x]), s_seen & 1, abortv, a.err, kApTimeoutNs);
+        ++s_seen;
+        if (!__all_sync(0xffffffffu, alive)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * i]));
+        tmem_wait_ld();
+        if (j * kApTile + kApTile - 1 > first) {  // a key tile that reaches past the tile's first position
+          const int32_t lim = pos - j * kApTile;  // keys 0 .. lim of the tile count
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > lim) s[i] = 0xFF800000u;
+        }
+        float m4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m4[i] = __uint_as_float(s[i]);
+#pragma unroll
+        for (int i = 4; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(s[i]));
+        const float big = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+        const bool grow = big > mc + kRescale;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2(mc - big) : 1.0f;  // 0 for the first key tile
+          if (grow) mc = big;
+          const uint64_t f2 = f32x2(f, f);
+          l2 = mul_f32x2(l2, f2);
+          if (j > 0) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + 32 * i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x32(to + 32 * i, o);
+            }
+          }
+        }
+        const uint64_t nm2 = f32x2(-mc, -mc);
+        uint32_t p[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const uint64_t y = fma_f32x2(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, nm2);
+          float y0, y1;
+          f32x2_unpack(y, y0, y1);
+          y0 = ex2(y0);
+          y1 = ex2(y1);
+          l2 = add_f32x2(l2, f32x2(y0, y1));
+          p[i] = bf16x2_rn(y0, y1);
+        }
+        tmem_st_32x32b_x32(ts, p);
+        tmem_st_32x32b_x32(ts + 32, p + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_full[x]));
+      }
+      if (!alive) break;
+      alive = mbar_wait_bounded(smem_u32(&o_full[x]), o_seen & 1, abortv, a.err, kApTimeoutNs);
+      ++o_seen;
+      if (!__all_sync(0xffffffffu, alive)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      float la, lb;
+      f32x2_unpack(l2, la, lb);
+      const float l = la + lb, inv = 1.0f / l;
+      const bool store = pos < it.len;
+      const int64_t token = (int64_t)it.start + pos;
+      uint16_t* dst = a.out + token * a.ldo + (int64_t)head * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(to + 32 * i, o);
+        tmem_wait_ld();
+        if (store) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              v[q] = bf16x2_rn(__uint_as_float(o[8 * e + 2 * q]) * inv, __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
+            *reinterpret_cast<uint4*>(dst + 32 * i + 8 * e) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+      if (store && a.lse) a.lse[token * a.hq + head] = fmaf(mc, kLn2, logf(l));
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ plan
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanLevels = 2048;
+
+// One CTA: items of every sequence sorted by their number of key tiles, the
+// most first (a counting sort over at most 2048 levels; the order among
+// equals is free: it only says which CTA computes an item).
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int32_t* __restrict__ cu, int32_t batch, int32_t total,
+                                                                int32_t span, int32_t capacity, int4* __restrict__ plan) {
+  __shared__ int32_t count[kPlanLevels];
+  __shared__ int32_t warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t top = (total + kApTile - 1) / kApTile;
+  int shift = 0;
+  while ((top >> shift) >= kPlanLevels) ++shift;
+  for (int i = tid; i < kPlanLevels; i += kPlanThreads) count[i] = 0;
+  __syncthreads();
+  auto each = [&](auto&& f) {
+    for (int32_t b = warp; b < batch; b += kPlanThreads / 32) {
+      const int32_t start = min(max(cu[b], 0), total), end = min(max(cu[b + 1], start), total);
+      for (int32_t p = lane * span; p < end - start; p += 32 * span) {
+        const int32_t tiles = (min(end - start, p + span) + kApTile - 1) / kApTile;
+        f(kPlanLevels - 1 - (tiles >> shift), start, end - start, p);
+      }
+    }
+  };
+  each([&](int level, int32_t, int32_t, int32_t) { atomicAdd(&count[level], 1); });
+  __syncthreads();
+  // exclusive scan, two levels a thread
+  const int32_t c0 = count[2 * tid], c1 = count[2 * tid + 1];
+  int32_t v = c0 + c1;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += y;
+  }
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int32_t s = warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += y;
+    }
+    warp_sum[lane] = s;
+  }
+  __syncthreads();
+  const int32_t before = (warp ? warp_sum[warp - 1] : 0) + v - c0 - c1;
+  count[2 * tid] = before;
+  count[2 * tid + 1] = before + c0;
+  const int32_t items = warp_sum[31];
+  __syncthreads();
+  each([&](int level, int32_t start, int32_t len, int32_t p) {
+    const int32_t at = atomicAdd(&count[level], 1);
+    if (at < capacity) plan[1 + at] = make_int4(start, len, p, 0);
+  });
+  if (tid == 0) *reinterpret_cast<PlanHeader*>(plan) = PlanHeader{min(items, capacity), span, total, batch};
+}
+
+// ------------------------------------------------------------------ host
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+  });
+  return fn;
+}
+
+// bf16 [tokens][heads][d], token stride ld elements: boxes of 64 columns x
+// box_heads heads x box_tokens tokens, 128-byte swizzle, zeros past the end
+bool make_map(CUtensorMap* map, const void* base, int64_t d, int64_t heads, int64_t tokens, int64_t ld, uint32_t box_heads,
+              uint32_t box_tokens) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
+  cuuint32_t box[3] = {64, box_heads, box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  return n;
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool heads_ok(int64_t q_heads, int64_t kv_heads) { return q_heads >= 1 && kv_heads >= 1 && q_heads <= 65536 && q_heads % kv_heads == 0; }
+
+// heads of a group in one tile: the largest power of two (at most 128) that divides it
+int64_t pack_of(int64_t group) {
+  int64_t p = 1;
+  while (p < kApTile && group % (2 * p) == 0) p *= 2;
+  return p;
+}
+
+int64_t plan_capacity(int64_t total, int64_t batch, int64_t pack) { return total / (2 * kApTile / pack) + batch; }
+
+template <int D>
+fp8rl_status launch_prefill(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const ApArgs& a,
+                            cudaStream_t stream) {
+  auto kernel = attn_prefill_kernel<D>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ApCfg<D>::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return FP8RL_ERR_CUDA;
+  }
+  const int64_t most = (int64_t)a.capacity * a.hkv * (a.group / a.pack);
+  kernel<<<(unsigned)std::max<int64_t>(1, std::min<int64_t>(sm_count(), most)), kApThreads, ApCfg<D>::kSmem, stream>>>(mq, mk, mv, a);
+  return cudaGetLastError() == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace fp8rl
+
+using namespace fp8rl;
+
+extern "C" FP8RL_API size_t fp8rl_attn_prefill_plan_size(int64_t total_tokens, int64_t batch, int64_t q_heads,
+                                                         int64_t kv_heads) {
+  if (total_tokens < 0 || total_tokens > (1 << 30) || batch < 0 || batch > (1 << 20) || !heads_ok(q_heads, kv_heads)) return 0;
+  return (size_t)(16 * (1 + plan_capacity(total_tokens, batch, pack_of(q_heads / kv_heads))));
+}
+
+extern "C" FP8RL_API fp8rl_status fp8rl_attn_prefill_plan(const int32_t* d_cu_seqlens, int64_t batch, int64_t total_tokens,
+                                                          int64_t q_heads, int64_t kv_heads, void* d_plan,
+                                                          size_t plan_bytes, void* stream) {
+  if (batch < 0 || total_tokens < 0 || !heads_ok(q_heads, kv_heads)) return FP8RL_ERR_INVALID_ARG;
+  if (total_tokens > (1 << 30) || batch > (1 << 20)) return FP8RL_ERR_SHAPE;
+  if (!d_plan || (batch > 0 && !d_cu_seqlens)) return FP8RL_ERR_INVALID_ARG;
+  if (plan_bytes < fp8rl_attn_prefill_plan_size(total_tokens, batch, q_heads, kv_heads)) return FP8RL_ERR_INVALID_ARG;
+  if (!aligned(d_plan, 16) || !aligned(d_cu_seqlens, 4)) return FP8RL_ERR_ALIGNMENT;
+  const int64_t pack = pack_of(q_heads / kv_heads);
+  attn_plan_kernel<<<1, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      d_cu_seqlens, (int32_t)batch, (int32_t)total_tokens, (int32_t)(2 * kApTile / pack),
+      (int32_t)plan_capacity(total_tokens, batch, pack), static_cast<int4*>(d_plan));
+  return cudaGetLastError() == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
+}
+
+extern "C" FP8RL_API fp8rl_status fp8rl_attn_prefill(const void* q_bf16, int64_t ldq, const void* k_bf16, int64_t ldk,
+                                                     const void* v_bf16, int64_t ldv, const void* d_plan,
+                                                     size_t plan_bytes, int64_t batch, int64_t total_tokens,
+                                                     int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                                     float softmax_scale, void* out_bf16, int64_t ldo, float* d_lse,
+                                                     void* stream) {
+  if (batch < 0 || total_tokens < 0 || !heads_ok(q_heads, kv_heads) || head_dim < 1 || !(softmax_scale > 0.0f) ||
+      !(softmax_scale <= FLT_MAX))
+    return FP8RL_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128) || total_tokens > (1 << 30) || batch > (1 << 20)) return FP8RL_ERR_SHAPE;
+  if (ldq < q_heads * head_dim || ldk < kv_heads * head_dim || ldv < kv_heads * head_dim || ldo < q_heads * head_dim)
+    return FP8RL_ERR_INVALID_ARG;
+  if (batch == 0 || total_tokens == 0) return FP8RL_OK;
+  if (!q_bf16 || !k_bf16 || !v_bf16 || !d_plan || !out_bf16) return FP8RL_ERR_INVALID_ARG;
+  if (plan_bytes < fp8rl_attn_prefill_plan_size(total_tokens, batch, q_heads, kv_heads)) return FP8RL_ERR_INVALID_ARG;
+  if (!aligned(q_bf16, 16) || !aligned(k_bf16, 16) || !aligned(v_bf16, 16) || !aligned(out_bf16, 16) || ldq % 8 != 0 ||
+      ldk % 8 != 0 || ldv % 8 != 0 || ldo % 8 != 0 || !aligned(d_plan, 16) || !aligned(d_lse, 4))
+    return FP8RL_ERR_ALIGNMENT;
+  ApArgs a{};
+  a.plan = static_cast<const int4*>(d_plan);
+  a.out = static_cast<uint16_t*>(out_bf16);
+  a.lse = d_lse;
+  a.ldo = ldo;
+  a.total = (int32_t)total_tokens;
+  a.hq = (int32_t)q_heads, a.hkv = (int32_t)kv_heads;
+  a.group = (int32_t)(q_heads / kv_heads);
+  a.pack = (int32_t)pack_of(a.group);
+  a.capacity = (int32_t)plan_capacity(total_tokens, batch, a.pack);
+  a.softmax_scale = softmax_scale;
+  a.err = device_error_word();
+  if (!a.err) return FP8RL_ERR_CUDA;
+  CUtensorMap mq, mk, mv;
+  if (!make_map(&mq, q_bf16, head_dim, q_heads, total_tokens, ldq, (uint32_t)a.pack, (uint32_t)(kApTile / a.pack)) ||
+      !make_map(&mk, k_bf16, head_dim, kv_heads, total_tokens, ldk, 1, kApTile) ||
+      !make_map(&mv, v_bf16, head_dim, kv_heads, total_tokens, ldv, 1, kApTile))
+    return FP8RL_ERR_CUDA;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return head_dim == 128 ? launch_prefill<128>(mq, mk, mv, a, cs) : launch_prefill<64>(mq, mk, mv, a, cs);
+}

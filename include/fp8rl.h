@@ -79,8 +79,9 @@ typedef enum {
     FP8RL_ERR_UNSUPPORTED = 4, /* device is not sm_103 / feature unavailable */
     FP8RL_ERR_CUDA = 5,        /* a CUDA runtime or driver call failed       */
     FP8RL_ERR_TIMEOUT = 6,     /* a device-side bounded wait ran out         */
-    FP8RL_ERR_DEVICE_CHECK = 7 /* a device-side bounds check failed (builds
-                                  with FP8RL_DEBUG only; the store was skipped) */
+    FP8RL_ERR_DEVICE_CHECK = 7 /* a device-side check failed: a store's bounds
+                                  (builds with FP8RL_DEBUG only; the store was
+                                  skipped), or an attention plan of other sizes */
 } fp8rl_status;
 
 typedef enum {
@@ -584,6 +585,47 @@ FP8RL_API fp8rl_status fp8rl_rmsnorm_quant(const void* x_bf16, int64_t ldx, cons
                                            const void* weight_bf16, float eps, int64_t m, int64_t k, void* h_bf16,
                                            int64_t ldh, void* q_e4m3, int64_t ldq, void* x_scale,
                                            fp8rl_scale_fmt fmt, void* stream);
+
+/*
+ * Causal attention over whole prompts packed behind one another, grouped
+ * heads: query head i reads KV head i / (q_heads / kv_heads).  Position i of a
+ * sequence sees its keys j <= i:
+ *   out_i = sum_j softmax_j(softmax_scale * (q_i . k_j)) v_j,
+ *   lse_i = ln sum_j exp(softmax_scale * (q_i . k_j)).
+ * fp8rl_attn_prefill_plan reads the sequences' ends and lays out the work; the
+ * plan serves every call with the same sequences and heads (all layers of a
+ * step).
+ *   d_cu_seqlens    device, int32 [batch + 1]: sequence b is tokens
+ *                   [d_cu_seqlens[b], d_cu_seqlens[b + 1]), not overlapping; device data, not read
+ *                   on the host, clamped to [0, total_tokens].  Empty sequences are fine.
+ *   d_plan          device, fp8rl_attn_prefill_plan_size() bytes, 16-byte aligned, no initial contents
+ *   q_bf16          device, bf16 [total_tokens][q_heads * head_dim], row stride ldq (a column range
+ *                   of the qkv linear's output: nothing needs to be copied apart)
+ *   k_bf16, v_bf16  device, bf16 [total_tokens][kv_heads * head_dim], row strides ldk, ldv
+ *   out_bf16        device, bf16 [total_tokens][q_heads * head_dim], row stride ldo
+ *   d_lse           device, fp32 [total_tokens][q_heads], or null
+ * Tokens of no sequence are not written.  Scores, statistics and sums are
+ * fp32, the probabilities are rounded to bf16 for the second product, the
+ * output once to bf16.  A sequence is not affected by what other sequences
+ * hold; within one, a NaN or infinity in v_j reaches the outputs of positions
+ * from the start of j's 128-key tile on (0 * NaN), one in k_j those from j on.
+ * The same bits on every run.
+ * Errors: INVALID_ARG (null pointers, negative sizes, short strides, q_heads not a multiple of
+ *         kv_heads, softmax_scale not positive and finite, plan too small), SHAPE (head_dim other
+ *         than 64 and 128, more than 2^30 tokens, 2^20 sequences), ALIGNMENT (q, k, v, out and their row
+ *         strides 16 bytes; plan 16 bytes; element alignment), CUDA.  A plan made for other heads
+ *         or another total_tokens writes nothing and is reported as DEVICE_CHECK by
+ *         fp8rl_sync_status, a device wait that ran out as TIMEOUT.
+ */
+FP8RL_API size_t fp8rl_attn_prefill_plan_size(int64_t total_tokens, int64_t batch, int64_t q_heads, int64_t kv_heads);
+FP8RL_API fp8rl_status fp8rl_attn_prefill_plan(const int32_t* d_cu_seqlens, int64_t batch, int64_t total_tokens,
+                                               int64_t q_heads, int64_t kv_heads, void* d_plan, size_t plan_bytes,
+                                               void* stream);
+FP8RL_API fp8rl_status fp8rl_attn_prefill(const void* q_bf16, int64_t ldq, const void* k_bf16, int64_t ldk,
+                                          const void* v_bf16, int64_t ldv, const void* d_plan, size_t plan_bytes,
+                                          int64_t batch, int64_t total_tokens, int64_t q_heads, int64_t kv_heads,
+                                          int64_t head_dim, float softmax_scale, void* out_bf16, int64_t ldo,
+                                          float* d_lse, void* stream);
 
 /*
  * Attention of one new token per sequence over the paged E4M3 KV cache

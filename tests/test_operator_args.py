@@ -60,6 +60,39 @@ def test_decode_workspace_size(lib):
     assert f(32, 5, 128) == 0 and f(32, 8, 96) == 0 and f(0, 1, 128) == 0 and f(8, 0, 128) == 0
 
 
+PREFILL = dict(q=P, ldq=6144, k=P, ldk=6144, v=P, ldv=6144, plan=P, plan_bytes=1 << 30, batch=2, total=100, hq=32, hkv=8, d=128,
+               scale=0.1, out=P, ldo=4096, lse=P, stream=None)
+
+
+@pytest.mark.parametrize("status,changes", [
+    (1, dict(q=None)), (1, dict(k=None)), (1, dict(v=None)), (1, dict(plan=None)), (1, dict(out=None)), (1, dict(batch=-1)),
+    (1, dict(total=-1)), (1, dict(hq=30)), (1, dict(hkv=0)), (1, dict(ldq=4088)), (1, dict(ldk=1016)), (1, dict(ldv=1016)),
+    (1, dict(ldo=4088)), (1, dict(scale=0.0)), (1, dict(scale=math.nan)), (1, dict(plan_bytes=16)), (2, dict(d=96)),
+    (2, dict(total=(1 << 30) + 1)), (2, dict(batch=(1 << 20) + 1)), (3, dict(q=P + 8)), (3, dict(k=P + 8)), (3, dict(v=P + 8)),
+    (3, dict(out=P + 8)), (3, dict(ldq=6145)), (3, dict(ldk=6148)), (3, dict(ldv=6148)), (3, dict(ldo=4100)), (3, dict(plan=P + 8)),
+    (3, dict(lse=P + 2)), (0, dict(batch=0)), (0, dict(total=0)),
+])
+def test_prefill(lib, status, changes):
+    assert call(lib, "fp8rl_attn_prefill", PREFILL, **changes) == status
+
+
+PLAN = dict(cu=P, batch=2, total=100, hq=32, hkv=8, plan=P, plan_bytes=1 << 20, stream=None)
+
+
+@pytest.mark.parametrize("status,changes", [
+    (1, dict(cu=None)), (1, dict(plan=None)), (1, dict(batch=-1)), (1, dict(total=-1)), (1, dict(hq=30)), (1, dict(plan_bytes=16)),
+    (2, dict(total=(1 << 30) + 1)), (2, dict(batch=(1 << 20) + 1)), (3, dict(cu=P + 2)), (3, dict(plan=P + 8)),
+])
+def test_prefill_plan(lib, status, changes):
+    assert call(lib, "fp8rl_attn_prefill_plan", PLAN, **changes) == status
+
+
+def test_prefill_plan_size(lib):
+    f = lib.fp8rl_attn_prefill_plan_size
+    assert f(1000, 3, 32, 8) >= 16 * (1 + 1000 // 64 + 3) and f(0, 0, 1, 1) == 16
+    assert f(-1, 1, 8, 8) == 0 and f(1, -1, 8, 8) == 0 and f(1, 1, 8, 3) == 0 and f((1 << 30) + 1, 1, 8, 8) == 0
+
+
 LP = dict(x=P, fp32=0, rows=4, vocab=100, ld=100, T=1.0, tokens=P, lp=P, ent=P, stats=P, topk=4, ids=P, top=P, stream=None)
 
 
@@ -94,6 +127,8 @@ def test_helpers_reject_host_tensors():
     u8 = torch.zeros(64, 128, dtype=torch.uint8)
     for one in (lambda: fp8rl.rmsnorm_quant(x, x[0]),
                 lambda: fp8rl.attn_decode(x.view(4, 2, 128), u8, u8, t.view(4, 1), t, f, 16),
+                lambda: fp8rl.attn_prefill_plan(t, 4, 2, 1),
+                lambda: fp8rl.attn_prefill(x.view(4, 2, 128), x.view(4, 2, 128), x.view(4, 2, 128), fp8rl.AttnPlan(t, 1, 4, 2, 2)),
                 lambda: fp8rl.logprobs(x, t),
                 lambda: fp8rl.logprobs_backward(x, t, f.view(2, 2), f, f)):
         with pytest.raises(ValueError, match="CUDA tensors"):
