@@ -19,11 +19,12 @@
 // HBM-bound: 2 d bytes per key and KV head, a few operations per byte, so
 // the products run on m16n8k16 tensor instructions with the roles swapped: the
 // 16 rows are keys (scores) or output columns (values), the 8 columns are the
-// query heads of the group, so a group of up to 8 heads costs one instruction
-// and codes go from global memory straight into operand registers.  A lane's 16
-// contiguous bytes of a key row are its operand words of four instructions
-// (the order of the d columns is free as long as q uses the same); for values
-// the bytes of two keys are interleaved by byte permutes.  Scores become the
+// query heads of the group, so a group of up to 8 heads costs one instruction.
+// Each warp streams its keys through a ring of its own in shared memory
+// (16-byte asynchronous copies: no registers wait for them, no CTA-wide
+// barrier).  A lane's 16 contiguous bytes of a key row are its operand words of
+// four instructions (the order of the d columns is free as long as q uses the
+// same); for values the bytes of two keys are interleaved by byte permutes.  Scores become the
 // second product's operand by an 8x8 transpose in registers.
 //
 // Work split: sequences, KV heads and 16-key steps form one list of tiles,
@@ -42,11 +43,16 @@ namespace {
 
 constexpr int kAdWarps = 4;
 constexpr int kAdThreads = kAdWarps * 32;
-constexpr int kAdStep = 16;                      // keys a warp takes at a time
+constexpr int kAdSubs = 2;                       // 16-key products of a step
+constexpr int kAdStep = 16 * kAdSubs;            // keys a warp takes at a time
 constexpr int kAdTile = kAdStep * kAdWarps;      // keys a CTA takes at a time
+constexpr int kAdStages = 2;                     // steps in a warp's ring
 constexpr int kAdMaxBatch = 8192;                // prefix sums held in shared memory
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;                 // a running maximum may lag by this much (base 2): p <= 2^8
+
+// resident CTAs per SM (registers): the work is shared out to exactly these
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 
 struct AdArgs {
   const uint16_t* q;
@@ -59,8 +65,9 @@ struct AdArgs {
   float* lse;  // or null
   uint32_t* tickets;
   float* parts;
-  int64_t ldq, ldc, num_slots, ldt, ldo;
-  int32_t batch, hq, hkv, group, sub, page, max_len;
+  int64_t ldq, num_slots, ldt, ldo;
+  uint32_t ldc16;  // cache row stride in units of 16 bytes
+  int32_t batch, hq, hkv, group, sub, page, page_shift, max_len;
   float softmax_scale;
 };
 
@@ -105,57 +112,67 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ uint4 ld_stream16(const uint8_t* p) {
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
   return v;
 }
-__device__ __forceinline__ uint2 ld_stream8(const uint8_t* p) {
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
   return v;
 }
+// 16-byte asynchronous global -> shared copy past L1; bytes = 0 writes zeros and reads nothing
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const uint8_t* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 
-// One step's codes of a warp: 16 keys of one KV head.  Lane (g, t) = (lane /
-// 4, lane % 4): of keys g and g + 8 the K bytes [64 j + 16 t, + 16); of keys
-// 2t, 2t + 1, 2t + 8, 2t + 9 the V bytes [D/8 g, + D/8).
+// A step of a warp in shared memory: kAdStep key rows of D bytes, then as many
+// value rows.  The 16-byte chunks of a row are permuted so that eight lanes
+// that read together (key reads: rows r, r + 1, four chunks each; value reads:
+// rows r, r + 2, r + 4, r + 6, two chunks each) meet all 32 banks.
 template <int D>
-struct Codes {
-  uint4 k[2][D / 64];
-  uint32_t v[4][D / 32];
+struct Ring {
+  static constexpr uint32_t kV = kAdStep * D;               // value rows' offset in a stage
+  static constexpr uint32_t kStage = 2 * kAdStep * D;
+  static __device__ __forceinline__ uint32_t key(uint32_t row, uint32_t c) {
+    return row * D + ((D == 128 ? c ^ ((row & 1u) << 2) : c) << 4);
+  }
+  static __device__ __forceinline__ uint32_t value(uint32_t row, uint32_t c) {
+    return kV + row * D + ((D == 128 ? c ^ (row & 6u) : c ^ ((row >> 1) & 3u)) << 4);
+  }
 };
 
-// slots: this lane's key's cache row (-1: masked), lane l < 16 key l of the step
+// request a step: off16 is this lane's key's cache row in units of 16 bytes
+// (lane l: key l of the step), kMasked for a key that does not count
+constexpr uint32_t kMasked = 0xFFFFFFFFu;
 template <int D>
-__device__ __forceinline__ void load_codes(Codes<D>& c, const AdArgs& a, const uint8_t* kc, const uint8_t* vc, int64_t slot) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+__device__ __forceinline__ void request(uint32_t stage, const uint8_t* kc, const uint8_t* vc, uint32_t off16) {
+  constexpr int kLanesPerRow = D / 16, kRowsPerPass = 32 / kLanesPerRow;
+  const int lane = threadIdx.x & 31, c = lane % kLanesPerRow, r0 = lane / kLanesPerRow;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t s = __shfl_sync(0xffffffffu, slot, g + 8 * i);
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j)
-      c.k[i][j] = s >= 0 ? ld_stream16(kc + s * a.ldc + 64 * j + 16 * t) : make_uint4(0u, 0u, 0u, 0u);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t s = __shfl_sync(0xffffffffu, slot, 2 * t + (i & 1) + 8 * (i >> 1));
-    if (D == 128) {
-      const uint4 u = s >= 0 ? ld_stream16(vc + s * a.ldc + 16 * g) : make_uint4(0u, 0u, 0u, 0u);
-      c.v[i][0] = u.x, c.v[i][1] = u.y, c.v[i][2 % (D / 32)] = u.z, c.v[i][3 % (D / 32)] = u.w;
-    } else {
-      const uint2 u = s >= 0 ? ld_stream8(vc + s * a.ldc + 8 * g) : make_uint2(0u, 0u);
-      c.v[i][0] = u.x, c.v[i][1] = u.y;
-    }
+  for (int i = 0; i < kAdStep / kRowsPerPass; ++i) {
+    const int row = r0 + i * kRowsPerPass;
+    const uint32_t o = __shfl_sync(0xffffffffu, off16, row);
+    const uint32_t n = o == kMasked ? 0u : 16u;
+    const uint64_t at = (uint64_t)(n ? o : 0u) * 16u + c * 16;
+    cp_async_16(stage + Ring<D>::key(row, c), kc + at, n);
+    cp_async_16(stage + Ring<D>::value(row, c), vc + at, n);
   }
 }
 
-// Shared memory of a CTA
+// A segment's accumulators of the warps, merged at its end (over the rings)
 template <int D, int NT>
-struct AdSmem {
-  float o[kAdWarps][8 * NT][D];  // a warp's accumulators at a segment's end
+struct AdMerge {
+  float o[kAdWarps][8 * NT][D];
   float m[kAdWarps][8 * NT], l[kAdWarps][8 * NT];
-  int32_t last;
 };
+
+template <int D, int NT>
+__host__ __device__ constexpr uint32_t ad_smem() {
+  constexpr uint32_t ring = kAdWarps * kAdStages * Ring<D>::kStage, merge = sizeof(AdMerge<D, NT>);
+  return ring > merge ? ring : merge;
+}
 
 // partial of a segment in the workspace: per head D accumulators, then m and l
 template <int D, int NT>
@@ -165,11 +182,14 @@ __host__ __device__ constexpr int64_t part_floats() {
 
 // D: head size (64 or 128); NT: 8-head columns of a group part (1 or 2)
 template <int D, int NT>
-__global__ void __launch_bounds__(kAdThreads) attn_decode_kernel(const AdArgs a) {
-  extern __shared__ int64_t prefix[];  // batch + 1 running tile counts, then AdSmem
+__global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kernel(const AdArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings, or the merge; then batch + 1 running tile counts
   __shared__ int64_t warp_sum[kAdWarps];
+  __shared__ int32_t last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  AdSmem<D, NT>& sm = *reinterpret_cast<AdSmem<D, NT>*>(prefix + ((a.batch + 2) & ~1));
+  AdMerge<D, NT>& sm = *reinterpret_cast<AdMerge<D, NT>*>(smem);
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + ad_smem<D, NT>());
+  const uint32_t ring = ptx::smem_u32(smem) + warp * kAdStages * Ring<D>::kStage;
   const int heads_sub = a.hkv * a.sub;  // items of a sequence: KV heads times parts of the group
 
   // running counts of the sequences' tiles (each times heads_sub)
@@ -284,61 +304,88 @@ __global__ void __launch_bounds__(kAdThreads) attn_decode_kernel(const AdArgs a)
       l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    // this warp's steps: keys [key, key + 16) for key = tile * 64 + warp * 16
+    // this warp's steps: keys [key, key + kAdStep), one tile apart
     const int32_t k1 = (int32_t)min((int64_t)n, (seg_w1 - item_w0) * kAdTile);
     int32_t key = (int32_t)(w - item_w0) * kAdTile + warp * kAdStep;
-    // the cache row of key + lane (lanes 0..15), or -1
-    auto slot_of = [&](int32_t key0) -> int64_t {
-      const int32_t kk = key0 + (lane & 15);
-      if (kk >= k1) return -1;
-      const int32_t pg = kk / a.page;
+    // the cache row of key0 + lane
+    auto row_of = [&](int32_t key0) -> uint32_t {
+      const int32_t kk = key0 + lane;
+      if (lane >= kAdStep || kk >= k1) return kMasked;
+      const int32_t pg = a.page_shift >= 0 ? kk >> a.page_shift : kk / a.page;
       const int64_t blk = table[pg];
       const int64_t s = blk * a.page + (kk - pg * a.page);
-      return blk >= 0 && s < a.num_slots ? s : -1;
+      return blk >= 0 && s < a.num_slots ? (uint32_t)s * a.ldc16 : kMasked;
     };
-    Codes<D> cur;
-    int64_t slot = slot_of(key), next_slot = slot_of(key + kAdTile);
-    if (key < k1) load_codes<D>(cur, a, kc, vc, slot);
+    // `row` of the step at hand, `ahead` of the steps requested after it
+    uint32_t row = row_of(key), ahead[kAdStages];
+    if (key < k1) request<D>(ring, kc, vc, row);
+    ptx::cp_async_commit();
+#pragma unroll
+    for (int i = 1; i < kAdStages; ++i) {
+      ahead[i - 1] = row_of(key + i * kAdTile);
+      if (i + 1 < kAdStages) {
+        if (key + i * kAdTile < k1) request<D>(ring + i * Ring<D>::kStage, kc, vc, ahead[i - 1]);
+        ptx::cp_async_commit();
+      }
+    }
+    uint32_t stage = 0;
     for (; key < k1; key += kAdTile) {
-      // request the next step's codes before this step's arithmetic
-      Codes<D> nxt;
-      const int64_t after = slot_of(key + 2 * kAdTile);
-      if (key + kAdTile < k1) load_codes<D>(nxt, a, kc, vc, next_slot);
-      const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0);  // bit i < 16: key i counts
+      // request the last step that fits the ring, look up the rows of the one after it
+      const uint32_t to = stage + kAdStages - 1 < kAdStages ? stage + kAdStages - 1 : stage - 1;
+      ahead[kAdStages - 1] = row_of(key + kAdStages * kAdTile);
+      if (key + (kAdStages - 1) * kAdTile < k1) request<D>(ring + to * Ring<D>::kStage, kc, vc, ahead[kAdStages - 2]);
+      ptx::cp_async_commit();
+      ptx::cp_async_wait<kAdStages - 1>();
+      __syncwarp();
+      const uint32_t at = ring + stage * Ring<D>::kStage;
+      const uint32_t live = __ballot_sync(0xffffffffu, row != kMasked);  // bit i: key i counts
 
-      float s[NT][4];
+      float s[kAdSubs][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+      for (int u = 0; u < kAdSubs; ++u) {
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        const uint32_t r0[4] = {cur.k[0][j].x, cur.k[0][j].y, cur.k[0][j].z, cur.k[0][j].w};
-        const uint32_t r1[4] = {cur.k[1][j].x, cur.k[1][j].y, cur.k[1][j].z, cur.k[1][j].w};
+        for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a0 = e4m3x2_to_f16x2(r0[i]), a2 = e4m3x2_to_f16x2_hi(r0[i]);
-          const uint32_t a1 = e4m3x2_to_f16x2(r1[i]), a3 = e4m3x2_to_f16x2_hi(r1[i]);
+        for (int j = 0; j < D / 64; ++j) {
+          const uint4 x0 = lds128(at + Ring<D>::key(16 * u + g, 4 * j + t)), x1 = lds128(at + Ring<D>::key(16 * u + g + 8, 4 * j + t));
+          const uint32_t r0[4] = {x0.x, x0.y, x0.z, x0.w}, r1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816(s[nt], a0, a1, a2, a3, qf[nt][j][i][0], qf[nt][j][i][1]);
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = e4m3x2_to_f16x2(r0[i]), a2 = e4m3x2_to_f16x2_hi(r0[i]);
+            const uint32_t a1 = e4m3x2_to_f16x2(r1[i]), a3 = e4m3x2_to_f16x2_hi(r1[i]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(s[u][nt], a0, a1, a2, a3, qf[nt][j][i][0], qf[nt][j][i][1]);
+          }
         }
       }
-      const bool on0 = live >> g & 1u, on1 = live >> (g + 8) & 1u;
-      uint32_t pb[NT][2];
+      uint32_t pb[kAdSubs][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        s[nt][0] = on0 ? s[nt][0] * qs[nt][0] : -INFINITY;
-        s[nt][1] = on0 ? s[nt][1] * qs[nt][1] : -INFINITY;
-        s[nt][2] = on1 ? s[nt][2] * qs[nt][0] : -INFINITY;
-        s[nt][3] = on1 ? s[nt][3] * qs[nt][1] : -INFINITY;
-        const float b0 = fmaxf(s[nt][0], s[nt][2]), b1 = fmaxf(s[nt][1], s[nt][3]);
+        float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kAdSubs; ++u) {
+          float(&x)[4] = s[u][nt];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] *= qs[nt][c & 1];
+          if (live != (kAdStep == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
+            const bool on0 = live >> (16 * u + g) & 1u, on1 = live >> (16 * u + g + 8) & 1u;
+            x[0] = on0 ? x[0] : -INFINITY;
+            x[1] = on0 ? x[1] : -INFINITY;
+            x[2] = on1 ? x[2] : -INFINITY;
+            x[3] = on1 ? x[3] : -INFINITY;
+          }
+          b0 = fmaxf(b0, fmaxf(x[0], x[2]));
+          b1 = fmaxf(b1, fmaxf(x[1], x[3]));
+        }
         if (__any_sync(0xffffffffu, b0 > m[nt][0] + kRescale || b1 > m[nt][1] + kRescale)) {
           float big[2] = {b0, b1};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) big[c] = fmaxf(big[c], __shfl_xor_sync(0xffffffffu, big[c], d));
-            const float to = fmaxf(m[nt][c], big[c]);
-            const float f = to == -INFINITY ? 1.0f : ex2(m[nt][c] - to);
-            m[nt][c] = to;
+            const float to_m = fmaxf(m[nt][c], big[c]);
+            const float f = to_m == -INFINITY ? 1.0f : ex2(m[nt][c] - to_m);
+            m[nt][c] = to_m;
             l[nt][c] *= f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -348,29 +395,51 @@ __global__ void __launch_bounds__(kAdThreads) attn_decode_kernel(const AdArgs a)
           }
         }
         const float r0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], r1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
-        const float p0 = ex2(s[nt][0] - r0), p1 = ex2(s[nt][1] - r1), p2 = ex2(s[nt][2] - r0), p3 = ex2(s[nt][3] - r1);
-        l[nt][0] += p0 + p2;
-        l[nt][1] += p1 + p3;
-        pb[nt][0] = transpose_8x8(f16x2_rn(p0, p1));
-        pb[nt][1] = transpose_8x8(f16x2_rn(p2, p3));
-      }
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        // bytes of d and d + 1 of two keys, side by side per d
-        const uint32_t x0 = __byte_perm(cur.v[0][i], cur.v[1][i], 0x5140), x1 = __byte_perm(cur.v[0][i], cur.v[1][i], 0x7362);
-        const uint32_t y0 = __byte_perm(cur.v[2][i], cur.v[3][i], 0x5140), y1 = __byte_perm(cur.v[2][i], cur.v[3][i], 0x7362);
-        const uint32_t a00 = e4m3x2_to_f16x2(x0), a01 = e4m3x2_to_f16x2_hi(x0), a02 = e4m3x2_to_f16x2(y0), a03 = e4m3x2_to_f16x2_hi(y0);
-        const uint32_t a10 = e4m3x2_to_f16x2(x1), a11 = e4m3x2_to_f16x2_hi(x1), a12 = e4m3x2_to_f16x2(y1), a13 = e4m3x2_to_f16x2_hi(y1);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_16816(o[nt][2 * i], a00, a01, a02, a03, pb[nt][0], pb[nt][1]);
-          mma_16816(o[nt][2 * i + 1], a10, a11, a12, a13, pb[nt][0], pb[nt][1]);
+        for (int u = 0; u < kAdSubs; ++u) {
+          const float p0 = ex2(s[u][nt][0] - r0), p1 = ex2(s[u][nt][1] - r1), p2 = ex2(s[u][nt][2] - r0), p3 = ex2(s[u][nt][3] - r1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          pb[u][nt][0] = transpose_8x8(f16x2_rn(p0, p1));
+          pb[u][nt][1] = transpose_8x8(f16x2_rn(p2, p3));
         }
       }
-      cur = nxt;
-      slot = next_slot;
-      next_slot = after;
+#pragma unroll
+      for (int u = 0; u < kAdSubs; ++u) {
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t r = 16 * u + 2 * t + (i & 1) + 8 * (i >> 1);
+          if (D == 128) {
+            const uint4 x = lds128(at + Ring<D>::value(r, g));
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2 % (D / 32)] = x.z, v[i][3 % (D / 32)] = x.w;
+          } else {
+            const uint2 x = lds64(at + Ring<D>::value(r, g >> 1) + 8 * (g & 1));
+            v[i][0] = x.x, v[i][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          // bytes of d and d + 1 of two keys, side by side per d
+          const uint32_t x0 = __byte_perm(v[0][i], v[1][i], 0x5140), x1 = __byte_perm(v[0][i], v[1][i], 0x7362);
+          const uint32_t y0 = __byte_perm(v[2][i], v[3][i], 0x5140), y1 = __byte_perm(v[2][i], v[3][i], 0x7362);
+          const uint32_t a00 = e4m3x2_to_f16x2(x0), a01 = e4m3x2_to_f16x2_hi(x0), a02 = e4m3x2_to_f16x2(y0), a03 = e4m3x2_to_f16x2_hi(y0);
+          const uint32_t a10 = e4m3x2_to_f16x2(x1), a11 = e4m3x2_to_f16x2_hi(x1), a12 = e4m3x2_to_f16x2(y1), a13 = e4m3x2_to_f16x2_hi(y1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(o[nt][2 * i], a00, a01, a02, a03, pb[u][nt][0], pb[u][nt][1]);
+            mma_16816(o[nt][2 * i + 1], a10, a11, a12, a13, pb[u][nt][0], pb[u][nt][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage: the next iteration's request may overwrite it
+      row = ahead[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kAdStages; ++i) ahead[i] = ahead[i + 1];
+      stage = stage + 1 < kAdStages ? stage + 1 : 0;
     }
+    ptx::cp_async_wait<0>();
+    __syncthreads();  // every warp is done with its ring
 
     // the warps' partials to shared memory; row d = D/8 g + 2 i (+ 1)
 #pragma unroll
@@ -426,11 +495,11 @@ __global__ void __launch_bounds__(kAdThreads) attn_decode_kernel(const AdArgs a)
       if (tid == 0) {
         // the item's ticket is its first CTA's: a CTA is the first of at most one split item
         const uint32_t got = atomicAdd(a.tickets + c0, 1u);
-        sm.last = got == (uint32_t)(c1 - c0);
-        if (sm.last) a.tickets[c0] = 0u;  // ready for the next call
+        last = got == (uint32_t)(c1 - c0);
+        if (last) a.tickets[c0] = 0u;  // ready for the next call
       }
       __syncthreads();
-      if (sm.last) {
+      if (last) {
         __threadfence();
         for (int i = tid; i < heads * D; i += kAdThreads) {
           const int h = i / D, d = i % D;
@@ -470,23 +539,22 @@ int sm_count() {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-constexpr int kAdCtasPerSm = 3;
 constexpr int64_t kAdMaxLen = (int64_t)1 << 30;  // 32-bit key numbers, two tiles of headroom
 
 int columns(int64_t group) { return group <= 8 ? 1 : 2; }
 
-int64_t ticket_bytes() { return ((int64_t)sm_count() * kAdCtasPerSm * 4 + 255) / 256 * 256; }
+int64_t ticket_bytes(int nt) { return ((int64_t)sm_count() * ctas_per_sm(nt) * 4 + 255) / 256 * 256; }
 
 template <int D, int NT>
 cudaError_t launch_decode(AdArgs a, void* workspace, cudaStream_t stream) {
   a.tickets = static_cast<uint32_t*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes());
-  const size_t smem = (size_t)((a.batch + 2) & ~1) * 8 + sizeof(AdSmem<D, NT>);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(NT));
+  const size_t smem = ad_smem<D, NT>() + ((size_t)a.batch + 1) * 8;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  attn_decode_kernel<D, NT><<<(unsigned)(sm_count() * kAdCtasPerSm), kAdThreads, smem, stream>>>(a);
+  attn_decode_kernel<D, NT><<<(unsigned)(sm_count() * ctas_per_sm(NT)), kAdThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -497,8 +565,9 @@ using namespace fp8rl;
 
 extern "C" FP8RL_API size_t fp8rl_attn_decode_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128)) return 0;
-  const int64_t part = (int64_t)8 * columns(q_heads / kv_heads) * (head_dim + 2) * 4;
-  return (size_t)(ticket_bytes() + 2 * (int64_t)sm_count() * kAdCtasPerSm * part);
+  const int nt = columns(q_heads / kv_heads);
+  const int64_t part = (int64_t)8 * nt * (head_dim + 2) * 4;
+  return (size_t)(ticket_bytes(nt) + 2 * (int64_t)sm_count() * ctas_per_sm(nt) * part);
 }
 
 extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t ldq, int64_t batch, int64_t q_heads,
@@ -517,6 +586,8 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t 
   if (batch == 0) return FP8RL_OK;
   if (!q_bf16 || !d_lens || !out_bf16 || !d_scales || !d_workspace) return FP8RL_ERR_INVALID_ARG;
   if (max_blocks > 0 && (!d_block_table || !k_cache || !v_cache)) return FP8RL_ERR_INVALID_ARG;
+  // cache rows are addressed by a 32-bit count of 16-byte units
+  if (ld_cache > 0 && num_slots > ((int64_t)1 << 36) / ld_cache) return FP8RL_ERR_SHAPE;
   if (batch > kAdMaxBatch || block_size > kAdMaxLen || max_blocks > kAdMaxLen / block_size) return FP8RL_ERR_SHAPE;
   if (workspace_bytes < fp8rl_attn_decode_workspace_size(q_heads, kv_heads, head_dim)) return FP8RL_ERR_INVALID_ARG;
   if (!aligned(q_bf16, 4) || ldq % 2 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) || ld_cache % 16 != 0 ||
@@ -532,12 +603,16 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t 
   a.scales = d_scales;
   a.out = static_cast<uint16_t*>(out_bf16);
   a.lse = d_lse;
-  a.ldq = ldq, a.ldc = ld_cache, a.num_slots = num_slots, a.ldt = ldt, a.ldo = ldo;
+  a.ldq = ldq, a.num_slots = num_slots, a.ldt = ldt, a.ldo = ldo;
+  a.ldc16 = (uint32_t)(ld_cache / 16);
   a.batch = (int32_t)batch, a.hq = (int32_t)q_heads, a.hkv = (int32_t)kv_heads;
   a.group = (int32_t)(q_heads / kv_heads);
   const int nt = columns(a.group);
   a.sub = (a.group + 8 * nt - 1) / (8 * nt);
   a.page = (int32_t)block_size;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (block_size == (int64_t)1 << i) a.page_shift = i;
   a.max_len = (int32_t)(max_blocks * block_size);
   a.softmax_scale = softmax_scale;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);

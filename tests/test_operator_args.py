@@ -45,7 +45,7 @@ DECODE = dict(q=P, ldq=4096, batch=2, hq=32, hkv=8, d=128, kc=P, vc=P, ldc=1024,
     (1, dict(out=None)), (1, dict(ws=None)), (1, dict(batch=-1)), (1, dict(hq=30)), (1, dict(hkv=0)), (1, dict(hq=0)),
     (1, dict(ldq=4095)), (1, dict(ldo=4095)), (1, dict(ldc=1023)), (1, dict(ldt=3)), (1, dict(page=0)), (1, dict(slots=-1)),
     (1, dict(blocks=-1)), (1, dict(scale=0.0)), (1, dict(scale=math.inf)), (1, dict(scale=math.nan)), (1, dict(ws_bytes=1000)),
-    (2, dict(d=96)), (2, dict(batch=8193)), (2, dict(blocks=1 << 27, ldt=1 << 27)), (2, dict(page=1 << 31)),
+    (2, dict(d=96)), (2, dict(batch=8193)), (2, dict(blocks=1 << 27, ldt=1 << 27)), (2, dict(page=1 << 31)), (2, dict(slots=1 << 27)),
     (3, dict(q=P + 2)), (3, dict(ldq=4097)), (3, dict(kc=P + 8)), (3, dict(vc=P + 8)), (3, dict(ldc=1032)), (3, dict(out=P + 1)),
     (3, dict(table=P + 2)), (3, dict(lens=P + 2)), (3, dict(scales=P + 2)), (3, dict(lse=P + 2)), (3, dict(ws=P + 8)),
     (0, dict(batch=0)),
