@@ -27,8 +27,9 @@
 // same); for values the bytes of two keys are interleaved by byte permutes.  Scores become the
 // second product's operand by an 8x8 transpose in registers.
 //
-// Work split: sequences, KV heads and 16-key steps form one list of tiles,
-// shared out to the CTAs in equal contiguous ranges, whatever the lengths.  An
+// Work split: the 128-key tiles of all sequences and KV heads form one list,
+// shared out to the CTAs in equal contiguous ranges, whatever the lengths (an
+// item of one sequence and KV head counts one tile more, for its start).  An
 // item (sequence, KV head) that spans CTAs leaves fp32 partials in the
 // workspace; the CTA that arrives last merges them in CTA order, so the
 // result has the same bits on every run.
@@ -47,6 +48,7 @@ constexpr int kAdSubs = 2;                       // 16-key products of a step
 constexpr int kAdStep = 16 * kAdSubs;            // keys a warp takes at a time
 constexpr int kAdTile = kAdStep * kAdWarps;      // keys a CTA takes at a time
 constexpr int kAdStages = 2;                     // steps in a warp's ring
+constexpr int kAdItemCost = 2;                   // fixed cost of an item, in tiles
 constexpr int kAdMaxBatch = 8192;                // prefix sums held in shared memory
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;                 // a running maximum may lag by this much (base 2): p <= 2^8
@@ -95,8 +97,10 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2_hi(uint32_t w) {
   return r;
 }
 
-__device__ __forceinline__ void store_bf16(uint16_t* p, float v) {
-  asm volatile("{.reg .b16 r;\n\tcvt.rn.bf16.f32 r, %1;\n\tst.global.b16 [%0], r;}" ::"l"(p), "f"(v) : "memory");
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -180,6 +184,20 @@ __host__ __device__ constexpr int64_t part_floats() {
   return (int64_t)8 * NT * (D + 2);
 }
 
+__device__ __forceinline__ void add_scaled(float4& a, float f, float4 v) {
+  a.x = fmaf(f, v.x, a.x);
+  a.y = fmaf(f, v.y, a.y);
+  a.z = fmaf(f, v.z, a.z);
+  a.w = fmaf(f, v.w, a.w);
+}
+
+// outputs d .. d + 3 of a head from its sums; a head without keys gives zeros
+__device__ __forceinline__ void finish(const AdArgs& a, int b, int h, int D, int d, float4 acc, float l, float m, float sv) {
+  const float f = l == 0.0f ? 0.0f : sv / l;
+  *reinterpret_cast<uint2*>(a.out + b * a.ldo + (int64_t)h * D + d) = make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
+  if (a.lse && d == 0) a.lse[(int64_t)b * a.hq + h] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
+}
+
 // D: head size (64 or 128); NT: 8-head columns of a group part (1 or 2)
 template <int D, int NT>
 __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kernel(const AdArgs a) {
@@ -198,7 +216,7 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
     for (int b0 = 0; b0 < a.batch; b0 += kAdThreads) {
       const int b = b0 + tid;
       const int32_t n = b < a.batch ? min(max(a.lens[b], 0), a.max_len) : 0;
-      int64_t x = (int64_t)((n + kAdTile - 1) / kAdTile) * heads_sub;
+      int64_t x = n > 0 ? (int64_t)((n + kAdTile - 1) / kAdTile + kAdItemCost) * heads_sub : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
@@ -248,10 +266,15 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
   while (w < w1) {
     while (prefix[b + 1] <= w) ++b;
     const int32_t n = min(a.lens[b], a.max_len);
-    const int64_t tiles = (prefix[b + 1] - prefix[b]) / heads_sub;
-    const int item = (int)((w - prefix[b]) / tiles);  // kv head * sub + part of the group
-    const int64_t item_w0 = prefix[b] + item * tiles, item_w1 = item_w0 + tiles;
+    const int64_t tiles = (prefix[b + 1] - prefix[b]) / heads_sub - kAdItemCost;
+    const int item = (int)((w - prefix[b]) / (tiles + kAdItemCost));  // kv head * sub + part of the group
+    const int64_t item_w0 = prefix[b] + item * (tiles + kAdItemCost), item_w1 = item_w0 + tiles + kAdItemCost;
     const int64_t seg_w1 = min(w1, item_w1);
+    // the first units of an item stand for its fixed cost, the others for its tiles
+    const int64_t t0 = max(w - item_w0 - kAdItemCost, (int64_t)0), t1 = max(seg_w1 - item_w0 - kAdItemCost, (int64_t)0);
+    w = seg_w1;
+    if (t0 == t1) break;  // this CTA's range ends before the item's first tile
+    const bool whole = t0 == 0 && t1 == tiles;
     const int kvh = item / a.sub, h0 = kvh * a.group + (item % a.sub) * 8 * NT;
     const int heads = min(8 * NT, (kvh + 1) * a.group - h0);
     const uint8_t* kc = a.kc + (int64_t)kvh * D;
@@ -305,8 +328,8 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
     }
 
     // this warp's steps: keys [key, key + kAdStep), one tile apart
-    const int32_t k1 = (int32_t)min((int64_t)n, (seg_w1 - item_w0) * kAdTile);
-    int32_t key = (int32_t)(w - item_w0) * kAdTile + warp * kAdStep;
+    const int32_t k1 = (int32_t)min((int64_t)n, t1 * kAdTile);
+    int32_t key = (int32_t)t0 * kAdTile + warp * kAdStep;
     // the cache row of key0 + lane
     auto row_of = [&](int32_t key0) -> uint32_t {
       const int32_t kk = key0 + lane;
@@ -459,27 +482,25 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
       }
     }
     __syncthreads();
-    const bool whole = w == item_w0 && seg_w1 == item_w1;
     float* part = a.parts + (2 * cta + (first_segment ? 0 : 1)) * part_floats<D, NT>();
-    for (int i = tid; i < heads * D; i += kAdThreads) {
-      const int h = i / D, d = i % D;
+    for (int i = tid; i < heads * (D / 4); i += kAdThreads) {
+      const int h = i / (D / 4), d = i % (D / 4) * 4;
       float mm = sm.m[0][h];
 #pragma unroll
       for (int x = 1; x < kAdWarps; ++x) mm = fmaxf(mm, sm.m[x][h]);
       const float ref = mm == -INFINITY ? 0.0f : mm;
-      float acc = 0.0f, ll = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float ll = 0.0f;
 #pragma unroll
       for (int x = 0; x < kAdWarps; ++x) {
         const float f = ex2(sm.m[x][h] - ref);
-        acc = fmaf(f, sm.o[x][h][d], acc);
+        add_scaled(acc, f, *reinterpret_cast<const float4*>(&sm.o[x][h][d]));
         ll = fmaf(f, sm.l[x][h], ll);
       }
       if (whole) {
-        const float y = ll == 0.0f ? 0.0f : acc * (sv / ll);
-        store_bf16(a.out + b * a.ldo + (int64_t)(h0 + h) * D + d, y);
-        if (a.lse && d == 0) a.lse[(int64_t)b * a.hq + h0 + h] = ll == 0.0f ? -INFINITY : fmaf(mm, kLn2, logf(ll));
+        finish(a, b, h0 + h, D, d, acc, ll, mm, sv);
       } else {
-        part[(int64_t)h * D + d] = acc;
+        *reinterpret_cast<float4*>(part + h * D + d) = acc;
         if (d == 0) {
           part[8 * NT * D + h] = mm;
           part[8 * NT * D + 8 * NT + h] = ll;
@@ -487,45 +508,60 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
       }
     }
     if (!whole) {
-      // CTAs [c0, c1] share this item: the one that holds tile x is
+      // CTAs [c0, c1] hold tiles of this item: the CTA of unit x is
       // floor(((x + 1) * ctas - 1) / total)
-      const int64_t c0 = ((item_w0 + 1) * ctas - 1) / total, c1 = (item_w1 * ctas - 1) / total;
+      const int64_t c0 = ((item_w0 + kAdItemCost + 1) * ctas - 1) / total, c1 = (item_w1 * ctas - 1) / total;
+      const int n_parts = (int)(c1 - c0) + 1;
       __threadfence();
       __syncthreads();
       if (tid == 0) {
         // the item's ticket is its first CTA's: a CTA is the first of at most one split item
-        const uint32_t got = atomicAdd(a.tickets + c0, 1u);
-        last = got == (uint32_t)(c1 - c0);
+        last = atomicAdd(a.tickets + c0, 1u) == (uint32_t)(n_parts - 1);
         if (last) a.tickets[c0] = 0u;  // ready for the next call
       }
       __syncthreads();
       if (last) {
         __threadfence();
-        for (int i = tid; i < heads * D; i += kAdThreads) {
-          const int h = i / D, d = i % D;
-          float mm = -INFINITY, acc = 0.0f, ll = 0.0f;
-          for (int64_t c = c0; c <= c1; ++c) {
-            // a CTA's first segment went to its slot 0; the item's first CTA
-            // holds it as its first one only if its range starts in the item
-            const bool starts = c * total / ctas >= item_w0;
-            const float* src = a.parts + (2 * c + (c == c0 && !starts ? 1 : 0)) * part_floats<D, NT>();
-            const float pm = __ldcg(src + 8 * NT * D + h), pl = __ldcg(src + 8 * NT * D + 8 * NT + h), po = __ldcg(src + (int64_t)h * D + d);
-            const float to = fmaxf(mm, pm);
-            if (to == -INFINITY) continue;
-            const float f0 = ex2(mm - to), f1 = ex2(pm - to);
-            acc = acc * f0 + po * f1;
-            ll = ll * f0 + pl * f1;
-            mm = to;
+        // A CTA's first segment went to its slot 0; the item's first CTA holds
+        // the item as its first segment only if its range starts in the item.
+        const bool second = c0 * total / ctas < item_w0;
+        auto part_of = [&](int c) { return a.parts + (2 * (c0 + c) + (c == 0 && second ? 1 : 0)) * part_floats<D, NT>(); };
+        // per head: the largest reference, each part's factor, the sum
+        float* factor = reinterpret_cast<float*>(smem);  // [part][8 NT], over the rings
+        float* head_m = factor + n_parts * 8 * NT;
+        float* head_l = head_m + 8 * NT;
+        for (int h = warp; h < heads; h += kAdWarps) {
+          float mm = -INFINITY, ll = 0.0f;
+          for (int c = lane; c < n_parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + 8 * NT * D + h));
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+          const float ref = mm == -INFINITY ? 0.0f : mm;
+          for (int c = lane; c < n_parts; c += 32) {
+            const float* src = part_of(c) + 8 * NT * D + h;
+            const float f = ex2(__ldcg(src) - ref);
+            factor[c * 8 * NT + h] = f;
+            ll = fmaf(f, __ldcg(src + 8 * NT), ll);
           }
-          const float y = ll == 0.0f ? 0.0f : acc * (sv / ll);
-          store_bf16(a.out + b * a.ldo + (int64_t)(h0 + h) * D + d, y);
-          if (a.lse && d == 0) a.lse[(int64_t)b * a.hq + h0 + h] = ll == 0.0f ? -INFINITY : fmaf(mm, kLn2, logf(ll));
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+          if (lane == 0) {
+            head_m[h] = mm;
+            head_l[h] = ll;
+          }
+        }
+        __syncthreads();
+        for (int i = tid; i < heads * (D / 4); i += kAdThreads) {
+          const int h = i / (D / 4), d = i % (D / 4) * 4;
+          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+          for (int c = 0; c < n_parts; ++c)
+            add_scaled(acc, factor[c * 8 * NT + h], __ldcg(reinterpret_cast<const float4*>(part_of(c) + h * D + d)));
+          finish(a, b, h0 + h, D, d, acc, head_l[h], head_m[h], sv);
         }
       }
     }
     __syncthreads();  // sm is free for the next segment
     first_segment = false;
-    w = seg_w1;
   }
 }
 
@@ -591,7 +627,7 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t 
   if (batch > kAdMaxBatch || block_size > kAdMaxLen || max_blocks > kAdMaxLen / block_size) return FP8RL_ERR_SHAPE;
   if (workspace_bytes < fp8rl_attn_decode_workspace_size(q_heads, kv_heads, head_dim)) return FP8RL_ERR_INVALID_ARG;
   if (!aligned(q_bf16, 4) || ldq % 2 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) || ld_cache % 16 != 0 ||
-      !aligned(out_bf16, 2) || !aligned(d_block_table, 4) || !aligned(d_lens, 4) || !aligned(d_scales, 4) ||
+      !aligned(out_bf16, 8) || ldo % 4 != 0 || !aligned(d_block_table, 4) || !aligned(d_lens, 4) || !aligned(d_scales, 4) ||
       !aligned(d_lse, 4) || !aligned(d_workspace, 16))
     return FP8RL_ERR_ALIGNMENT;
   AdArgs a{};

@@ -655,7 +655,7 @@ FP8RL_API fp8rl_status fp8rl_attn_prefill(const void* q_bf16, int64_t ldq, const
  * Errors: INVALID_ARG (null pointers, negative sizes, short strides, q_heads not a multiple
  *         of kv_heads, softmax_scale not positive and finite, workspace too small),
  *         SHAPE (head_dim other than 64 and 128, batch > 8192, more than 2^30 keys a sequence, a
- *         cache of more than 64 GB), ALIGNMENT (q 4-byte with an even ldq; caches 16-byte with ld_cache % 16 == 0;
+ *         cache of more than 64 GB), ALIGNMENT (q 4-byte with an even ldq; out 8-byte with ldo % 4 == 0; caches 16-byte with ld_cache % 16 == 0;
  *         workspace 16-byte; element alignment), CUDA.
  */
 FP8RL_API size_t fp8rl_attn_decode_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
