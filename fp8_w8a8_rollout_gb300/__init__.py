@@ -148,8 +148,15 @@ def _p(x) -> int | None:
     return int(x)
 
 
+# the current stream's handle without building a Stream object (a call's host
+# time is most of what a small launch costs)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if torch.cuda.is_initialized() and _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
@@ -417,10 +424,23 @@ def canaries_enabled() -> bool:
 
 def _out(shape, dtype, device):
     """An output tensor: plain torch.empty, or guarded when FP8RL_CANARY=1."""
+    if not canaries_enabled():
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _guarded(shape, dtype, device)
+
+
+def _outs(specs, device):
+    """Output tensors of several (shape, dtype): _out of each, with one look at
+    the environment."""
+    make = _guarded if canaries_enabled() else None
+    return [make(shape, dtype, device) if make else torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+
+
+def _guarded(shape, dtype, device):
     numel = 1
     for d in shape:
         numel *= int(d)
-    if not canaries_enabled() or numel == 0:
+    if numel == 0:
         return torch.empty(shape, dtype=dtype, device=device)
     nbytes = numel * torch.empty((), dtype=dtype).element_size()
     buf = torch.full((_CANARY_PRE + nbytes + _CANARY_POST,), CANARY_BYTE, dtype=torch.uint8, device=device)
@@ -450,16 +470,13 @@ def _check_cuda(*tensors):
     """The kernels dereference device pointers on the current device: every
     tensor argument of a helper must be a CUDA tensor on it (None and
     non-tensor arguments are skipped)."""
-    cur = None
+    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else None
     for t in tensors:
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, torch.Tensor) or t.get_device() == cur:  # -1 for a host tensor
             continue
         if not t.is_cuda:
             raise ValueError("fp8rl helpers take CUDA tensors; a host tensor's pointer would reach the kernels")
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.device.index != cur:
-            raise ValueError(f"a tensor on {t.device} while the current device is cuda:{cur}")
+        raise ValueError(f"a tensor on {t.device} while the current device is cuda:{cur}")
 
 
 def _check_bf16_2d(t: torch.Tensor, name: str):
@@ -739,9 +756,11 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
         if residual.shape != x.shape:
             raise ValueError("residual must have x's shape")
     if out is None:
-        q = _out((m, k), torch.uint8, x.device)
-        s = _out(((k + 127) // 128, m), _scale_dtype(fmt), x.device)
-        h = None if residual is None else _out((m, k), torch.bfloat16, x.device)
+        specs = [((m, k), torch.uint8), (((k + 127) // 128, m), _scale_dtype(fmt))]
+        if residual is None:
+            (q, s), h = _outs(specs, x.device), None
+        else:
+            q, s, h = _outs(specs + [((m, k), torch.bfloat16)], x.device)
     else:
         q, s, h = out
         _check_out(q, (m, k), torch.uint8, "q", rows=True)
@@ -818,7 +837,7 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPl
     if (plan.total_tokens, plan.q_heads, plan.kv_heads) != (tokens, hq, hkv):
         raise ValueError("the plan was made for other sizes")
     if out is None:
-        out = (_out((tokens, hq, d), torch.bfloat16, q.device), _out((tokens, hq), torch.float32, q.device))
+        out = tuple(_outs((((tokens, hq, d), torch.bfloat16), ((tokens, hq), torch.float32)), q.device))
     else:
         _check_out(out[0], (tokens, hq, d), torch.bfloat16, "out")
         _check_out(out[1], (tokens, hq), torch.float32, "lse")
@@ -865,7 +884,7 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     if workspace is None:
         workspace = attn_decode_workspace(hq, hkv, d, q.device)
     if out is None:
-        out = (_out((batch, hq, d), torch.bfloat16, q.device), _out((batch, hq), torch.float32, q.device))
+        out = tuple(_outs((((batch, hq, d), torch.bfloat16), ((batch, hq), torch.float32)), q.device))
     else:
         _check_out(out[0], (batch, hq, d), torch.bfloat16, "out")
         _check_out(out[1], (batch, hq), torch.float32, "lse")
@@ -892,13 +911,14 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.
     _check_cuda(logits, tokens, *(out or ()))
     _check_logits(logits, tokens)
     rows, vocab = logits.shape
-    dev = logits.device
-    shapes = (((rows,), torch.float32, "lp"), ((rows,), torch.float32, "entropy"), ((rows, 2), torch.float32, "stats")) + \
-        ((((rows, topk), torch.int32, "top_ids"), ((rows, topk), torch.float32, "top_lp")) if topk > 0 else ())
+    specs = [((rows,), torch.float32), ((rows,), torch.float32), ((rows, 2), torch.float32)]
+    if topk > 0:
+        specs += [((rows, topk), torch.int32), ((rows, topk), torch.float32)]
     if out is None:
-        out = tuple(_out(shape, dtype, dev) for shape, dtype, _ in shapes) + ((None, None) if topk <= 0 else ())
+        out = _outs(specs, logits.device)
+        out = (*out, None, None) if topk <= 0 else tuple(out)
     else:
-        for t, (shape, dtype, name) in zip(out, shapes):
+        for t, (shape, dtype), name in zip(out, specs, ("lp", "entropy", "stats", "top_ids", "top_lp")):
             _check_out(t, shape, dtype, name)
     fp8rl_logprob(logits, int(logits.dtype == torch.float32), rows, vocab, _ld(logits), temperature, tokens, out[0],
                   out[1], out[2], topk, out[3], out[4], stream)

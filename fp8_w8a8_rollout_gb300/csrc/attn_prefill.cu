@@ -32,6 +32,7 @@
 // range first; CTAs take them in snake order, which evens the causal lengths
 // out.  Every wait is bounded.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <mutex>
 
@@ -630,9 +631,17 @@ template <int D>
 fp8rl_status launch_prefill(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const ApArgs& a,
                             cudaStream_t stream) {
   auto kernel = attn_prefill_kernel<D>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ApCfg<D>::kSmem) != cudaSuccess) {
-    cudaGetLastError();
-    return FP8RL_ERR_CUDA;
+  // the attribute lives in the context: set once per device and context
+  static std::atomic<uint64_t> ready[64];
+  int dev = 0;
+  const uint64_t ctx = current_context_id();
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || !ctx) return FP8RL_ERR_CUDA;
+  if (ready[dev].load(std::memory_order_acquire) != ctx) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ApCfg<D>::kSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return FP8RL_ERR_CUDA;
+    }
+    ready[dev].store(ctx, std::memory_order_release);
   }
   const int64_t most = (int64_t)a.capacity * a.hkv * (a.group / a.pack);
   kernel<<<(unsigned)std::max<int64_t>(1, std::min<int64_t>(sm_count(), most)), kApThreads, ApCfg<D>::kSmem, stream>>>(mq, mk, mv, a);
