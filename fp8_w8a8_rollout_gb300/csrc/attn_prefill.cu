@@ -91,6 +91,13 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   return r;
 }
 
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -199,7 +206,9 @@ __global__ void __launch_bounds__(kApThreads, 1)
   uint64_t* s_full = q_empty + 1;           // scores of a tile in TMEM
   uint64_t* p_full = s_full + 2;            // P of a tile in TMEM, O rescaled (128 threads)
   uint64_t* o_full = p_full + 2;            // O of a tile finished
-  uint64_t* drain = o_full + 2;
+  uint64_t* mended = o_full + 2;            // the item's ragged value tile has been zeroed past its end
+  uint64_t* to_mend = mended + 1;           // it has arrived
+  uint64_t* drain = to_mend + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   volatile int* abortv = abort_flag;
@@ -212,6 +221,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
     }
     mbar_init(smem_u32(q_empty), 1);
     mbar_init(smem_u32(drain), 1);
+    mbar_init(smem_u32(mended), 1);
+    mbar_init(smem_u32(to_mend), 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&q_full[x]), 1);
       mbar_init(smem_u32(&s_full[x]), 1);
@@ -294,104 +305,121 @@ __global__ void __launch_bounds__(kApThreads, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer (all lanes wait, lane 0 issues)
-      constexpr uint32_t kDescQk = idesc_bf16(kApTile, kApTile, false), kDescPv = idesc_bf16(kApTile, D, true);
-      uint32_t g = 0;                    // stages consumed
-      uint32_t q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
-      bool alive = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), parity, abortv, a.err, kApTimeoutNs)) != 0;
-      };
-      auto scores = [&](int x, uint32_t stage) {  // S_x = Q_x K^T
-        if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer: one elected thread
+      if (elect_one()) {
+        constexpr uint32_t kDescQk = idesc_bf16(kApTile, kApTile, false), kDescPv = idesc_bf16(kApTile, D, true);
+        // descriptors differ in their address field alone (units of 16 bytes)
+        const uint64_t q_desc = sw128_kmajor_desc(base), k_desc = sw128_kmajor_desc(base + C::kRing),
+                       v_desc = sw128_nmajor_desc(base + C::kRing, C::kHalfBytes);
+        uint32_t g = 0;  // stages consumed
+        uint32_t q_seen[2] = {0, 0}, p_seen[2] = {0, 0}, mends = 0;
+        bool alive = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          return mbar_wait_bounded(smem_u32(bar), parity, abortv, a.err, kApTimeoutNs);
+        };
+        auto scores = [&](int x, uint32_t stage) {  // S_x = Q_x K^T
+          const uint64_t qd = q_desc + x * (C::kTileBytes >> 4), kd = k_desc + stage * (C::kTileBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_bf16_ss(tmem + C::kTmemS + 128 * x, sw128_kmajor_desc(base + x * C::kTileBytes + (k >> 2) * C::kHalfBytes + (k & 3) * 32),
-                        sw128_kmajor_desc(base + C::kRing + stage * C::kTileBytes + (k >> 2) * C::kHalfBytes + (k & 3) * 32), kDescQk,
-                        k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = ((k >> 2) * C::kHalfBytes + (k & 3) * 32) >> 4;
+            mma_bf16_ss(tmem + C::kTmemS + 128 * x, qd + at, kd + at, kDescQk, k > 0);
+          }
           mma_commit(smem_u32(&s_full[x]));
-        }
-        __syncwarp();
-      };
-      auto values = [&](int x, uint32_t stage, bool first) {  // O_x (+)= P_x V
-        if (lane == 0) {
+        };
+        auto values = [&](int x, uint32_t stage, bool first) {  // O_x (+)= P_x V
+          const uint64_t vd = v_desc + stage * (C::kTileBytes >> 4);
 #pragma unroll
           for (int k = 0; k < kApTile / 16; ++k)
-            mma_bf16_ts(tmem + C::kTmemO + 128 * x, tmem + C::kTmemS + 128 * x + 8 * k,
-                        sw128_nmajor_desc(base + C::kRing + stage * C::kTileBytes + k * 2048, C::kHalfBytes), kDescPv, !first || k > 0);
+            mma_bf16_ts(tmem + C::kTmemO + 128 * x, tmem + C::kTmemS + 128 * x + 8 * k, vd + k * (2048 >> 4), kDescPv, !first || k > 0);
+        };
+        for (int64_t r = 0; alive; ++r) {
+          const int64_t w = work_of(r);
+          if (r * grid >= work) break;
+          if (w >= work) continue;
+          const Item it = item_of(a, w, parts);
+          const int32_t n = max(it.n[0], it.n[1]);
+          if (n == 0) continue;
+          const uint32_t ks = g % kApStages;
+          alive = wait(&kv_full[ks], (g / kApStages) & 1);
+          ++g;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (it.n[x] == 0) continue;
+            alive = alive && wait(&q_full[x], q_seen[x] & 1);
+            ++q_seen[x];
+            if (!alive) break;
+            tc_fence_after();
+            scores(x, ks);
+          }
+          if (!alive) break;
+          mma_commit(smem_u32(&kv_empty[ks]));
+          if (n == 1) mma_commit(smem_u32(q_empty));
+          for (int32_t j = 0; j < n; ++j) {
+            const uint32_t vs = g % kApStages;
+            alive = wait(&kv_full[vs], (g / kApStages) & 1);
+            ++g;
+            if (alive && it.len - j * kApTile < kApTile) {
+              mbar_arrive(smem_u32(to_mend));
+              alive = wait(mended, mends++ & 1);
+            }
+            const uint32_t kn = g % kApStages;
+            if (j + 1 < n) {
+              alive = alive && wait(&kv_full[kn], (g / kApStages) & 1);
+              ++g;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (j < it.n[x]) {
+                alive = alive && wait(&p_full[x], p_seen[x] & 1);
+                ++p_seen[x];
+                if (!alive) break;
+                tc_fence_after();
+                values(x, vs, j == 0);
+                if (j + 1 == it.n[x]) mma_commit(smem_u32(&o_full[x]));
+              }
+              if (x == 1) mma_commit(smem_u32(&kv_empty[vs]));
+              if (j + 1 < it.n[x]) scores(x, kn);
+            }
+            if (!alive) break;
+            if (j + 1 < n) mma_commit(smem_u32(&kv_empty[kn]));
+            if (j + 2 == n) mma_commit(smem_u32(q_empty));  // the item's last scores are issued
+          }
         }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (lane == 0) mma_commit(smem_u32(bar));
-        __syncwarp();
-      };
+        // every product issued so far has finished with shared memory and TMEM
+        mma_commit(smem_u32(drain));
+        mbar_wait_bounded(smem_u32(drain), 0, nullptr, a.err, kApTimeoutNs);
+      }
+      __syncwarp();
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ mender
+      // Rows of a sequence's last value tile that lie past its end are
+      // another sequence's, and a probability of 0 does not cancel a NaN: zero them
+      // before the tile is multiplied.
+      uint32_t g = 0, mends = 0;
+      bool alive = true;
       for (int64_t r = 0; alive; ++r) {
         const int64_t w = work_of(r);
         if (r * grid >= work) break;
         if (w >= work) continue;
         const Item it = item_of(a, w, parts);
         const int32_t n = max(it.n[0], it.n[1]);
-        if (n == 0) continue;
-        uint32_t ks = g % kApStages;
-        alive = wait(&kv_full[ks], (g / kApStages) & 1);
-        ++g;
-        for (int x = 0; x < 2 && alive; ++x) {
-          if (it.n[x] == 0) continue;
-          alive = wait(&q_full[x], q_seen[x] & 1);
-          ++q_seen[x];
-          if (alive) {
-            tc_fence_after();
-            scores(x, ks);
-          }
-        }
+        g += 2 * n;
+        const int32_t valid = it.len - (n - 1) * kApTile;
+        if (n == 0 || valid >= kApTile) continue;
+        const uint32_t vs = (g - 1) % kApStages;  // the item's last stage
+        // (the MMA thread asks once the tile has arrived: waiting on the tile's own
+        // barrier from here could mistake an earlier round of the ring for it)
+        alive = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(to_mend), mends++ & 1, abortv, a.err, kApTimeoutNs));
         if (!alive) break;
-        commit(&kv_empty[ks]);
-        if (n == 1) commit(q_empty);
-        for (int32_t j = 0; j < n && alive; ++j) {
-          const uint32_t vs = g % kApStages;
-          alive = wait(&kv_full[vs], (g / kApStages) & 1);
-          ++g;
-          if (!alive) break;
-          const int32_t valid = it.len - j * kApTile;
-          if (valid < kApTile) {
-            // Rows past the sequence's end are another sequence's values, and
-            // a probability of 0 does not cancel a NaN: zero them.
-            const uint32_t v0 = C::kRing + vs * C::kTileBytes;
-            for (int32_t i = valid * 8 + lane; i < kApTile * 8; i += 32)
+        const uint32_t v0 = C::kRing + vs * C::kTileBytes;
+        for (int32_t i = valid * 8 + lane; i < kApTile * 8; i += 32)
 #pragma unroll
-              for (int h = 0; h < C::kHalves; ++h)
-                *reinterpret_cast<uint4*>(base_ptr + v0 + h * C::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_shared();
-            __syncwarp();
-          }
-          const uint32_t kn = g % kApStages;
-          if (j + 1 < n) {
-            alive = wait(&kv_full[kn], (g / kApStages) & 1);
-            ++g;
-            if (!alive) break;
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (j < it.n[x]) {
-              alive = alive && wait(&p_full[x], p_seen[x] & 1);
-              ++p_seen[x];
-              if (!alive) break;
-              tc_fence_after();
-              values(x, vs, j == 0);
-              if (j + 1 == it.n[x]) commit(&o_full[x]);
-            }
-            if (x == 1) commit(&kv_empty[vs]);
-            if (j + 1 < it.n[x]) scores(x, kn);
-          }
-          if (!alive) break;
-          if (j + 1 < n) commit(&kv_empty[kn]);
-          if (j + 2 == n) commit(q_empty);  // the item's last scores are issued
-        }
+          for (int h = 0; h < C::kHalves; ++h)
+            *reinterpret_cast<uint4*>(base_ptr + v0 + h * C::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(mended));
       }
-      // every product issued so far has finished with shared memory and TMEM
-      commit(drain);
-      mbar_wait_bounded(smem_u32(drain), 0, nullptr, a.err, kApTimeoutNs);
     }
   } else {
     // ------------------------------------------------------------ softmax: thread = row
