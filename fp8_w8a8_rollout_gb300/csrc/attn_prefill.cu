@@ -44,10 +44,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kApThreads = 384;     // warps 0-3: roles, 4-7 and 8-11: softmax of tile 0 and 1
+constexpr int kApThreads = 512;     // warps 0-3: roles, 4-7 and 8-11: softmax of tile 0 and 1, 12-15: outputs
 constexpr int kApTile = 128;        // query rows of a tile, keys of a key tile
 constexpr int kApStages = 5;
-constexpr int kApRoleRegs = 64, kApSoftmaxRegs = 216;
+// shares of the launch's 128 x 512 registers (setmaxnreg: their sum may not exceed it)
+constexpr int kApRoleRegs = 88, kApSoftmaxRegs = 176, kApOutRegs = 72;
+static_assert(128 * (kApRoleRegs + 2 * kApSoftmaxRegs + kApOutRegs) <= 128 * kApThreads, "register split");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;
 constexpr uint64_t kApTimeoutNs = 2000000000ull;
@@ -65,6 +67,7 @@ struct ApArgs {
   uint32_t* err;
   int64_t ldo;
   int32_t capacity, total, hq, hkv, group, pack;
+  int32_t wide;  // output rows start on 32-byte boundaries
   float softmax_scale;
 };
 
@@ -75,7 +78,8 @@ struct ApCfg {
   static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
   static constexpr uint32_t kRing = 2 * kTileBytes;           // byte offset of the key/value stages
   static constexpr uint32_t kBook = kRing + kApStages * kTileBytes;
-  static constexpr uint32_t kSmem = kBook + 256 + 1024;       // barriers; alignment
+  static constexpr uint32_t kRows = kBook + 256;              // row sums of the two tiles for the output warps
+  static constexpr uint32_t kSmem = kRows + 2 * kApTile * 8 + 512;  // alignment
   static constexpr uint32_t kTmemS = 0, kTmemO = 256;         // S of tile x at 128 x, O at 256 + 128 x
 };
 
@@ -153,15 +157,43 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* v) {
+// tcgen05.wait::ld that the loaded registers pass through, so that nothing
+// that uses them is moved ahead of it
+__device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// the largest of three
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 16 columns of this thread's lane, waited for
+__device__ __forceinline__ void tmem_ld_32x32b_x16_wait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 
@@ -172,9 +204,10 @@ struct Item {
 };
 
 // work index w of the snake order, round r: item w / heads, head part w % heads
-__device__ __forceinline__ Item item_of(const ApArgs& a, int64_t w, int32_t parts) {
-  const int4 p = a.plan[1 + w / (a.hkv * parts)];
-  const int32_t hp = (int32_t)(w % (a.hkv * parts));
+__device__ __forceinline__ Item item_of(const ApArgs& a, uint32_t w, int32_t parts) {
+  const uint32_t per = (uint32_t)(a.hkv * parts), at = w / per;
+  const int4 p = a.plan[1 + at];
+  const int32_t hp = (int32_t)(w - at * per);
   Item it;
   it.start = p.x;
   it.len = p.y;
@@ -195,7 +228,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const ApArgs a) {
   using C = ApCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - raw);
@@ -204,9 +237,12 @@ __global__ void __launch_bounds__(kApThreads, 1)
   uint64_t* q_full = kv_empty + kApStages;  // one per tile
   uint64_t* q_empty = q_full + 2;           // both tiles' scores of an item are done
   uint64_t* s_full = q_empty + 1;           // scores of a tile in TMEM
-  uint64_t* p_full = s_full + 2;            // P of a tile in TMEM, O rescaled (128 threads)
+  uint64_t* p_half = s_full + 2;            // half of P of a tile in TMEM, O rescaled (128 threads)
+  uint64_t* p_full = p_half + 2;            // the other half
   uint64_t* o_full = p_full + 2;            // O of a tile finished
-  uint64_t* mended = o_full + 2;            // the item's ragged value tile has been zeroed past its end
+  uint64_t* l_full = o_full + 2;            // its row sums in shared memory (128 threads)
+  uint64_t* o_empty = l_full + 2;           // both read by the output warps (128 threads)
+  uint64_t* mended = o_empty + 2;           // the item's ragged value tile has been zeroed past its end
   uint64_t* to_mend = mended + 1;           // it has arrived
   uint64_t* drain = to_mend + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -226,8 +262,11 @@ __global__ void __launch_bounds__(kApThreads, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&q_full[x]), 1);
       mbar_init(smem_u32(&s_full[x]), 1);
+      mbar_init(smem_u32(&p_half[x]), kApTile);
       mbar_init(smem_u32(&p_full[x]), kApTile);
       mbar_init(smem_u32(&o_full[x]), 1);
+      mbar_init(smem_u32(&l_full[x]), kApTile);
+      mbar_init(smem_u32(&o_empty[x]), kApTile);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -237,15 +276,16 @@ __global__ void __launch_bounds__(kApThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  float2* row_sum = reinterpret_cast<float2*>(base_ptr + C::kRows);  // [tile][row]: reference maximum, sum
 
   const PlanHeader head = *reinterpret_cast<const PlanHeader*>(a.plan);
   const int32_t parts = a.group / a.pack;
   const bool fits = head.span == 2 * kApTile / a.pack && head.total == a.total && head.items >= 0 && head.items <= a.capacity;
   if (!fits && threadIdx.x == 0 && a.err) atomicOr(a.err, kErrDeviceCheck);
-  const int64_t work = fits ? (int64_t)head.items * a.hkv * parts : 0;
-  const int64_t grid = gridDim.x;
+  const uint32_t work = fits ? (uint32_t)head.items * (uint32_t)(a.hkv * parts) : 0u;  // the host keeps it below 2^31
+  const uint32_t grid = gridDim.x;
   // this CTA's r-th work index, or past the end
-  auto work_of = [&](int64_t r) { return r * grid + ((r & 1) ? grid - 1 - blockIdx.x : blockIdx.x); };
+  auto work_of = [&](uint32_t r) { return r * grid + ((r & 1) ? grid - 1 - blockIdx.x : blockIdx.x); };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kApRoleRegs));
@@ -269,8 +309,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
           ++g;
           return true;
         };
-        for (int64_t r = 0; alive; ++r) {
-          const int64_t w = work_of(r);
+        for (uint32_t r = 0; alive; ++r) {
+          const uint32_t w = work_of(r);
           if (r * grid >= work) break;
           if (w >= work) continue;
           const Item it = item_of(a, w, parts);
@@ -312,7 +352,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         const uint64_t q_desc = sw128_kmajor_desc(base), k_desc = sw128_kmajor_desc(base + C::kRing),
                        v_desc = sw128_nmajor_desc(base + C::kRing, C::kHalfBytes);
         uint32_t g = 0;  // stages consumed
-        uint32_t q_seen[2] = {0, 0}, p_seen[2] = {0, 0}, mends = 0;
+        uint32_t q_seen[2] = {0, 0}, p_seen[2] = {0, 0}, o_seen[2] = {0, 0}, mends = 0;
         bool alive = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           return mbar_wait_bounded(smem_u32(bar), parity, abortv, a.err, kApTimeoutNs);
@@ -326,14 +366,16 @@ __global__ void __launch_bounds__(kApThreads, 1)
           }
           mma_commit(smem_u32(&s_full[x]));
         };
-        auto values = [&](int x, uint32_t stage, bool first) {  // O_x (+)= P_x V
+        auto values = [&](int x, uint32_t stage, int half, bool first) {  // O_x (+)= P_x V, 64 keys
           const uint64_t vd = v_desc + stage * (C::kTileBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < kApTile / 16; ++k)
+          for (int i = 0; i < kApTile / 32; ++i) {
+            const int k = half * (kApTile / 32) + i;
             mma_bf16_ts(tmem + C::kTmemO + 128 * x, tmem + C::kTmemS + 128 * x + 8 * k, vd + k * (2048 >> 4), kDescPv, !first || k > 0);
+          }
         };
-        for (int64_t r = 0; alive; ++r) {
-          const int64_t w = work_of(r);
+        for (uint32_t r = 0; alive; ++r) {
+          const uint32_t w = work_of(r);
           if (r * grid >= work) break;
           if (w >= work) continue;
           const Item it = item_of(a, w, parts);
@@ -370,11 +412,17 @@ __global__ void __launch_bounds__(kApThreads, 1)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               if (j < it.n[x]) {
-                alive = alive && wait(&p_full[x], p_seen[x] & 1);
+                // the previous item's outputs have left O_x
+                if (j == 0) alive = alive && wait(&o_empty[x], o_seen[x]++ & 1 ^ 1);
+                alive = alive && wait(&p_half[x], p_seen[x] & 1);
+                if (!alive) break;
+                tc_fence_after();
+                values(x, vs, 0, j == 0);
+                alive = wait(&p_full[x], p_seen[x] & 1);
                 ++p_seen[x];
                 if (!alive) break;
                 tc_fence_after();
-                values(x, vs, j == 0);
+                values(x, vs, 1, false);
                 if (j + 1 == it.n[x]) mma_commit(smem_u32(&o_full[x]));
               }
               if (x == 1) mma_commit(smem_u32(&kv_empty[vs]));
@@ -397,8 +445,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
       // before the tile is multiplied.
       uint32_t g = 0, mends = 0;
       bool alive = true;
-      for (int64_t r = 0; alive; ++r) {
-        const int64_t w = work_of(r);
+      for (uint32_t r = 0; alive; ++r) {
+        const uint32_t w = work_of(r);
         if (r * grid >= work) break;
         if (w >= work) continue;
         const Item it = item_of(a, w, parts);
@@ -421,7 +469,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(mended));
       }
     }
-  } else {
+  } else if (warp < 12) {
     // ------------------------------------------------------------ softmax: thread = row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kApSoftmaxRegs));
     const int x = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
@@ -431,16 +479,16 @@ __global__ void __launch_bounds__(kApThreads, 1)
     const uint64_t c2 = f32x2(c, c);
     uint32_t s_seen = 0, o_seen = 0;
     bool alive = true;
-    for (int64_t r = 0; alive; ++r) {
-      const int64_t w = work_of(r);
+    for (uint32_t r = 0; alive; ++r) {
+      const uint32_t w = work_of(r);
       if (r * grid >= work) break;
       if (w >= work) continue;
       const Item it = item_of(a, w, parts);
       const int32_t n = it.n[x];
       if (n == 0) continue;
-      const int32_t first = it.pos0 + x * (kApTile / a.pack), pos = first + row / a.pack, head = it.head0 + row % a.pack;
+      const int32_t first = it.pos0 + x * (kApTile / a.pack), pos = first + row / a.pack;
       float mc = -INFINITY;  // reference maximum times c
-      uint64_t l2 = f32x2(0.0f, 0.0f);
+      uint64_t l2[2] = {f32x2(0.0f, 0.0f), f32x2(0.0f, 0.0f)};
       for (int32_t j = 0; j < n; ++j) {
         alive = mbar_wait_bounded(smem_u32(&s_full[x]), s_seen & 1, abortv, a.err, kApTimeoutNs);
         ++s_seen;
@@ -449,90 +497,140 @@ __global__ void __launch_bounds__(kApThreads, 1)
           break;
         }
         tc_fence_after();
-        uint32_t s[128];
+        // the row's scores, in quarters; the maximum of the first two while the others arrive
+        uint32_t s[4][32];
+        const bool edge = j * kApTile + kApTile - 1 > first;  // a key tile that reaches past the tile's first position
+        const int32_t lim = pos - j * kApTile;                // there, keys 0 .. lim of the tile count
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto largest = [&](int q) {
+          if (edge) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * i]));
-        tmem_wait_ld();
-        if (j * kApTile + kApTile - 1 > first) {  // a key tile that reaches past the tile's first position
-          const int32_t lim = pos - j * kApTile;  // keys 0 .. lim of the tile count
+            for (int i = 0; i < 32; ++i)
+              if (32 * q + i > lim) s[q][i] = 0xFF800000u;
+          }
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i > lim) s[i] = 0xFF800000u;
-        }
-        float m4[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m4[i] = __uint_as_float(s[i]);
-#pragma unroll
-        for (int i = 4; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(s[i]));
+          for (int i = 0; i < 32; i += 2)
+            m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
+        };
+        tmem_ld_32x32b_x32(ts, s[0]);
+        tmem_ld_32x32b_x32(ts + 32, s[1]);
+        tmem_wait_ld_regs(s[0]);
+        tmem_wait_ld_regs(s[1]);
+        tmem_ld_32x32b_x32(ts + 64, s[2]);
+        tmem_ld_32x32b_x32(ts + 96, s[3]);
+        largest(0);
+        largest(1);
+        tmem_wait_ld_regs(s[2]);
+        tmem_wait_ld_regs(s[3]);
+        largest(2);
+        largest(3);
         const float big = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
         const bool grow = big > mc + kRescale;
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? ex2(mc - big) : 1.0f;  // 0 for the first key tile
           if (grow) mc = big;
           const uint64_t f2 = f32x2(f, f);
-          l2 = mul_f32x2(l2, f2);
+          l2[0] = mul_f32x2(l2[0], f2);
+          l2[1] = mul_f32x2(l2[1], f2);
           if (j > 0) {
+            // O holds the products up to j - 1 (their completion came before s_full's)
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16_wait(to + 16 * i, o);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to + 32 * i, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st_32x32b_x32(to + 32 * i, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x16(to + 16 * i, o);
             }
           }
         }
         const uint64_t nm2 = f32x2(-mc, -mc);
-        uint32_t p[64];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const uint64_t y = fma_f32x2(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, nm2);
-          float y0, y1;
-          f32x2_unpack(y, y0, y1);
-          y0 = ex2(y0);
-          y1 = ex2(y1);
-          l2 = add_f32x2(l2, f32x2(y0, y1));
-          p[i] = bf16x2_rn(y0, y1);
-        }
-        tmem_st_32x32b_x32(ts, p);
-        tmem_st_32x32b_x32(ts + 32, p + 32);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(smem_u32(&p_full[x]));
-      }
-      if (!alive) break;
-      alive = mbar_wait_bounded(smem_u32(&o_full[x]), o_seen & 1, abortv, a.err, kApTimeoutNs);
-      ++o_seen;
-      if (!__all_sync(0xffffffffu, alive)) {
-        alive = false;
-        break;
-      }
-      tc_fence_after();
-      float la, lb;
-      f32x2_unpack(l2, la, lb);
-      const float l = la + lb, inv = 1.0f / l;
-      const bool store = pos < it.len;
-      const int64_t token = (int64_t)it.start + pos;
-      uint16_t* dst = a.out + token * a.ldo + (int64_t)head * D;
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[16];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(to + 32 * i, o);
-        tmem_wait_ld();
-        if (store) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t v[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              v[q] = bf16x2_rn(__uint_as_float(o[8 * e + 2 * q]) * inv, __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + 32 * i + 8 * e) = make_uint4(v[0], v[1], v[2], v[3]);
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t y = fma_f32x2(f32x2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, nm2);
+            float y0, y1;
+            f32x2_unpack(y, y0, y1);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            l2[i & 1] = add_f32x2(l2[i & 1], f32x2(y0, y1));
+            p[i] = bf16x2_rn(y0, y1);
+          }
+          tmem_st_32x32b_x16(ts + 16 * q, p);
+          if (q & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_u32(q == 1 ? &p_half[x] : &p_full[x]));
           }
         }
       }
-      if (store && a.lse) a.lse[token * a.hq + head] = fmaf(mc, kLn2, logf(l));
-      tc_fence_before();
+      if (!alive) break;
+      // the row's sum for the output warps, once they have read the previous item's
+      alive = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&o_empty[x]), (o_seen++ & 1) ^ 1, abortv, a.err, kApTimeoutNs));
+      if (!alive) break;
+      float la, lb;
+      f32x2_unpack(add_f32x2(l2[0], l2[1]), la, lb);
+      row_sum[x * kApTile + row] = make_float2(mc, la + lb);
+      mbar_arrive(smem_u32(&l_full[x]));
+    }
+  } else {
+    // ------------------------------------------------------------ outputs: thread = row, the tiles in turn
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kApOutRegs));
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    uint32_t seen[2] = {0, 0};
+    bool alive = true;
+    for (uint32_t r = 0; alive; ++r) {
+      const uint32_t w = work_of(r);
+      if (r * grid >= work) break;
+      if (w >= work) continue;
+      const Item it = item_of(a, w, parts);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (it.n[x] == 0) continue;
+        alive = mbar_wait_bounded(smem_u32(&l_full[x]), seen[x] & 1, abortv, a.err, kApTimeoutNs) &&
+                mbar_wait_bounded(smem_u32(&o_full[x]), seen[x] & 1, abortv, a.err, kApTimeoutNs);
+        ++seen[x];
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) break;
+        tc_fence_after();
+        const float2 ml = row_sum[x * kApTile + row];
+        const float inv = 1.0f / ml.y;
+        const int32_t pos = it.pos0 + x * (kApTile / a.pack) + row / a.pack, head = it.head0 + row % a.pack;
+        const bool store = pos < it.len;
+        const int64_t token = (int64_t)it.start + pos;
+        uint16_t* dst = a.out + token * a.ldo + (int64_t)head * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(tmem + lanes + C::kTmemO + 128 * x + 32 * i, o);
+          tmem_wait_ld_regs(o);
+          uint32_t v[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) v[q] = bf16x2_rn(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
+          if (i == D / 32 - 1) {  // O and the sums have been read: the next item may write them
+            tc_fence_before();
+            mbar_arrive(smem_u32(&o_empty[x]));
+          }
+          if (store) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint4 lo = make_uint4(v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3]);
+              const uint4 hi = make_uint4(v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]);
+              uint16_t* to = dst + 32 * i + 16 * q;
+              if (a.wide) {
+                st_global_v8(to, lo, hi);
+              } else {
+                *reinterpret_cast<uint4*>(to) = lo;
+                *reinterpret_cast<uint4*>(to + 8) = hi;
+              }
+            }
+          }
+        }
+        if (store && a.lse) a.lse[token * a.hq + head] = fmaf(ml.x, kLn2, logf(ml.y));
+      }
     }
   }
   tc_fence_before();
@@ -730,7 +828,10 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_prefill(const void* q_bf16, int64_t
   a.group = (int32_t)(q_heads / kv_heads);
   a.pack = (int32_t)pack_of(a.group);
   a.capacity = (int32_t)plan_capacity(total_tokens, batch, a.pack);
+  a.wide = aligned(out_bf16, 32) && ldo % 16 == 0;
   a.softmax_scale = softmax_scale;
+  // work is numbered in 32 bits (with a round of CTAs to spare)
+  if ((int64_t)a.capacity * kv_heads * (a.group / a.pack) > INT32_MAX - 4096) return FP8RL_ERR_SHAPE;
   a.err = device_error_word();
   if (!a.err) return FP8RL_ERR_CUDA;
   CUtensorMap mq, mk, mv;
