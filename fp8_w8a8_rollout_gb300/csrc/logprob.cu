@@ -57,6 +57,26 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Masked logits.  An exponent of -inf would meet e = 0 in a product, so
+// elements below kFloor are read as kFloor: beside a maximum within
+// +-kFloor / 2 and with log2(e) / T at most kMaxScale their e is 0 all the same,
+// and every exponent is finite.  Rows outside these limits take exponents one
+// by one, clamped.  (-1e30 rounded to bf16, so that both types clamp alike.)
+constexpr float kFloor = -0x1.94p+99f, kMaxScale = 1e6f;
+constexpr uint32_t kFloorBf16x2 = 0xF14AF14Au;
+__device__ __forceinline__ bool within_floor(float m, float c) { return fabsf(m) <= -0.5f * kFloor && c <= kMaxScale; }
+
 // A row's 16-byte pieces, counted from the 16-byte boundary at or below its
 // first element: piece p holds elements [p * N - off, (p + 1) * N - off).
 template <typename In>
@@ -119,6 +139,23 @@ __device__ __forceinline__ void values(uint4 u, float (&v)[Row<In>::N]) {
     } else {
       v[i] = __uint_as_float(w[i]);
     }
+  }
+}
+
+// the values of a piece as fp32 pairs, none below kFloor
+template <typename In>
+__device__ __forceinline__ void floored_pairs(uint4 u, uint64_t (&v)[Row<In>::N / 2]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if (sizeof(In) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t f = max_nan_bf16x2(w[i], kFloorBf16x2);
+      v[i % (Row<In>::N / 2)] = pair_of(bf16_lo(f), bf16_hi(f));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      v[i] = pair_of(max_nan(__uint_as_float(w[2 * i]), kFloor), max_nan(__uint_as_float(w[2 * i + 1]), kFloor));
   }
 }
 
@@ -200,6 +237,33 @@ __device__ __forceinline__ void offer(uint64_t& list, uint64_t key, int top) {
   }
 }
 
+// The 32 largest of two sorted lists, sorted: the larger of list[i] and
+// other[31 - i] are those 32, and rise then fall, so five exchange steps order
+// them (Batcher's bitonic merge).
+__device__ __forceinline__ uint64_t merge_lists(uint64_t list, uint64_t other) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t rev = __shfl_sync(0xffffffffu, other, 31 - lane);
+  list = list > rev ? list : rev;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, list, d);
+    list = ((lane & d) == 0) == (list > o) ? list : o;
+  }
+  return list;
+}
+
+// Merge of the warps' lists: warp 0 returns the CTA's.  Every warp takes part.
+__device__ __forceinline__ uint64_t merge_warps(uint64_t list, uint64_t (&lists)[kLpWarps][kMaxTop]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int n = kLpWarps / 2; n > 0; n >>= 1) {
+    if (warp >= n && warp < 2 * n) lists[warp][lane] = list;
+    __syncthreads();
+    if (warp < n) list = merge_lists(list, lists[warp + n][lane]);
+  }
+  return list;
+}
+
 struct LpArgs {
   const void* x;
   const int32_t* tokens;
@@ -242,25 +306,59 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
   const float c = kLog2e / a.temperature;
 
   Stat st{-INFINITY, 0.0f, 0.0f};
+  uint64_t s2 = pair_of(0.0f, 0.0f), w2 = s2;  // s and w in two halves
+  const uint64_t c2 = pair_of(c, c);
+  auto fold = [&] {
+    float lo, hi;
+    ptx::f32x2_unpack(s2, lo, hi);
+    st.s += lo + hi;
+    ptx::f32x2_unpack(w2, lo, hi);
+    st.w += lo + hi;
+    s2 = w2 = pair_of(0.0f, 0.0f);
+  };
+  // (loading the next round ahead of this one's arithmetic costs the
+  // registers of a third of the resident CTAs: 213 us for 195 at 4096 x 151936)
   for (int32_t p = p0 + tid; p < p1; p += U * kLpThreads) {
     uint4 u[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) u[i] = p + i * kLpThreads < p1 ? row.load(p + i * kLpThreads) : absent<In>();
     const float big = largest<In>(u);
-    if (big > st.m) move_to(st, big, c);
-    const float m = st.m == -INFINITY ? 0.0f : st.m;
+    if (big > st.m) {
+      fold();
+      move_to(st, big, c);
+    }
+    if (within_floor(st.m, c)) {
+      const uint64_t nm2 = pair_of(-st.m, -st.m);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      float v[N];
-      values<In>(u[i], v);
+      for (int i = 0; i < U; ++i) {
+        uint64_t v[N / 2];
+        floored_pairs<In>(u[i], v);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float y = max_nan((v[e] - m) * c, kTinyExp2), p2 = ex2(y);
-        st.s += p2;
-        st.w = fmaf(p2, y, st.w);
+        for (int e = 0; e < N / 2; ++e) {
+          const uint64_t y = pair_mul(add2(v[e], nm2), c2);
+          float y0, y1;
+          ptx::f32x2_unpack(y, y0, y1);
+          const uint64_t p2 = pair_of(ex2(y0), ex2(y1));
+          s2 = add2(s2, p2);
+          w2 = pair_fma(p2, y, w2);
+        }
+      }
+    } else {
+      const float m = st.m == -INFINITY ? 0.0f : st.m;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float v[N];
+        values<In>(u[i], v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float y = max_nan((v[e] - m) * c, kTinyExp2), p2 = ex2(y);
+          st.s += p2;
+          st.w = fmaf(p2, y, st.w);
+        }
       }
     }
   }
+  fold();
   const float mine = st.m;  // the largest of this thread's elements
 
   __shared__ Stat warp_stat[kLpWarps];
@@ -284,11 +382,13 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
     cta_stat = st;
   }
 
+  uint64_t top_list = 0;
   if (TOP) {
     // tau: the top-th largest thread maximum (0 while fewer threads hold any)
-    const uint32_t own = p0 + tid < p1 ? max(ordered(mine), 1u) : 0u;
+    constexpr int kShift = sizeof(In) == 2 ? 16 : 0;  // bf16 values differ in the upper half alone
+    const uint32_t own = p0 + tid < p1 ? max(ordered(mine) >> kShift, 1u) : 0u;
     uint32_t lo = 0u;
-    for (int b = 31; b >= 0; --b) {
+    for (int b = 31 - kShift; b >= 0; --b) {
       const uint32_t mid = lo | 1u << b;
       if (__syncthreads_count(own >= mid) >= a.top) lo = mid;
     }
@@ -307,33 +407,36 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const int32_t j = p * N - row.off + e;
-        const bool in = p < p1 && j >= 0 && j < a.vocab && max(ordered(v[e]), 1u) >= lo;
+        const bool in = p < p1 && j >= 0 && j < a.vocab && max(ordered(v[e]) >> kShift, 1u) >= lo;
         offer(list, in ? key_of(v[e], j) : 0, a.top);
       }
     }
-    lists[warp][lane] = lane < a.top ? list : 0;
-    __syncthreads();
-    if (warp == 0) {
-      for (int i = 1; i < kLpWarps; ++i) offer(list, lists[i][lane], a.top);
-      cta_list[lane] = lane < a.top ? list : 0;
-    }
+    top_list = merge_warps(list, lists);
+    if (warp == 0) cta_list[lane] = top_list;
   }
 
-  if (ranks > 1) ptx::cluster_sync();
+  if (ranks > 1) {
+    ptx::cluster_sync();
+    if (TOP && rank == 0) {  // warp i takes rank i's list
+      uint64_t list = top_list;
+      if (warp > 0) {
+        const uint32_t l = ptx::mapa_shared(ptx::smem_u32(&cta_list[lane]), warp < ranks ? warp : 0);
+        list = warp < ranks ? (uint64_t)ptx::ld_dsmem_u32(l + 4) << 32 | ptx::ld_dsmem_u32(l) : 0;
+      }
+      top_list = merge_warps(list, lists);
+    }
+  }
   if (rank == 0 && warp == 0) {
     __syncwarp();
     Stat all = cta_stat;
-    uint64_t list = TOP ? cta_list[lane] : 0;
-    for (int i = 1; i < ranks; ++i) {
-      const uint32_t base = ptx::mapa_shared(ptx::smem_u32(&cta_stat), i);
+    if (ranks > 1) {  // lane i reads rank i's sums; they are merged in rank order
+      const uint32_t base = ptx::mapa_shared(ptx::smem_u32(&cta_stat), lane < ranks ? lane : 0);
       const Stat o{__uint_as_float(ptx::ld_dsmem_u32(base)), __uint_as_float(ptx::ld_dsmem_u32(base + 4)),
                    __uint_as_float(ptx::ld_dsmem_u32(base + 8))};
-      all = merge(all, o, c);
-      if (TOP) {
-        const uint32_t l = ptx::mapa_shared(ptx::smem_u32(&cta_list[lane]), i);
-        offer(list, (uint64_t)ptx::ld_dsmem_u32(l + 4) << 32 | ptx::ld_dsmem_u32(l), a.top);
-      }
+      for (int i = 1; i < ranks; ++i)
+        all = merge(all, Stat{__shfl_sync(0xffffffffu, o.m, i), __shfl_sync(0xffffffffu, o.s, i), __shfl_sync(0xffffffffu, o.w, i)}, c);
     }
+    const uint64_t list = top_list;
     // a row of -inf alone: every log-probability -inf, entropy 0
     const bool none = all.m == -INFINITY && all.s == 0.0f;
     const float ln_s = logf(all.s);
@@ -370,8 +473,10 @@ struct LpGradArgs {
   float temperature;
 };
 
+// dx_j = p (a + b log2 p) with a = -(g + g_H H) / T and b = -g_H ln 2 / T;
+// the token's own element has g / T on top
 struct GradRow {
-  float m, c, l2, g, gh, h, inv_t;
+  float m, c, l2, a, b, top;
   int32_t t;
   bool zero;
 };
@@ -379,10 +484,8 @@ struct GradRow {
 // dx of element j with value v
 __device__ __forceinline__ float grad_of(const GradRow& q, float v, int32_t j) {
   const float y = max_nan(fmaf(v - q.m, q.c, -q.l2), kTinyExp2);  // log2 p
-  const float p = ex2(y);
-  float d = -p * fmaf(q.gh, fmaf(y, kLn2, q.h), q.g);
-  if (j == q.t) d += q.g;
-  return d * q.inv_t;
+  const float d = ex2(y) * fmaf(q.b, y, q.a);
+  return j == q.t ? d + q.top : d;
 }
 
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
@@ -417,10 +520,10 @@ __global__ void __launch_bounds__(kLpThreads) logprob_grad_kernel(const LpGradAr
   q.m = st.x;
   q.c = kLog2e / a.temperature;
   q.l2 = st.y * kLog2e;
-  q.inv_t = 1.0f / a.temperature;
-  q.g = a.g_lp[r];
-  q.gh = a.g_ent ? a.g_ent[r] : 0.0f;
-  q.h = a.g_ent ? a.entropy[r] : 0.0f;
+  const float g = a.g_lp[r], gh = a.g_ent ? a.g_ent[r] : 0.0f, inv_t = 1.0f / a.temperature;
+  q.a = -(a.g_ent ? fmaf(gh, a.entropy[r], g) : g) * inv_t;
+  q.b = -gh * kLn2 * inv_t;
+  q.top = g * inv_t;
   const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
   const int32_t stride = gridDim.x * kLpThreads, first = blockIdx.x * kLpThreads + threadIdx.x;
   if (!same) {  // rows that start at different places of a 16-byte piece: element by element
@@ -433,22 +536,43 @@ __global__ void __launch_bounds__(kLpThreads) logprob_grad_kernel(const LpGradAr
     return;
   }
   const Row<In> row(x, a.vocab);
+  const bool plain = !q.zero && within_floor(q.m, q.c);
+  const uint64_t nm2 = pair_of(-q.m, -q.m), c2 = pair_of(q.c, q.c), nl2 = pair_of(-q.l2, -q.l2), a2 = pair_of(q.a, q.a),
+                 b2 = pair_of(q.b, q.b);
   for (int32_t p = first; p < row.pieces; p += U * stride) {
     uint4 u[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int32_t pi = p + i * stride;
-      if (pi < row.pieces && row.whole(pi)) u[i] = *reinterpret_cast<const uint4*>(x + (pi * N - row.off));
+      if (pi < row.pieces && row.whole(pi) && !q.zero) u[i] = *reinterpret_cast<const uint4*>(x + (pi * N - row.off));
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int32_t pi = p + i * stride, j0 = pi * N - row.off;
       if (pi >= row.pieces) break;
       if (row.whole(pi)) {
-        float v[N], d[N];
-        values<In>(u[i], v);
+        float d[N];
+        if (plain) {
+          uint64_t v[N / 2];
+          floored_pairs<In>(u[i], v);
 #pragma unroll
-        for (int e = 0; e < N; ++e) d[e] = q.zero ? 0.0f : grad_of(q, v[e], j0 + e);
+          for (int e = 0; e < N / 2; ++e) {
+            const uint64_t y = pair_fma(add2(v[e], nm2), c2, nl2);
+            float y0, y1;
+            ptx::f32x2_unpack(y, y0, y1);
+            ptx::f32x2_unpack(pair_mul(pair_of(ex2(y0), ex2(y1)), pair_fma(b2, y, a2)), d[2 * e], d[2 * e + 1]);
+          }
+          if ((uint32_t)(q.t - j0) < (uint32_t)N) {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+              if (j0 + e == q.t) d[e] += q.top;
+          }
+        } else {
+          float v[N];
+          values<In>(u[i], v);
+#pragma unroll
+          for (int e = 0; e < N; ++e) d[e] = q.zero ? 0.0f : grad_of(q, v[e], j0 + e);
+        }
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = sizeof(In) == 2 ? bf16x2_rn(d[(2 * e) % N], d[(2 * e + 1) % N]) : __float_as_uint(d[e]);
@@ -578,9 +702,13 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, i
     a.ldd = ldd;
     a.vocab = (int32_t)vocab;
     a.temperature = temperature;
-    // one load round (four pieces a thread) per CTA: elementwise work needs no long-lived CTA
+    // A load round is four pieces a thread.  CTAs of up to five rounds once
+    // that leaves four times the resident CTAs (4096 x 151936: 356 us, with one
+    // round each 403, ten 363); one round each for small work.
     const int64_t round = (int64_t)kLpThreads * kLpUnroll * (16 / (int64_t)size);
-    const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(65535, (vocab + round - 1) / round)), (unsigned)n);
+    const int64_t rounds = (vocab + round - 1) / round;
+    const int64_t each = std::max<int64_t>(1, std::min<int64_t>(5, rounds * n / ((int64_t)sm_count() * 24)));
+    const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(65535, (rounds + each - 1) / each)), (unsigned)n);
     if (logits_fp32) logprob_grad_kernel<float><<<grid, kLpThreads, 0, cs>>>(a);
     else logprob_grad_kernel<uint16_t><<<grid, kLpThreads, 0, cs>>>(a);
   }

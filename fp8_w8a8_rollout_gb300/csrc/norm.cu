@@ -23,6 +23,8 @@ namespace {
 
 constexpr int64_t kNormMaxK = 32768;  // a row's pieces held in registers: 1024 threads x 4 pieces x 8
 
+constexpr int kNormThreadsPerSm = 1024;  // resident threads per SM: 64 registers each
+
 struct NormArgs {
   const uint16_t* x;
   const uint16_t* res;     // or null
@@ -75,92 +77,106 @@ __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
 // VEC: k and every stride a multiple of 8 elements, every pointer 16-byte
 // aligned (codes 8-byte): whole pieces only
 template <int T, int NP, bool VEC, bool UE8M0>
-__global__ void __launch_bounds__(T) rmsnorm_quant_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_kernel(const NormArgs a) {
+  // rows of up to 8192 columns: the next row waits in registers
+  constexpr bool kAhead = T * NP <= 1024;
   // as the activation quantiser: the next kernel may start, and this one
   // waits for the one before it ahead of its first read or write
   ptx::grid_dep_launch_dependents();
   ptx::grid_dep_wait();
-  const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
-  const uint16_t* xr = a.x + row * a.ldx;
-  const uint16_t* rr = a.res ? a.res + row * a.ldr : nullptr;
   uint4 xv[NP], rv[NP];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    const int32_t c = (tid + j * T) * 8;
-    xv[j] = load8<VEC>(xr, c, a.k);
-    if (rr) rv[j] = load8<VEC>(rr, c, a.k);
-  }
-  float h[NP][8];
-  float ss = 0.0f;
-#pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    unpack8(xv[j], h[j]);
-    if (rr) {
-      float r[8];
-      unpack8(rv[j], r);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[j][e] += r[e];
+    for (int j = 0; j < NP; ++j) {
+      const int32_t c = (tid + j * T) * 8;
+      xv[j] = load8<VEC>(a.x + row * a.ldx, c, a.k);
+      if (a.res) rv[j] = load8<VEC>(a.res + row * a.ldr, c, a.k);
     }
+  };
+  if (kAhead) fetch(blockIdx.x);
+  __shared__ float part[2][T / 32];  // alternating rows: one barrier a row
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x, turn ^= 1) {
+    if (!kAhead) fetch(row);
+    float h[NP][8];
+    float ss = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(h[j][e], h[j][e], ss);
-  }
-  if (a.h) {
-    uint16_t* hr = a.h + row * a.ldh;
+    for (int j = 0; j < NP; ++j) {
+      unpack8(xv[j], h[j]);
+      if (a.res) {
+        float r[8];
+        unpack8(rv[j], r);
 #pragma unroll
-    for (int j = 0; j < NP; ++j) store8_bf16<VEC>(hr, (tid + j * T) * 8, a.k, h[j]);
-  }
-  // the row's sum of squares: a fixed tree, the same bits on every run
-  __shared__ float part[T / 32];
+        for (int e = 0; e < 8; ++e) h[j][e] += r[e];
+      }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-  if ((tid & 31) == 0) part[tid >> 5] = ss;
-  __syncthreads();
-  ss = part[0];
-#pragma unroll
-  for (int w = 1; w < T / 32; ++w) ss += part[w];
-  const float rms = rsqrtf(ss / (float)a.k + a.eps);
-  uint8_t* qr = a.q + row * a.ldq;
-#pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    const int32_t c = (tid + j * T) * 8;
-    float w[8];
-    unpack8(load8<VEC>(a.weight, c, a.k), w);
-    float amax = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      h[j][e] = h[j][e] * rms * w[e];
-      amax = fmaxf(amax, fabsf(h[j][e]));
+      for (int e = 0; e < 8; ++e) ss = fmaf(h[j][e], h[j][e], ss);
     }
-    // 16 consecutive lanes hold one 128-column group
+    if (kAhead && row + gridDim.x < a.m) fetch(row + gridDim.x);  // the next row's loads before this one's barrier
+    if (a.h) {
+      uint16_t* hr = a.h + row * a.ldh;
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    if (c >= a.k) continue;
-    uint32_t code[2];
-    if (UE8M0) {
-      const int e2 = scale_ue8m0_exponent(amax);
-      const float f = exp2_neg(e2);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        code[i] = e4m3x2(h[j][4 * i] * f, h[j][4 * i + 1] * f) | (e4m3x2(h[j][4 * i + 2] * f, h[j][4 * i + 3] * f) << 16);
-      if ((tid & 15) == 0) static_cast<uint8_t*>(a.scale)[(int64_t)(c / kBlock) * a.m + row] = (uint8_t)(e2 + 127);
-    } else {
-      const float s = scale_fp32(amax), r = __frcp_rn(s);
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = s >= kFastDivMinScale ? div_by_scale(h[j][e], s, r) : __fdiv_rn(h[j][e], s);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) code[i] = e4m3x2(y[4 * i], y[4 * i + 1]) | (e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
-      if ((tid & 15) == 0) static_cast<float*>(a.scale)[(int64_t)(c / kBlock) * a.m + row] = s;
+      for (int j = 0; j < NP; ++j) store8_bf16<VEC>(hr, (tid + j * T) * 8, a.k, h[j]);
     }
-    if (VEC) {
-      if (dcheck(c + 8 <= a.k, a.err)) *reinterpret_cast<uint2*>(qr + c) = make_uint2(code[0], code[1]);
-    } else {
+    // the row's sum of squares: a fixed tree, the same bits on every run
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < a.k) qr[c + e] = (uint8_t)(code[e >> 2] >> (8 * (e & 3)));
+    for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    if ((tid & 31) == 0) part[turn][tid >> 5] = ss;
+    __syncthreads();
+    ss = part[turn][0];
+#pragma unroll
+    for (int w = 1; w < T / 32; ++w) ss += part[turn][w];
+    const float rms = rsqrtf(ss / (float)a.k + a.eps);
+    uint8_t* qr = a.q + row * a.ldq;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int32_t c = (tid + j * T) * 8;
+      float w[8];
+      unpack8(load8<VEC>(a.weight, c, a.k), w);
+      float amax = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[j][e] = h[j][e] * rms * w[e];
+        amax = fmaxf(amax, fabsf(h[j][e]));
+      }
+      // 16 consecutive lanes hold one 128-column group
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      if (c >= a.k) continue;
+      uint32_t code[2];
+      if (UE8M0) {
+        const int e2 = scale_ue8m0_exponent(amax);
+        const float f = exp2_neg(e2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          code[i] = e4m3x2(h[j][4 * i] * f, h[j][4 * i + 1] * f) | (e4m3x2(h[j][4 * i + 2] * f, h[j][4 * i + 3] * f) << 16);
+        if ((tid & 15) == 0) static_cast<uint8_t*>(a.scale)[(int64_t)(c / kBlock) * a.m + row] = (uint8_t)(e2 + 127);
+      } else {
+        const float s = scale_fp32(amax), r = __frcp_rn(s);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = s >= kFastDivMinScale ? div_by_scale(h[j][e], s, r) : __fdiv_rn(h[j][e], s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) code[i] = e4m3x2(y[4 * i], y[4 * i + 1]) | (e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
+        if ((tid & 15) == 0) static_cast<float*>(a.scale)[(int64_t)(c / kBlock) * a.m + row] = s;
+      }
+      if (VEC) {
+        if (dcheck(c + 8 <= a.k, a.err)) *reinterpret_cast<uint2*>(qr + c) = make_uint2(code[0], code[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < a.k) qr[c + e] = (uint8_t)(code[e >> 2] >> (8 * (e & 3)));
+      }
     }
   }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  return n;
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -168,7 +184,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 template <int T, int NP>
 cudaError_t launch_norm(const NormArgs& a, bool vec, bool ue8m0, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.m);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(a.m, (int64_t)sm_count() * std::max(1, kNormThreadsPerSm / T)));
   cfg.blockDim = dim3(T);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
