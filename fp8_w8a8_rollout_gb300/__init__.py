@@ -72,6 +72,8 @@ def library_path() -> str:
 def load_library(build_if_missing: bool = False):
     """Load the library (raises if it is missing and building is not asked for)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -141,11 +143,9 @@ def load_library(build_if_missing: bool = False):
 
 def _p(x) -> int | None:
     """A device pointer from a tensor, an int, or None."""
-    if x is None:
-        return None
     if isinstance(x, torch.Tensor):
         return x.data_ptr()
-    return int(x)
+    return None if x is None else int(x)
 
 
 # the current stream's handle without building a Stream object (a call's host
@@ -767,16 +767,15 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
         _check_out(s, ((k + 127) // 128, m), _scale_dtype(fmt), "scale")
         if h is not None:
             _check_out(h, (m, k), torch.bfloat16, "h", rows=True)
-    fp8rl_rmsnorm_quant(x, _ld(x), residual, _ld(residual), weight, eps, m, k, h, _ld(h), q, _ld(q), s, fmt, stream)
+    fp8rl_rmsnorm_quant(x, _ld(x, m, k), residual, 0 if residual is None else _ld(residual, m, k), weight, eps, m, k,
+                        h, 0 if h is None else _ld(h, m, k), q, _ld(q, m, k), s, fmt, stream)
     return q, s, h
 
 
-def _ld(t: torch.Tensor | None) -> int:
-    """Leading dimension in elements (torch leaves the stride of a single row
-    unspecified: then it is a row's own length); 0 for None."""
-    if t is None:
-        return 0
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t[0].numel() if t.shape[0] else 0)
+def _ld(t: torch.Tensor, rows: int, cols: int) -> int:
+    """Leading dimension in elements of [rows, cols...]: torch leaves the
+    stride of a single row unspecified, so that one counts its columns."""
+    return t.stride(0) if rows > 1 else cols
 
 
 def _check_out(t: torch.Tensor, shape, dtype, name: str, rows=False):
@@ -841,8 +840,8 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPl
     else:
         _check_out(out[0], (tokens, hq, d), torch.bfloat16, "out")
         _check_out(out[1], (tokens, hq), torch.float32, "lse")
-    fp8rl_attn_prefill(q, _ld(q), k, _ld(k), v, _ld(v), plan.data, plan.data.numel(), plan.batch, tokens, hq, hkv, d,
-                       d ** -0.5 if softmax_scale is None else softmax_scale, out[0], hq * d, out[1], stream)
+    fp8rl_attn_prefill(q, _ld(q, tokens, hq * d), k, _ld(k, tokens, hkv * d), v, _ld(v, tokens, hkv * d), plan.data,
+                       plan.data.numel(), plan.batch, tokens, hq, hkv, d, d ** -0.5 if softmax_scale is None else softmax_scale, out[0], hq * d, out[1], stream)
     return out
 
 
@@ -868,19 +867,20 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     _check_cuda(q, k_cache, v_cache, block_table, lens, scales, workspace, *(out or ()))
     _check_heads(q, "q")
     batch, hq, d = q.shape
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != torch.uint8 or t.dim() != 2 or t.stride(1) != 1 or t.shape[1] % d:
-            raise ValueError(f"{name} must be a uint8 [num_slots, kv_heads * head_dim] tensor with unit column stride")
-    if k_cache.shape != v_cache.shape or k_cache.stride(0) != v_cache.stride(0):
+    slots, width = k_cache.shape
+    ldc = _ld(k_cache, slots, width)
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8 or k_cache.stride(1) != 1 or v_cache.stride(1) != 1 or width % d:
+        raise ValueError("the caches must be uint8 [num_slots, kv_heads * head_dim] tensors with unit column stride")
+    if v_cache.shape != k_cache.shape or _ld(v_cache, slots, width) != ldc:
         raise ValueError("k_cache and v_cache must have one shape and stride")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch or \
-            (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+    rows, blocks = block_table.shape
+    if block_table.dtype != torch.int32 or rows != batch or (block_table.stride(1) != 1 and blocks > 1):
         raise ValueError("block_table must be an int32 [batch, max_blocks] tensor with unit column stride")
     if lens.dtype != torch.int32 or lens.shape != (batch,) or not lens.is_contiguous():
         raise ValueError("lens must be a contiguous int32 [batch] tensor")
     if scales.dtype != torch.float32 or scales.numel() < 2 or not scales.is_contiguous():
         raise ValueError("scales must hold the fp32 K and V scales")
-    hkv = k_cache.shape[1] // d
+    hkv = width // d
     if workspace is None:
         workspace = attn_decode_workspace(hq, hkv, d, q.device)
     if out is None:
@@ -888,10 +888,10 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     else:
         _check_out(out[0], (batch, hq, d), torch.bfloat16, "out")
         _check_out(out[1], (batch, hq), torch.float32, "lse")
-    fp8rl_attn_decode(q, _ld(q), batch, hq, hkv, d, k_cache, v_cache, _ld(k_cache), k_cache.shape[0],
-                      block_table, _ld(block_table), block_table.shape[1], block_size, lens, scales,
+    fp8rl_attn_decode(q, _ld(q, batch, hq * d), batch, hq, hkv, d, k_cache, v_cache, ldc, slots, block_table,
+                      _ld(block_table, batch, blocks), blocks, block_size, lens, scales,
                       d ** -0.5 if softmax_scale is None else softmax_scale, out[0], hq * d, out[1], workspace,
-                      workspace.numel(), stream)
+                      workspace.numel() * workspace.element_size(), stream)
     return out
 
 
@@ -920,7 +920,7 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.
     else:
         for t, (shape, dtype), name in zip(out, specs, ("lp", "entropy", "stats", "top_ids", "top_lp")):
             _check_out(t, shape, dtype, name)
-    fp8rl_logprob(logits, int(logits.dtype == torch.float32), rows, vocab, _ld(logits), temperature, tokens, out[0],
+    fp8rl_logprob(logits, int(logits.dtype == torch.float32), rows, vocab, _ld(logits, rows, vocab), temperature, tokens, out[0],
                   out[1], out[2], topk, out[3], out[4], stream)
     return out
 
@@ -943,8 +943,8 @@ def logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: torch.T
         out = _out((rows, vocab), logits.dtype, logits.device)
     else:
         _check_out(out, (rows, vocab), logits.dtype, "out", rows=True)
-    fp8rl_logprob_backward(logits, int(logits.dtype == torch.float32), rows, vocab, _ld(logits), temperature, tokens,
-                           stats, entropy, grad_lp, grad_entropy, out, _ld(out), stream)
+    fp8rl_logprob_backward(logits, int(logits.dtype == torch.float32), rows, vocab, _ld(logits, rows, vocab), temperature,
+                           tokens, stats, entropy, grad_lp, grad_entropy, out, _ld(out, rows, vocab), stream)
     return out
 
 
