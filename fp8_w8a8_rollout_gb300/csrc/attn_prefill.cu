@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(base_ptr + C::kBook);
   uint64_t* kv_empty = kv_full + kApStages;
   uint64_t* q_full = kv_empty + kApStages;  // one per tile
-  uint64_t* q_empty = q_full + 2;           // both tiles' scores of an item are done
-  uint64_t* s_full = q_empty + 1;           // scores of a tile in TMEM
+  uint64_t* q_empty = q_full + 2;           // a tile's scores of an item are done
+  uint64_t* s_full = q_empty + 2;           // scores of a tile in TMEM
   uint64_t* p_half = s_full + 2;            // half of P of a tile in TMEM, O rescaled (128 threads)
   uint64_t* p_full = p_half + 2;            // the other half
   uint64_t* o_full = p_full + 2;            // O of a tile finished
@@ -255,12 +255,12 @@ __global__ void __launch_bounds__(kApThreads, 1)
       mbar_init(smem_u32(&kv_full[s]), 1);
       mbar_init(smem_u32(&kv_empty[s]), 1);
     }
-    mbar_init(smem_u32(q_empty), 1);
     mbar_init(smem_u32(drain), 1);
     mbar_init(smem_u32(mended), 1);
     mbar_init(smem_u32(to_mend), 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&q_full[x]), 1);
+      mbar_init(smem_u32(&q_empty[x]), 1);
       mbar_init(smem_u32(&s_full[x]), 1);
       mbar_init(smem_u32(&p_half[x]), kApTile);
       mbar_init(smem_u32(&p_full[x]), kApTile);
@@ -284,8 +284,21 @@ __global__ void __launch_bounds__(kApThreads, 1)
   if (!fits && threadIdx.x == 0 && a.err) atomicOr(a.err, kErrDeviceCheck);
   const uint32_t work = fits ? (uint32_t)head.items * (uint32_t)(a.hkv * parts) : 0u;  // the host keeps it below 2^31
   const uint32_t grid = gridDim.x;
-  // this CTA's r-th work index, or past the end
-  auto work_of = [&](uint32_t r) { return r * grid + ((r & 1) ? grid - 1 - blockIdx.x : blockIdx.x); };
+  // This CTA's work in snake order: round r is index r * grid plus its place
+  // in the round.  Finds the next item with a key tile from round r on; false
+  // past the end.
+  auto next_item = [&](uint32_t& r, Item& it) {
+    for (; r * grid < work; ++r) {
+      const uint32_t w = r * grid + ((r & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
+      if (w >= work) continue;
+      it = item_of(a, w, parts);
+      if (it.n[0] > 0) {
+        ++r;
+        return true;
+      }
+    }
+    return false;
+  };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kApRoleRegs));
@@ -295,7 +308,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         prefetch_tensormap(&map_q);
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
-        uint32_t g = 0, items = 0;
+        uint32_t g = 0;
         uint32_t q_issued[2] = {0, 0};
         bool alive = true;
         auto load_kv = [&](const CUtensorMap* map, const Item& it, int32_t j) {
@@ -309,31 +322,23 @@ __global__ void __launch_bounds__(kApThreads, 1)
           ++g;
           return true;
         };
-        for (uint32_t r = 0; alive; ++r) {
-          const uint32_t w = work_of(r);
-          if (r * grid >= work) break;
-          if (w >= work) continue;
-          const Item it = item_of(a, w, parts);
-          const int32_t n = max(it.n[0], it.n[1]);
-          if (n == 0) continue;
-          if (!mbar_wait_bounded(smem_u32(q_empty), (items & 1) ^ 1, abortv, a.err, kApTimeoutNs)) break;
-          ++items;
-          for (int x = 0; x < 2; ++x) {
-            if (it.n[x] == 0) continue;
-            const uint32_t bar = smem_u32(&q_full[x]);
-            mbar_arrive_expect_tx(bar, C::kTileBytes);
+        auto load_q = [&](int x, const Item& it) {
+          if (!mbar_wait_bounded(smem_u32(&q_empty[x]), (q_issued[x] & 1) ^ 1, abortv, a.err, kApTimeoutNs)) return false;
+          const uint32_t bar = smem_u32(&q_full[x]);
+          mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
-            for (int h = 0; h < C::kHalves; ++h)
-              tma_load_3d(base + x * C::kTileBytes + h * C::kHalfBytes, &map_q, 64 * h, it.head0,
-                          it.start + it.pos0 + x * (kApTile / a.pack), bar);
-            ++q_issued[x];
-            if (x == 0) alive = load_kv(&map_k, it, 0);  // the first tile's scores need no more than this
-            if (!alive) break;
-          }
-          for (int32_t j = 0; j < n && alive; ++j) {
-            alive = load_kv(&map_v, it, j);
-            if (alive && j + 1 < n) alive = load_kv(&map_k, it, j + 1);
-          }
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(base + x * C::kTileBytes + h * C::kHalfBytes, &map_q, 64 * h, it.head0,
+                        it.start + it.pos0 + x * (kApTile / a.pack), bar);
+          ++q_issued[x];
+          return true;
+        };
+        Item it;
+        for (uint32_t r = 0; alive && next_item(r, it);) {
+          const int32_t n = max(it.n[0], it.n[1]);
+          // the first tile's scores need no more than these two
+          alive = load_q(0, it) && load_kv(&map_k, it, 0) && (it.n[1] == 0 || load_q(1, it));
+          for (int32_t j = 0; j < n && alive; ++j) alive = load_kv(&map_v, it, j) && (j + 1 == n || load_kv(&map_k, it, j + 1));
         }
         if (*abortv) {
           // let the copies still in flight land before shared memory is released
@@ -374,29 +379,31 @@ __global__ void __launch_bounds__(kApThreads, 1)
             mma_bf16_ts(tmem + C::kTmemO + 128 * x, tmem + C::kTmemS + 128 * x + 8 * k, vd + k * (2048 >> 4), kDescPv, !first || k > 0);
           }
         };
-        for (uint32_t r = 0; alive; ++r) {
-          const uint32_t w = work_of(r);
-          if (r * grid >= work) break;
-          if (w >= work) continue;
-          const Item it = item_of(a, w, parts);
-          const int32_t n = max(it.n[0], it.n[1]);
-          if (n == 0) continue;
-          const uint32_t ks = g % kApStages;
-          alive = wait(&kv_full[ks], (g / kApStages) & 1);
-          ++g;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (it.n[x] == 0) continue;
-            alive = alive && wait(&q_full[x], q_seen[x] & 1);
+        // S_x of an item's key tile j from ring stage `stage`; the item's last
+        // one frees Q_x
+        auto item_scores = [&](const Item& it, int x, int32_t j, uint32_t stage) {
+          if (j == 0) {
+            if (!wait(&q_full[x], q_seen[x] & 1)) return false;
             ++q_seen[x];
-            if (!alive) break;
             tc_fence_after();
-            scores(x, ks);
           }
-          if (!alive) break;
-          mma_commit(smem_u32(&kv_empty[ks]));
-          if (n == 1) mma_commit(smem_u32(q_empty));
-          for (int32_t j = 0; j < n; ++j) {
+          scores(x, stage);
+          if (j + 1 == it.n[x]) mma_commit(smem_u32(&q_empty[x]));
+          return true;
+        };
+        uint32_t r = 0;
+        Item it, next;
+        bool more = next_item(r, it);
+        if (more) {
+          alive = wait(&kv_full[0], 0);
+          ++g;
+          for (int x = 0; x < 2; ++x) alive = alive && (it.n[x] == 0 || item_scores(it, x, 0, 0));
+          mma_commit(smem_u32(&kv_empty[0]));
+        }
+        while (more && alive) {
+          const int32_t n = max(it.n[0], it.n[1]);
+          more = next_item(r, next);
+          for (int32_t j = 0; j < n && alive; ++j) {
             const uint32_t vs = g % kApStages;
             alive = wait(&kv_full[vs], (g / kApStages) & 1);
             ++g;
@@ -404,16 +411,17 @@ __global__ void __launch_bounds__(kApThreads, 1)
               mbar_arrive(smem_u32(to_mend));
               alive = wait(mended, mends++ & 1);
             }
-            const uint32_t kn = g % kApStages;
-            if (j + 1 < n) {
-              alive = alive && wait(&kv_full[kn], (g / kApStages) & 1);
-              ++g;
-            }
+            // The scores to issue behind this step's products: of the next key
+            // tile, or of the next item's first one, so that its softmax starts
+            // while this item ends.
+            const bool last = j + 1 == n, ahead = !last || more;
+            const uint32_t kn = g % kApStages, kn_parity = (g / kApStages) & 1;
+            bool arrived = false;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               if (j < it.n[x]) {
                 // the previous item's outputs have left O_x
-                if (j == 0) alive = alive && wait(&o_empty[x], o_seen[x]++ & 1 ^ 1);
+                if (j == 0) alive = alive && wait(&o_empty[x], (o_seen[x]++ & 1) ^ 1);
                 alive = alive && wait(&p_half[x], p_seen[x] & 1);
                 if (!alive) break;
                 tc_fence_after();
@@ -426,12 +434,22 @@ __global__ void __launch_bounds__(kApThreads, 1)
                 if (j + 1 == it.n[x]) mma_commit(smem_u32(&o_full[x]));
               }
               if (x == 1) mma_commit(smem_u32(&kv_empty[vs]));
-              if (j + 1 < it.n[x]) scores(x, kn);
+              const Item& to = last ? next : it;
+              const int32_t tj = last ? 0 : j + 1;
+              if (ahead && tj < to.n[x]) {
+                if (!arrived) alive = wait(&kv_full[kn], kn_parity);
+                arrived = true;
+                alive = alive && item_scores(to, x, tj, kn);
+                if (!alive) break;
+              }
             }
             if (!alive) break;
-            if (j + 1 < n) mma_commit(smem_u32(&kv_empty[kn]));
-            if (j + 2 == n) mma_commit(smem_u32(q_empty));  // the item's last scores are issued
+            if (ahead) {
+              mma_commit(smem_u32(&kv_empty[kn]));
+              ++g;
+            }
           }
+          it = next;
         }
         // every product issued so far has finished with shared memory and TMEM
         mma_commit(smem_u32(drain));
@@ -445,15 +463,12 @@ __global__ void __launch_bounds__(kApThreads, 1)
       // before the tile is multiplied.
       uint32_t g = 0, mends = 0;
       bool alive = true;
-      for (uint32_t r = 0; alive; ++r) {
-        const uint32_t w = work_of(r);
-        if (r * grid >= work) break;
-        if (w >= work) continue;
-        const Item it = item_of(a, w, parts);
+      Item it;
+      for (uint32_t r = 0; alive && next_item(r, it);) {
         const int32_t n = max(it.n[0], it.n[1]);
         g += 2 * n;
         const int32_t valid = it.len - (n - 1) * kApTile;
-        if (n == 0 || valid >= kApTile) continue;
+        if (valid >= kApTile) continue;
         const uint32_t vs = (g - 1) % kApStages;  // the item's last stage
         // (the MMA thread asks once the tile has arrived: waiting on the tile's own
         // barrier from here could mistake an earlier round of the ring for it)
@@ -479,11 +494,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
     const uint64_t c2 = f32x2(c, c);
     uint32_t s_seen = 0, o_seen = 0;
     bool alive = true;
-    for (uint32_t r = 0; alive; ++r) {
-      const uint32_t w = work_of(r);
-      if (r * grid >= work) break;
-      if (w >= work) continue;
-      const Item it = item_of(a, w, parts);
+    Item it;
+    for (uint32_t r = 0; alive && next_item(r, it);) {
       const int32_t n = it.n[x];
       if (n == 0) continue;
       const int32_t first = it.pos0 + x * (kApTile / a.pack), pos = first + row / a.pack;
@@ -582,11 +594,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     uint32_t seen[2] = {0, 0};
     bool alive = true;
-    for (uint32_t r = 0; alive; ++r) {
-      const uint32_t w = work_of(r);
-      if (r * grid >= work) break;
-      if (w >= work) continue;
-      const Item it = item_of(a, w, parts);
+    Item it;
+    for (uint32_t r = 0; alive && next_item(r, it);) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (it.n[x] == 0) continue;
