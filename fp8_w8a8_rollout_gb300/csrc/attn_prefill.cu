@@ -52,7 +52,7 @@ constexpr int kApRoleRegs = 88, kApSoftmaxRegs = 176, kApOutRegs = 72;
 static_assert(128 * (kApRoleRegs + 2 * kApSoftmaxRegs + kApOutRegs) <= 128 * kApThreads, "register split");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;
-constexpr uint64_t kApTimeoutNs = 2000000000ull;
+constexpr uint32_t kApTimeoutNs = 2000000000u;  // of a 32-bit nanosecond counter
 
 // the plan: a header, then one int4 per item {first token of the sequence,
 // its length, first position of the item, 0}
@@ -78,7 +78,8 @@ struct ApCfg {
   static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
   static constexpr uint32_t kRing = 2 * kTileBytes;           // byte offset of the key/value stages
   static constexpr uint32_t kBook = kRing + kApStages * kTileBytes;
-  static constexpr uint32_t kRows = kBook + 256;              // row sums of the two tiles for the output warps
+  static constexpr uint32_t kItems = kBook + 384;             // the items at hand
+  static constexpr uint32_t kRows = kBook + 512;              // row sums of the two tiles for the output warps
   static constexpr uint32_t kSmem = kRows + 2 * kApTile * 8 + 512;  // alignment
   static constexpr uint32_t kTmemS = 0, kTmemO = 256;         // S of tile x at 128 x, O at 256 + 128 x
 };
@@ -197,13 +198,39 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16_wait(uint32_t taddr, uint32_t
       : "memory");
 }
 
-struct Item {
+// A bounded wait in few instructions (there are some thirty in the kernel,
+// which has to fit the instruction cache): suspended tries until the phase
+// completes, another thread has given up, or the limit runs out; then raises
+// *abort, which the teardown reports.
+__device__ __forceinline__ uint32_t timer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = timer_lo();
+  while (!mbar_try_wait_suspend(bar, parity, 20000u)) {
+    if (*abort) return false;
+    if (timer_lo() - t0 > kApTimeoutNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+struct alignas(16) Item {
   int32_t start, len, pos0;  // sequence's first token, its length, first position
   int32_t head0, kvh;        // first query head, KV head
-  int32_t n[2];              // key tiles of the two query tiles
+  int32_t n0, n1;            // key tiles of the two query tiles; n0 = 0: no more items
+  int32_t pad;
+  __device__ __forceinline__ int32_t n(int x) const { return x ? n1 : n0; }
 };
+constexpr int kApItems = 4;           // items handed out ahead
+constexpr int kApItemReaders = 15;    // TMA, MMA, mender, 8 softmax and 4 output warps
 
-// work index w of the snake order, round r: item w / heads, head part w % heads
+// work index w: item w / heads, head part w % heads
 __device__ __forceinline__ Item item_of(const ApArgs& a, uint32_t w, int32_t parts) {
   const uint32_t per = (uint32_t)(a.hkv * parts), at = w / per;
   const int4 p = a.plan[1 + at];
@@ -214,12 +241,11 @@ __device__ __forceinline__ Item item_of(const ApArgs& a, uint32_t w, int32_t par
   it.pos0 = p.z;
   it.kvh = hp / parts;
   it.head0 = it.kvh * a.group + (hp % parts) * a.pack;
+  it.pad = 0;
   const int32_t span = kApTile / a.pack;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int32_t first = it.pos0 + x * span;
-    it.n[x] = first < it.len ? (min(it.len, first + span) + kApTile - 1) / kApTile : 0;
-  }
+  auto tiles = [&](int32_t first) { return first < it.len ? (min(it.len, first + span) + kApTile - 1) / kApTile : 0; };
+  it.n0 = tiles(it.pos0);
+  it.n1 = tiles(it.pos0 + span);
   return it;
 }
 
@@ -245,7 +271,9 @@ __global__ void __launch_bounds__(kApThreads, 1)
   uint64_t* mended = o_empty + 2;           // the item's ragged value tile has been zeroed past its end
   uint64_t* to_mend = mended + 1;           // it has arrived
   uint64_t* drain = to_mend + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* item_full = drain + 1;          // an item's slot is filled
+  uint64_t* item_empty = item_full + kApItems;  // every reader has copied it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_empty + kApItems);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   volatile int* abortv = abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -256,6 +284,10 @@ __global__ void __launch_bounds__(kApThreads, 1)
       mbar_init(smem_u32(&kv_empty[s]), 1);
     }
     mbar_init(smem_u32(drain), 1);
+    for (int i = 0; i < kApItems; ++i) {
+      mbar_init(smem_u32(&item_full[i]), 1);
+      mbar_init(smem_u32(&item_empty[i]), kApItemReaders);
+    }
     mbar_init(smem_u32(mended), 1);
     mbar_init(smem_u32(to_mend), 1);
     for (int x = 0; x < 2; ++x) {
@@ -284,22 +316,25 @@ __global__ void __launch_bounds__(kApThreads, 1)
   if (!fits && threadIdx.x == 0 && a.err) atomicOr(a.err, kErrDeviceCheck);
   const uint32_t work = fits ? (uint32_t)head.items * (uint32_t)(a.hkv * parts) : 0u;  // the host keeps it below 2^31
   const uint32_t grid = gridDim.x;
-  // This CTA's work in snake order: round r is index r * grid plus its place
-  // in the round.  Finds the next item with a key tile from round r on; false
-  // past the end.
-  auto next_item = [&](uint32_t& r, Item& it) {
-    for (; r * grid < work; ++r) {
-      const uint32_t w = r * grid + ((r & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
-      if (w >= work) continue;
-      it = item_of(a, w, parts);
-      if (it.n[0] > 0) {
-        ++r;
-        return true;
-      }
-    }
-    return false;
+  // This CTA's items reach its warps through a ring of slots that a warp of
+  // its own fills ahead (the plan's latency and the divisions off everyone's
+  // path).  take() copies the i-th one; false past the end or after an abort.
+  Item* slots = reinterpret_cast<Item*>(base_ptr + C::kItems);
+  auto take = [&](uint32_t& i, Item& it, bool arrive) {
+    const uint32_t slot = i % kApItems;
+    if (!wait_for(smem_u32(&item_full[slot]), (i / kApItems) & 1, abortv)) return false;
+    it = slots[slot];
+    ++i;
+    if (arrive) mbar_arrive(smem_u32(&item_empty[slot]));
+    return it.n0 > 0;
   };
-
+  // the same for a whole warp
+  auto take_warp = [&](uint32_t& i, Item& it) {
+    const bool got = take(i, it, false);
+    const bool all = __all_sync(0xffffffffu, got);  // (every lane has its copy)
+    if (lane == 0) mbar_arrive(smem_u32(&item_empty[(i - 1) % kApItems]));
+    return all;
+  };
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kApRoleRegs));
     if (warp == 0) {
@@ -309,11 +344,11 @@ __global__ void __launch_bounds__(kApThreads, 1)
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
         uint32_t g = 0;
-        uint32_t q_issued[2] = {0, 0};
+        uint32_t q_issued0 = 0, q_issued1 = 0;
         bool alive = true;
         auto load_kv = [&](const CUtensorMap* map, const Item& it, int32_t j) {
           const int s = g % kApStages;
-          if (!mbar_wait_bounded(smem_u32(&kv_empty[s]), ((g / kApStages) & 1) ^ 1, abortv, a.err, kApTimeoutNs)) return false;
+          if (!wait_for(smem_u32(&kv_empty[s]), ((g / kApStages) & 1) ^ 1, abortv)) return false;
           const uint32_t bar = smem_u32(&kv_full[s]);
           mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
@@ -323,29 +358,34 @@ __global__ void __launch_bounds__(kApThreads, 1)
           return true;
         };
         auto load_q = [&](int x, const Item& it) {
-          if (!mbar_wait_bounded(smem_u32(&q_empty[x]), (q_issued[x] & 1) ^ 1, abortv, a.err, kApTimeoutNs)) return false;
+          if (!wait_for(smem_u32(&q_empty[x]), ((x ? q_issued1 : q_issued0) & 1) ^ 1, abortv)) return false;
           const uint32_t bar = smem_u32(&q_full[x]);
           mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h)
             tma_load_3d(base + x * C::kTileBytes + h * C::kHalfBytes, &map_q, 64 * h, it.head0,
                         it.start + it.pos0 + x * (kApTile / a.pack), bar);
-          ++q_issued[x];
+          if (x) ++q_issued1;
+          else ++q_issued0;
           return true;
         };
         Item it;
-        for (uint32_t r = 0; alive && next_item(r, it);) {
-          const int32_t n = max(it.n[0], it.n[1]);
-          // the first tile's scores need no more than these two
-          alive = load_q(0, it) && load_kv(&map_k, it, 0) && (it.n[1] == 0 || load_q(1, it));
-          for (int32_t j = 0; j < n && alive; ++j) alive = load_kv(&map_v, it, j) && (j + 1 == n || load_kv(&map_k, it, j + 1));
+        for (uint32_t i = 0; alive && take(i, it, true);) {
+          const int32_t n = max(it.n0, it.n1);
+          // K of key tile 0, V of 0, K of 1, ...: the order of their use; the
+          // queries around the first (the first tile's scores need no more)
+#pragma unroll 1
+          for (int32_t t = 0; t < 2 * n && alive; ++t) {
+            if (t < 2 && it.n(t) > 0) alive = load_q(t, it);
+            alive = alive && load_kv(t & 1 ? &map_v : &map_k, it, t >> 1);
+          }
         }
         if (*abortv) {
           // let the copies still in flight land before shared memory is released
           for (uint32_t j = g > (uint32_t)kApStages ? g - kApStages : 0; j < g; ++j)
             mbar_wait_bounded(smem_u32(&kv_full[j % kApStages]), (j / kApStages) & 1, nullptr, nullptr, 10000000ull);
-          for (int x = 0; x < 2; ++x)
-            if (q_issued[x]) mbar_wait_bounded(smem_u32(&q_full[x]), (q_issued[x] - 1) & 1, nullptr, nullptr, 10000000ull);
+          if (q_issued0) mbar_wait_bounded(smem_u32(&q_full[0]), (q_issued0 - 1) & 1, nullptr, nullptr, 10000000ull);
+          if (q_issued1) mbar_wait_bounded(smem_u32(&q_full[1]), (q_issued1 - 1) & 1, nullptr, nullptr, 10000000ull);
         }
       }
       __syncwarp();
@@ -356,11 +396,14 @@ __global__ void __launch_bounds__(kApThreads, 1)
         // descriptors differ in their address field alone (units of 16 bytes)
         const uint64_t q_desc = sw128_kmajor_desc(base), k_desc = sw128_kmajor_desc(base + C::kRing),
                        v_desc = sw128_nmajor_desc(base + C::kRing, C::kHalfBytes);
-        uint32_t g = 0;  // stages consumed
-        uint32_t q_seen[2] = {0, 0}, p_seen[2] = {0, 0}, o_seen[2] = {0, 0}, mends = 0;
+        uint32_t stage = 0, parity = 0;  // of the next tile in the ring
+        auto advance = [&] {
+          if (++stage == kApStages) stage = 0, parity ^= 1;
+        };
+        uint32_t q_phase = 0, p_phase = 0, o_phase = 3, mends = 0;  // bit x: the parity that tile x waits for next
         bool alive = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-          return mbar_wait_bounded(smem_u32(bar), parity, abortv, a.err, kApTimeoutNs);
+          return wait_for(smem_u32(bar), parity, abortv);
         };
         auto scores = [&](int x, uint32_t stage) {  // S_x = Q_x K^T
           const uint64_t qd = q_desc + x * (C::kTileBytes >> 4), kd = k_desc + stage * (C::kTileBytes >> 4);
@@ -379,34 +422,35 @@ __global__ void __launch_bounds__(kApThreads, 1)
             mma_bf16_ts(tmem + C::kTmemO + 128 * x, tmem + C::kTmemS + 128 * x + 8 * k, vd + k * (2048 >> 4), kDescPv, !first || k > 0);
           }
         };
-        // S_x of an item's key tile j from ring stage `stage`; the item's last
-        // one frees Q_x
-        auto item_scores = [&](const Item& it, int x, int32_t j, uint32_t stage) {
+        // S_x of key tile j (of n) of an item from ring stage `stage`; the
+        // last one frees Q_x
+        auto item_scores = [&](int32_t n, int x, int32_t j, uint32_t stage) {
           if (j == 0) {
-            if (!wait(&q_full[x], q_seen[x] & 1)) return false;
-            ++q_seen[x];
+            if (!wait(&q_full[x], q_phase >> x & 1)) return false;
+            q_phase ^= 1u << x;
             tc_fence_after();
           }
           scores(x, stage);
-          if (j + 1 == it.n[x]) mma_commit(smem_u32(&q_empty[x]));
+          if (j + 1 == n) mma_commit(smem_u32(&q_empty[x]));
           return true;
         };
-        uint32_t r = 0;
+        uint32_t i = 0;
         Item it, next;
-        bool more = next_item(r, it);
+        bool more = take(i, it, true);
         if (more) {
           alive = wait(&kv_full[0], 0);
-          ++g;
-          for (int x = 0; x < 2; ++x) alive = alive && (it.n[x] == 0 || item_scores(it, x, 0, 0));
+          advance();
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) alive = alive && (it.n(x) == 0 || item_scores(it.n(x), x, 0, 0));
           mma_commit(smem_u32(&kv_empty[0]));
         }
         while (more && alive) {
-          const int32_t n = max(it.n[0], it.n[1]);
-          more = next_item(r, next);
+          const int32_t n = max(it.n0, it.n1);
+          more = take(i, next, true);
           for (int32_t j = 0; j < n && alive; ++j) {
-            const uint32_t vs = g % kApStages;
-            alive = wait(&kv_full[vs], (g / kApStages) & 1);
-            ++g;
+            const uint32_t vs = stage;
+            alive = wait(&kv_full[vs], parity);
+            advance();
             if (alive && it.len - j * kApTile < kApTile) {
               mbar_arrive(smem_u32(to_mend));
               alive = wait(mended, mends++ & 1);
@@ -415,45 +459,72 @@ __global__ void __launch_bounds__(kApThreads, 1)
             // tile, or of the next item's first one, so that its softmax starts
             // while this item ends.
             const bool last = j + 1 == n, ahead = !last || more;
-            const uint32_t kn = g % kApStages, kn_parity = (g / kApStages) & 1;
+            const uint32_t kn = stage, kn_parity = parity;
             bool arrived = false;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (j < it.n[x]) {
+              if (j < it.n(x)) {
                 // the previous item's outputs have left O_x
-                if (j == 0) alive = alive && wait(&o_empty[x], (o_seen[x]++ & 1) ^ 1);
-                alive = alive && wait(&p_half[x], p_seen[x] & 1);
+                if (j == 0) {
+                  alive = wait(&o_empty[x], o_phase >> x & 1);
+                  o_phase ^= 1u << x;
+                }
+                alive = alive && wait(&p_half[x], p_phase >> x & 1);
                 if (!alive) break;
                 tc_fence_after();
                 values(x, vs, 0, j == 0);
-                alive = wait(&p_full[x], p_seen[x] & 1);
-                ++p_seen[x];
+                alive = wait(&p_full[x], p_phase >> x & 1);
+                p_phase ^= 1u << x;
                 if (!alive) break;
                 tc_fence_after();
                 values(x, vs, 1, false);
-                if (j + 1 == it.n[x]) mma_commit(smem_u32(&o_full[x]));
+                if (j + 1 == it.n(x)) mma_commit(smem_u32(&o_full[x]));
               }
               if (x == 1) mma_commit(smem_u32(&kv_empty[vs]));
-              const Item& to = last ? next : it;
-              const int32_t tj = last ? 0 : j + 1;
-              if (ahead && tj < to.n[x]) {
+              const int32_t to_n = last ? next.n(x) : it.n(x), tj = last ? 0 : j + 1;
+              if (ahead && tj < to_n) {
                 if (!arrived) alive = wait(&kv_full[kn], kn_parity);
                 arrived = true;
-                alive = alive && item_scores(to, x, tj, kn);
+                alive = alive && item_scores(to_n, x, tj, kn);
                 if (!alive) break;
               }
             }
             if (!alive) break;
             if (ahead) {
               mma_commit(smem_u32(&kv_empty[kn]));
-              ++g;
+              advance();
             }
           }
           it = next;
         }
         // every product issued so far has finished with shared memory and TMEM
         mma_commit(smem_u32(drain));
-        mbar_wait_bounded(smem_u32(drain), 0, nullptr, a.err, kApTimeoutNs);
+        mbar_wait_bounded(smem_u32(drain), 0, nullptr, a.err, kApTimeoutNs);  // (whoever else gave up)
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ items: snake order over the plan
+      if (lane == 0) {
+        uint32_t i = 0;
+        Item it;
+        for (uint32_t r = 0;; ++r) {
+          // round r is index r * grid plus this CTA's place in the round
+          const uint32_t w = r * grid + ((r & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
+          const bool end = r * grid >= work;
+          if (!end) {
+            if (w >= work) continue;
+            it = item_of(a, w, parts);
+            if (it.n0 == 0) continue;
+          } else {
+            it.n0 = it.n1 = 0;
+          }
+          const uint32_t slot = i % kApItems;
+          if (!wait_for(smem_u32(&item_empty[slot]), ((i / kApItems) & 1) ^ 1, abortv)) break;
+          slots[slot] = it;
+          mbar_arrive(smem_u32(&item_full[slot]));
+          ++i;
+          if (end) break;
+        }
       }
       __syncwarp();
     } else if (warp == 3) {
@@ -464,15 +535,15 @@ __global__ void __launch_bounds__(kApThreads, 1)
       uint32_t g = 0, mends = 0;
       bool alive = true;
       Item it;
-      for (uint32_t r = 0; alive && next_item(r, it);) {
-        const int32_t n = max(it.n[0], it.n[1]);
+      for (uint32_t i = 0; alive && take_warp(i, it);) {
+        const int32_t n = max(it.n0, it.n1);
         g += 2 * n;
         const int32_t valid = it.len - (n - 1) * kApTile;
         if (valid >= kApTile) continue;
         const uint32_t vs = (g - 1) % kApStages;  // the item's last stage
         // (the MMA thread asks once the tile has arrived: waiting on the tile's own
         // barrier from here could mistake an earlier round of the ring for it)
-        alive = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(to_mend), mends++ & 1, abortv, a.err, kApTimeoutNs));
+        alive = __all_sync(0xffffffffu, wait_for(smem_u32(to_mend), mends++ & 1, abortv));
         if (!alive) break;
         const uint32_t v0 = C::kRing + vs * C::kTileBytes;
         for (int32_t i = valid * 8 + lane; i < kApTile * 8; i += 32)
@@ -495,34 +566,55 @@ __global__ void __launch_bounds__(kApThreads, 1)
     uint32_t s_seen = 0, o_seen = 0;
     bool alive = true;
     Item it;
-    for (uint32_t r = 0; alive && next_item(r, it);) {
-      const int32_t n = it.n[x];
+    for (uint32_t i = 0; alive && take_warp(i, it);) {
+      const int32_t n = it.n(x);
       if (n == 0) continue;
       const int32_t first = it.pos0 + x * (kApTile / a.pack), pos = first + row / a.pack;
       float mc = -INFINITY;  // reference maximum times c
-      uint64_t l2[2] = {f32x2(0.0f, 0.0f), f32x2(0.0f, 0.0f)};
+      uint64_t l2[4];        // the row's sum, in eight strands
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l2[i] = f32x2(0.0f, 0.0f);
       for (int32_t j = 0; j < n; ++j) {
-        alive = mbar_wait_bounded(smem_u32(&s_full[x]), s_seen & 1, abortv, a.err, kApTimeoutNs);
+        alive = wait_for(smem_u32(&s_full[x]), s_seen & 1, abortv);
         ++s_seen;
         if (!__all_sync(0xffffffffu, alive)) {
           alive = false;
           break;
         }
         tc_fence_after();
-        // the row's scores, in quarters; the maximum of the first two while the others arrive
+        // the row's scores, in quarters; the maximum of the first two while the
+        // others arrive
         uint32_t s[4][32];
         const bool edge = j * kApTile + kApTile - 1 > first;  // a key tile that reaches past the tile's first position
         const int32_t lim = pos - j * kApTile;                // there, keys 0 .. lim of the tile count
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto largest = [&](int q) {
+        auto mask = [&](int q) {
           if (edge) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (32 * q + i > lim) s[q][i] = 0xFF800000u;
           }
+        };
+        auto largest = [&](int q) {
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
             m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
+        };
+        // P of a quarter into TMEM, and its sum into l2
+        auto exponentials = [&](int q) {
+          const uint64_t nm2 = f32x2(-mc, -mc);
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t y = fma_f32x2(f32x2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, nm2);
+            float y0, y1;
+            f32x2_unpack(y, y0, y1);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            l2[i & 3] = add_f32x2(l2[i & 3], f32x2(y0, y1));
+            p[i] = bf16x2_rn(y0, y1);
+          }
+          tmem_st_32x32b_x16(ts + 16 * q, p);
         };
         tmem_ld_32x32b_x32(ts, s[0]);
         tmem_ld_32x32b_x32(ts + 32, s[1]);
@@ -530,10 +622,14 @@ __global__ void __launch_bounds__(kApThreads, 1)
         tmem_wait_ld_regs(s[1]);
         tmem_ld_32x32b_x32(ts + 64, s[2]);
         tmem_ld_32x32b_x32(ts + 96, s[3]);
+        mask(0);
+        mask(1);
         largest(0);
         largest(1);
         tmem_wait_ld_regs(s[2]);
         tmem_wait_ld_regs(s[3]);
+        mask(2);
+        mask(3);
         largest(2);
         largest(3);
         const float big = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
@@ -542,8 +638,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
           const float f = grow ? ex2(mc - big) : 1.0f;  // 0 for the first key tile
           if (grow) mc = big;
           const uint64_t f2 = f32x2(f, f);
-          l2[0] = mul_f32x2(l2[0], f2);
-          l2[1] = mul_f32x2(l2[1], f2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l2[i] = mul_f32x2(l2[i], f2);
           if (j > 0) {
             // O holds the products up to j - 1 (their completion came before s_full's)
 #pragma unroll 1
@@ -556,34 +652,23 @@ __global__ void __launch_bounds__(kApThreads, 1)
             }
           }
         }
-        const uint64_t nm2 = f32x2(-mc, -mc);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t y = fma_f32x2(f32x2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, nm2);
-            float y0, y1;
-            f32x2_unpack(y, y0, y1);
-            y0 = ex2(y0);
-            y1 = ex2(y1);
-            l2[i & 1] = add_f32x2(l2[i & 1], f32x2(y0, y1));
-            p[i] = bf16x2_rn(y0, y1);
-          }
-          tmem_st_32x32b_x16(ts + 16 * q, p);
-          if (q & 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(smem_u32(q == 1 ? &p_half[x] : &p_full[x]));
-          }
-        }
+        exponentials(0);
+        exponentials(1);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_half[x]));
+        exponentials(2);
+        exponentials(3);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_full[x]));
       }
       if (!alive) break;
       // the row's sum for the output warps, once they have read the previous item's
-      alive = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&o_empty[x]), (o_seen++ & 1) ^ 1, abortv, a.err, kApTimeoutNs));
+      alive = __all_sync(0xffffffffu, wait_for(smem_u32(&o_empty[x]), (o_seen++ & 1) ^ 1, abortv));
       if (!alive) break;
       float la, lb;
-      f32x2_unpack(add_f32x2(l2[0], l2[1]), la, lb);
+      f32x2_unpack(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])), la, lb);
       row_sum[x * kApTile + row] = make_float2(mc, la + lb);
       mbar_arrive(smem_u32(&l_full[x]));
     }
@@ -592,16 +677,15 @@ __global__ void __launch_bounds__(kApThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kApOutRegs));
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    uint32_t seen[2] = {0, 0};
+    uint32_t phase = 0;  // bit x: the parity that tile x waits for next
     bool alive = true;
     Item it;
-    for (uint32_t r = 0; alive && next_item(r, it);) {
-#pragma unroll
+    for (uint32_t i = 0; alive && take_warp(i, it);) {
+#pragma unroll 1
       for (int x = 0; x < 2; ++x) {
-        if (it.n[x] == 0) continue;
-        alive = mbar_wait_bounded(smem_u32(&l_full[x]), seen[x] & 1, abortv, a.err, kApTimeoutNs) &&
-                mbar_wait_bounded(smem_u32(&o_full[x]), seen[x] & 1, abortv, a.err, kApTimeoutNs);
-        ++seen[x];
+        if (it.n(x) == 0) continue;
+        alive = wait_for(smem_u32(&l_full[x]), phase >> x & 1, abortv) && wait_for(smem_u32(&o_full[x]), phase >> x & 1, abortv);
+        phase ^= 1u << x;
         alive = __all_sync(0xffffffffu, alive);
         if (!alive) break;
         tc_fence_after();
@@ -644,6 +728,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abortv) atomicOr(a.err, kErrTimeout);
   if (warp == 2) tmem_dealloc(tmem, 512);
 }
 
