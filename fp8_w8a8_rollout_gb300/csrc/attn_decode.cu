@@ -204,6 +204,8 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings, or the merge; then batch + 1 running tile counts
   __shared__ int64_t warp_sum[kAdWarps];
   __shared__ int32_t last;
+  ptx::grid_dep_launch_dependents();
+  ptx::grid_dep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   AdMerge<D, NT>& sm = *reinterpret_cast<AdMerge<D, NT>*>(smem);
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + ad_smem<D, NT>());
@@ -281,6 +283,31 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
     const uint8_t* vc = a.vc + (int64_t)kvh * D;
     const int32_t* table = a.table + (int64_t)b * a.ldt;
 
+    // This warp's steps: keys [key, key + kAdStep), one tile apart.  The
+    // first ones are requested before the queries are read.
+    const int32_t k1 = (int32_t)min((int64_t)n, t1 * kAdTile);
+    int32_t key = (int32_t)t0 * kAdTile + warp * kAdStep;
+    // the cache row of key0 + lane
+    auto row_of = [&](int32_t key0) -> uint32_t {
+      const int32_t kk = key0 + lane;
+      if (lane >= kAdStep || kk >= k1) return kMasked;
+      const int32_t pg = a.page_shift >= 0 ? kk >> a.page_shift : kk / a.page;
+      const int64_t blk = table[pg];
+      const int64_t s = blk * a.page + (kk - pg * a.page);
+      return blk >= 0 && s < a.num_slots ? (uint32_t)s * a.ldc16 : kMasked;
+    };
+    // `row` of the step at hand, `ahead` of the steps requested after it
+    uint32_t row = row_of(key), ahead[kAdStages];
+    if (key < k1) request<D>(ring, kc, vc, row);
+    ptx::cp_async_commit();
+#pragma unroll
+    for (int i = 1; i < kAdStages; ++i) {
+      ahead[i - 1] = row_of(key + i * kAdTile);
+      if (i + 1 < kAdStages) {
+        if (key + i * kAdTile < k1) request<D>(ring + i * Ring<D>::kStage, kc, vc, ahead[i - 1]);
+        ptx::cp_async_commit();
+      }
+    }
     // the query heads as operand words (column = head): lane (g, t) holds
     // head g's columns d = 64 j + 16 t + [0, 16)
     uint32_t qf[NT][D / 64][4][2];
@@ -327,30 +354,6 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
       l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    // this warp's steps: keys [key, key + kAdStep), one tile apart
-    const int32_t k1 = (int32_t)min((int64_t)n, t1 * kAdTile);
-    int32_t key = (int32_t)t0 * kAdTile + warp * kAdStep;
-    // the cache row of key0 + lane
-    auto row_of = [&](int32_t key0) -> uint32_t {
-      const int32_t kk = key0 + lane;
-      if (lane >= kAdStep || kk >= k1) return kMasked;
-      const int32_t pg = a.page_shift >= 0 ? kk >> a.page_shift : kk / a.page;
-      const int64_t blk = table[pg];
-      const int64_t s = blk * a.page + (kk - pg * a.page);
-      return blk >= 0 && s < a.num_slots ? (uint32_t)s * a.ldc16 : kMasked;
-    };
-    // `row` of the step at hand, `ahead` of the steps requested after it
-    uint32_t row = row_of(key), ahead[kAdStages];
-    if (key < k1) request<D>(ring, kc, vc, row);
-    ptx::cp_async_commit();
-#pragma unroll
-    for (int i = 1; i < kAdStages; ++i) {
-      ahead[i - 1] = row_of(key + i * kAdTile);
-      if (i + 1 < kAdStages) {
-        if (key + i * kAdTile < k1) request<D>(ring + i * Ring<D>::kStage, kc, vc, ahead[i - 1]);
-        ptx::cp_async_commit();
-      }
-    }
     uint32_t stage = 0;
     for (; key < k1; key += kAdTile) {
       // request the last step that fits the ring, look up the rows of the one after it
@@ -590,8 +593,17 @@ cudaError_t launch_decode(AdArgs a, void* workspace, cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  attn_decode_kernel<D, NT><<<(unsigned)(sm_count() * ctas_per_sm(NT)), kAdThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sm_count() * ctas_per_sm(NT)));
+  cfg.blockDim = dim3(kAdThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NT>, a);
 }
 
 }  // namespace
@@ -654,5 +666,9 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t 
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e = head_dim == 128 ? (nt == 1 ? launch_decode<128, 1>(a, d_workspace, cs) : launch_decode<128, 2>(a, d_workspace, cs))
                                         : (nt == 1 ? launch_decode<64, 1>(a, d_workspace, cs) : launch_decode<64, 2>(a, d_workspace, cs));
-  return e == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return FP8RL_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
 }

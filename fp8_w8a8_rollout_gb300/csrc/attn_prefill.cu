@@ -308,6 +308,9 @@ __global__ void __launch_bounds__(kApThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // everything above touches this CTA alone; from here on the kernel before counts
+  grid_dep_launch_dependents();
+  grid_dep_wait();
   float2* row_sum = reinterpret_cast<float2*>(base_ptr + C::kRows);  // [tile][row]: reference maximum, sum
 
   const PlanHeader head = *reinterpret_cast<const PlanHeader*>(a.plan);
@@ -864,7 +867,20 @@ fp8rl_status launch_prefill(const CUtensorMap& mq, const CUtensorMap& mk, const 
     ready[dev].store(ctx, std::memory_order_release);
   }
   const int64_t most = (int64_t)a.capacity * a.hkv * (a.group / a.pack);
-  kernel<<<(unsigned)std::max<int64_t>(1, std::min<int64_t>(sm_count(), most)), kApThreads, ApCfg<D>::kSmem, stream>>>(mq, mk, mv, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(sm_count(), most)));
+  cfg.blockDim = dim3(kApThreads);
+  cfg.dynamicSmemBytes = ApCfg<D>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a) != cudaSuccess) {
+    cudaGetLastError();
+    return FP8RL_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
 }
 

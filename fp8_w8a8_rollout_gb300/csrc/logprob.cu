@@ -282,6 +282,8 @@ struct LpArgs {
 template <typename In, bool TOP>
 __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
   constexpr int N = Row<In>::N, U = kLpUnroll;
+  ptx::grid_dep_launch_dependents();
+  ptx::grid_dep_wait();
   const int64_t r = blockIdx.y;
   const int rank = blockIdx.x, ranks = gridDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t t = a.tokens[r];
@@ -509,6 +511,8 @@ __device__ __forceinline__ void store1<float>(float* p, float v) {
 template <typename In>
 __global__ void __launch_bounds__(kLpThreads) logprob_grad_kernel(const LpGradArgs a) {
   constexpr int N = Row<In>::N, U = kLpUnroll;
+  ptx::grid_dep_launch_dependents();
+  ptx::grid_dep_wait();
   const int64_t r = blockIdx.y;
   const In* x = static_cast<const In*>(a.x) + r * a.ldx;
   In* dx = static_cast<In*>(a.dx) + r * a.ldd;
@@ -615,12 +619,14 @@ cudaError_t launch_logprob(const LpArgs& a, int64_t rows, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned)cluster, (unsigned)rows);
   cfg.blockDim = dim3(kLpThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, logprob_kernel<In, TOP>, a);
 }
 
@@ -709,8 +715,21 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, i
     const int64_t rounds = (vocab + round - 1) / round;
     const int64_t each = std::max<int64_t>(1, std::min<int64_t>(5, rounds * n / ((int64_t)sm_count() * 24)));
     const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(65535, (rounds + each - 1) / each)), (unsigned)n);
-    if (logits_fp32) logprob_grad_kernel<float><<<grid, kLpThreads, 0, cs>>>(a);
-    else logprob_grad_kernel<uint16_t><<<grid, kLpThreads, 0, cs>>>(a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = cs;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    const cudaError_t e = logits_fp32 ? cudaLaunchKernelEx(&cfg, logprob_grad_kernel<float>, a)
+                                      : cudaLaunchKernelEx(&cfg, logprob_grad_kernel<uint16_t>, a);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return FP8RL_ERR_CUDA;
+    }
   }
   return cudaGetLastError() == cudaSuccess ? FP8RL_OK : FP8RL_ERR_CUDA;
 }

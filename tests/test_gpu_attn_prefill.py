@@ -73,7 +73,7 @@ def check(lens, hq, hkv, d, seed=0, scale=None, **more):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (8, 2), (32, 4), (6, 2), (12, 2), (5, 1), (40, 4), (16, 1), (64, 1), (256, 1)])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (8, 2), (32, 4), (6, 2), (12, 2), (5, 1), (36, 4), (16, 1), (64, 1), (256, 1)])
 def test_heads(hq, hkv, d):
     check([300, 77, 1], hq, hkv, d, seed=hq + d)
 
