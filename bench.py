@@ -89,7 +89,8 @@ def parse():
     ap.add_argument("--case", default=None,
                     help="time one kernel alone (for profiling): gemm:M:N:K[:fmt], aqg:M:N:K[:fmt], grouped:gate_up|down[:fmt], "
                          "wq:layer[:fmt], aq:M:K[:fmt], fused:M[:fmt], fused_moe[:fmt], kv:TOKENS, "
-                         "kvcal:TOKENS, moe_plan, moe_dispatch, moe_combine, tis[:RESPONSES]")
+                         "kvcal:TOKENS, moe_plan, moe_dispatch, moe_combine, tis[:RESPONSES], op:NAME (a case of "
+                         "perf/operators.py, through the binding's helpers)")
     ap.add_argument("--bn", type=int, default=0, help="with --case: force the GEMM tile width (128 or 256)")
     ap.add_argument("--wait-mode", type=int, default=0, help="with --case: GEMM wait style (test hook 4)")
     ap.add_argument("--l2-prefetch", type=int, default=-1, help="with --case: GEMM L2 prefetch distance (test hook 5)")
@@ -1209,6 +1210,17 @@ def main_case(args):
         kl = torch.empty(3, dtype=torch.float64, device=dev)
         fn = lambda: fp8rl.fp8rl_tis_weights(lt, lr, msk, n, 2.0, w, kl, ws, ws.numel())
         work = {"bytes": 13 * n}
+    elif kind == "op":
+        from perf import operators as ops
+        case = next((c for c in ops.listed() if c["name"] == parts[1]), None)
+        if case is None:
+            raise SystemExit(f"no case named {parts[1]!r}: " + ", ".join(c["name"] for c in ops.listed()))
+        ops.own = True
+        state = ops.prepare(case, 0)
+        fn = lambda: ops.run(state)
+        work = ops.work(case)
+        if work["bytes"] < 2 * L2_BYTES:
+            flush = l2_flusher(torch, dev)
     elif kind == "wq":
         fmt = int(parts[2]) if len(parts) > 2 else 0
         layer = [w for _, w in synth.qwen3_8b_layer(0, 0, device=dev)]

@@ -34,6 +34,7 @@
 // workspace; the CTA that arrives last merges them in CTA order, so the
 // result has the same bits on every run.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 
 #include "common.cuh"
@@ -589,9 +590,18 @@ cudaError_t launch_decode(AdArgs a, void* workspace, cudaStream_t stream) {
   a.tickets = static_cast<uint32_t*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(NT));
   const size_t smem = ad_smem<D, NT>() + ((size_t)a.batch + 1) * 8;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the attribute lives in the context: set once per device and context, for the largest batch
+  static std::atomic<uint64_t> ready[64];
+  int dev = 0;
+  const uint64_t ctx = current_context_id();
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !ctx) return cudaErrorInvalidDevice;
+  if (ready[dev].load(std::memory_order_acquire) != ctx) {
+    e = cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(ad_smem<D, NT>() + (kAdMaxBatch + 1) * 8));
     if (e != cudaSuccess) return e;
+    ready[dev].store(ctx, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sm_count() * ctas_per_sm(NT)));

@@ -695,8 +695,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
         const float2 ml = row_sum[x * kApTile + row];
         const float inv = 1.0f / ml.y;
         const int32_t pos = it.pos0 + x * (kApTile / a.pack) + row / a.pack, head = it.head0 + row % a.pack;
-        const bool store = pos < it.len;
         const int64_t token = (int64_t)it.start + pos;
+        const bool store = pos < it.len && dcheck(token < a.total, a.err);
         uint16_t* dst = a.out + token * a.ldo + (int64_t)head * D;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {

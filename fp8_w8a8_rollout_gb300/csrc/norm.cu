@@ -213,6 +213,8 @@ extern "C" FP8RL_API fp8rl_status fp8rl_rmsnorm_quant(const void* x_bf16, int64_
     return FP8RL_ERR_INVALID_ARG;
   if (m == 0 || k == 0) return FP8RL_OK;
   if (!x_bf16 || !weight_bf16 || !q_e4m3 || !x_scale) return FP8RL_ERR_INVALID_ARG;
+  // in place, h's rows are those it replaces
+  if (h_bf16 && ((h_bf16 == residual_bf16 && ldh != ldr) || (h_bf16 == x_bf16 && ldh != ldx))) return FP8RL_ERR_INVALID_ARG;
   if (k > kNormMaxK || m > INT32_MAX) return FP8RL_ERR_SHAPE;
   if (!aligned(x_bf16, 2) || !aligned(residual_bf16, 2) || !aligned(weight_bf16, 2) || !aligned(h_bf16, 2))
     return FP8RL_ERR_ALIGNMENT;

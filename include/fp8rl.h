@@ -36,14 +36,16 @@
  *   - Calls are asynchronous on `stream` (a cudaStream_t passed as void*;
  *     NULL is the legacy default stream).  Results are ready once the stream
  *     is synchronised.
- *   - Overlapped launches: fp8rl_quant_act_group, fp8rl_rmsnorm_quant and the GEMMs at decode
+ *   - Overlapped launches: fp8rl_quant_act_group, fp8rl_rmsnorm_quant,
+ *     fp8rl_attn_prefill, fp8rl_attn_decode, fp8rl_logprob,
+ *     fp8rl_logprob_backward and the GEMMs at decode
  *     sizes (dense, m <= 64, and up to 128 for the narrow shapes that debug
  *     key 10 lists; fp8rl_gemm_act_quant at m <= 16) are launched
  *     with programmatic stream serialisation, and let the next kernel of the
  *     stream start before they complete.  Such a kernel may begin while the kernel before it on the
  *     stream is still running; it waits for that kernel's completion before
- *     it reads any activation or scale of X and before it writes anything,
- *     but the decode GEMM reads its first weight tiles (wq) before that wait.
+ *     it reads any input and before it writes anything, but
+ *     the decode GEMM reads its first weight tiles (wq) before that wait.
  *     No kernel of this library that lets a dependent start early writes
  *     weights; a caller whose own kernel writes wq and triggers its
  *     dependents early (griddepcontrol.launch_dependents) must not enqueue a
@@ -570,7 +572,8 @@ FP8RL_API fp8rl_status fp8rl_tis_weights(const float* d_lp_train, const float* d
  *   residual_bf16 device, bf16 [m][k], row stride ldr; null: none
  *   weight_bf16   device, bf16 [k]
  *   h_bf16        device, bf16 [m][k], row stride ldh, out: h rounded once (the next
- *                 residual); null: not written.  May be residual_bf16 or x_bf16 itself.
+ *                 residual); null: not written.  May be residual_bf16 or x_bf16 itself
+ *                 (with that one's row stride), no other overlap.
  *   q_e4m3        device, E4M3 [m][k], row stride ldq
  *   x_scale       device, [ceil(k/128)][m], fp32 or uint8 (fmt)
  * Rows that are 16-byte aligned (k and the strides multiples of 8) take the
@@ -655,8 +658,9 @@ FP8RL_API fp8rl_status fp8rl_attn_prefill(const void* q_bf16, int64_t ldq, const
  * Errors: INVALID_ARG (null pointers, negative sizes, short strides, q_heads not a multiple
  *         of kv_heads, softmax_scale not positive and finite, workspace too small),
  *         SHAPE (head_dim other than 64 and 128, batch > 8192, more than 2^30 keys a sequence, a
- *         cache of more than 64 GB), ALIGNMENT (q 4-byte with an even ldq; out 8-byte with ldo % 4 == 0; caches 16-byte with ld_cache % 16 == 0;
- *         workspace 16-byte; element alignment), CUDA.
+ *         cache of more than 64 GB), ALIGNMENT (q 4-byte with an even ldq; out 8-byte with
+ *         ldo % 4 == 0; caches 16-byte with ld_cache % 16 == 0; workspace 16-byte; element
+ *         alignment), CUDA.
  */
 FP8RL_API size_t fp8rl_attn_decode_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t ldq, int64_t batch, int64_t q_heads,
