@@ -31,7 +31,7 @@ __all__ = [
     "fp8rl_gemm_blockscaled_static", "fp8rl_gemm_swiglu_quant", "fp8rl_grouped_gemm_swiglu_quant",
     "gemm_swiglu_quant", "grouped_gemm_swiglu_quant", "quant_gate_up_interleaved",
     "fp8rl_kv_calibrate", "fp8rl_kv_append", "kv_calibrate", "kv_append",
-    "fp8rl_attn_prefill_plan_size", "fp8rl_attn_prefill_plan", "fp8rl_attn_prefill", "attn_prefill_plan", "attn_prefill",
+    "fp8rl_attn_prefill_plan_size", "fp8rl_attn_prefill_plan", "fp8rl_attn_prefill", "attn_prefill_plan", "attn_prefill", "AttnPlan",
     "fp8rl_rmsnorm_quant", "rmsnorm_quant", "fp8rl_attn_decode_workspace_size", "fp8rl_attn_decode",
     "attn_decode_workspace", "attn_decode", "fp8rl_logprob", "fp8rl_logprob_backward", "logprobs", "logprobs_backward",
     "fp8rl_e4m3_encode", "fp8rl_debug_set", "fp8rl_sync_status", "fp8rl_status_string", "fp8rl_version",
@@ -814,7 +814,7 @@ def attn_prefill_plan(cu_seqlens: torch.Tensor, total_tokens: int, q_heads: int,
     batch = cu_seqlens.numel() - 1
     nbytes = fp8rl_attn_prefill_plan_size(total_tokens, batch, q_heads, kv_heads)
     if nbytes == 0:
-        raise ValueError("q_heads must be a multiple of kv_heads, at most 2^30 tokens and 2^20 sequences")
+        raise ValueError("q_heads must be a multiple of kv_heads, at most 2^26 tokens and 2^20 sequences")
     data = _out((nbytes,), torch.uint8, cu_seqlens.device)
     fp8rl_attn_prefill_plan(cu_seqlens, batch, total_tokens, q_heads, kv_heads, data, nbytes, stream)
     return AttnPlan(data, batch, total_tokens, q_heads, kv_heads)
@@ -841,7 +841,8 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPl
         _check_out(out[0], (tokens, hq, d), torch.bfloat16, "out")
         _check_out(out[1], (tokens, hq), torch.float32, "lse")
     fp8rl_attn_prefill(q, _ld(q, tokens, hq * d), k, _ld(k, tokens, hkv * d), v, _ld(v, tokens, hkv * d), plan.data,
-                       plan.data.numel(), plan.batch, tokens, hq, hkv, d, d ** -0.5 if softmax_scale is None else softmax_scale, out[0], hq * d, out[1], stream)
+                       plan.data.numel(), plan.batch, tokens, hq, hkv, d,
+                       d ** -0.5 if softmax_scale is None else softmax_scale, out[0], hq * d, out[1], stream)
     return out
 
 

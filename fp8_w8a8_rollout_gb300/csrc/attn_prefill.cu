@@ -54,6 +54,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;
 constexpr uint32_t kApTimeoutNs = 2000000000u;  // of a 32-bit nanosecond counter
 
+// a step of the longest item's waits stays well inside the limit (2^19 key tiles of about 1.5 us)
+constexpr int64_t kApMaxTokens = (int64_t)1 << 26;
+
 // the plan: a header, then one int4 per item {first token of the sequence,
 // its length, first position of the item, 0}
 struct PlanHeader {
@@ -891,7 +894,7 @@ using namespace fp8rl;
 
 extern "C" FP8RL_API size_t fp8rl_attn_prefill_plan_size(int64_t total_tokens, int64_t batch, int64_t q_heads,
                                                          int64_t kv_heads) {
-  if (total_tokens < 0 || total_tokens > (1 << 30) || batch < 0 || batch > (1 << 20) || !heads_ok(q_heads, kv_heads)) return 0;
+  if (total_tokens < 0 || total_tokens > kApMaxTokens || batch < 0 || batch > (1 << 20) || !heads_ok(q_heads, kv_heads)) return 0;
   return (size_t)(16 * (1 + plan_capacity(total_tokens, batch, pack_of(q_heads / kv_heads))));
 }
 
@@ -899,7 +902,7 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_prefill_plan(const int32_t* d_cu_se
                                                           int64_t q_heads, int64_t kv_heads, void* d_plan,
                                                           size_t plan_bytes, void* stream) {
   if (batch < 0 || total_tokens < 0 || !heads_ok(q_heads, kv_heads)) return FP8RL_ERR_INVALID_ARG;
-  if (total_tokens > (1 << 30) || batch > (1 << 20)) return FP8RL_ERR_SHAPE;
+  if (total_tokens > kApMaxTokens || batch > (1 << 20)) return FP8RL_ERR_SHAPE;
   if (!d_plan || (batch > 0 && !d_cu_seqlens)) return FP8RL_ERR_INVALID_ARG;
   if (plan_bytes < fp8rl_attn_prefill_plan_size(total_tokens, batch, q_heads, kv_heads)) return FP8RL_ERR_INVALID_ARG;
   if (!aligned(d_plan, 16) || !aligned(d_cu_seqlens, 4)) return FP8RL_ERR_ALIGNMENT;
@@ -919,7 +922,7 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_prefill(const void* q_bf16, int64_t
   if (batch < 0 || total_tokens < 0 || !heads_ok(q_heads, kv_heads) || head_dim < 1 || !(softmax_scale > 0.0f) ||
       !(softmax_scale <= FLT_MAX))
     return FP8RL_ERR_INVALID_ARG;
-  if ((head_dim != 64 && head_dim != 128) || total_tokens > (1 << 30) || batch > (1 << 20)) return FP8RL_ERR_SHAPE;
+  if ((head_dim != 64 && head_dim != 128) || total_tokens > kApMaxTokens || batch > (1 << 20)) return FP8RL_ERR_SHAPE;
   if (ldq < q_heads * head_dim || ldk < kv_heads * head_dim || ldv < kv_heads * head_dim || ldo < q_heads * head_dim)
     return FP8RL_ERR_INVALID_ARG;
   if (batch == 0 || total_tokens == 0) return FP8RL_OK;

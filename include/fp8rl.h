@@ -615,7 +615,7 @@ FP8RL_API fp8rl_status fp8rl_rmsnorm_quant(const void* x_bf16, int64_t ldx, cons
  * The same bits on every run.
  * Errors: INVALID_ARG (null pointers, negative sizes, short strides, q_heads not a multiple of
  *         kv_heads, softmax_scale not positive and finite, plan too small), SHAPE (head_dim other
- *         than 64 and 128, more than 2^30 tokens, 2^20 sequences), ALIGNMENT (q, k, v, out and their row
+ *         than 64 and 128, more than 2^26 tokens, 2^20 sequences), ALIGNMENT (q, k, v, out and their row
  *         strides 16 bytes; plan 16 bytes; element alignment), CUDA.  A plan made for other heads
  *         or another total_tokens writes nothing and is reported as DEVICE_CHECK by
  *         fp8rl_sync_status, a device wait that ran out as TIMEOUT.

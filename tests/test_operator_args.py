@@ -68,7 +68,7 @@ PREFILL = dict(q=P, ldq=6144, k=P, ldk=6144, v=P, ldv=6144, plan=P, plan_bytes=1
     (1, dict(q=None)), (1, dict(k=None)), (1, dict(v=None)), (1, dict(plan=None)), (1, dict(out=None)), (1, dict(batch=-1)),
     (1, dict(total=-1)), (1, dict(hq=30)), (1, dict(hkv=0)), (1, dict(ldq=4088)), (1, dict(ldk=1016)), (1, dict(ldv=1016)),
     (1, dict(ldo=4088)), (1, dict(scale=0.0)), (1, dict(scale=math.nan)), (1, dict(plan_bytes=16)), (2, dict(d=96)),
-    (2, dict(total=(1 << 30) + 1)), (2, dict(batch=(1 << 20) + 1)), (3, dict(q=P + 8)), (3, dict(k=P + 8)), (3, dict(v=P + 8)),
+    (2, dict(total=(1 << 26) + 1)), (2, dict(batch=(1 << 20) + 1)), (3, dict(q=P + 8)), (3, dict(k=P + 8)), (3, dict(v=P + 8)),
     (3, dict(out=P + 8)), (3, dict(ldq=6145)), (3, dict(ldk=6148)), (3, dict(ldv=6148)), (3, dict(ldo=4100)), (3, dict(plan=P + 8)),
     (3, dict(lse=P + 2)), (0, dict(batch=0)), (0, dict(total=0)),
 ])
@@ -81,7 +81,7 @@ PLAN = dict(cu=P, batch=2, total=100, hq=32, hkv=8, plan=P, plan_bytes=1 << 20, 
 
 @pytest.mark.parametrize("status,changes", [
     (1, dict(cu=None)), (1, dict(plan=None)), (1, dict(batch=-1)), (1, dict(total=-1)), (1, dict(hq=30)), (1, dict(plan_bytes=16)),
-    (2, dict(total=(1 << 30) + 1)), (2, dict(batch=(1 << 20) + 1)), (3, dict(cu=P + 2)), (3, dict(plan=P + 8)),
+    (2, dict(total=(1 << 26) + 1)), (2, dict(batch=(1 << 20) + 1)), (3, dict(cu=P + 2)), (3, dict(plan=P + 8)),
 ])
 def test_prefill_plan(lib, status, changes):
     assert call(lib, "fp8rl_attn_prefill_plan", PLAN, **changes) == status
@@ -90,7 +90,7 @@ def test_prefill_plan(lib, status, changes):
 def test_prefill_plan_size(lib):
     f = lib.fp8rl_attn_prefill_plan_size
     assert f(1000, 3, 32, 8) >= 16 * (1 + 1000 // 64 + 3) and f(0, 0, 1, 1) == 16
-    assert f(-1, 1, 8, 8) == 0 and f(1, -1, 8, 8) == 0 and f(1, 1, 8, 3) == 0 and f((1 << 30) + 1, 1, 8, 8) == 0
+    assert f(-1, 1, 8, 8) == 0 and f(1, -1, 8, 8) == 0 and f(1, 1, 8, 3) == 0 and f((1 << 26) + 1, 1, 8, 8) == 0 and f(1 << 26, 1, 8, 8) > 0
 
 
 LP = dict(x=P, fp32=0, rows=4, vocab=100, ld=100, T=1.0, tokens=P, lp=P, ent=P, stats=P, topk=4, ids=P, top=P, stream=None)
