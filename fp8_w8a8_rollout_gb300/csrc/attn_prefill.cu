@@ -65,6 +65,8 @@ struct PlanHeader {
 
 struct ApArgs {
   const int4* plan;
+  const uint16_t *q, *k, *v;  // for rows that are taken again (the tensor maps serve the others)
+  int64_t ldq, ldk, ldv;
   uint16_t* out;
   float* lse;  // or null
   uint32_t* err;
@@ -252,6 +254,41 @@ __device__ __forceinline__ Item item_of(const ApArgs& a, uint32_t w, int32_t par
   return it;
 }
 
+// One output row by plain arithmetic from its final reference maximum (times
+// the scale) and 1 / sum: sum_j p_j v_j over the keys that it sees and no
+// others.  For items with a non-finite value in their last key tiles.
+template <int D>
+__device__ __forceinline__ void take_again(const ApArgs& a, const Item& it, int32_t pos, int32_t head, bool store, float mc,
+                                           float inv, uint16_t* dst) {
+  if (!store) return;
+  const float c = a.softmax_scale * kLog2e;
+  const uint16_t* q = a.q + ((int64_t)it.start + pos) * a.ldq + (int64_t)head * D;
+#pragma unroll 1
+  for (int d0 = 0; d0 < D; d0 += 8) {
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int32_t j = 0; j <= pos; ++j) {
+      const uint16_t* k = a.k + ((int64_t)it.start + j) * a.ldk + (int64_t)it.kvh * D;
+      float s = 0.0f;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 2) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(q + d), y = *reinterpret_cast<const uint32_t*>(k + d);
+        s = fmaf(bf16_hi(x), bf16_hi(y), fmaf(bf16_lo(x), bf16_lo(y), s));
+      }
+      const float p = ex2(fmaf(s, c, -mc));
+      const uint4 v = *reinterpret_cast<const uint4*>(a.v + ((int64_t)it.start + j) * a.ldv + (int64_t)it.kvh * D + d0);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[2 * e] = fmaf(p, bf16_lo(w[e]), acc[2 * e]);
+        acc[2 * e + 1] = fmaf(p, bf16_hi(w[e]), acc[2 * e + 1]);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + d0) = make_uint4(bf16x2_rn(acc[0] * inv, acc[1] * inv), bf16x2_rn(acc[2] * inv, acc[3] * inv),
+                                                     bf16x2_rn(acc[4] * inv, acc[5] * inv), bf16x2_rn(acc[6] * inv, acc[7] * inv));
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kApThreads, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -271,28 +308,27 @@ __global__ void __launch_bounds__(kApThreads, 1)
   uint64_t* o_full = p_full + 2;            // O of a tile finished
   uint64_t* l_full = o_full + 2;            // its row sums in shared memory (128 threads)
   uint64_t* o_empty = l_full + 2;           // both read by the output warps (128 threads)
-  uint64_t* mended = o_empty + 2;           // the item's ragged value tile has been zeroed past its end
-  uint64_t* to_mend = mended + 1;           // it has arrived
-  uint64_t* drain = to_mend + 1;
+  uint64_t* mended = o_empty + 2;           // the mender is done with a stage (one per stage, in the ring's phases)
+  uint64_t* drain = mended + kApStages;
   uint64_t* item_full = drain + 1;          // an item's slot is filled
   uint64_t* item_empty = item_full + kApItems;  // every reader has copied it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_empty + kApItems);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  volatile int* flags = abort_flag + 1;     // per item slot: values that its masks cannot cancel
   volatile int* abortv = abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kApStages; ++s) {
       mbar_init(smem_u32(&kv_full[s]), 1);
-      mbar_init(smem_u32(&kv_empty[s]), 1);
+      mbar_init(smem_u32(&mended[s]), 1);
+      mbar_init(smem_u32(&kv_empty[s]), 2);  // the products', the mender's
     }
     mbar_init(smem_u32(drain), 1);
     for (int i = 0; i < kApItems; ++i) {
       mbar_init(smem_u32(&item_full[i]), 1);
       mbar_init(smem_u32(&item_empty[i]), kApItemReaders);
     }
-    mbar_init(smem_u32(mended), 1);
-    mbar_init(smem_u32(to_mend), 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&q_full[x]), 1);
       mbar_init(smem_u32(&q_empty[x]), 1);
@@ -406,7 +442,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         auto advance = [&] {
           if (++stage == kApStages) stage = 0, parity ^= 1;
         };
-        uint32_t q_phase = 0, p_phase = 0, o_phase = 3, mends = 0;  // bit x: the parity that tile x waits for next
+        uint32_t q_phase = 0, p_phase = 0, o_phase = 3;  // bit x: the parity that tile x waits for next
         bool alive = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           return wait_for(smem_u32(bar), parity, abortv);
@@ -454,13 +490,10 @@ __global__ void __launch_bounds__(kApThreads, 1)
           const int32_t n = max(it.n0, it.n1);
           more = take(i, next, true);
           for (int32_t j = 0; j < n && alive; ++j) {
+            // (value tiles that the item does not see whole come by way of the mender)
             const uint32_t vs = stage;
-            alive = wait(&kv_full[vs], parity);
+            alive = wait(j >= it.pos0 / kApTile ? &mended[vs] : &kv_full[vs], parity);
             advance();
-            if (alive && it.len - j * kApTile < kApTile) {
-              mbar_arrive(smem_u32(to_mend));
-              alive = wait(mended, mends++ & 1);
-            }
             // The scores to issue behind this step's products: of the next key
             // tile, or of the next item's first one, so that its softmax starts
             // while this item ends.
@@ -535,30 +568,46 @@ __global__ void __launch_bounds__(kApThreads, 1)
       __syncwarp();
     } else if (warp == 3) {
       // ------------------------------------------------------------ mender
-      // Rows of a sequence's last value tile that lie past its end are
-      // another sequence's, and a probability of 0 does not cancel a NaN: zero them
-      // before the tile is multiplied.
-      uint32_t g = 0, mends = 0;
+      // A probability of 0 does not cancel a NaN or an infinity.  In the key
+      // tiles that an item does not see whole, the value rows past its last
+      // position (later ones, or another sequence's) are zeroed before they are
+      // multiplied; those from its first position on, which some of its rows see
+      // and some do not, are looked through, and if one is not finite the output
+      // warps take the item's rows again without the tensor cores.  Every tile
+      // passes here and is held until it has: no phase of the ring is missed,
+      // and none is signalled twice before the MMA thread has seen it.
+      uint32_t stage = 0, parity = 0;
       bool alive = true;
       Item it;
       for (uint32_t i = 0; alive && take_warp(i, it);) {
         const int32_t n = max(it.n0, it.n1);
-        g += 2 * n;
-        const int32_t valid = it.len - (n - 1) * kApTile;
-        if (valid >= kApTile) continue;
-        const uint32_t vs = (g - 1) % kApStages;  // the item's last stage
-        // (the MMA thread asks once the tile has arrived: waiting on the tile's own
-        // barrier from here could mistake an earlier round of the ring for it)
-        alive = __all_sync(0xffffffffu, wait_for(smem_u32(to_mend), mends++ & 1, abortv));
-        if (!alive) break;
-        const uint32_t v0 = C::kRing + vs * C::kTileBytes;
-        for (int32_t i = valid * 8 + lane; i < kApTile * 8; i += 32)
+        const int32_t end = min(it.len, it.pos0 + 2 * (kApTile / a.pack));
+        uint32_t worst = 0;  // packed magnitudes
+        for (int32_t t = 0; t < 2 * n; ++t) {
+          alive = __all_sync(0xffffffffu, wait_for(smem_u32(&kv_full[stage]), parity, abortv));
+          if (!alive) break;
+          const int32_t k0 = (t >> 1) * kApTile;
+          if ((t & 1) && k0 + kApTile > it.pos0) {
+            uint8_t* tile = base_ptr + C::kRing + stage * C::kTileBytes;
+            const int32_t r0 = max(it.pos0 - k0, 0), r1 = min(end - k0, kApTile);
+            for (int32_t e = r0 * 8 + lane; e < kApTile * 8; e += 32)
 #pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-            *reinterpret_cast<uint4*>(base_ptr + v0 + h * C::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(mended));
+              for (int h = 0; h < C::kHalves; ++h) {
+                uint4* p = reinterpret_cast<uint4*>(tile + h * C::kHalfBytes + e * 16);
+                if (e < r1 * 8) worst = absmax_u4(worst, *p);
+                else *p = make_uint4(0u, 0u, 0u, 0u);
+              }
+            const bool bad = __any_sync(0xffffffffu, max(worst & 0xFFFFu, worst >> 16) >= 0x7F80u);
+            if (lane == 0) flags[(i - 1) % kApItems] = bad;
+            fence_proxy_async_shared();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&mended[stage]));
+            mbar_arrive(smem_u32(&kv_empty[stage]));
+          }
+          if (++stage == kApStages) stage = 0, parity ^= 1;
+        }
       }
     }
   } else if (warp < 12) {
@@ -701,15 +750,21 @@ __global__ void __launch_bounds__(kApThreads, 1)
         const int64_t token = (int64_t)it.start + pos;
         const bool store = pos < it.len && dcheck(token < a.total, a.err);
         uint16_t* dst = a.out + token * a.ldo + (int64_t)head * D;
+        if (flags[(i - 1) % kApItems]) {
+          take_again<D>(a, it, pos, head, store, ml.x, inv, dst);
+          mbar_arrive(smem_u32(&o_empty[x]));
+          if (store && a.lse) a.lse[token * a.hq + head] = fmaf(ml.x, kLn2, logf(ml.y));
+          continue;
+        }
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
+        for (int e = 0; e < D / 32; ++e) {
           uint32_t o[32];
-          tmem_ld_32x32b_x32(tmem + lanes + C::kTmemO + 128 * x + 32 * i, o);
+          tmem_ld_32x32b_x32(tmem + lanes + C::kTmemO + 128 * x + 32 * e, o);
           tmem_wait_ld_regs(o);
           uint32_t v[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) v[q] = bf16x2_rn(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
-          if (i == D / 32 - 1) {  // O and the sums have been read: the next item may write them
+          if (e == D / 32 - 1) {  // O and the sums have been read: the next item may write them
             tc_fence_before();
             mbar_arrive(smem_u32(&o_empty[x]));
           }
@@ -718,7 +773,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
             for (int q = 0; q < 2; ++q) {
               const uint4 lo = make_uint4(v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3]);
               const uint4 hi = make_uint4(v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]);
-              uint16_t* to = dst + 32 * i + 16 * q;
+              uint16_t* to = dst + 32 * e + 16 * q;
               if (a.wide) {
                 st_global_v8(to, lo, hi);
               } else {
@@ -933,6 +988,8 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_prefill(const void* q_bf16, int64_t
     return FP8RL_ERR_ALIGNMENT;
   ApArgs a{};
   a.plan = static_cast<const int4*>(d_plan);
+  a.q = static_cast<const uint16_t*>(q_bf16), a.k = static_cast<const uint16_t*>(k_bf16), a.v = static_cast<const uint16_t*>(v_bf16);
+  a.ldq = ldq, a.ldk = ldk, a.ldv = ldv;
   a.out = static_cast<uint16_t*>(out_bf16);
   a.lse = d_lse;
   a.ldo = ldo;

@@ -609,9 +609,10 @@ FP8RL_API fp8rl_status fp8rl_rmsnorm_quant(const void* x_bf16, int64_t ldx, cons
  *   d_lse           device, fp32 [total_tokens][q_heads], or null
  * Tokens of no sequence are not written.  Scores, statistics and sums are
  * fp32, the probabilities are rounded to bf16 for the second product, the
- * output once to bf16.  A sequence is not affected by what other sequences
- * hold; within one, a NaN or infinity in v_j reaches the outputs of positions
- * from the start of j's 128-key tile on (0 * NaN), one in k_j those from j on.
+ * output once to bf16.  An output depends on its own sequence's positions up
+ * to its own alone, whatever the others hold (NaN and infinities included; rows
+ * whose last key tiles hold a non-finite value are computed by plain fp32
+ * arithmetic, slowly).
  * The same bits on every run.
  * Errors: INVALID_ARG (null pointers, negative sizes, short strides, q_heads not a multiple of
  *         kv_heads, softmax_scale not positive and finite, plan too small), SHAPE (head_dim other

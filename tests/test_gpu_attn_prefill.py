@@ -92,6 +92,25 @@ def test_packed():
     check([200] * 40 + [1500], 16, 2, 64, seed=3)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (1, 1, 64), (8, 1, 128), (32, 8, 64)])
+def test_many_short_prompts(hq, hkv, d):
+    """Thousands of items of one or two key tiles: every ring of the kernel
+    turns over many times with nothing to wait for in between.  Checked against
+    the same prompts alone."""
+    g = torch.Generator().manual_seed(hq)
+    kinds = [int(x) for x in torch.randint(1, 200, (12,), generator=g)] + [1, 128, 129]
+    order = [kinds[int(x)] for x in torch.randint(0, len(kinds), (3000,), generator=g)]
+    q, k, v, cu = make(order, hq, hkv, d, seed=hq)
+    plan = fp8rl.attn_prefill_plan(cu, q.shape[0], hq, hkv)
+    outs = [fp8rl.attn_prefill(q, k, v, plan) for _ in range(5)]
+    assert fp8rl.fp8rl_sync_status() == 0
+    for o, z in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(z, outs[0][1])
+    starts = cu.tolist()
+    for b in range(0, 3000, 211):
+        compare(*outs[0], q, k, v, starts[b], order[b])
+
+
 def test_long_prompt():
     check([5001], 4, 1, 128, seed=4)
     check([4100], 2, 2, 64, seed=5)
@@ -109,6 +128,40 @@ def test_other_sequences_do_not_leak():
     assert fp8rl.fp8rl_sync_status() == 0
     compare(out, lse, q, k, v, 0, 100)
     compare(out, lse, q, k, v, 157, 131)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (2, 2, 128), (16, 2, 64), (2, 2, 64)])
+@pytest.mark.parametrize("bad", [0, 1, 63, 64, 100, 127, 128, 200, 299])
+def test_later_positions_do_not_leak(hq, hkv, d, bad):
+    """A NaN or an infinity in v_j or k_j reaches no position before j; from j
+    on the formula's own NaN or infinity appears."""
+    n = 300
+    q, k, v, cu = make([n], hq, hkv, d, seed=bad + 1)
+    plan = fp8rl.attn_prefill_plan(cu, n, hq, hkv)
+    for value in (math.nan, math.inf, -math.inf):
+        vv = v.clone()
+        vv[bad, 0, 3] = value
+        out, lse = fp8rl.attn_prefill(q, k, vv, plan)
+        assert fp8rl.fp8rl_sync_status() == 0
+        clean = torch.where(torch.isfinite(vv), vv, 0.0)
+        if bad:
+            compare(out, lse, q, k, vv, 0, bad)
+        group = hq // hkv
+        hit = out[bad:, :group, 3].float()
+        assert bool(torch.isnan(hit).all()) if math.isnan(value) else bool((~torch.isfinite(hit)).all())
+        # every other column and the other KV heads are as without it
+        want, want_lse = fp8rl.attn_prefill(q, k, clean, plan)
+        keep = torch.ones(hq, d, dtype=torch.bool, device="cuda")
+        keep[:group, 3] = False
+        diff = (out.float() - want.float()).abs()[:, keep]
+        assert bool((diff <= 2.0 ** -6 * want.float().abs()[:, keep] + 2.0 ** -6).all())
+        assert torch.equal(lse, want_lse)
+    kk = k.clone()
+    kk[bad, hkv - 1, 5] = math.nan
+    out, lse = fp8rl.attn_prefill(q, kk, v, plan)
+    if bad:
+        compare(out, lse, q, kk, v, 0, bad)
+    assert bool(torch.isnan(out[bad:, hq - 1].float()).all()) and bool(torch.isnan(lse[bad:, hq - 1]).all())
 
 
 def test_tokens_of_no_sequence_are_not_written():
