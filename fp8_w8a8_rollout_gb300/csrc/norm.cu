@@ -9,7 +9,8 @@
 // next residual branch reads is rounded to bf16.
 //
 // HBM-bound: 7 bytes an element with a residual (x, residual, h, the code),
-// 3 without.  A CTA takes one row and holds it in registers (8-column pieces,
+// 3 without; 8192 x 4096 takes 38.4 us back to back, 35 alone (6.1 and 6.7 TB/s;
+// 128 threads with four pieces each 67, 512 with one 45).  A CTA takes one row and holds it in registers (8-column pieces,
 // 16 consecutive lanes to a 128-column group), so each input is read once:
 // all its loads, one CTA-wide sum of squares, then the group maxima by four
 // shuffles.  Threads per row and pieces per thread follow k alone.
