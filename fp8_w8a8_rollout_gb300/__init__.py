@@ -143,20 +143,22 @@ def load_library(build_if_missing: bool = False):
 
 def _p(x) -> int | None:
     """A device pointer from a tensor, an int, or None."""
-    if isinstance(x, torch.Tensor):
-        return x.data_ptr()
-    return None if x is None else int(x)
+    if x is None or type(x) is int:
+        return x
+    return x.data_ptr() if isinstance(x, torch.Tensor) else int(x)
 
 
-# the current stream's handle without building a Stream object (a call's host
-# time is most of what a small launch costs)
+# the current stream's handle and the current device without torch's wrappers
+# around them (a call's host time is most of what a small launch costs); both
+# are asked only once CUDA is initialised
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int | None:
     if stream is None:
         if torch.cuda.is_initialized() and _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
         if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
@@ -430,10 +432,14 @@ def _out(shape, dtype, device):
 
 
 def _outs(specs, device):
-    """Output tensors of several (shape, dtype): _out of each, with one look at
-    the environment."""
-    make = _guarded if canaries_enabled() else None
-    return [make(shape, dtype, device) if make else torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    """Output tensors of several (shape, dtype): _out of each (None for None),
+    with one look at the environment."""
+    make = _guarded if canaries_enabled() else _empty
+    return [make(*spec, device) if spec else None for spec in specs]
+
+
+def _empty(shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _guarded(shape, dtype, device):
@@ -470,9 +476,9 @@ def _check_cuda(*tensors):
     """The kernels dereference device pointers on the current device: every
     tensor argument of a helper must be a CUDA tensor on it (None and
     non-tensor arguments are skipped)."""
-    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    cur = _current_device() if torch.cuda.is_initialized() else None
     for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.get_device() == cur:  # -1 for a host tensor
+        if t is None or not isinstance(t, torch.Tensor) or t.get_device() == cur:  # -1 for a host tensor
             continue
         if not t.is_cuda:
             raise ValueError("fp8rl helpers take CUDA tensors; a host tensor's pointer would reach the kernels")
@@ -753,22 +759,21 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
         raise ValueError("weight must be a contiguous bf16 [k] tensor")
     if residual is not None:
         _check_bf16_2d(residual, "residual")
-        if residual.shape != x.shape:
+        if residual.shape != (m, k):
             raise ValueError("residual must have x's shape")
     if out is None:
-        specs = [((m, k), torch.uint8), (((k + 127) // 128, m), _scale_dtype(fmt))]
-        if residual is None:
-            (q, s), h = _outs(specs, x.device), None
-        else:
-            q, s, h = _outs(specs + [((m, k), torch.bfloat16)], x.device)
+        q, s, h = _outs((((m, k), torch.uint8), (((k + 127) // 128, m), _scale_dtype(fmt)),
+                         None if residual is None else ((m, k), torch.bfloat16)), x.device)
+        ldq = ldh = k
     else:
         q, s, h = out
         _check_out(q, (m, k), torch.uint8, "q", rows=True)
         _check_out(s, ((k + 127) // 128, m), _scale_dtype(fmt), "scale")
         if h is not None:
             _check_out(h, (m, k), torch.bfloat16, "h", rows=True)
-    fp8rl_rmsnorm_quant(x, _ld(x, m, k), residual, 0 if residual is None else _ld(residual, m, k), weight, eps, m, k,
-                        h, 0 if h is None else _ld(h, m, k), q, _ld(q, m, k), s, fmt, stream)
+        ldq, ldh = _ld(q, m, k), 0 if h is None else _ld(h, m, k)
+    fp8rl_rmsnorm_quant(x.data_ptr(), _ld(x, m, k), residual, 0 if residual is None else _ld(residual, m, k),
+                        weight.data_ptr(), eps, m, k, h, ldh, q.data_ptr(), ldq, s.data_ptr(), fmt, stream)
     return q, s, h
 
 
@@ -792,7 +797,9 @@ def _check_heads(t: torch.Tensor, name: str):
     a wider projection output is fine)."""
     if t.dtype != torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{name} must be a bf16 [tokens, heads, head_dim] tensor")
-    if (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+    _, heads, d = t.shape
+    _, by_head, by_column = t.stride()
+    if (by_column != 1 and d > 1) or (by_head != d and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
 
 
@@ -840,9 +847,10 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPl
     else:
         _check_out(out[0], (tokens, hq, d), torch.bfloat16, "out")
         _check_out(out[1], (tokens, hq), torch.float32, "lse")
-    fp8rl_attn_prefill(q, _ld(q, tokens, hq * d), k, _ld(k, tokens, hkv * d), v, _ld(v, tokens, hkv * d), plan.data,
-                       plan.data.numel(), plan.batch, tokens, hq, hkv, d,
-                       d ** -0.5 if softmax_scale is None else softmax_scale, out[0], hq * d, out[1], stream)
+    fp8rl_attn_prefill(q.data_ptr(), _ld(q, tokens, hq * d), k.data_ptr(), _ld(k, tokens, hkv * d), v.data_ptr(),
+                       _ld(v, tokens, hkv * d), plan.data.data_ptr(), plan.data.numel(), plan.batch, tokens, hq, hkv, d,
+                       d ** -0.5 if softmax_scale is None else softmax_scale, out[0].data_ptr(), hq * d,
+                       out[1].data_ptr(), stream)
     return out
 
 
@@ -889,10 +897,10 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     else:
         _check_out(out[0], (batch, hq, d), torch.bfloat16, "out")
         _check_out(out[1], (batch, hq), torch.float32, "lse")
-    fp8rl_attn_decode(q, _ld(q, batch, hq * d), batch, hq, hkv, d, k_cache, v_cache, ldc, slots, block_table,
-                      _ld(block_table, batch, blocks), blocks, block_size, lens, scales,
-                      d ** -0.5 if softmax_scale is None else softmax_scale, out[0], hq * d, out[1], workspace,
-                      workspace.numel() * workspace.element_size(), stream)
+    fp8rl_attn_decode(q.data_ptr(), _ld(q, batch, hq * d), batch, hq, hkv, d, k_cache.data_ptr(), v_cache.data_ptr(), ldc,
+                      slots, block_table.data_ptr(), _ld(block_table, batch, blocks), blocks, block_size, lens.data_ptr(),
+                      scales.data_ptr(), d ** -0.5 if softmax_scale is None else softmax_scale, out[0].data_ptr(), hq * d,
+                      out[1].data_ptr(), workspace.data_ptr(), workspace.nbytes, stream)
     return out
 
 
@@ -917,10 +925,12 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.
         specs += [((rows, topk), torch.int32), ((rows, topk), torch.float32)]
     if out is None:
         out = _outs(specs, logits.device)
-        out = (*out, None, None) if topk <= 0 else tuple(out)
     else:
+        if len(out) < len(specs):
+            raise ValueError(f"out must hold {len(specs)} tensors")
         for t, (shape, dtype), name in zip(out, specs, ("lp", "entropy", "stats", "top_ids", "top_lp")):
             _check_out(t, shape, dtype, name)
+    out = tuple(out) if topk > 0 else (*out[:3], None, None)
     fp8rl_logprob(logits, int(logits.dtype == torch.float32), rows, vocab, _ld(logits, rows, vocab), temperature, tokens, out[0],
                   out[1], out[2], topk, out[3], out[4], stream)
     return out
