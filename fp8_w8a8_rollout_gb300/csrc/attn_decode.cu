@@ -591,12 +591,15 @@ constexpr int64_t kAdMaxLen = (int64_t)1 << 30;  // 32-bit key numbers, two tile
 
 int columns(int64_t group) { return group <= 8 ? 1 : 2; }
 
-int64_t ticket_bytes(int nt) { return ((int64_t)sm_count() * ctas_per_sm(nt) * 4 + 255) / 256 * 256; }
+// The workspace starts with the items' counters: an area of one size for every
+// shape, so that one workspace can serve several (partials never land on counters).
+constexpr int kAdMaxCtas = 4;
+int64_t ticket_bytes() { return ((int64_t)sm_count() * kAdMaxCtas * 4 + 255) / 256 * 256; }
 
 template <int D, int NT>
 cudaError_t launch_decode(AdArgs a, void* workspace, cudaStream_t stream) {
   a.tickets = static_cast<uint32_t*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(NT));
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes());
   const size_t smem = ad_smem<D, NT>() + ((size_t)a.batch + 1) * 8;
   // the attribute lives in the context: set once per device and context, for the largest batch
   static std::atomic<uint64_t> ready[64];
@@ -633,7 +636,7 @@ extern "C" FP8RL_API size_t fp8rl_attn_decode_workspace_size(int64_t q_heads, in
   if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128)) return 0;
   const int nt = columns(q_heads / kv_heads);
   const int64_t part = (int64_t)8 * nt * (head_dim + 2) * 4;
-  return (size_t)(ticket_bytes(nt) + 2 * (int64_t)sm_count() * ctas_per_sm(nt) * part);
+  return (size_t)(ticket_bytes() + 2 * (int64_t)sm_count() * ctas_per_sm(nt) * part);
 }
 
 extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t ldq, int64_t batch, int64_t q_heads,

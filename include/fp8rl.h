@@ -648,7 +648,8 @@ FP8RL_API fp8rl_status fp8rl_attn_prefill(const void* q_bf16, int64_t ldq, const
  *   d_lse           device, fp32 [batch][q_heads]: ln sum_j exp(s_j); or null
  *   d_workspace     device scratch of fp8rl_attn_decode_workspace_size() bytes, owned by the
  *                   caller, 16-byte aligned, zeroed once when it is allocated (every call leaves
- *                   its counters zero).  One call at a time per workspace.
+ *                   its counters zero); one of the largest size serves several shapes.  One call
+ *                   at a time per workspace.
  * Codes enter the products exactly; scores, softmax statistics and sums are
  * fp32, the probabilities are rounded to f16, the output once to bf16.  The
  * table and the lengths are device data and are not read on the host: a key

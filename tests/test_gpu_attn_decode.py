@@ -206,6 +206,20 @@ def test_one_workspace_across_calls_and_same_bits():
     assert torch.equal(out[0], got[0])
 
 
+def test_one_workspace_across_shapes():
+    """Shapes that need it in different sizes, on one workspace: the counters of
+    one are never another's partials."""
+    shapes = [(32, 8, 128), (40, 4, 128), (16, 16, 64), (9, 1, 64), (32, 4, 64), (12, 3, 64)]
+    ws = max((fp8rl.attn_decode_workspace(*x) for x in shapes), key=torch.Tensor.numel)
+    for turn in range(2):
+        for hq, hkv, d in shapes:
+            q, kc, vc, table, ln, scales = make([6000, 3000, 7, 9000] * 4, hq, hkv, d, 16, seed=hq)
+            want = fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16, workspace=fp8rl.attn_decode_workspace(hq, hkv, d))
+            got = fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16, workspace=ws,
+                                    out=(torch.full_like(want[0], 7), torch.full_like(want[1], 7)))
+            assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
 def test_reads_what_the_append_wrote():
     """kv_calibrate, kv_append, then attention: against fp64 attention on the
     cache's own dequantised rows."""
