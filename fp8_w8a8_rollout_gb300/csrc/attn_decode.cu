@@ -20,6 +20,13 @@
 // the products run on m16n8k16 tensor instructions with the roles swapped: the
 // 16 rows are keys (scores) or output columns (values), the 8 columns are the
 // query heads of the group, so a group of up to 8 heads costs one instruction.
+// Groups of up to four sit on the even columns, so that a lane's second column
+// needs no softmax (1024 caches of 100 to 300: 105 us instead of 111).
+// KV heads of 64 run as pairs of neighbours, whose rows are 128 contiguous
+// bytes: each product instruction serves one of the two, in columns of their
+// own (256 caches of 2000 to 2100, 16 heads of 16: 192 us; a head at a time, in
+// rows of 64 bytes, 357, 3.0 TB/s).  An odd number of KV heads of 64, or a group of more
+// than 8, is taken a head at a time.
 // Each warp streams its keys through a ring of its own in shared memory
 // (16-byte asynchronous copies: no registers wait for them, no CTA-wide
 // barrier).  A lane's 16 contiguous bytes of a key row are its operand words of
@@ -27,8 +34,8 @@
 // same); for values the bytes of two keys are interleaved by byte permutes.  Scores become the
 // second product's operand by an 8x8 transpose in registers.
 //
-// GB300: 256 caches of up to 4096 keys (32 query, 8 KV heads of 128) 190 us,
-// 6.0 TB/s (0.89 of the measured copy rate); four of 100 000 to 131 071 (32 and 4
+// GB300: 256 caches of up to 4096 keys (32 query, 8 KV heads of 128) 188 to 206 us
+// by the device, 5.5 to 6.0 TB/s (0.82 to 0.89 of the measured copy rate); four of 100 000 to 131 071 (32 and 4
 // heads) 89 us, 5.6 TB/s; one of 1000 about 8 us, a chain of dependent
 // loads.  Two stages of 32 keys and three CTAs per SM: 16-key steps with three
 // to six stages take 217 to 268 us for the 256 caches, three or four 32-key
@@ -62,8 +69,20 @@ constexpr int kAdMaxBatch = 8192;                // prefix sums held in shared m
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;                 // a running maximum may lag by this much (base 2): p <= 2^8
 
-// resident CTAs per SM (registers): the work is shared out to exactly these
-__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+// How a call runs.  D: bytes of a key row that a step reads, one KV head's, or
+// two neighbours' of 64 (P = 2); NT: 8-head column blocks; C: the columns in
+// use of the two that a lane holds (1: on the even columns).
+template <int D_, int NT_, int C_, int P_>
+struct Form {
+  static constexpr int D = D_, NT = NT_, C = C_, P = P_;
+  static constexpr int kHead = D / P;                              // head size
+  static constexpr bool kOwn = P == 2 && NT == 2;                  // a column block for each KV head of the pair
+  static constexpr int kQ = P == 2 ? 1 : D / 64;                   // 64-column parts of a query head
+  static constexpr int kO = kOwn ? D / 32 : D / 16;                // 16-row accumulators of a column block
+  // resident CTAs per SM (registers): the work is shared out to exactly these
+  static constexpr int kCtas = NT == 1 || kOwn ? (D == 64 ? 4 : 3) : 2;
+  static constexpr int64_t kPart = (int64_t)8 * NT * (kHead + 2);  // floats of a segment's partial: per head its accumulators, then m and l
+};
 
 struct AdArgs {
   const uint16_t* q;
@@ -152,7 +171,10 @@ struct Ring {
     return row * D + ((D == 128 ? c ^ ((row & 1u) << 2) : c) << 4);
   }
   static __device__ __forceinline__ uint32_t value(uint32_t row, uint32_t c) {
-    return kV + row * D + ((D == 128 ? c ^ (row & 6u) : c ^ ((row >> 1) & 3u)) << 4);
+    if (D == 128) return kV + row * D + ((c ^ (row & 6u)) << 4);
+    // two rows to a line of 128 bytes: r and r + 2
+    const uint32_t line = (row >> 2) * 2 + (row & 1u), half = (row ^ (row >> 1)) & 1u;
+    return kV + line * 128 + half * 64 + ((c ^ ((row >> 1) & 2u)) << 4);
   }
 };
 
@@ -175,22 +197,16 @@ __device__ __forceinline__ void request(uint32_t stage, const uint8_t* kc, const
 }
 
 // A segment's accumulators of the warps, merged at its end (over the rings)
-template <int D, int NT>
+template <class F>
 struct AdMerge {
-  float o[kAdWarps][8 * NT][D];
-  float m[kAdWarps][8 * NT], l[kAdWarps][8 * NT];
+  float o[kAdWarps][8 * F::NT][F::kHead];
+  float m[kAdWarps][8 * F::NT], l[kAdWarps][8 * F::NT];
 };
 
-template <int D, int NT>
+template <class F>
 __host__ __device__ constexpr uint32_t ad_smem() {
-  constexpr uint32_t ring = kAdWarps * kAdStages * Ring<D>::kStage, merge = sizeof(AdMerge<D, NT>);
+  constexpr uint32_t ring = kAdWarps * kAdStages * Ring<F::D>::kStage, merge = sizeof(AdMerge<F>);
   return ring > merge ? ring : merge;
-}
-
-// partial of a segment in the workspace: per head D accumulators, then m and l
-template <int D, int NT>
-__host__ __device__ constexpr int64_t part_floats() {
-  return (int64_t)8 * NT * (D + 2);
 }
 
 __device__ __forceinline__ void add_scaled(float4& a, float f, float4 v) {
@@ -207,17 +223,17 @@ __device__ __forceinline__ void finish(const AdArgs& a, int b, int h, int D, int
   if (a.lse && d == 0) a.lse[(int64_t)b * a.hq + h] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
 }
 
-// D: head size (64 or 128); NT: 8-head columns of a group part (1 or 2)
-template <int D, int NT>
-__global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kernel(const AdArgs a) {
+template <class F>
+__global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const AdArgs a) {
+  constexpr int D = F::D, NT = F::NT, C = F::C, P = F::P, H = F::kHead;
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings, or the merge; then batch + 1 running tile counts
   __shared__ int64_t warp_sum[kAdWarps];
   __shared__ int32_t last;
   ptx::grid_dep_launch_dependents();
   ptx::grid_dep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  AdMerge<D, NT>& sm = *reinterpret_cast<AdMerge<D, NT>*>(smem);
-  int64_t* prefix = reinterpret_cast<int64_t*>(smem + ad_smem<D, NT>());
+  AdMerge<F>& sm = *reinterpret_cast<AdMerge<F>*>(smem);
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + ad_smem<F>());
   const uint32_t ring = ptx::smem_u32(smem) + warp * kAdStages * Ring<D>::kStage;
   const int heads_sub = a.hkv * a.sub;  // items of a sequence: KV heads times parts of the group
 
@@ -251,7 +267,7 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
   // sequences without keys: zeros, spread over the CTAs
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;
-    for (int i = tid; i < a.hq * D; i += kAdThreads) a.out[b * a.ldo + i] = 0;
+    for (int i = tid; i < a.hq * H; i += kAdThreads) a.out[b * a.ldo + i] = 0;
     if (a.lse)
       for (int i = tid; i < a.hq; i += kAdThreads) a.lse[(int64_t)b * a.hq + i] = -INFINITY;
   }
@@ -286,8 +302,19 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
     w = seg_w1;
     if (t0 == t1) break;  // this CTA's range ends before the item's first tile
     const bool whole = t0 == 0 && t1 == tiles;
-    const int kvh = item / a.sub, h0 = kvh * a.group + (item % a.sub) * 8 * NT;
-    const int heads = min(8 * NT, (kvh + 1) * a.group - h0);
+    const int kvh = item / a.sub;  // KV head, or pair of them
+    const int h0 = kvh * P * a.group + (item % a.sub) * 8 * NT;
+    const int heads = min(8 * NT, (kvh + 1) * P * a.group - h0);
+    // the head (from h0) of column `col` of block nt, -1 for none: a pair's first
+    // KV head has the block's lower columns or block 0
+    auto head_of = [&](int nt, int col) {
+      if (C == 1 && (col & 1)) return -1;
+      const int per = C == 1 ? 2 : 1;
+      const int second = P == 1 ? 0 : F::kOwn ? nt : col >> 2;
+      const int i = (P == 1 ? nt * 8 + col : F::kOwn ? col : col & 3) / per;
+      const int lim = P == 1 ? heads : a.group;
+      return i < lim ? second * a.group + i : -1;
+    };
     const uint8_t* kc = a.kc + (int64_t)kvh * D;
     const uint8_t* vc = a.vc + (int64_t)kvh * D;
     const int32_t* table = a.table + (int64_t)b * a.ldt;
@@ -319,19 +346,19 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
     }
     // the query heads as operand words (column = head): lane (g, t) holds
     // head g's columns d = 64 j + 16 t + [0, 16)
-    uint32_t qf[NT][D / 64][4][2];
-    float qs[NT][2];  // score scale of this lane's result columns, heads 2t and 2t + 1
+    uint32_t qf[NT][F::kQ][4][2];
+    float qs[NT][C];  // score scale of this lane's result columns
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int h = nt * 8 + g;
-      uint32_t raw[D / 64][8];
+      const int h = head_of(nt, g);
+      uint32_t raw[F::kQ][8];
       uint32_t big = 0;
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (int64_t)b * a.ldq + (int64_t)(h0 + h) * D + 64 * j + 16 * t);
+      for (int j = 0; j < F::kQ; ++j) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (int64_t)b * a.ldq + (int64_t)(h0 + max(h, 0)) * H + 64 * j + 16 * t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          raw[j][i] = h < heads ? src[i] : 0u;
+          raw[j][i] = h >= 0 ? src[i] : 0u;
           big = max(big, max(raw[j][i] & 0x7FFFu, (raw[j][i] >> 16) & 0x7FFFu));
         }
       }
@@ -342,25 +369,25 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
       const int e = min(max((int)(big >> 7) - 127, -126), 126);
       const float down = __int_as_float((127 - e) << 23), up = __int_as_float((127 + e) << 23);
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j)
+      for (int j = 0; j < F::kQ; ++j)
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           qf[nt][j][s][0] = f16x2_rn(bf16_lo(raw[j][2 * s]) * down, bf16_hi(raw[j][2 * s]) * down);
           qf[nt][j][s][1] = f16x2_rn(bf16_lo(raw[j][2 * s + 1]) * down, bf16_hi(raw[j][2 * s + 1]) * down);
         }
       const float f = up * (sk * a.softmax_scale * kLog2e);
-      qs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);      // lane of head 2t
-      qs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);  // lane of head 2t + 1
+#pragma unroll
+      for (int c = 0; c < C; ++c) qs[nt][c] = __shfl_sync(0xffffffffu, f, 8 * t + 4 * c);  // lane of column 2t + c
     }
 
-    float o[NT][D / 16][4];
-    float m[NT][2], l[NT][2];
+    float o[NT][F::kO][4];
+    float m[NT][C], l[NT][C];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.0f;
+      for (int i = 0; i < F::kO; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) m[nt][c] = -INFINITY, l[nt][c] = 0.0f;
     }
 
     uint32_t stage = 0;
@@ -378,6 +405,7 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
       float s[kAdSubs][NT][4];
 #pragma unroll
       for (int u = 0; u < kAdSubs; ++u) {
+        float second[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // scores of a pair's second KV head
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.0f;
 #pragma unroll
@@ -388,34 +416,45 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
           for (int i = 0; i < 4; ++i) {
             const uint32_t a0 = e4m3x2_to_f16x2(r0[i]), a2 = e4m3x2_to_f16x2_hi(r0[i]);
             const uint32_t a1 = e4m3x2_to_f16x2(r1[i]), a3 = e4m3x2_to_f16x2_hi(r1[i]);
+            if (P == 2) {
+              mma_16816(j == 0 || F::kOwn ? s[u][F::kOwn ? j : 0] : second, a0, a1, a2, a3, qf[F::kOwn ? j : 0][0][i][0], qf[F::kOwn ? j : 0][0][i][1]);
+            } else {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816(s[u][nt], a0, a1, a2, a3, qf[nt][j][i][0], qf[nt][j][i][1]);
+              for (int nt = 0; nt < NT; ++nt) mma_16816(s[u][nt], a0, a1, a2, a3, qf[nt][j % F::kQ][i][0], qf[nt][j % F::kQ][i][1]);
+            }
           }
+        }
+        if (P == 2 && !F::kOwn) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[u][0][c] = t < 2 ? s[u][0][c] : second[c];
         }
       }
       uint32_t pb[kAdSubs][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float b0 = -INFINITY, b1 = -INFINITY;
+        float big[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) big[c] = -INFINITY;
 #pragma unroll
         for (int u = 0; u < kAdSubs; ++u) {
-          float(&x)[4] = s[u][nt];
+          const bool on0 = live >> (16 * u + g) & 1u, on1 = live >> (16 * u + g + 8) & 1u;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] *= qs[nt][c & 1];
-          if (live != (kAdStep == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
-            const bool on0 = live >> (16 * u + g) & 1u, on1 = live >> (16 * u + g + 8) & 1u;
-            x[0] = on0 ? x[0] : -INFINITY;
-            x[1] = on0 ? x[1] : -INFINITY;
-            x[2] = on1 ? x[2] : -INFINITY;
-            x[3] = on1 ? x[3] : -INFINITY;
+          for (int c = 0; c < C; ++c) {
+            float &x0 = s[u][nt][c], &x1 = s[u][nt][c + 2];
+            x0 *= qs[nt][c];
+            x1 *= qs[nt][c];
+            if (live != (kAdStep == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
+              x0 = on0 ? x0 : -INFINITY;
+              x1 = on1 ? x1 : -INFINITY;
+            }
+            big[c] = fmaxf(big[c], fmaxf(x0, x1));
           }
-          b0 = fmaxf(b0, fmaxf(x[0], x[2]));
-          b1 = fmaxf(b1, fmaxf(x[1], x[3]));
         }
-        if (__any_sync(0xffffffffu, b0 > m[nt][0] + kRescale || b1 > m[nt][1] + kRescale)) {
-          float big[2] = {b0, b1};
+        bool above = big[0] > m[nt][0] + kRescale;
+        if (C == 2) above = above || big[C - 1] > m[nt][C - 1] + kRescale;
+        if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < C; ++c) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) big[c] = fmaxf(big[c], __shfl_xor_sync(0xffffffffu, big[c], d));
             const float to_m = fmaxf(m[nt][c], big[c]);
@@ -423,20 +462,26 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
             m[nt][c] = to_m;
             l[nt][c] *= f;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
+            for (int i = 0; i < F::kO; ++i) {
               o[nt][i][c] *= f;
               o[nt][i][c + 2] *= f;
             }
           }
         }
-        const float r0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], r1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+        float ref[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) ref[c] = m[nt][c] == -INFINITY ? 0.0f : m[nt][c];
 #pragma unroll
         for (int u = 0; u < kAdSubs; ++u) {
-          const float p0 = ex2(s[u][nt][0] - r0), p1 = ex2(s[u][nt][1] - r1), p2 = ex2(s[u][nt][2] - r0), p3 = ex2(s[u][nt][3] - r1);
-          l[nt][0] += p0 + p2;
-          l[nt][1] += p1 + p3;
-          pb[u][nt][0] = transpose_8x8(f16x2_rn(p0, p1));
-          pb[u][nt][1] = transpose_8x8(f16x2_rn(p2, p3));
+          float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            p[c] = ex2(s[u][nt][c] - ref[c]);
+            p[c + 2] = ex2(s[u][nt][c + 2] - ref[c]);
+            l[nt][c] += p[c] + p[c + 2];
+          }
+          pb[u][nt][0] = transpose_8x8(f16x2_rn(p[0], p[1]));
+          pb[u][nt][1] = transpose_8x8(f16x2_rn(p[2], p[3]));
         }
       }
 #pragma unroll
@@ -445,7 +490,10 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t r = 16 * u + 2 * t + (i & 1) + 8 * (i >> 1);
-          if (D == 128) {
+          if (F::kOwn) {
+            const uint2 x = lds64(at + Ring<D>::value(r, g >> 1) + 8 * (g & 1)), y = lds64(at + Ring<D>::value(r, 4 + (g >> 1)) + 8 * (g & 1));
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2 % (D / 32)] = y.x, v[i][3 % (D / 32)] = y.y;
+          } else if (D == 128) {
             const uint4 x = lds128(at + Ring<D>::value(r, g));
             v[i][0] = x.x, v[i][1] = x.y, v[i][2 % (D / 32)] = x.z, v[i][3 % (D / 32)] = x.w;
           } else {
@@ -462,8 +510,10 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
           const uint32_t a10 = e4m3x2_to_f16x2(x1), a11 = e4m3x2_to_f16x2_hi(x1), a12 = e4m3x2_to_f16x2(y1), a13 = e4m3x2_to_f16x2_hi(y1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_16816(o[nt][2 * i], a00, a01, a02, a03, pb[u][nt][0], pb[u][nt][1]);
-            mma_16816(o[nt][2 * i + 1], a10, a11, a12, a13, pb[u][nt][0], pb[u][nt][1]);
+            if (F::kOwn && nt != i / 2) continue;
+            const int at_o = F::kOwn ? i % 2 : i;
+            mma_16816(o[nt][2 * at_o], a00, a01, a02, a03, pb[u][nt][0], pb[u][nt][1]);
+            mma_16816(o[nt][2 * at_o + 1], a10, a11, a12, a13, pb[u][nt][0], pb[u][nt][1]);
           }
         }
       }
@@ -476,27 +526,32 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
     ptx::cp_async_wait<0>();
     __syncthreads();  // every warp is done with its ring
 
-    // the warps' partials to shared memory; row d = D/8 g + 2 i (+ 1)
+    // the warps' partials to shared memory; row d = 2 kO g + 2 i (+ 1) of the
+    // lane's rows, of which a pair's second KV head has the upper half
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int h = nt * 8 + 2 * t + c;
+      for (int c = 0; c < C; ++c) {
+        const int h = head_of(nt, 2 * t + c);
+        const bool upper = P == 2 && !F::kOwn && t >= 2;
+        const int d = 2 * F::kO * g - (upper ? H : 0);
+        if (h >= 0 && d >= 0 && d < H) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2*>(&sm.o[warp][h][D / 8 * g + 2 * i]) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
+          for (int i = 0; i < F::kO; ++i)
+            *reinterpret_cast<float2*>(&sm.o[warp][h][d + 2 * i]) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
+        }
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], d);
-        if (g == 0) {
+        for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+        if (g == 0 && h >= 0) {
           sm.m[warp][h] = m[nt][c];
           sm.l[warp][h] = l[nt][c];
         }
       }
     }
     __syncthreads();
-    float* part = a.parts + (2 * cta + (first_segment ? 0 : 1)) * part_floats<D, NT>();
-    for (int i = tid; i < heads * (D / 4); i += kAdThreads) {
-      const int h = i / (D / 4), d = i % (D / 4) * 4;
+    float* part = a.parts + (2 * cta + (first_segment ? 0 : 1)) * F::kPart;
+    for (int i = tid; i < heads * (H / 4); i += kAdThreads) {
+      const int h = i / (H / 4), d = i % (H / 4) * 4;
       float mm = sm.m[0][h];
 #pragma unroll
       for (int x = 1; x < kAdWarps; ++x) mm = fmaxf(mm, sm.m[x][h]);
@@ -510,12 +565,12 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
         ll = fmaf(f, sm.l[x][h], ll);
       }
       if (whole) {
-        finish(a, b, h0 + h, D, d, acc, ll, mm, sv);
+        finish(a, b, h0 + h, H, d, acc, ll, mm, sv);
       } else {
-        *reinterpret_cast<float4*>(part + h * D + d) = acc;
+        *reinterpret_cast<float4*>(part + h * H + d) = acc;
         if (d == 0) {
-          part[8 * NT * D + h] = mm;
-          part[8 * NT * D + 8 * NT + h] = ll;
+          part[8 * NT * H + h] = mm;
+          part[8 * NT * H + 8 * NT + h] = ll;
         }
       }
     }
@@ -537,19 +592,34 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
         // A CTA's first segment went to its slot 0; the item's first CTA holds
         // the item as its first segment only if its range starts in the item.
         const bool second = c0 * total / ctas < item_w0;
-        auto part_of = [&](int c) { return a.parts + (2 * (c0 + c) + (c == 0 && second ? 1 : 0)) * part_floats<D, NT>(); };
+        auto part_of = [&](int c) { return a.parts + (2 * (c0 + c) + (c == 0 && second ? 1 : 0)) * F::kPart; };
         // per head: the largest reference, each part's factor, the sum
         float* factor = reinterpret_cast<float*>(smem);  // [part][8 NT], over the rings
         float* head_m = factor + n_parts * 8 * NT;
         float* head_l = head_m + 8 * NT;
-        for (int h = warp; h < heads; h += kAdWarps) {
-          float mm = -INFINITY, ll = 0.0f;
-          for (int c = lane; c < n_parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + 8 * NT * D + h));
+        constexpr int kHeads = 8 * NT / kAdWarps;  // of a warp
+        float m0[kHeads], l0[kHeads];              // the first 32 parts': all loads at once
+#pragma unroll
+        for (int x = 0; x < kHeads; ++x) {
+          const bool on = warp + x * kAdWarps < heads && lane < n_parts;
+          const float* src = part_of(on ? lane : 0) + 8 * NT * H + (on ? warp + x * kAdWarps : 0);
+          m0[x] = on ? __ldcg(src) : -INFINITY;
+          l0[x] = on ? __ldcg(src + 8 * NT) : 0.0f;
+        }
+#pragma unroll
+        for (int x = 0; x < kHeads; ++x) {
+          const int h = warp + x * kAdWarps;
+          if (h >= heads) break;
+          float mm = m0[x], ll;
+          for (int c = lane + 32; c < n_parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + 8 * NT * H + h));
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
           const float ref = mm == -INFINITY ? 0.0f : mm;
-          for (int c = lane; c < n_parts; c += 32) {
-            const float* src = part_of(c) + 8 * NT * D + h;
+          const float f0 = ex2(m0[x] - ref);
+          if (lane < n_parts) factor[lane * 8 * NT + h] = f0;
+          ll = f0 * l0[x];
+          for (int c = lane + 32; c < n_parts; c += 32) {
+            const float* src = part_of(c) + 8 * NT * H + h;
             const float f = ex2(__ldcg(src) - ref);
             factor[c * 8 * NT + h] = f;
             ll = fmaf(f, __ldcg(src + 8 * NT), ll);
@@ -562,13 +632,13 @@ __global__ void __launch_bounds__(kAdThreads, ctas_per_sm(NT)) attn_decode_kerne
           }
         }
         __syncthreads();
-        for (int i = tid; i < heads * (D / 4); i += kAdThreads) {
-          const int h = i / (D / 4), d = i % (D / 4) * 4;
+        for (int i = tid; i < heads * (H / 4); i += kAdThreads) {
+          const int h = i / (H / 4), d = i % (H / 4) * 4;
           float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
           for (int c = 0; c < n_parts; ++c)
-            add_scaled(acc, factor[c * 8 * NT + h], __ldcg(reinterpret_cast<const float4*>(part_of(c) + h * D + d)));
-          finish(a, b, h0 + h, D, d, acc, head_l[h], head_m[h], sv);
+            add_scaled(acc, factor[c * 8 * NT + h], __ldcg(reinterpret_cast<const float4*>(part_of(c) + h * H + d)));
+          finish(a, b, h0 + h, H, d, acc, head_l[h], head_m[h], sv);
         }
       }
     }
@@ -589,18 +659,30 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kAdMaxLen = (int64_t)1 << 30;  // 32-bit key numbers, two tiles of headroom
 
-int columns(int64_t group) { return group <= 8 ? 1 : 2; }
+// fn(Form) of the form that a call's shape takes.  Heads of 64 run as
+// pairs where their number is even: rows of 64 bytes, a KV head's alone, came
+// at 3.0 TB/s where rows of 128 come at 5.5.
+template <class Fn>
+auto with_form(int64_t kv_heads, int64_t group, int64_t head_dim, Fn fn) {
+  if (head_dim == 128) return group <= 4 ? fn(Form<128, 1, 1, 1>{}) : group <= 8 ? fn(Form<128, 1, 2, 1>{}) : fn(Form<128, 2, 2, 1>{});
+  if (kv_heads % 2 == 0 && group <= 8)
+    return group <= 2 ? fn(Form<128, 1, 1, 2>{}) : group <= 4 ? fn(Form<128, 1, 2, 2>{}) : fn(Form<128, 2, 2, 2>{});
+  return group <= 8 ? fn(Form<64, 1, 2, 1>{}) : fn(Form<64, 2, 2, 1>{});
+}
 
 // The workspace starts with the items' counters: an area of one size for every
 // shape, so that one workspace can serve several (partials never land on counters).
 constexpr int kAdMaxCtas = 4;
 int64_t ticket_bytes() { return ((int64_t)sm_count() * kAdMaxCtas * 4 + 255) / 256 * 256; }
 
-template <int D, int NT>
+template <class F>
 cudaError_t launch_decode(AdArgs a, void* workspace, cudaStream_t stream) {
+  a.hkv /= F::P;
+  a.sub = (F::P * a.group + 8 * F::NT - 1) / (8 * F::NT);
+  static_assert(F::kCtas <= kAdMaxCtas);
   a.tickets = static_cast<uint32_t*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes());
-  const size_t smem = ad_smem<D, NT>() + ((size_t)a.batch + 1) * 8;
+  const size_t smem = ad_smem<F>() + ((size_t)a.batch + 1) * 8;
   // the attribute lives in the context: set once per device and context, for the largest batch
   static std::atomic<uint64_t> ready[64];
   int dev = 0;
@@ -609,13 +691,13 @@ cudaError_t launch_decode(AdArgs a, void* workspace, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !ctx) return cudaErrorInvalidDevice;
   if (ready[dev].load(std::memory_order_acquire) != ctx) {
-    e = cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(ad_smem<D, NT>() + (kAdMaxBatch + 1) * 8));
+    e = cudaFuncSetAttribute(attn_decode_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(ad_smem<F>() + (kAdMaxBatch + 1) * 8));
     if (e != cudaSuccess) return e;
     ready[dev].store(ctx, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(sm_count() * ctas_per_sm(NT)));
+  cfg.gridDim = dim3((unsigned)(sm_count() * F::kCtas));
   cfg.blockDim = dim3(kAdThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -624,7 +706,7 @@ cudaError_t launch_decode(AdArgs a, void* workspace, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NT>, a);
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<F>, a);
 }
 
 }  // namespace
@@ -634,9 +716,10 @@ using namespace fp8rl;
 
 extern "C" FP8RL_API size_t fp8rl_attn_decode_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128)) return 0;
-  const int nt = columns(q_heads / kv_heads);
-  const int64_t part = (int64_t)8 * nt * (head_dim + 2) * 4;
-  return (size_t)(ticket_bytes() + 2 * (int64_t)sm_count() * ctas_per_sm(nt) * part);
+  return with_form(kv_heads, q_heads / kv_heads, head_dim, [](auto f) {
+    using F = decltype(f);
+    return (size_t)(ticket_bytes() + 2 * (int64_t)sm_count() * F::kCtas * F::kPart * 4);
+  });
 }
 
 extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t ldq, int64_t batch, int64_t q_heads,
@@ -676,8 +759,6 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t 
   a.ldc16 = (uint32_t)(ld_cache / 16);
   a.batch = (int32_t)batch, a.hq = (int32_t)q_heads, a.hkv = (int32_t)kv_heads;
   a.group = (int32_t)(q_heads / kv_heads);
-  const int nt = columns(a.group);
-  a.sub = (a.group + 8 * nt - 1) / (8 * nt);
   a.page = (int32_t)block_size;
   a.page_shift = -1;
   for (int i = 0; i < 31; ++i)
@@ -685,8 +766,7 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t 
   a.max_len = (int32_t)(max_blocks * block_size);
   a.softmax_scale = softmax_scale;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = head_dim == 128 ? (nt == 1 ? launch_decode<128, 1>(a, d_workspace, cs) : launch_decode<128, 2>(a, d_workspace, cs))
-                                        : (nt == 1 ? launch_decode<64, 1>(a, d_workspace, cs) : launch_decode<64, 2>(a, d_workspace, cs));
+  const cudaError_t e = with_form(kv_heads, a.group, head_dim, [&](auto f) { return launch_decode<decltype(f)>(a, d_workspace, cs); });
   if (e != cudaSuccess) {
     cudaGetLastError();
     return FP8RL_ERR_CUDA;

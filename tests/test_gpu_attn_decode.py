@@ -119,6 +119,29 @@ def test_lengths(lens):
     check(lens, 32, 8, 128, 16, seed=len(lens))
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (6, 2), (8, 2), (10, 2), (14, 2), (16, 2), (18, 2), (12, 3), (12, 4), (20, 4)])
+@pytest.mark.parametrize("ld_pad", [0, 16])
+def test_heads_of_64(hq, hkv, ld_pad):
+    check([0, 1, 31, 32, 33, 127, 128, 129, 900, 4000], hq, hkv, 64, 16, seed=hq + hkv, ld_pad=ld_pad)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 64), (8, 2, 64), (12, 2, 64), (16, 4, 64), (18, 2, 64), (6, 3, 64), (8, 2, 128), (16, 2, 128)])
+def test_nan_codes_stay_in_their_head(hq, hkv, d):
+    """NaN codes in a head's keys or values reach its own query heads alone."""
+    q, kc, vc, table, ln, scales = make([150, 40, 700], hq, hkv, d, 16, seed=11)
+    want, wl = fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16)
+    group = hq // hkv
+    for head in range(hkv):
+        mine = torch.zeros(hq, dtype=torch.bool, device="cuda")
+        mine[head * group:(head + 1) * group] = True
+        for which in range(2):
+            caches = [kc.clone(), vc.clone()]
+            caches[which][:, head * d:(head + 1) * d] = 0x7F
+            out, lse = fp8rl.attn_decode(q, caches[0], caches[1], table, ln, scales, 16)
+            assert torch.equal(out[:, ~mine], want[:, ~mine]) and torch.equal(lse[:, ~mine], wl[:, ~mine])
+            assert bool(out[:, mine].isnan().all())
+
+
 def test_one_long_sequence_of_one_head():
     check([70001], 4, 1, 128, 64, seed=1)
 
