@@ -34,18 +34,20 @@
 // same); for values the bytes of two keys are interleaved by byte permutes.  Scores become the
 // second product's operand by an 8x8 transpose in registers.
 //
-// GB300: 256 caches of up to 4096 keys (32 query, 8 KV heads of 128) 188 to 206 us
-// by the device, 5.5 to 6.0 TB/s (0.82 to 0.89 of the measured copy rate); four of 100 000 to 131 071 (32 and 4
-// heads) 89 us, 5.6 TB/s; one of 1000 about 8 us, a chain of dependent
-// loads.  Two stages of 32 keys and three CTAs per SM: 16-key steps with three
-// to six stages take 217 to 268 us for the 256 caches, three or four 32-key
-// stages with two CTAs per SM 217 and 252.
+// GB300: 256 caches of up to 4096 keys (32 query, 8 KV heads of 128) 182 to 186 us
+// by the device, 6.2 TB/s (0.91 to 0.93 of the measured copy rate); four of
+// 100 000 to 131 071 (32 and 4 heads) 89 us, 5.6 TB/s; one of 1000 about 8 us, a
+// chain of dependent loads.  Two stages of 32 keys and three CTAs per SM: with
+// items of one head (205 us), 16-key steps with three to six stages took 217 to
+// 268 us for the 256 caches, three or four 32-key stages with two CTAs per SM
+// 217 and 252.
 //
 // Work split: the 128-key tiles of all sequences and KV heads form one list,
 // shared out to the CTAs in equal contiguous ranges, whatever the lengths (an
 // item of one sequence and KV head counts two tiles more, for its start:
-// 209 us instead of 258 for the 256 caches).  An
-// item (sequence, KV head) that spans CTAs leaves fp32 partials in the
+// 209 us instead of 258 for the 256 caches, measured with items of one head).
+// Where a call has many items, an item is two neighbouring heads (or pairs), each
+// with two of the CTA's warps.  An item that spans CTAs leaves fp32 partials in the
 // workspace; the CTA that arrives last merges them in CTA order, so the
 // result has the same bits on every run.
 #include <algorithm>
@@ -62,7 +64,6 @@ constexpr int kAdWarps = 4;
 constexpr int kAdThreads = kAdWarps * 32;
 constexpr int kAdSubs = 2;                       // 16-key products of a step
 constexpr int kAdStep = 16 * kAdSubs;            // keys a warp takes at a time
-constexpr int kAdTile = kAdStep * kAdWarps;      // keys a CTA takes at a time
 constexpr int kAdStages = 2;                     // steps in a warp's ring
 constexpr int kAdItemCost = 2;                   // fixed cost of an item, in tiles
 constexpr int kAdMaxBatch = 8192;                // prefix sums held in shared memory
@@ -71,17 +72,19 @@ constexpr float kRescale = 8.0f;                 // a running maximum may lag by
 
 // How a call runs.  D: bytes of a key row that a step reads, one KV head's, or
 // two neighbours' of 64 (P = 2); NT: 8-head column blocks; C: the columns in
-// use of the two that a lane holds (1: on the even columns).
-template <int D_, int NT_, int C_, int P_>
+// use of the two that a lane holds (1: on the even columns); W: neighbouring KV
+// heads (or pairs) of an item, each with warps of its own.
+template <int D_, int NT_, int C_, int P_, int W_>
 struct Form {
-  static constexpr int D = D_, NT = NT_, C = C_, P = P_;
+  static constexpr int D = D_, NT = NT_, C = C_, P = P_, W = W_;
+  static constexpr int kTile = kAdStep * kAdWarps / W;             // keys a CTA takes at a time
   static constexpr int kHead = D / P;                              // head size
   static constexpr bool kOwn = P == 2 && NT == 2;                  // a column block for each KV head of the pair
   static constexpr int kQ = P == 2 ? 1 : D / 64;                   // 64-column parts of a query head
   static constexpr int kO = kOwn ? D / 32 : D / 16;                // 16-row accumulators of a column block
   // resident CTAs per SM (registers): the work is shared out to exactly these
   static constexpr int kCtas = NT == 1 || kOwn ? (D == 64 ? 4 : 3) : 2;
-  static constexpr int64_t kPart = (int64_t)8 * NT * (kHead + 2);  // floats of a segment's partial: per head its accumulators, then m and l
+  static constexpr int64_t kPart = (int64_t)8 * NT * (kHead + 2);  // floats of a KV head's (or pair's) partial: per head its accumulators, then m and l
 };
 
 struct AdArgs {
@@ -225,7 +228,7 @@ __device__ __forceinline__ void finish(const AdArgs& a, int b, int h, int D, int
 
 template <class F>
 __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const AdArgs a) {
-  constexpr int D = F::D, NT = F::NT, C = F::C, P = F::P, H = F::kHead;
+  constexpr int D = F::D, NT = F::NT, C = F::C, P = F::P, W = F::W, H = F::kHead, kTile = F::kTile;
   extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings, or the merge; then batch + 1 running tile counts
   __shared__ int64_t warp_sum[kAdWarps];
   __shared__ int32_t last;
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
   AdMerge<F>& sm = *reinterpret_cast<AdMerge<F>*>(smem);
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + ad_smem<F>());
   const uint32_t ring = ptx::smem_u32(smem) + warp * kAdStages * Ring<D>::kStage;
-  const int heads_sub = a.hkv * a.sub;  // items of a sequence: KV heads times parts of the group
+  const int heads_sub = a.hkv / W * a.sub;  // items of a sequence: KV heads by W, times parts of the group
 
   // running counts of the sequences' tiles (each times heads_sub)
   {
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
     for (int b0 = 0; b0 < a.batch; b0 += kAdThreads) {
       const int b = b0 + tid;
       const int32_t n = b < a.batch ? min(max(a.lens[b], 0), a.max_len) : 0;
-      int64_t x = n > 0 ? (int64_t)((n + kAdTile - 1) / kAdTile + kAdItemCost) * heads_sub : 0;
+      int64_t x = n > 0 ? (int64_t)((n + kTile - 1) / kTile + kAdItemCost) * heads_sub : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
@@ -304,9 +307,9 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
     w = seg_w1;
     if (t0 == t1) break;  // this CTA's range ends before the item's first tile
     const bool whole = t0 == 0 && t1 == tiles;
-    const int kvh = item / a.sub;  // KV head, or pair of them
+    const int kvh = item / a.sub * W + warp % W;  // KV head, or pair of them
     const int h0 = kvh * P * a.group + (item % a.sub) * 8 * NT;
-    const int heads = min(8 * NT, (kvh + 1) * P * a.group - h0);
+    const int heads = min(8 * NT, P * a.group - (item % a.sub) * 8 * NT);
     // the head (from h0) of column `col` of block nt, -1 for none: a pair's first
     // KV head has the block's lower columns or block 0
     auto head_of = [&](int nt, int col) {
@@ -323,8 +326,8 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
 
     // This warp's steps: keys [key, key + kAdStep), one tile apart.  The
     // first ones are requested before the queries are read.
-    const int32_t k1 = (int32_t)min((int64_t)n, t1 * kAdTile);
-    int32_t key = (int32_t)t0 * kAdTile + warp * kAdStep;
+    const int32_t k1 = (int32_t)min((int64_t)n, t1 * kTile);
+    int32_t key = (int32_t)t0 * kTile + warp / W * kAdStep;
     // the cache row of key0 + lane
     auto row_of = [&](int32_t key0) -> uint32_t {
       const int32_t kk = key0 + lane;
@@ -340,9 +343,9 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
     ptx::cp_async_commit();
 #pragma unroll
     for (int i = 1; i < kAdStages; ++i) {
-      ahead[i - 1] = row_of(key + i * kAdTile);
+      ahead[i - 1] = row_of(key + i * kTile);
       if (i + 1 < kAdStages) {
-        if (key + i * kAdTile < k1) request<D>(ring + i * Ring<D>::kStage, kc, vc, ahead[i - 1]);
+        if (key + i * kTile < k1) request<D>(ring + i * Ring<D>::kStage, kc, vc, ahead[i - 1]);
         ptx::cp_async_commit();
       }
     }
@@ -393,11 +396,11 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
     }
 
     uint32_t stage = 0;
-    for (; key < k1; key += kAdTile) {
+    for (; key < k1; key += kTile) {
       // request the last step that fits the ring, look up the rows of the one after it
       const uint32_t to = stage + kAdStages - 1 < kAdStages ? stage + kAdStages - 1 : stage - 1;
-      ahead[kAdStages - 1] = row_of(key + kAdStages * kAdTile);
-      if (key + (kAdStages - 1) * kAdTile < k1) request<D>(ring + to * Ring<D>::kStage, kc, vc, ahead[kAdStages - 2]);
+      ahead[kAdStages - 1] = row_of(key + kAdStages * kTile);
+      if (key + (kAdStages - 1) * kTile < k1) request<D>(ring + to * Ring<D>::kStage, kc, vc, ahead[kAdStages - 2]);
       ptx::cp_async_commit();
       ptx::cp_async_wait<kAdStages - 1>();
       __syncwarp();
@@ -551,28 +554,30 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
       }
     }
     __syncthreads();
-    float* part = a.parts + (2 * cta + (first_segment ? 0 : 1)) * F::kPart;
-    for (int i = tid; i < heads * (H / 4); i += kAdThreads) {
-      const int h = i / (H / 4), d = i % (H / 4) * 4;
-      float mm = sm.m[0][h];
+    float* part = a.parts + (2 * cta + (first_segment ? 0 : 1)) * W * F::kPart;
+    const int h_item = h0 - warp % W * P * a.group, pieces = heads * (H / 4);
+    for (int i = tid; i < W * pieces; i += kAdThreads) {
+      const int wi = W == 2 && i >= pieces, h = (i - wi * pieces) / (H / 4), d = i % (H / 4) * 4;
+      float mm = sm.m[wi][h];
 #pragma unroll
-      for (int x = 1; x < kAdWarps; ++x) mm = fmaxf(mm, sm.m[x][h]);
+      for (int x = W; x < kAdWarps; x += W) mm = fmaxf(mm, sm.m[wi + x][h]);
       const float ref = mm == -INFINITY ? 0.0f : mm;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float ll = 0.0f;
 #pragma unroll
-      for (int x = 0; x < kAdWarps; ++x) {
-        const float f = ex2(sm.m[x][h] - ref);
-        add_scaled(acc, f, *reinterpret_cast<const float4*>(&sm.o[x][h][d]));
-        ll = fmaf(f, sm.l[x][h], ll);
+      for (int x = 0; x < kAdWarps; x += W) {
+        const float f = ex2(sm.m[wi + x][h] - ref);
+        add_scaled(acc, f, *reinterpret_cast<const float4*>(&sm.o[wi + x][h][d]));
+        ll = fmaf(f, sm.l[wi + x][h], ll);
       }
       if (whole) {
-        finish(a, b, h0 + h, H, d, acc, ll, mm, sv);
+        finish(a, b, h_item + wi * P * a.group + h, H, d, acc, ll, mm, sv);
       } else {
-        *reinterpret_cast<float4*>(part + h * H + d) = acc;
+        float* to = part + wi * F::kPart;
+        *reinterpret_cast<float4*>(to + h * H + d) = acc;
         if (d == 0) {
-          part[8 * NT * H + h] = mm;
-          part[8 * NT * H + 8 * NT + h] = ll;
+          to[8 * NT * H + h] = mm;
+          to[8 * NT * H + 8 * NT + h] = ll;
         }
       }
     }
@@ -594,53 +599,58 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
         // A CTA's first segment went to its slot 0; the item's first CTA holds
         // the item as its first segment only if its range starts in the item.
         const bool second = c0 * total / ctas < item_w0;
-        auto part_of = [&](int c) { return a.parts + (2 * (c0 + c) + (c == 0 && second ? 1 : 0)) * F::kPart; };
-        // per head: the largest reference, each part's factor, the sum
-        float* factor = reinterpret_cast<float*>(smem);  // [part][8 NT], over the rings
-        float* head_m = factor + n_parts * 8 * NT;
-        float* head_l = head_m + 8 * NT;
-        constexpr int kHeads = 8 * NT / kAdWarps;  // of a warp
-        float m0[kHeads], l0[kHeads];              // the first 32 parts': all loads at once
+        auto part_of = [&](int c) { return a.parts + (2 * (c0 + c) + (c == 0 && second ? 1 : 0)) * W * F::kPart; };
+        // per head ("slot") of the item: the largest reference, each part's factor, the sum
+        const int slots = W * heads;
+        auto stat_of = [&](int c, int slot) {
+          const int wi = W == 2 && slot >= heads;
+          return part_of(c) + wi * F::kPart + 8 * NT * H + slot - wi * heads;
+        };
+        float* factor = reinterpret_cast<float*>(smem);  // [part][8 NT W], over the rings
+        float* head_m = factor + n_parts * 8 * NT * W;
+        float* head_l = head_m + 8 * NT * W;
+        constexpr int kSlots = 8 * NT * W / kAdWarps;  // of a warp
+        float m0[kSlots], l0[kSlots];                  // the first 32 parts': all loads at once
 #pragma unroll
-        for (int x = 0; x < kHeads; ++x) {
-          const bool on = warp + x * kAdWarps < heads && lane < n_parts;
-          const float* src = part_of(on ? lane : 0) + 8 * NT * H + (on ? warp + x * kAdWarps : 0);
+        for (int x = 0; x < kSlots; ++x) {
+          const bool on = warp + x * kAdWarps < slots && lane < n_parts;
+          const float* src = stat_of(on ? lane : 0, on ? warp + x * kAdWarps : 0);
           m0[x] = on ? __ldcg(src) : -INFINITY;
           l0[x] = on ? __ldcg(src + 8 * NT) : 0.0f;
         }
 #pragma unroll
-        for (int x = 0; x < kHeads; ++x) {
-          const int h = warp + x * kAdWarps;
-          if (h >= heads) break;
+        for (int x = 0; x < kSlots; ++x) {
+          const int slot = warp + x * kAdWarps;
+          if (slot >= slots) break;
           float mm = m0[x], ll;
-          for (int c = lane + 32; c < n_parts; c += 32) mm = fmaxf(mm, __ldcg(part_of(c) + 8 * NT * H + h));
+          for (int c = lane + 32; c < n_parts; c += 32) mm = fmaxf(mm, __ldcg(stat_of(c, slot)));
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
           const float ref = mm == -INFINITY ? 0.0f : mm;
           const float f0 = ex2(m0[x] - ref);
-          if (lane < n_parts) factor[lane * 8 * NT + h] = f0;
+          if (lane < n_parts) factor[lane * 8 * NT * W + slot] = f0;
           ll = f0 * l0[x];
           for (int c = lane + 32; c < n_parts; c += 32) {
-            const float* src = part_of(c) + 8 * NT * H + h;
+            const float* src = stat_of(c, slot);
             const float f = ex2(__ldcg(src) - ref);
-            factor[c * 8 * NT + h] = f;
+            factor[c * 8 * NT * W + slot] = f;
             ll = fmaf(f, __ldcg(src + 8 * NT), ll);
           }
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
           if (lane == 0) {
-            head_m[h] = mm;
-            head_l[h] = ll;
+            head_m[slot] = mm;
+            head_l[slot] = ll;
           }
         }
         __syncthreads();
-        for (int i = tid; i < heads * (H / 4); i += kAdThreads) {
-          const int h = i / (H / 4), d = i % (H / 4) * 4;
+        for (int i = tid; i < W * pieces; i += kAdThreads) {
+          const int wi = W == 2 && i >= pieces, h = (i - wi * pieces) / (H / 4), d = i % (H / 4) * 4, slot = wi * heads + h;
           float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
           for (int c = 0; c < n_parts; ++c)
-            add_scaled(acc, factor[c * 8 * NT + h], __ldcg(reinterpret_cast<const float4*>(part_of(c) + h * H + d)));
-          finish(a, b, h0 + h, H, d, acc, head_l[h], head_m[h], sv);
+            add_scaled(acc, factor[c * 8 * NT * W + slot], __ldcg(reinterpret_cast<const float4*>(part_of(c) + wi * F::kPart + h * H + d)));
+          finish(a, b, h_item + wi * P * a.group + h, H, d, acc, head_l[slot], head_m[slot], sv);
         }
       }
     }
@@ -661,15 +671,28 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kAdMaxLen = (int64_t)1 << 30;  // 32-bit key numbers, two tiles of headroom
 
-// fn(Form) of the form that a call's shape takes.  Heads of 64 run as
-// pairs where their number is even: rows of 64 bytes, a KV head's alone, came
-// at 3.0 TB/s where rows of 128 come at 5.5.
-template <class Fn>
-auto with_form(int64_t kv_heads, int64_t group, int64_t head_dim, Fn fn) {
-  if (head_dim == 128) return group <= 4 ? fn(Form<128, 1, 1, 1>{}) : group <= 8 ? fn(Form<128, 1, 2, 1>{}) : fn(Form<128, 2, 2, 1>{});
+// fn(Form) of the form that a call's shape takes.  Heads of 64 run as pairs where
+// their number is even: rows of 64 bytes, a KV head's alone, came at 3.0 TB/s
+// where rows of 128 come at 5.5.
+template <int W, class Fn>
+auto with_shape(int64_t kv_heads, int64_t group, int64_t head_dim, Fn fn) {
+  if (head_dim == 128) return group <= 4 ? fn(Form<128, 1, 1, 1, W>{}) : group <= 8 ? fn(Form<128, 1, 2, 1, W>{}) : fn(Form<128, 2, 2, 1, W>{});
   if (kv_heads % 2 == 0 && group <= 8)
-    return group <= 2 ? fn(Form<128, 1, 1, 2>{}) : group <= 4 ? fn(Form<128, 1, 2, 2>{}) : fn(Form<128, 2, 2, 2>{});
-  return group <= 8 ? fn(Form<64, 1, 2, 1>{}) : fn(Form<64, 2, 2, 1>{});
+    return group <= 2 ? fn(Form<128, 1, 1, 2, W>{}) : group <= 4 ? fn(Form<128, 1, 2, 2, W>{}) : fn(Form<128, 2, 2, 2, W>{});
+  return group <= 8 ? fn(Form<64, 1, 2, 1, 1>{}) : fn(Form<64, 2, 2, 1, 1>{});
+}
+
+// Two neighbouring heads' rows of 128 bytes at a time come faster (256 caches to 4096:
+// 185 us instead of 208; on a GPU with faster memory 182 instead of 189), but an item of
+// two has more to merge where CTAs share it: taken from two items a CTA (with
+// one, 256 caches of 2000 to 2100 and 4 KV heads, 96 instead of 94 us).  Items of four
+// took 195 and 110 us for the two.
+constexpr int64_t kAdTwoHeads = 2 * 3;  // items an SM (three CTAs)
+template <class Fn>
+auto with_form(int64_t batch, int64_t kv_heads, int64_t group, int64_t head_dim, Fn fn) {
+  const int64_t rows = head_dim == 64 && group <= 8 && kv_heads % 2 == 0 ? kv_heads / 2 : kv_heads;
+  return rows % 2 == 0 && batch * (rows / 2) >= kAdTwoHeads * sm_count() ? with_shape<2>(kv_heads, group, head_dim, fn)
+                                                                             : with_shape<1>(kv_heads, group, head_dim, fn);
 }
 
 // The workspace starts with the items' counters: an area of one size for every
@@ -718,9 +741,9 @@ using namespace fp8rl;
 
 extern "C" FP8RL_API size_t fp8rl_attn_decode_workspace_size(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128)) return 0;
-  return with_form(kv_heads, q_heads / kv_heads, head_dim, [](auto f) {
+  return with_form(kAdMaxBatch, kv_heads, q_heads / kv_heads, head_dim, [](auto f) {  // the larger of a batch's forms
     using F = decltype(f);
-    return (size_t)(ticket_bytes() + 2 * (int64_t)sm_count() * F::kCtas * F::kPart * 4);
+    return (size_t)(ticket_bytes() + 2 * (int64_t)sm_count() * F::kCtas * F::W * F::kPart * 4);
   });
 }
 
@@ -768,7 +791,7 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t 
   a.max_len = (int32_t)(max_blocks * block_size);
   a.softmax_scale = softmax_scale;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = with_form(kv_heads, a.group, head_dim, [&](auto f) { return launch_decode<decltype(f)>(a, d_workspace, cs); });
+  const cudaError_t e = with_form(batch, kv_heads, a.group, head_dim, [&](auto f) { return launch_decode<decltype(f)>(a, d_workspace, cs); });
   if (e != cudaSuccess) {
     cudaGetLastError();
     return FP8RL_ERR_CUDA;

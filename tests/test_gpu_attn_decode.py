@@ -142,6 +142,24 @@ def test_nan_codes_stay_in_their_head(hq, hkv, d):
             assert bool(out[:, mine].isnan().all())
 
 
+@pytest.mark.parametrize("batch,hq,hkv,d", [(470, 8, 4, 128), (920, 16, 2, 128), (920, 24, 2, 128), (920, 4, 4, 64), (920, 16, 4, 64),
+                                            (920, 32, 4, 64), (920, 3, 3, 64), (470, 36, 4, 128)])
+def test_many_caches(batch, hq, hkv, d):
+    """Enough sequences for items of two heads, of ragged lengths, some of them shared by CTAs."""
+    g = torch.Generator().manual_seed(batch + hq)
+    lens = torch.randint(0, 300, (batch,), generator=g).tolist()
+    lens[3], lens[batch // 2], lens[-1] = 5000, 0, 2500
+    q, kc, vc, table, ln, scales, out, lse = check(lens, hq, hkv, d, 16, seed=hq)
+    group = hq // hkv
+    mine = torch.zeros(hq, dtype=torch.bool, device="cuda")
+    mine[group:2 * group] = True
+    vc = vc.clone()
+    vc[:, d:2 * d] = 0x7F  # NaN codes of one KV head stay in its query heads
+    got, got_lse = fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16)
+    assert torch.equal(got[:, ~mine], out[:, ~mine]) and torch.equal(got_lse, lse)
+    assert bool(got[ln > 0][:, mine].isnan().all())
+
+
 def test_one_long_sequence_of_one_head():
     check([70001], 4, 1, 128, 64, seed=1)
 
