@@ -247,6 +247,20 @@ def test_one_workspace_across_calls_and_same_bits():
     assert torch.equal(out[0], got[0])
 
 
+@pytest.mark.parametrize("lens,hq,hkv,d", [([9000], 40, 4, 128), ([50000], 32, 4, 64), ([30000, 5, 20000], 12, 2, 64), ([60000], 16, 1, 128),
+                                           ([40000], 3, 3, 64), ([7000], 8, 1, 128), ([100000, 200], 8, 1, 64)])
+def test_partials_merged_in_two_steps(lens, hq, hkv, d):
+    """Few long sequences, each over hundreds of CTAs: right, the same bits again on the
+    same workspace, and the workspace's counters left at zero."""
+    q, kc, vc, table, ln, scales, out, lse = check(lens, hq, hkv, d, 16, seed=hq)
+    ws = fp8rl.attn_decode_workspace(hq, hkv, d)
+    for _ in range(3):
+        got = fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16, workspace=ws)
+        assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+        sms = torch.cuda.get_device_properties(0).multi_processor_count
+        assert not bool(ws[:sms * 4 * 3 * 4].any())
+
+
 def test_one_workspace_across_shapes():
     """Shapes that need it in different sizes, on one workspace: the counters of
     one are never another's partials."""
