@@ -17,16 +17,18 @@
 // the largest of its elements, so the k-th largest thread maximum tau is a
 // lower bound of the k-th largest element, and every element that is at least
 // tau lies with a thread whose maximum is at least tau: about k threads (ties
-// aside) of the CTA's 256, whose elements are read a second time and ranked by
-// (value, lower index first) in sorted lists of one key per lane.
+// aside) of the CTA's 256, whose elements are read a second time.  Those at or
+// above tau are few and one warp sorts them by (value, lower index first) (8192 x
+// 1313: 39 us; with every warp's offered one by one to a list, 68); a row of many
+// equal ones goes through sorted lists of one key per lane.
 //
 // Backward: dx_j = (g ([j = t] - p_j) - g_H p_j (log p_j + H)) / T from the
 // saved (m, ln S) and H; elementwise, so dx may be x.
 //
 // Both are HBM-bound (one read; one read and one write): 4096 x 151936 bf16
-// takes 187 us forward (6.7 TB/s; 1/32 of the rows there have no token and are
+// takes 185 us forward (6.7 TB/s; 1/32 of the rows there have no token and are
 // not read) and 354 us backward (7.0 TB/s).  16 rows with 20 alternatives
-// take 13 us, on clusters of 8.
+// take 9.5 us, on clusters of 8.
 #include <algorithm>
 #include <cfloat>
 
@@ -40,6 +42,7 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpUnroll = 4;  // 16-byte pieces a thread loads before it uses the first
 constexpr int kMaxTop = 32;   // one key per lane
+constexpr int kHits = 2 * kMaxTop;  // elements at or above the bound that are sorted at once
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kTinyExp2 = -200.0f;  // 2^-200 is 0 in fp32: exponents below it change nothing, and stay finite
 
@@ -209,6 +212,21 @@ __device__ __forceinline__ Stat merge(Stat a, Stat b, float c) {
   return a;
 }
 
+// the sums of groups of L neighbouring lanes, in a tree that both lanes of a pair
+// add up alike: the largest first, so that each lane moves once
+template <int L>
+__device__ __forceinline__ void merge_lanes(Stat& a, float c) {
+  float m = a.m;
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (a.m != m) move_to(a, m, c);
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) {
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, d);
+    a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
+  }
+}
+
 // Keys that order like (value, lower index first): the value's bits as an
 // ordered integer (-0 as 0, NaN below everything) above the complemented index.
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -255,11 +273,27 @@ __device__ __forceinline__ uint64_t merge_lists(uint64_t list, uint64_t other) {
   return list;
 }
 
+// the warp's keys, largest first (Batcher's bitonic sort)
+__device__ __forceinline__ uint64_t sort_keys(uint64_t key) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 2; n <= 32; n <<= 1) {
+#pragma unroll
+    for (int d = n >> 1; d > 0; d >>= 1) {
+      const uint64_t o = __shfl_xor_sync(0xffffffffu, key, d);
+      const bool larger = ((lane & d) == 0) == ((lane & n) == 0);
+      key = larger == (key > o) ? key : o;
+    }
+  }
+  return key;
+}
+
 // Merge of the warps' lists: warp 0 returns the CTA's.  Every warp takes part.
-__device__ __forceinline__ uint64_t merge_warps(uint64_t list, uint64_t (&lists)[kLpWarps][kMaxTop]) {
+template <int W>
+__device__ __forceinline__ uint64_t merge_warps(uint64_t list, uint64_t (&lists)[W][kMaxTop]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int n = kLpWarps / 2; n > 0; n >>= 1) {
+  for (int n = W / 2; n > 0; n >>= 1) {
     if (warp >= n && warp < 2 * n) lists[warp][lane] = list;
     __syncthreads();
     if (warp < n) list = merge_lists(list, lists[warp + n][lane]);
@@ -282,9 +316,9 @@ struct LpArgs {
 
 // grid (cluster, rows), clusters of gridDim.x CTAs: a CTA takes the pieces
 // [rank, rank + 1) * ceil(pieces / cluster) of its row
-template <typename In, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
-  constexpr int N = Row<In>::N, U = kLpUnroll;
+template <typename In, bool TOP, int T>
+__global__ void __launch_bounds__(T) logprob_kernel(const LpArgs a) {
+  constexpr int N = Row<In>::N, U = kLpUnroll, W = T / 32;
   ptx::grid_dep_launch_dependents();
   ptx::grid_dep_wait();
   const int64_t r = blockIdx.y;
@@ -309,6 +343,11 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
   const int32_t share = (row.pieces + ranks - 1) / ranks;
   const int32_t p0 = rank * share, p1 = min(row.pieces, p0 + share);
   const float c = kLog2e / a.temperature;
+  float xt = 0.0f;  // needed at the end, requested now
+  if (tid == 0 && rank == 0) {
+    if (sizeof(In) == 2) xt = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(xr)[t]);
+    else xt = reinterpret_cast<const float*>(xr)[t];
+  }
 
   Stat st{-INFINITY, 0.0f, 0.0f};
   uint64_t s2 = pair_of(0.0f, 0.0f), w2 = s2;  // s and w in two halves
@@ -323,10 +362,10 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
   };
   // (loading the next round ahead of this one's arithmetic costs the
   // registers of a third of the resident CTAs: 213 us for 195 at 4096 x 151936)
-  for (int32_t p = p0 + tid; p < p1; p += U * kLpThreads) {
+  for (int32_t p = p0 + tid; p < p1; p += U * T) {
     uint4 u[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) u[i] = p + i * kLpThreads < p1 ? row.load(p + i * kLpThreads) : absent<In>();
+    for (int i = 0; i < U; ++i) u[i] = p + i * T < p1 ? row.load(p + i * T) : absent<In>();
     const float big = largest<In>(u);
     if (big > st.m) {
       fold();
@@ -366,31 +405,27 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
   fold();
   const float mine = st.m;  // the largest of this thread's elements
 
-  __shared__ Stat warp_stat[kLpWarps];
+  __shared__ Stat warp_stat[W];
   __shared__ Stat cta_stat;
-  __shared__ uint64_t lists[kLpWarps][kMaxTop];
+  __shared__ uint64_t lists[W][kMaxTop];
   __shared__ uint64_t cta_list[kMaxTop];
-  __shared__ int16_t cand[kLpThreads];
-  __shared__ int cands;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const Stat o{__shfl_xor_sync(0xffffffffu, st.m, d), __shfl_xor_sync(0xffffffffu, st.s, d),
-                 __shfl_xor_sync(0xffffffffu, st.w, d)};
-    // both lanes of a pair merge in the same order
-    st = (lane & d) ? merge(o, st, c) : merge(st, o, c);
-  }
+  __shared__ int16_t cand[T];
+  __shared__ uint64_t hits[kHits];
+  __shared__ int cands, n_hits;
+  merge_lanes<32>(st, c);
   if (lane == 0) warp_stat[warp] = st;
-  if (tid == 0) cands = 0;
+  if (tid == 0) cands = n_hits = 0;
   __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kLpWarps; ++i) st = merge(st, warp_stat[i], c);
-    cta_stat = st;
+  if (warp == 0) {
+    st = warp_stat[lane % W];
+    merge_lanes<W>(st, c);
+    if (lane == 0) cta_stat = st;
   }
 
   uint64_t top_list = 0;
   if (TOP) {
     // tau: the top-th largest thread maximum (0 while fewer threads hold any)
-    constexpr int kShift = sizeof(In) == 2 ? 16 : 0;  // bf16 values differ in the upper half alone
+    constexpr int kShift = 16;  // the upper half: all of a bf16 value, a lower bound of an fp32 one
     const uint32_t own = p0 + tid < p1 ? max(ordered(mine) >> kShift, 1u) : 0u;
     uint32_t lo = 0u;
     for (int b = 31 - kShift; b >= 0; --b) {
@@ -400,27 +435,49 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
     if (own >= lo && own > 0u) cand[atomicAdd(&cands, 1)] = (int16_t)tid;
     __syncthreads();
     // the candidates' pieces, spread over all threads
-    const int32_t each = (p1 - p0 + kLpThreads - 1) / kLpThreads;
+    const int32_t each = (p1 - p0 + T - 1) / T;
     const int32_t total = cands * each;
-    uint64_t list = 0;
-    for (int32_t f0 = warp * 32; f0 < total; f0 += kLpThreads) {
-      const int32_t f = f0 + lane;
-      const int32_t p = f < total ? p0 + cand[f / each] + (f % each) * kLpThreads : p1;
-      const uint4 u = p < p1 ? row.load(p) : absent<In>();
+    auto piece_of = [&](int32_t f) { return f < total ? p0 + cand[f / each] + (f % each) * T : p1; };
+    auto key_at = [&](int32_t p, int e, float v) -> uint64_t {
+      const int32_t j = p * N - row.off + e;
+      return p < p1 && j >= 0 && j < a.vocab && max(ordered(v) >> kShift, 1u) >= lo ? key_of(v, j) : 0;
+    };
+    for (int32_t f = tid; f < total; f += T) {
+      const int32_t p = piece_of(f);
+      const uint4 u[1] = {p < p1 ? row.load(p) : absent<In>()};
+      if (max(ordered(largest<In>(u)) >> kShift, 1u) < lo) continue;
       float v[N];
-      values<In>(u, v);
+      values<In>(u[0], v);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const int32_t j = p * N - row.off + e;
-        const bool in = p < p1 && j >= 0 && j < a.vocab && max(ordered(v[e]) >> kShift, 1u) >= lo;
-        offer(list, in ? key_of(v[e], j) : 0, a.top);
+        const uint64_t key = key_at(p, e, v[e]);
+        if (key == 0) continue;
+        const int at = atomicAdd(&n_hits, 1);
+        if (at < kHits) hits[at] = key;
       }
     }
-    top_list = merge_warps(list, lists);
+    __syncthreads();
+    if (n_hits <= kHits) {  // all but rows with many equal logits: sorted by one warp
+      if (warp == 0) {
+        top_list = sort_keys(lane < n_hits ? hits[lane] : 0);
+        if (n_hits > 32) top_list = merge_lists(top_list, sort_keys(lane + 32 < n_hits ? hits[lane + 32] : 0));
+      }
+    } else {
+      uint64_t list = 0;
+      for (int32_t f0 = warp * 32; f0 < total; f0 += T) {
+        const int32_t p = piece_of(f0 + lane);
+        const uint4 u = p < p1 ? row.load(p) : absent<In>();
+        float v[N];
+        values<In>(u, v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) offer(list, key_at(p, e, v[e]), a.top);
+      }
+      top_list = merge_warps(list, lists);
+    }
     if (warp == 0) cta_list[lane] = top_list;
   }
 
-  if (ranks > 1) {
+  if (T == kLpThreads && ranks > 1) {
     ptx::cluster_sync();
     if (TOP && rank == 0) {  // warp i takes rank i's list
       uint64_t list = top_list;
@@ -434,7 +491,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
   if (rank == 0 && warp == 0) {
     __syncwarp();
     Stat all = cta_stat;
-    if (ranks > 1) {  // lane i reads rank i's sums; they are merged in rank order
+    if (T == kLpThreads && ranks > 1) {  // lane i reads rank i's sums; they are merged in rank order
       const uint32_t base = ptx::mapa_shared(ptx::smem_u32(&cta_stat), lane < ranks ? lane : 0);
       const Stat o{__uint_as_float(ptx::ld_dsmem_u32(base)), __uint_as_float(ptx::ld_dsmem_u32(base + 4)),
                    __uint_as_float(ptx::ld_dsmem_u32(base + 8))};
@@ -447,9 +504,6 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
     const float ln_s = logf(all.s);
     auto log_prob = [&](float v) { return none ? -INFINITY : (v - all.m) / a.temperature - ln_s; };
     if (lane == 0) {
-      float xt;
-      if (sizeof(In) == 2) xt = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(xr)[t]);
-      else xt = reinterpret_cast<const float*>(xr)[t];
       a.lp[r] = log_prob(xt);
       a.entropy[r] = none ? 0.0f : ln_s - kLn2 * (all.w / all.s);
       a.stats[r] = make_float2(all.m, ln_s);
@@ -460,7 +514,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpArgs a) {
     }
   }
   __syncwarp();
-  if (ranks > 1) ptx::cluster_sync();  // rank 0 has read the others' shared memory
+  if (T == kLpThreads && ranks > 1) ptx::cluster_sync();  // rank 0 has read the others' shared memory
 }
 
 // ------------------------------------------------------------------ backward
@@ -610,17 +664,18 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 constexpr int64_t kMaxRows = 65535;             // grid y
 constexpr int64_t kMaxVocab = (int64_t)1 << 30;  // 32-bit element and piece numbers
 
-template <typename In, bool TOP>
+template <typename In, bool TOP, int T>
 cudaError_t launch_logprob(const LpArgs& a, int64_t rows, cudaStream_t stream) {
-  // Two CTAs per SM keep the memory pipes busy; fewer rows than that are
-  // split over a cluster, down to one load round (four pieces a thread) per CTA.
-  const int64_t want = 2 * (int64_t)sm_count();
+  // Fewer rows than four CTAs per SM are split over a cluster, down to one load
+  // round (four pieces a thread) per CTA (338 x 151936: 27 us, 39 with two CTAs
+  // per SM; 200 x 50257: 8.8, 11.6 with six).
+  const int64_t want = 4 * (int64_t)sm_count();
   const int64_t round = (int64_t)kLpThreads * kLpUnroll * Row<In>::N;
   int cluster = 1;
-  while (cluster < 8 && rows * cluster < want && (int64_t)a.vocab > cluster * round) cluster *= 2;
+  while (T == kLpThreads && cluster < 8 && rows * cluster < want && (int64_t)a.vocab > cluster * round) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster, (unsigned)rows);
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.blockDim = dim3(T);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -630,7 +685,19 @@ cudaError_t launch_logprob(const LpArgs& a, int64_t rows, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprob_kernel<In, TOP>, a);
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<In, TOP, T>, a);
+}
+
+// Short rows are bound by a row's chain of waits, so they run in smaller CTAs, more of
+// them at a time: 8192 x 1313 bf16 18 us with 64 threads, 34 with 256; 8192 x 14 506
+// 55 with 128, 60 with 256 (at 50 257 256 are faster: 92 and 101).  Few rows
+// gain from 256 threads as soon as they have work for them.
+template <typename In, bool TOP>
+cudaError_t launch_rows(const LpArgs& a, int64_t rows, cudaStream_t stream) {
+  const int64_t pieces = ((int64_t)a.vocab + Row<In>::N - 1) / Row<In>::N;
+  if (pieces <= 256) return launch_logprob<In, TOP, 64>(a, rows, stream);
+  if (pieces <= 2048 && rows >= 2 * (int64_t)sm_count()) return launch_logprob<In, TOP, 128>(a, rows, stream);
+  return launch_logprob<In, TOP, kLpThreads>(a, rows, stream);
 }
 
 }  // namespace
@@ -668,8 +735,8 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob(const void* d_logits, int32_t lo
     a.top = (int32_t)topk;
     a.temperature = temperature;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = logits_fp32 ? (topk ? launch_logprob<float, true>(a, n, cs) : launch_logprob<float, false>(a, n, cs))
-                                      : (topk ? launch_logprob<uint16_t, true>(a, n, cs) : launch_logprob<uint16_t, false>(a, n, cs));
+    const cudaError_t e = logits_fp32 ? (topk ? launch_rows<float, true>(a, n, cs) : launch_rows<float, false>(a, n, cs))
+                                      : (topk ? launch_rows<uint16_t, true>(a, n, cs) : launch_rows<uint16_t, false>(a, n, cs));
     if (e != cudaSuccess) {
       cudaGetLastError();
       return FP8RL_ERR_CUDA;

@@ -91,6 +91,33 @@ def test_logprob_unaligned_rows(offset, pad, dtype):
     check(x, t, topk=17)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,pieces", [(400, 255), (400, 256), (400, 257), (400, 2048), (400, 2049), (30, 256), (30, 2047), (303, 1000), (608, 2100)])
+def test_row_lengths_where_the_split_changes(rows, pieces, dtype):
+    """Rows of so many 16-byte pieces, give or take an element."""
+    n = 8 if dtype == torch.bfloat16 else 4
+    for vocab in (pieces * n - 1, pieces * n, pieces * n + 1):
+        x, t = make(rows, vocab, dtype, seed=vocab, ld=vocab + 3)
+        check(x, t, topk=20)
+        check(x, t)
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 131), (400, 900), (400, 5000), (20, 40000)])
+def test_top_of_values_that_differ_in_their_low_bits(rows, vocab):
+    """fp32 logits that share their upper 16 bits: as many at the bound as elements;
+    then a few dozen above the rest."""
+    g = torch.Generator("cuda").manual_seed(vocab)
+    x = 1.0 + torch.rand(rows, vocab, generator=g, device="cuda") * 2.0 ** -9
+    t = torch.randint(0, vocab, (rows,), generator=g, device="cuda").int()
+    check(x, t, topk=32)
+    for extra in (30, 33, 63, 64, 65, 100):
+        y = x.clone()
+        at = torch.rand(rows, vocab, generator=g, device="cuda").argsort(1)[:, :extra]
+        y.scatter_(1, at, 2.0 + torch.rand(rows, extra, generator=g, device="cuda") * 2.0 ** -9)
+        check(y, t, topk=32)
+        check(y.bfloat16(), t, topk=25)
+
+
 @pytest.mark.parametrize("rows", [1, 30, 700])
 def test_top_ties_go_to_the_lower_id(rows):
     """Few distinct values, constant rows, ascending and descending rows, and
