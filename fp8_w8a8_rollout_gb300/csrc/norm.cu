@@ -40,14 +40,8 @@ struct NormArgs {
 };
 
 // columns c .. c + 7 of a row; columns at or past k read as zero
-template <bool VEC>
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int32_t c, int32_t k) {
-  if (VEC) return c < k ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (c + e < k) w[e >> 1] |= (uint32_t)row[c + e] << (16 * (e & 1));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return c < k ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
@@ -56,18 +50,11 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   return r;
 }
 
-template <bool VEC>
 __device__ __forceinline__ void store8_bf16(uint16_t* row, int32_t c, int32_t k, const float (&v)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = bf16x2_rn(v[2 * i], v[2 * i + 1]);
-  if (VEC) {
-    if (c < k) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < k) row[c + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-  }
+  if (c < k) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
@@ -75,9 +62,23 @@ __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
   v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
 }
 
-// VEC: k and every stride a multiple of 8 elements, every pointer 16-byte
-// aligned (codes 8-byte): whole pieces only
-template <int T, int NP, bool VEC, bool UE8M0>
+// the row's sum of squares from the threads': a fixed tree, the same bits on
+// every run; part alternates between rows, so one barrier a row is enough
+template <int T>
+__device__ __forceinline__ float row_sum(float ss, float (&part)[T / 32]) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  ss = part[0];
+#pragma unroll
+  for (int w = 1; w < T / 32; ++w) ss += part[w];
+  return ss;
+}
+
+// k and every stride a multiple of 8 elements, every pointer 16-byte aligned
+// (codes 8-byte): whole pieces only
+template <int T, int NP, bool UE8M0>
 __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_kernel(const NormArgs a) {
   // rows of up to 8192 columns: the next row waits in registers
   constexpr bool kAhead = T * NP <= 1024;
@@ -91,8 +92,8 @@ __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_kernel
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int32_t c = (tid + j * T) * 8;
-      xv[j] = load8<VEC>(a.x + row * a.ldx, c, a.k);
-      if (a.res) rv[j] = load8<VEC>(a.res + row * a.ldr, c, a.k);
+      xv[j] = load8(a.x + row * a.ldx, c, a.k);
+      if (a.res) rv[j] = load8(a.res + row * a.ldr, c, a.k);
     }
   };
   if (kAhead) fetch(blockIdx.x);
@@ -118,23 +119,16 @@ __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_kernel
     if (a.h) {
       uint16_t* hr = a.h + row * a.ldh;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) store8_bf16<VEC>(hr, (tid + j * T) * 8, a.k, h[j]);
+      for (int j = 0; j < NP; ++j) store8_bf16(hr, (tid + j * T) * 8, a.k, h[j]);
     }
-    // the row's sum of squares: a fixed tree, the same bits on every run
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    if ((tid & 31) == 0) part[turn][tid >> 5] = ss;
-    __syncthreads();
-    ss = part[turn][0];
-#pragma unroll
-    for (int w = 1; w < T / 32; ++w) ss += part[turn][w];
+    ss = row_sum<T>(ss, part[turn]);
     const float rms = rsqrtf(ss / (float)a.k + a.eps);
     uint8_t* qr = a.q + row * a.ldq;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int32_t c = (tid + j * T) * 8;
       float w[8];
-      unpack8(load8<VEC>(a.weight, c, a.k), w);
+      unpack8(load8(a.weight, c, a.k), w);
       float amax = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -162,12 +156,102 @@ __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_kernel
         for (int i = 0; i < 2; ++i) code[i] = e4m3x2(y[4 * i], y[4 * i + 1]) | (e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
         if ((tid & 15) == 0) static_cast<float*>(a.scale)[(int64_t)(c / kBlock) * a.m + row] = s;
       }
-      if (VEC) {
-        if (dcheck(c + 8 <= a.k, a.err)) *reinterpret_cast<uint2*>(qr + c) = make_uint2(code[0], code[1]);
-      } else {
+      if (dcheck(c + 8 <= a.k, a.err)) *reinterpret_cast<uint2*>(qr + c) = make_uint2(code[0], code[1]);
+    }
+  }
+}
+
+// Any k, strides and alignment, an element at a time: a warp takes whole groups,
+// lane l their columns l, l + 32, l + 64 and l + 96, so that each access of the
+// warp is contiguous (4392 x 6918: 79 us; pieces of eight columns a lane, each in
+// eight accesses with a stride, 131).  Bound by the accesses' issue.
+template <int T, int NP, bool UE8M0>
+__global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_any_kernel(const NormArgs a) {
+  constexpr int G = 2 * NP, W = T / 32;  // groups of a warp
+  constexpr bool kAhead = T * NP <= 1024;
+  ptx::grid_dep_launch_dependents();
+  ptx::grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto column = [&](int j, int i) { return (warp + j * W) * (int)kBlock + 32 * i + lane; };
+  auto load2 = [&](const uint16_t* row, int j, int i) {
+    const int32_t c = column(j, i);
+    return (c < a.k ? (uint32_t)row[c] : 0u) | (c + 32 < a.k ? (uint32_t)row[c + 32] << 16 : 0u);
+  };
+  uint32_t xv[G][2], rv[G][2];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < a.k) qr[c + e] = (uint8_t)(code[e >> 2] >> (8 * (e & 3)));
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        xv[j][i] = load2(a.x + row * a.ldx, j, 2 * i);
+        if (a.res) rv[j][i] = load2(a.res + row * a.ldr, j, 2 * i);
+      }
+  };
+  if (kAhead) fetch(blockIdx.x);
+  __shared__ float part[2][W];
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x, turn ^= 1) {
+    if (!kAhead) fetch(row);
+    float h[G][4];
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[j][i] = i & 1 ? bf16_hi(xv[j][i >> 1]) : bf16_lo(xv[j][i >> 1]);
+        if (a.res) h[j][i] += i & 1 ? bf16_hi(rv[j][i >> 1]) : bf16_lo(rv[j][i >> 1]);
+        ss = fmaf(h[j][i], h[j][i], ss);
+      }
+    if (kAhead && row + gridDim.x < a.m) fetch(row + gridDim.x);
+    if (a.h) {
+      uint16_t* hr = a.h + row * a.ldh;
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t v = bf16x2_rn(h[j][2 * i], h[j][2 * i + 1]);
+          const int32_t c = column(j, 2 * i);
+          if (c < a.k) hr[c] = (uint16_t)v;
+          if (c + 32 < a.k) hr[c + 32] = (uint16_t)(v >> 16);
+        }
+    }
+    ss = row_sum<T>(ss, part[turn]);
+    const float rms = rsqrtf(ss / (float)a.k + a.eps);
+    uint8_t* qr = a.q + row * a.ldq;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const int32_t group = warp + j * W;
+      if (group * (int)kBlock >= a.k) continue;
+      const uint32_t w[2] = {load2(a.weight, j, 0), load2(a.weight, j, 2)};
+      float amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[j][i] = h[j][i] * rms * (i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]));
+        amax = fmaxf(amax, fabsf(h[j][i]));
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      uint32_t code[2];
+      if (UE8M0) {
+        const int e2 = scale_ue8m0_exponent(amax);
+        const float f = exp2_neg(e2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) code[i] = e4m3x2(h[j][2 * i] * f, h[j][2 * i + 1] * f);
+        if (lane == 0) static_cast<uint8_t*>(a.scale)[(int64_t)group * a.m + row] = (uint8_t)(e2 + 127);
+      } else {
+        const float s = scale_fp32(amax), r = __frcp_rn(s);
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = s >= kFastDivMinScale ? div_by_scale(h[j][i], s, r) : __fdiv_rn(h[j][i], s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) code[i] = e4m3x2(y[2 * i], y[2 * i + 1]);
+        if (lane == 0) static_cast<float*>(a.scale)[(int64_t)group * a.m + row] = s;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int32_t c = column(j, 2 * i);
+        if (c < a.k) qr[c] = (uint8_t)code[i];
+        if (c + 32 < a.k) qr[c + 32] = (uint8_t)(code[i] >> 8);
       }
     }
   }
@@ -194,10 +278,10 @@ cudaError_t launch_norm(const NormArgs& a, bool vec, bool ue8m0, cudaStream_t st
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
   if (vec)
-    return ue8m0 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, true, true>, a)
-                 : cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, true, false>, a);
-  return ue8m0 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, false, true>, a)
-               : cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, false, false>, a);
+    return ue8m0 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, true>, a)
+                 : cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<T, NP, false>, a);
+  return ue8m0 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_any_kernel<T, NP, true>, a)
+               : cudaLaunchKernelEx(&cfg, rmsnorm_quant_any_kernel<T, NP, false>, a);
 }
 
 }  // namespace
