@@ -18,7 +18,7 @@
 // lower bound of the k-th largest element, and every element that is at least
 // tau lies with a thread whose maximum is at least tau: about k threads (ties
 // aside) of the CTA's 256, whose elements are read a second time.  Those at or
-// above tau are few and one warp sorts them by (value, lower index first) (8192 x
+// above tau are few and are sorted by (value, lower index first), 32 to a warp (8192 x
 // 1313: 39 us; with every warp's offered one by one to a list, 68); a row of many
 // equal ones goes through sorted lists of one key per lane.
 //
@@ -39,10 +39,10 @@ namespace fp8rl {
 namespace {
 
 constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kGradThreads = 128;  // the gradient's
 constexpr int kLpUnroll = 4;  // 16-byte pieces a thread loads before it uses the first
 constexpr int kMaxTop = 32;   // one key per lane
-constexpr int kHits = 2 * kMaxTop;  // elements at or above the bound that are sorted at once
+constexpr int kHits = 256;    // elements at or above the bound that are sorted, 32 at a time
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kTinyExp2 = -200.0f;  // 2^-200 is 0 in fp32: exponents below it change nothing, and stay finite
 
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(T) logprob_kernel(const LpArgs a) {
     constexpr int kShift = 16;  // the upper half: all of a bf16 value, a lower bound of an fp32 one
     const uint32_t own = p0 + tid < p1 ? max(ordered(mine) >> kShift, 1u) : 0u;
     uint32_t lo = 0u;
-    for (int b = 31 - kShift; b >= 0; --b) {
+    for (int b = p1 - p0 < a.top ? -1 : 31 - kShift; b >= 0; --b) {
       const uint32_t mid = lo | 1u << b;
       if (__syncthreads_count(own >= mid) >= a.top) lo = mid;
     }
@@ -457,11 +457,12 @@ __global__ void __launch_bounds__(T) logprob_kernel(const LpArgs a) {
       }
     }
     __syncthreads();
-    if (n_hits <= kHits) {  // all but rows with many equal logits: sorted by one warp
-      if (warp == 0) {
-        top_list = sort_keys(lane < n_hits ? hits[lane] : 0);
-        if (n_hits > 32) top_list = merge_lists(top_list, sort_keys(lane + 32 < n_hits ? hits[lane + 32] : 0));
+    if (n_hits <= kHits) {  // all but rows with many equal logits
+      for (int h0 = warp * 32; h0 < n_hits; h0 += T) {
+        const uint64_t more = sort_keys(h0 + lane < n_hits ? hits[h0 + lane] : 0);
+        top_list = h0 < T ? more : merge_lists(top_list, more);
       }
+      if (n_hits > 32) top_list = merge_warps(top_list, lists);
     } else {
       uint64_t list = 0;
       for (int32_t f0 = warp * 32; f0 < total; f0 += T) {
@@ -566,7 +567,7 @@ __device__ __forceinline__ void store1<float>(float* p, float v) {
 
 // grid (slices, rows); dx may be x, so neither is read through the read-only path
 template <typename In>
-__global__ void __launch_bounds__(kLpThreads) logprob_grad_kernel(const LpGradArgs a) {
+__global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const LpGradArgs a) {
   constexpr int N = Row<In>::N, U = kLpUnroll;
   ptx::grid_dep_launch_dependents();
   ptx::grid_dep_wait();
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_grad_kernel(const LpGradAr
   q.b = -gh * kLn2 * inv_t;
   q.top = g * inv_t;
   const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
-  const int32_t stride = gridDim.x * kLpThreads, first = blockIdx.x * kLpThreads + threadIdx.x;
+  const int32_t stride = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + threadIdx.x;
   if (!same) {  // rows that start at different places of a 16-byte piece: element by element
     for (int32_t j = first; j < a.vocab; j += stride) {
       float v;
@@ -666,10 +667,10 @@ constexpr int64_t kMaxVocab = (int64_t)1 << 30;  // 32-bit element and piece num
 
 template <typename In, bool TOP, int T>
 cudaError_t launch_logprob(const LpArgs& a, int64_t rows, cudaStream_t stream) {
-  // Fewer rows than four CTAs per SM are split over a cluster, down to one load
-  // round (four pieces a thread) per CTA (338 x 151936: 27 us, 39 with two CTAs
-  // per SM; 200 x 50257: 8.8, 11.6 with six).
-  const int64_t want = 4 * (int64_t)sm_count();
+  // Fewer rows than three and a half CTAs per SM are split over a cluster, down to one
+  // load round (four pieces a thread) per CTA (338 x 151936: 27 us on clusters of two, 39
+  // on one CTA; 200 x 50257: 8.8 on four, 10.1 on two, 11.6 on eight).
+  const int64_t want = 7 * (int64_t)sm_count() / 2;
   const int64_t round = (int64_t)kLpThreads * kLpUnroll * Row<In>::N;
   int cluster = 1;
   while (T == kLpThreads && cluster < 8 && rows * cluster < want && (int64_t)a.vocab > cluster * round) cluster *= 2;
@@ -778,16 +779,20 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, i
     a.ldd = ldd;
     a.vocab = (int32_t)vocab;
     a.temperature = temperature;
-    // A load round is four pieces a thread.  CTAs of up to five rounds once
-    // that leaves four times the resident CTAs (4096 x 151936: 356 us, with one
-    // round each 403, ten 363); one round each for small work.
-    const int64_t round = (int64_t)kLpThreads * kLpUnroll * (16 / (int64_t)size);
+    // Small CTAs, so that many rows are under way (8192 x 1000 fp32: 9.3 us with 64
+    // threads, 11 with 128, 16 with 256; 8192 x 4000 43, 41 and 43).  A load round is
+    // four pieces a thread.  CTAs of up to five rounds once that leaves many times
+    // the resident CTAs (4096 x 151936 with 256 threads: 356 us, with one round
+    // each 403, ten 363); one round each for small work.
+    const int64_t pieces = (vocab * (int64_t)size + 15) / 16;
+    const int threads = pieces <= 640 ? 64 : kGradThreads;
+    const int64_t round = (int64_t)threads * kLpUnroll * (16 / (int64_t)size);
     const int64_t rounds = (vocab + round - 1) / round;
     const int64_t each = std::max<int64_t>(1, std::min<int64_t>(5, rounds * n / ((int64_t)sm_count() * 24)));
     const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(65535, (rounds + each - 1) / each)), (unsigned)n);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = cs;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
