@@ -13,6 +13,7 @@ with torch and call the same entry points.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -165,6 +166,18 @@ def _stream(stream) -> int | None:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _on(stream, device):
+    """The context in which torch's own allocations and fills belong to the stream
+    that a call's kernels take: scratch that a helper makes for one call is cleared
+    ahead of them, and reused behind them alone."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        # (ExternalStream takes a null handle for a new stream)
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _ok(status: int, what: str) -> None:
@@ -891,7 +904,8 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
         raise ValueError("scales must hold the fp32 K and V scales")
     hkv = width // d
     if workspace is None:
-        workspace = attn_decode_workspace(hq, hkv, d, q.device)
+        with _on(stream, q.device):
+            workspace = attn_decode_workspace(hq, hkv, d, q.device)
     if out is None:
         out = tuple(_outs((((batch, hq, d), torch.bfloat16), ((batch, hq), torch.float32)), q.device))
     else:

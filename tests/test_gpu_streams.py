@@ -1,0 +1,56 @@
+"""The helpers with an explicit ``stream`` other than torch's current one: what
+a helper makes and clears for one call belongs to that stream.  The current
+stream is kept busy, so that anything left on it would come too late, and memory
+of the same size is filled right after the call, so that scratch given back to
+the current stream too early would be overwritten."""
+import pytest
+import torch
+
+import fp8_w8a8_rollout_gb300 as fp8rl
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    fp8rl.load_library(build_if_missing=True)
+
+
+def aside(call, nbytes):
+    """call(stream handle) on a stream of its own while the current stream is busy;
+    freed memory of `nbytes` on either stream holds ones."""
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about a tenth of a second
+    got = call(side.cuda_stream)
+    trample = [torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    del trample
+    assert fp8rl.fp8rl_sync_status() == 0
+    return got
+
+
+def same(want, got):
+    for a, b in zip(want, got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", [([9000], 32, 8, 128), ([70, 4000, 0, 1], 8, 2, 64)])
+def test_attn_decode_without_a_workspace(lens, hq, hkv, d):
+    g = torch.Generator("cuda").manual_seed(1)
+    blocks = -(-max(lens) // 16)
+    kc, vc = (torch.randint(0, 0x78, (len(lens) * blocks * 16, hkv * d), generator=g, device="cuda").to(torch.uint8) for _ in range(2))
+    table = torch.arange(len(lens) * blocks, device="cuda").int().view(len(lens), blocks)
+    q = torch.randn(len(lens), hq, d, generator=g, device="cuda").bfloat16()
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    scales = torch.tensor([0.001, 0.01], device="cuda")
+    ws = fp8rl.attn_decode_workspace(hq, hkv, d)
+    want = fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16, workspace=ws)
+    same(want, aside(lambda s: fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16, stream=s), ws.numel()))
+    # the legacy default stream by its null handle
+    same(want, fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16, stream=0))
