@@ -753,7 +753,8 @@ def tis_weights(lp_train: torch.Tensor, lp_rollout: torch.Tensor, mask: torch.Te
     dev = lp_train.device
     need = fp8rl_tis_workspace_size(n)
     if workspace is None:
-        workspace = torch.zeros(max(need, 32), dtype=torch.uint8, device=dev)  # header zeroed once
+        with _on(stream, dev):
+            workspace = torch.zeros(max(need, 32), dtype=torch.uint8, device=dev)  # header zeroed once
     w, kl = out if out is not None else (_out((n,), torch.float32, dev),
                                          _out((3,), torch.float64, dev))
     fp8rl_tis_weights(lp_train, lp_rollout, mask, n, clip, w, kl, workspace, workspace.numel(), stream)

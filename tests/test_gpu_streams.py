@@ -54,3 +54,13 @@ def test_attn_decode_without_a_workspace(lens, hq, hkv, d):
     same(want, aside(lambda s: fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16, stream=s), ws.numel()))
     # the legacy default stream by its null handle
     same(want, fp8rl.attn_decode(q, kc, vc, table, ln, scales, 16, stream=0))
+
+
+@pytest.mark.parametrize("n", [1, 100_000, 3_000_001])
+def test_tis_weights_without_a_workspace(n):
+    g = torch.Generator("cuda").manual_seed(2)
+    lt, lr = (-torch.rand(n, generator=g, device="cuda") for _ in range(2))
+    mask = (torch.rand(n, generator=g, device="cuda") < 0.7).to(torch.uint8)
+    need = max(fp8rl.fp8rl_tis_workspace_size(n), 32)
+    want = fp8rl.tis_weights(lt, lr, mask, workspace=torch.zeros(need, dtype=torch.uint8, device="cuda"))
+    same(want, aside(lambda s: fp8rl.tis_weights(lt, lr, mask, stream=s), need))
