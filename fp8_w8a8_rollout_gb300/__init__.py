@@ -697,7 +697,8 @@ def moe_plan(topk: torch.Tensor, experts: int, workspace: torch.Tensor | None = 
     dev = topk.device
     need = fp8rl_moe_plan_workspace_size(tokens, k, experts)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        with _on(stream, dev):
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     offsets = _out((experts + 1,), torch.int32, dev)
     row_of_pair = _out((tokens * k,), torch.int32, dev)
     token_of_row = _out((tokens * k,), torch.int32, dev)

@@ -64,3 +64,11 @@ def test_tis_weights_without_a_workspace(n):
     need = max(fp8rl.fp8rl_tis_workspace_size(n), 32)
     want = fp8rl.tis_weights(lt, lr, mask, workspace=torch.zeros(need, dtype=torch.uint8, device="cuda"))
     same(want, aside(lambda s: fp8rl.tis_weights(lt, lr, mask, stream=s), need))
+
+
+def test_moe_plan_without_a_workspace():
+    g = torch.Generator("cuda").manual_seed(3)
+    topk = torch.rand(5000, 64, generator=g, device="cuda").argsort(1)[:, :8].int().contiguous()
+    need = max(fp8rl.fp8rl_moe_plan_workspace_size(5000, 8, 64), 256)
+    want = fp8rl.moe_plan(topk, 64, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    same(want, aside(lambda s: fp8rl.moe_plan(topk, 64, stream=s), need))
