@@ -669,7 +669,11 @@ def kv_calibrate(k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None
     _check_cuda(k, v, q, out)
     for name, t in (("k", k), ("v", v)) + ((("q", q),) if q is not None else ()):
         _check_bf16_2d(t, name)
-    scales = out if out is not None else _out((3,), torch.float32, k.device).zero_()
+    scales = out
+    if out is None:
+        scales = _out((3,), torch.float32, k.device)
+        with _on(stream, k.device):
+            scales.zero_()
     tokens, dim = k.shape
     fp8rl_kv_calibrate(k, v, q, tokens, dim, k.stride(0), v.stride(0), 0 if q is None else q.shape[1],
                        0 if q is None else q.stride(0), scales, stream)

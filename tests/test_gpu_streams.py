@@ -72,3 +72,13 @@ def test_moe_plan_without_a_workspace():
     need = max(fp8rl.fp8rl_moe_plan_workspace_size(5000, 8, 64), 256)
     want = fp8rl.moe_plan(topk, 64, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
     same(want, aside(lambda s: fp8rl.moe_plan(topk, 64, stream=s), need))
+
+
+@pytest.mark.parametrize("with_q", [False, True])
+def test_kv_calibrate(with_q):
+    g = torch.Generator("cuda").manual_seed(4)
+    k, v, q = (torch.randn(3000, 256, generator=g, device="cuda").bfloat16() for _ in range(3))
+    q = q if with_q else None
+    want = fp8rl.kv_calibrate(k, v, q)
+    assert bool((want[:2] > 0).all()) and bool(want[2] > 0) == with_q
+    same([want], aside(lambda s: [fp8rl.kv_calibrate(k, v, q, stream=s)], 512))
