@@ -463,6 +463,8 @@ def _guarded(shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
     nbytes = numel * torch.empty((), dtype=dtype).element_size()
     buf = torch.full((_CANARY_PRE + nbytes + _CANARY_POST,), CANARY_BYTE, dtype=torch.uint8, device=device)
+    if buf.is_cuda and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(buf.device).synchronize()  # the call's kernels may go to another stream
     with _guards_lock:
         _guards.append((buf, nbytes))
     return buf[_CANARY_PRE:_CANARY_PRE + nbytes].view(dtype).view(tuple(shape))

@@ -82,3 +82,11 @@ def test_kv_calibrate(with_q):
     want = fp8rl.kv_calibrate(k, v, q)
     assert bool((want[:2] > 0).all()) and bool(want[2] > 0) == with_q
     same([want], aside(lambda s: [fp8rl.kv_calibrate(k, v, q, stream=s)], 512))
+
+
+def test_guarded_outputs(monkeypatch):
+    """The guards' fill does not land on what the other stream's kernel wrote."""
+    monkeypatch.setenv("FP8RL_CANARY", "1")
+    x = torch.randn(300, 512, device="cuda").bfloat16()
+    want = fp8rl.quant_act(x)
+    same(want, aside(lambda s: fp8rl.quant_act(x, stream=s), 1 << 18))
