@@ -34,8 +34,10 @@
 // and accumulators are fp32, the output is rounded once.
 //
 // An output depends on its own positions alone: in the key tiles that an item
-// does not see whole, a warp zeroes the value rows past the item's end and looks
-// the partly visible ones over before they are multiplied (0 * NaN).
+// does not see whole, a warp zeroes the value rows past the item's end and takes
+// non-finite values out of the partly visible ones before they are multiplied
+// (0 * NaN); the rows that see such a value get its term when they are stored, a
+// handful of operations whatever the prompt's length.
 //
 // The plan (one per step, used by every layer) lists the items, longest key
 // range first; CTAs take them in snake order, which evens the causal lengths
@@ -77,7 +79,7 @@ struct PlanHeader {
 
 struct ApArgs {
   const int4* plan;
-  const uint16_t *q, *k, *v;  // for rows that are taken again (the tensor maps serve the others)
+  const uint16_t *q, *k, *v;  // for the terms of non-finite values (the tensor maps serve all others)
   int64_t ldq, ldk, ldv;
   uint16_t* out;
   float* lse;  // or null
@@ -97,7 +99,8 @@ struct ApCfg {
   static constexpr uint32_t kBook = kRing + kApStages * kTileBytes;
   static constexpr uint32_t kItems = kBook + 384;             // the items at hand
   static constexpr uint32_t kRows = kBook + 512;              // row sums of the two tiles for the output warps
-  static constexpr uint32_t kSmem = kRows + 2 * kApTile * 8 + 512;  // alignment
+  static constexpr uint32_t kMarks = kRows + 2 * kApTile * 8; // per item at hand, which of its positions have values taken out
+  static constexpr uint32_t kSmem = kMarks + 128 + 384;       // alignment
   static constexpr uint32_t kTmemS = 0, kTmemO = 256;         // S of tile x at 128 x, O at 256 + 128 x
 };
 
@@ -266,21 +269,36 @@ __device__ __forceinline__ Item item_of(const ApArgs& a, uint32_t w, int32_t par
   return it;
 }
 
-// One output row by plain arithmetic from its final reference maximum (times
-// the scale) and 1 / sum: sum_j p_j v_j over the keys that it sees and no
-// others.  For items with a non-finite value in their last key tiles.
+constexpr int kApMarks = 8;  // words of an item: a bit for each of its (at most 256) positions
+
+__device__ __forceinline__ bool any_marks(uint32_t p) {
+  uint32_t a, b, c, d;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(p) : "memory");
+  return (a | b | c | d) != 0;
+}
+
+__device__ __forceinline__ bool non_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7F80u) == 0x7F80u; }
+
+// The terms p_j v_j of the values that were taken out of the product, onto the
+// stored output row of position `pos`: of marked positions up to its own, from
+// the row's final reference maximum (times the scale).  p_j's factor 1 / sum is
+// left out: the terms are infinities and NaN.
 template <int D>
-__device__ __forceinline__ void take_again(const ApArgs& a, const Item& it, int32_t pos, int32_t head, bool store, float mc,
-                                           float inv, uint16_t* dst) {
-  if (!store) return;
+__device__ __forceinline__ void add_taken_out(const ApArgs& a, const Item& it, const volatile uint32_t* marks, int32_t pos,
+                                              int32_t head, float mc, uint16_t* dst) {
   const float c = a.softmax_scale * kLog2e;
+  const int32_t rel = pos - it.pos0;
   const uint16_t* q = a.q + ((int64_t)it.start + pos) * a.ldq + (int64_t)head * D;
+  asm volatile("" ::: "memory");  // the row's stores, of other types, come first
 #pragma unroll 1
-  for (int d0 = 0; d0 < D; d0 += 8) {
-    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (int32_t w = 0; w <= rel >> 5; ++w) {
+    uint32_t m = marks[w];
+    if (w == rel >> 5) m &= (2u << (rel & 31)) - 1u;
 #pragma unroll 1
-    for (int32_t j = 0; j <= pos; ++j) {
-      const uint16_t* k = a.k + ((int64_t)it.start + j) * a.ldk + (int64_t)it.kvh * D;
+    for (; m; m &= m - 1u) {
+      const int64_t token = (int64_t)it.start + it.pos0 + 32 * w + __ffs(m) - 1;
+      const uint16_t* k = a.k + token * a.ldk + (int64_t)it.kvh * D;
+      const uint16_t* v = a.v + token * a.ldv + (int64_t)it.kvh * D;
       float s = 0.0f;
 #pragma unroll 1
       for (int d = 0; d < D; d += 2) {
@@ -288,16 +306,10 @@ __device__ __forceinline__ void take_again(const ApArgs& a, const Item& it, int3
         s = fmaf(bf16_hi(x), bf16_hi(y), fmaf(bf16_lo(x), bf16_lo(y), s));
       }
       const float p = ex2(fmaf(s, c, -mc));
-      const uint4 v = *reinterpret_cast<const uint4*>(a.v + ((int64_t)it.start + j) * a.ldv + (int64_t)it.kvh * D + d0);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[2 * e] = fmaf(p, bf16_lo(w[e]), acc[2 * e]);
-        acc[2 * e + 1] = fmaf(p, bf16_hi(w[e]), acc[2 * e + 1]);
-      }
+#pragma unroll 1
+      for (int d = 0; d < D; ++d)
+        if (non_finite(v[d])) dst[d] = (uint16_t)bf16x2_rn(fmaf(p, bf16_lo(v[d]), bf16_lo(dst[d])), 0.0f);
     }
-    *reinterpret_cast<uint4*>(dst + d0) = make_uint4(bf16x2_rn(acc[0] * inv, acc[1] * inv), bf16x2_rn(acc[2] * inv, acc[3] * inv),
-                                                     bf16x2_rn(acc[4] * inv, acc[5] * inv), bf16x2_rn(acc[6] * inv, acc[7] * inv));
   }
 }
 
@@ -326,7 +338,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
   uint64_t* item_empty = item_full + kApItems;  // every reader has copied it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_empty + kApItems);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  volatile int* flags = abort_flag + 1;     // per item slot: values that its masks cannot cancel
+  uint32_t* marks = reinterpret_cast<uint32_t*>(base_ptr + C::kMarks);  // [item slot][kApMarks]
   volatile int* abortv = abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -583,18 +595,19 @@ __global__ void __launch_bounds__(kApThreads, 1)
       // A probability of 0 does not cancel a NaN or an infinity.  In the key
       // tiles that an item does not see whole, the value rows past its last
       // position (later ones, or another sequence's) are zeroed before they are
-      // multiplied; those from its first position on, which some of its rows see
-      // and some do not, are looked through, and if one is not finite the output
-      // warps take the item's rows again without the tensor cores.  Every tile
-      // passes here and is held until it has: no phase of the ring is missed,
-      // and none is signalled twice before the MMA thread has seen it.
+      // multiplied; in those from its first position on, which some of its rows see
+      // and some do not, non-finite values are zeroed and their positions marked
+      // for the output warps.  Every tile passes here and is held until it has: no
+      // phase of the ring is missed, and none is signalled twice before the MMA
+      // thread has seen it.  (An item's marks are written when its own tile is
+      // mended, so never while the item four before it is still being stored: the
+      // queries between them wait for its outputs.)
       uint32_t stage = 0, parity = 0;
       bool alive = true;
       Item it;
       for (uint32_t i = 0; alive && take_warp(i, it);) {
         const int32_t n = max(it.n0, it.n1);
         const int32_t end = min(it.len, it.pos0 + 2 * (kApTile / a.pack));
-        uint32_t worst = 0;  // packed magnitudes
         for (int32_t t = 0; t < 2 * n; ++t) {
           alive = __all_sync(0xffffffffu, wait_for(smem_u32(&kv_full[stage]), parity, abortv));
           if (!alive) break;
@@ -602,6 +615,10 @@ __global__ void __launch_bounds__(kApThreads, 1)
           if ((t & 1) && k0 + kApTile > it.pos0) {
             uint8_t* tile = base_ptr + C::kRing + stage * C::kTileBytes;
             const int32_t r0 = max(it.pos0 - k0, 0), r1 = min(end - k0, kApTile);
+            // the tile's own words: an item has 256 positions in two tiles, or fewer in one
+            uint32_t* words = marks + ((i - 1) % kApItems) * kApMarks;
+            if (lane < kApMarks / 2) words[(k0 > it.pos0 ? kApMarks / 2 : 0) + lane] = 0u;
+            uint32_t worst = 0;  // packed magnitudes
             for (int32_t e = r0 * 8 + lane; e < kApTile * 8; e += 32)
 #pragma unroll
               for (int h = 0; h < C::kHalves; ++h) {
@@ -609,8 +626,20 @@ __global__ void __launch_bounds__(kApThreads, 1)
                 if (e < r1 * 8) worst = absmax_u4(worst, *p);
                 else *p = make_uint4(0u, 0u, 0u, 0u);
               }
-            const bool bad = __any_sync(0xffffffffu, max(worst & 0xFFFFu, worst >> 16) >= 0x7F80u);
-            if (lane == 0) flags[(i - 1) % kApItems] = bad;
+            if (__any_sync(0xffffffffu, max(worst & 0xFFFFu, worst >> 16) >= 0x7F80u)) {
+              __syncwarp();
+#pragma unroll 1
+              for (int32_t e = r0 * 8 + lane; e < r1 * 8; e += 32)
+#pragma unroll 1
+                for (int h = 0; h < 4 * C::kHalves; ++h) {
+                  uint32_t* p = reinterpret_cast<uint32_t*>(tile + (h >> 2) * C::kHalfBytes + e * 16) + (h & 3);
+                  const uint32_t keep = (non_finite(*p) ? 0u : 0xFFFFu) | (non_finite(*p >> 16) ? 0u : 0xFFFF0000u);
+                  if (keep == 0xFFFFFFFFu) continue;
+                  *p &= keep;
+                  const int32_t rel = k0 + (e >> 3) - it.pos0;
+                  atomicOr(&words[rel >> 5], 1u << (rel & 31));
+                }
+            }
             fence_proxy_async_shared();
           }
           __syncwarp();
@@ -762,12 +791,9 @@ __global__ void __launch_bounds__(kApThreads, 1)
         const int64_t token = (int64_t)it.start + pos;
         const bool store = pos < it.len && dcheck(token < a.total, a.err);
         uint16_t* dst = a.out + token * a.ldo + (int64_t)head * D;
-        if (flags[(i - 1) % kApItems]) {
-          take_again<D>(a, it, pos, head, store, ml.x, inv, dst);
-          mbar_arrive(smem_u32(&o_empty[x]));
-          if (store && a.lse) a.lse[token * a.hq + head] = fmaf(ml.x, kLn2, logf(ml.y));
-          continue;
-        }
+        // (the second words are those of an item's second 128 positions: the second tile's)
+        const uint32_t* words = marks + ((i - 1) % kApItems) * kApMarks;
+        const bool taken_out = any_marks(smem_u32(words)) || (x == 1 && a.pack == 1 && any_marks(smem_u32(words + kApMarks / 2)));
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
           uint32_t o[32];
@@ -796,6 +822,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
           }
         }
         if (store && a.lse) a.lse[token * a.hq + head] = fmaf(ml.x, kLn2, logf(ml.y));
+        if (store && taken_out) add_taken_out<D>(a, it, words, pos, head, ml.x, dst);
       }
     }
   }

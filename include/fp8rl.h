@@ -610,9 +610,7 @@ FP8RL_API fp8rl_status fp8rl_rmsnorm_quant(const void* x_bf16, int64_t ldx, cons
  * Tokens of no sequence are not written.  Scores, statistics and sums are
  * fp32, the probabilities are rounded to bf16 for the second product, the
  * output once to bf16.  An output depends on its own sequence's positions up
- * to its own alone, whatever the others hold (NaN and infinities included; rows
- * whose last key tiles hold a non-finite value are computed by plain fp32
- * arithmetic, slowly).
+ * to its own alone, whatever the others hold (NaN and infinities included).
  * The same bits on every run.
  * Errors: INVALID_ARG (null pointers, negative sizes, short strides, q_heads not a multiple of
  *         kv_heads, softmax_scale not positive and finite, plan too small), SHAPE (head_dim other
