@@ -698,7 +698,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
         };
         // P of a quarter into TMEM, and its sum into l2
         auto exponentials = [&](int q) {
-          const uint64_t nm2 = f32x2(-mc, -mc);
+          const float ref = mc == -INFINITY ? 0.0f : mc;  // scores of -inf alone so far: p = 0
+          const uint64_t nm2 = f32x2(-ref, -ref);
           uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {

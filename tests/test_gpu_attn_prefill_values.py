@@ -93,3 +93,32 @@ def test_all_values_of_the_last_positions(hq, hkv, d):
     want, want_lse = fp8rl.attn_prefill(q, k, v, plan)
     assert torch.equal(out[:n - bad], want[:n - bad]) and torch.equal(lse, want_lse)
     assert bool(out[n - bad:].isnan().all())
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+@pytest.mark.parametrize("masked", [1, 127, 128, 129, 300])
+def test_scores_of_minus_infinity(hq, hkv, d, masked):
+    """Keys whose scores are -inf for every query have probability 0, whole key
+    tiles of them at a prompt's start too; a row of them alone is NaN, as the
+    formula's 0 / 0."""
+    n = 500
+    q, k, v, plan = make([n], hq, hkv, d, seed=masked)
+    q, k = q.contiguous(), k.contiguous()
+    q[:, :, 0] = q[:, :, 0].abs().clamp(min=0.25)
+    k[:masked, :, 0] = -math.inf
+    out, lse = fp8rl.attn_prefill(q, k, v, plan)
+    assert fp8rl.fp8rl_sync_status() == 0
+    assert bool(out[:masked].isnan().all())
+    later = torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1)
+    for h in range(0, hq, max(1, hq // 3)):
+        kh = h // (hq // hkv)
+        s = (q[:, h].double() @ k[:, kh].double().T * d ** -0.5).masked_fill(later, -math.inf)[masked:]
+        assert bool((s[:, :masked] == -math.inf).all())
+        z = torch.logsumexp(s, 1)
+        p = torch.exp(s - z[:, None])
+        ref = p @ v[:, kh].double()
+        size = (q[masked:, h].double().abs() @ k[masked:, kh].double().abs().T * d ** -0.5).masked_fill(later[masked:, masked:], 0)
+        eps = size.amax(1) * (2.0 ** -19 + 2.0 ** -21 + 2.0 ** -22)
+        tol = (2.0 ** -8 + 2.0 ** -10 + 4 * eps)[:, None] * (p @ v[:, kh].double().abs()) + ref.abs() * 2.0 ** -8
+        assert bool(((out[masked:, h].double() - ref).abs() <= tol).all())
+        assert bool(((lse[masked:, h].double() - z).abs() <= 4 * eps + 2.0 ** -19 + z.abs() * 2.0 ** -22).all())
