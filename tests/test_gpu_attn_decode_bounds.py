@@ -97,3 +97,20 @@ def test_many_small_beside_a_large_one_of_each_warp(gap, at, hq, hkv, d):
     k[sinks], v[sinks] = 8.0, 0.0
     q = torch.ones(batch, hq, d, device="cuda").bfloat16()
     check(q, [(codes(k), codes(v))] * batch, torch.tensor([1.0, 1.0], device="cuda"), [n] * batch, gap / (d * 47 / 12), shared=True)
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", [([100000, 200], 8, 1, 64), ([70001], 4, 1, 128), ([50000], 32, 4, 64), ([9000], 40, 4, 128),
+                                           ([30000, 5, 20000], 12, 2, 64), ([60000], 16, 1, 128), ([40000], 3, 3, 64), ([7000], 8, 1, 128),
+                                           ([2500, 800, 1300] * 60, 32, 8, 128), ([3000] * 310, 8, 4, 128)])
+def test_every_part_of_a_cache_counts_once(lens, hq, hkv, d):
+    """Column d of the values is 1 in a range of the keys of its own and 0 outside,
+    so the output is the ranges' shares of the probability: a partial that is left
+    out, counted twice or scaled wrongly changes a column by far more than its bound."""
+    g = torch.Generator("cuda").manual_seed(sum(lens) + hq)
+    kv = []
+    for n in lens:
+        k = codes(torch.randn(n, hkv, d, generator=g, device="cuda") * 80)
+        v = torch.nn.functional.one_hot(torch.arange(n, device="cuda") * d // n, d).float()
+        kv.append((k, (v[:, None] * torch.arange(1, hkv + 1, device="cuda")[:, None]).to(E4M3)))
+    q = (torch.randn(len(lens), hq, d, generator=g, device="cuda") * 0.5).bfloat16()
+    check(q, kv, torch.tensor([0.0121, 1.0], device="cuda"), lens, d ** -0.5, seed=hq)
