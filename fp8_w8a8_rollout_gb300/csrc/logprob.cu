@@ -76,12 +76,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // Masked logits.  An exponent of -inf would meet e = 0 in a product, so
 // elements below kFloor are read as kFloor: beside a maximum within
-// +-kFloor / 2 and with log2(e) / T at most kMaxScale their e is 0 all the same,
-// and every exponent is finite.  Rows outside these limits take exponents one
-// by one, clamped.  (-1e30 rounded to bf16, so that both types clamp alike.)
-constexpr float kFloor = -0x1.94p+99f, kMaxScale = 1e6f;
+// +-kFloor / 2 and with log2(e) / T within kMinScale and kMaxScale their e is 0
+// all the same (their exponents are below -600), and every exponent is finite.
+// Rows outside these limits take exponents one by one, clamped.  (-1e30 rounded to
+// bf16, so that both types clamp alike.)
+constexpr float kFloor = -0x1.94p+99f, kMinScale = 1e-27f, kMaxScale = 1e6f;
 constexpr uint32_t kFloorBf16x2 = 0xF14AF14Au;
-__device__ __forceinline__ bool within_floor(float m, float c) { return fabsf(m) <= -0.5f * kFloor && c <= kMaxScale; }
+__device__ __forceinline__ bool within_floor(float m, float c) { return fabsf(m) <= -0.5f * kFloor && c >= kMinScale && c <= kMaxScale; }
 
 // A row's 16-byte pieces, counted from the 16-byte boundary at or below its
 // first element: piece p holds elements [p * N - off, (p + 1) * N - off).
