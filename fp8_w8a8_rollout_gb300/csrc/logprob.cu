@@ -545,7 +545,8 @@ struct GradRow {
 // dx of element j with value v
 __device__ __forceinline__ float grad_of(const GradRow& q, float v, int32_t j) {
   const float y = max_nan(fmaf(v - q.m, q.c, -q.l2), kTinyExp2);  // log2 p
-  const float d = ex2(y) * fmaf(q.b, y, q.a);
+  const float p = ex2(y), f = fmaf(q.b, y, q.a);
+  const float d = p == 0.0f && fabsf(f) == INFINITY ? 0.0f : p * f;
   return j == q.t ? d + q.top : d;
 }
 
@@ -599,7 +600,10 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const LpGrad
     return;
   }
   const Row<In> row(x, a.vocab);
-  const bool plain = !q.zero && within_floor(q.m, q.c);
+  // elements that are read as kFloor: p = 0 beside exponents y of up to `reach`, and
+  // a + b y has to be finite for their product to be 0
+  const float reach = fmaf(-1.5f * kFloor, q.c, fabsf(q.l2));
+  const bool plain = !q.zero && within_floor(q.m, q.c) && fmaf(fabsf(q.b), reach, fabsf(q.a)) < 0.5f * FLT_MAX;
   const uint64_t nm2 = pair_of(-q.m, -q.m), c2 = pair_of(q.c, q.c), nl2 = pair_of(-q.l2, -q.l2), a2 = pair_of(q.a, q.a),
                  b2 = pair_of(q.b, q.b);
   for (int32_t p = first; p < row.pieces; p += U * stride) {

@@ -703,7 +703,8 @@ FP8RL_API fp8rl_status fp8rl_logprob(const void* d_logits, int32_t logits_fp32, 
  *   d_grad_entropy      device, fp32 [rows], or null
  *   d_dlogits           device, [rows][vocab] of the logits' type, row stride ldd; may be d_logits
  *                       itself (with ldd = ld), no other overlap
- * Rows without a token and rows of -inf alone get zeros.  Errors: as fp8rl_logprob.
+ * Rows without a token and rows of -inf alone get zeros; so do elements with p_j below 2^-126.
+ * Errors: as fp8rl_logprob.
  */
 FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, int32_t logits_fp32, int64_t rows, int64_t vocab,
                                               int64_t ld, float temperature, const int32_t* d_tokens,

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fp8_w8a8_rollout_gb300 as fp8rl
-from test_gpu_logprob import check, grad64
+from test_gpu_logprob import check, forward64, grad64
 
 pytestmark = pytest.mark.gpu
 
@@ -49,5 +49,26 @@ def test_high_temperatures_keep_masked_logits_out(rows, vocab, temperature, pad,
         g = torch.full((rows,), temperature, device="cuda").clamp(max=1e30)
         got = fp8rl.logprobs_backward(x, t, stats, ent, g, g, temperature=temperature)
         d, tol = grad64(x, t, g, g, temperature)
+        assert bool(((got.double() - d).abs() <= tol).all())
+        assert bool((got[x == -math.inf] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad,offset", LAYOUTS)
+@pytest.mark.parametrize("temperature", [1e-1, 1e-3, 1e-4, 1e-5, 2e-6, 1e-6])
+@pytest.mark.parametrize("gh", [0.01, -1.0, 300.0, 1e6])
+def test_gradient_of_masked_logits_at_low_temperatures(gh, temperature, pad, offset, dtype):
+    """The entropy's gradient has a factor 1 / T beside exponents of its own 1 / T."""
+    rows, vocab = 4, 5003
+    for spread in (2.0, 3 * temperature):
+        x, t = make(rows, vocab, dtype, spread, seed=5, pad=pad, offset=offset)
+        _, ent, stats = check(x, t, temperature=temperature)
+        g = torch.tensor([1.0, -0.5, 0.0, 2.0], device="cuda")
+        gg = torch.full((rows,), gh, device="cuda")
+        got = fp8rl.logprobs_backward(x, t, stats, ent, g, gg, temperature=temperature)
+        d, tol = grad64(x, t, g, gg, temperature)
+        # exponentials below 2^-126 are flushed: such an element is its value, or 0
+        tol += torch.where(forward64(x, t, temperature)[1] < 2.0 ** -125, d.abs(), 0.0)
+        assert not bool(got.isnan().any())
         assert bool(((got.double() - d).abs() <= tol).all())
         assert bool((got[x == -math.inf] == 0).all())
