@@ -82,6 +82,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // bf16, so that both types clamp alike.)
 constexpr float kFloor = -0x1.94p+99f, kMinScale = 1e-27f, kMaxScale = 1e6f;
 constexpr uint32_t kFloorBf16x2 = 0xF14AF14Au;
+// log2(e) / T, finite for the smallest T too (0 times it is 0)
+__device__ __forceinline__ float exp2_scale(float temperature) { return fminf(kLog2e / temperature, FLT_MAX); }
 __device__ __forceinline__ bool within_floor(float m, float c) { return fabsf(m) <= -0.5f * kFloor && c >= kMinScale && c <= kMaxScale; }
 
 // A row's 16-byte pieces, counted from the 16-byte boundary at or below its
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(T) logprob_kernel(const LpArgs a) {
   const Row<In> row(xr, a.vocab);
   const int32_t share = (row.pieces + ranks - 1) / ranks;
   const int32_t p0 = rank * share, p1 = min(row.pieces, p0 + share);
-  const float c = kLog2e / a.temperature;
+  const float c = exp2_scale(a.temperature);
   float xt = 0.0f;  // needed at the end, requested now
   if (tid == 0 && rank == 0) {
     if (sizeof(In) == 2) xt = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(xr)[t]);
@@ -582,12 +584,13 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const LpGrad
   // no token, or a row of -inf alone (a NaN beside them left its mark in st.y)
   q.zero = q.t < 0 || q.t >= a.vocab || (st.x == -INFINITY && st.y == -INFINITY);
   q.m = st.x;
-  q.c = kLog2e / a.temperature;
+  q.c = exp2_scale(a.temperature);
   q.l2 = st.y * kLog2e;
   const float g = a.g_lp[r], gh = a.g_ent ? a.g_ent[r] : 0.0f, inv_t = 1.0f / a.temperature;
-  q.a = -(a.g_ent ? fmaf(gh, a.entropy[r], g) : g) * inv_t;
-  q.b = -gh * kLn2 * inv_t;
-  q.top = g * inv_t;
+  auto over_t = [&](float v) { return inv_t <= FLT_MAX ? v * inv_t : v / a.temperature; };
+  q.a = over_t(-(a.g_ent ? fmaf(gh, a.entropy[r], g) : g));
+  q.b = over_t(-gh * kLn2);
+  q.top = over_t(g);
   const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
   const int32_t stride = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + threadIdx.x;
   if (!same) {  // rows that start at different places of a 16-byte piece: element by element

@@ -72,3 +72,28 @@ def test_gradient_of_masked_logits_at_low_temperatures(gh, temperature, pad, off
         assert not bool(got.isnan().any())
         assert bool(((got.double() - d).abs() <= tol).all())
         assert bool((got[x == -math.inf] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("temperature", [1e-39, 2.5e-39, 4e-39, 8e-39])
+def test_temperatures_whose_inverse_overflows(temperature, dtype):
+    """The largest logits share the probability, the others have none."""
+    x = torch.full((3, 1001), -1.0, dtype=dtype, device="cuda")
+    x[:, 500:] = -math.inf
+    x[0, 7], x[1, 100:104], x[2, ::100] = 2.0, 0.0, 1.0
+    most = torch.tensor([1.0, 4.0, 11.0], device="cuda", dtype=torch.float64)
+    t = torch.tensor([7, 103, 900], dtype=torch.int32, device="cuda")
+    lp, ent, stats, ids, top_lp = fp8rl.logprobs(x, t, temperature=temperature, topk=2)
+    assert fp8rl.fp8rl_sync_status() == 0
+    assert bool(((lp.double() + most.log()).abs() <= 2.0 ** -21).all()) and bool(((ent.double() - most.log()).abs() <= 2.0 ** -21).all())
+    assert ids.tolist() == [[7, 0], [100, 101], [0, 100]] and top_lp[0].tolist() == [0.0, -math.inf]
+    # g / T within fp32 (about 1e33); with no gradient for the entropy: its factor log p is that of the shares alone
+    g = torch.tensor([1.0, 0.0, 1.0], device="cuda") * 1e33 * torch.tensor(temperature, dtype=torch.float64).item()
+    got = fp8rl.logprobs_backward(x, t, stats, ent, g, g, temperature=temperature).double()
+    p = (x == x.amax(1, keepdim=True)).double() / most[:, None]
+    pick = torch.zeros_like(p).scatter_(1, t.long()[:, None], 1.0)
+    want = g.double()[:, None] * (pick - p) / torch.tensor(temperature, dtype=torch.float32).double().item()
+    # the entropy's own gradient is 0 in exact arithmetic: -p (log p + H) with equal shares
+    size = g.double()[:, None] / torch.tensor(temperature, dtype=torch.float32).double().item()
+    out = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -20
+    assert bool(((got - want).abs() <= want.abs() * out + size * p * 2.0 ** -17 + size * pick * 2.0 ** -17).all())
