@@ -149,7 +149,8 @@ def decode(cfg: Config, weights, q8, tokens, lens, cache: Cache):
 
 
 def train_logits(cfg: Config, weights, tokens, cu, pos):
-    """The training policy's logits (bf16 linears) of packed sequences."""
+    """The training policy's logits (bf16 linears) of packed sequences, for scoring:
+    the attention has no backward pass, so gradients end at these logits."""
     plan = fp8rl.attn_prefill_plan(cu, tokens.numel(), cfg.q_heads, cfg.kv_heads)
 
     def norm(x, w):

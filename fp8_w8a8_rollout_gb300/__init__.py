@@ -768,11 +768,33 @@ def tis_weights(lp_train: torch.Tensor, lp_rollout: torch.Tensor, mask: torch.Te
     return w, kl
 
 
+class _NoBackward(torch.autograd.Function):
+    """Outputs of a call without a backward pass, tied to the inputs that require a
+    gradient: a backward pass that reaches them ends in an error instead of in
+    gradients that miss the call."""
+
+    @staticmethod
+    def forward(ctx, name, outputs, *inputs):
+        ctx.name = name
+        return tuple(t.detach() for t in outputs)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} has no backward pass; call it under torch.no_grad() or on detached tensors")
+
+
+def _no_backward(name, outputs, *inputs):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        return _NoBackward.apply(name, tuple(outputs), *inputs)
+    return outputs
+
+
 def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
                   fmt=SCALE_FP32, out=None, stream=None):
     """(q uint8 [m, k], scale [ceil(k/128), m], h bf16 [m, k]): the RMS norm of
     h = x + residual times weight, quantised 1x128; h is None without a
-    residual.  `out` is such a triple (its h may be the residual itself)."""
+    residual.  `out` is such a triple (its h may be the residual itself).  No
+    backward pass: one that reaches h raises."""
     _check_cuda(x, weight, residual, *(out or ()))
     _check_bf16_2d(x, "x")
     m, k = x.shape
@@ -795,6 +817,8 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
         ldq, ldh = _ld(q, m, k), 0 if h is None else _ld(h, m, k)
     fp8rl_rmsnorm_quant(x.data_ptr(), _ld(x, m, k), residual, 0 if residual is None else _ld(residual, m, k),
                         weight.data_ptr(), eps, m, k, h, ldh, q.data_ptr(), ldq, s.data_ptr(), fmt, stream)
+    if h is not None:
+        h, = _no_backward("rmsnorm_quant", (h,), x, weight, residual)
     return q, s, h
 
 
@@ -853,7 +877,8 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPl
     """(out bf16 [tokens, q_heads, d], lse fp32 [tokens, q_heads]): causal
     attention over packed prompts (q [tokens, q_heads, d], k and v [tokens,
     kv_heads, d]; column ranges of one projection's output are fine).
-    softmax_scale defaults to d ** -0.5."""
+    softmax_scale defaults to d ** -0.5.  No backward pass: one that reaches the
+    outputs raises."""
     _check_cuda(q, k, v, plan.data, *(out or ()))
     for name, t in (("q", q), ("k", k), ("v", v)):
         _check_heads(t, name)
@@ -872,7 +897,7 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPl
                        _ld(v, tokens, hkv * d), plan.data.data_ptr(), plan.data.numel(), plan.batch, tokens, hq, hkv, d,
                        d ** -0.5 if softmax_scale is None else softmax_scale, out[0].data_ptr(), hq * d,
                        out[1].data_ptr(), stream)
-    return out
+    return _no_backward("attn_prefill", out, q, k, v)
 
 
 def attn_decode_workspace(q_heads: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
@@ -893,7 +918,8 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     ([num_slots, kv_heads * d] uint8, as kv_append writes them), the pages of
     sequence b in block_table[b] (int32 [batch, max_blocks]), its number of
     keys in lens[b] (int32).  softmax_scale defaults to d ** -0.5; keep one
-    workspace per stream (attn_decode_workspace) rather than one per call."""
+    workspace per stream (attn_decode_workspace) rather than one per call.  No
+    backward pass: one that reaches the outputs raises."""
     _check_cuda(q, k_cache, v_cache, block_table, lens, scales, workspace, *(out or ()))
     _check_heads(q, "q")
     batch, hq, d = q.shape
@@ -923,7 +949,7 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
                       slots, block_table.data_ptr(), _ld(block_table, batch, blocks), blocks, block_size, lens.data_ptr(),
                       scales.data_ptr(), d ** -0.5 if softmax_scale is None else softmax_scale, out[0].data_ptr(), hq * d,
                       out[1].data_ptr(), workspace.data_ptr(), workspace.nbytes, stream)
-    return out
+    return _no_backward("attn_decode", out, q)
 
 
 def _check_logits(logits: torch.Tensor, tokens: torch.Tensor):
@@ -938,7 +964,40 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.
     int32 [rows, topk], top_lp fp32 [rows, topk]) of logits (bf16 or fp32
     [rows, vocab]) at a temperature; the last two are None with topk = 0.
     Rows whose token is outside the vocabulary (-1: padding) give zeros and
-    ids -1.  stats is for logprobs_backward; lp goes to tis_weights."""
+    ids -1.  stats is for logprobs_backward; lp goes to tis_weights.  With logits
+    that require a gradient, lp and entropy have theirs (logprobs_backward, on the
+    current stream of the backward pass); one that comes from stats or top_lp raises."""
+    if torch.is_grad_enabled() and logits.requires_grad:
+        return _LogProbs.apply(logits, tokens, temperature, topk, out, stream)
+    return _logprobs(logits, tokens, temperature, topk, out, stream)
+
+
+class _LogProbs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, temperature, topk, out, stream):
+        lp, entropy, stats, ids, top_lp = (None if t is None else t.detach()
+                                           for t in _logprobs(logits, tokens, temperature, topk, out, stream))
+        ctx.save_for_backward(logits, tokens, stats, entropy)
+        ctx.temperature = temperature
+        ctx.set_materialize_grads(False)
+        if ids is not None:
+            ctx.mark_non_differentiable(ids)
+        return lp, entropy, stats, ids, top_lp
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_lp, grad_entropy, grad_stats, _, grad_top_lp):
+        if grad_stats is not None or grad_top_lp is not None:
+            raise RuntimeError("logprobs has a backward pass from lp and entropy, not from stats or top_lp")
+        if grad_lp is None and grad_entropy is None:
+            return (None,) * 6
+        logits, tokens, stats, entropy = ctx.saved_tensors
+        grad_lp = torch.zeros_like(entropy) if grad_lp is None else grad_lp.contiguous()
+        grad_entropy = None if grad_entropy is None else grad_entropy.contiguous()
+        return (logprobs_backward(logits, tokens, stats, entropy, grad_lp, grad_entropy, ctx.temperature), *(None,) * 5)
+
+
+def _logprobs(logits, tokens, temperature, topk, out, stream):
     _check_cuda(logits, tokens, *(out or ()))
     _check_logits(logits, tokens)
     rows, vocab = logits.shape
