@@ -83,8 +83,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 constexpr float kFloor = -0x1.94p+99f, kMinScale = 1e-27f, kMaxScale = 1e6f;
 constexpr uint32_t kFloorBf16x2 = 0xF14AF14Au;
 // log2(e) / T, finite for the smallest T too (0 times it is 0)
-__device__ __forceinline__ float exp2_scale(float temperature) { return fminf(kLog2e / temperature, FLT_MAX); }
-__device__ __forceinline__ bool within_floor(float m, float c) { return fabsf(m) <= -0.5f * kFloor && c >= kMinScale && c <= kMaxScale; }
+__host__ __device__ __forceinline__ float exp2_scale(float temperature) { return fminf(kLog2e / temperature, FLT_MAX); }
+// the largest |m| for which exponents with scale c need no care (negative: none); from
+// the host: tested beside c in the loop it costs the fp32 kernel with alternatives a
+// sixth of its resident CTAs (4096 x 32000, top 20: 113 us; 107 so)
+__host__ __device__ __forceinline__ float floor_limit(float c) { return c >= kMinScale && c <= kMaxScale ? -0.5f * kFloor : -1.0f; }
 
 // A row's 16-byte pieces, counted from the 16-byte boundary at or below its
 // first element: piece p holds elements [p * N - off, (p + 1) * N - off).
@@ -314,7 +317,7 @@ struct LpArgs {
   float* top_lp;
   int64_t ld;
   int32_t vocab, top;
-  float temperature;
+  float temperature, limit;
 };
 
 // grid (cluster, rows), clusters of gridDim.x CTAs: a CTA takes the pieces
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(T) logprob_kernel(const LpArgs a) {
       fold();
       move_to(st, big, c);
     }
-    if (within_floor(st.m, c)) {
+    if (fabsf(st.m) <= a.limit) {
       const uint64_t nm2 = pair_of(-st.m, -st.m);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
@@ -533,7 +536,7 @@ struct LpGradArgs {
   const float* g_ent;  // or null
   int64_t ldx, ldd;
   int32_t vocab;
-  float temperature;
+  float temperature, limit;
 };
 
 // dx_j = p (a + b log2 p) with a = -(g + g_H H) / T and b = -g_H ln 2 / T;
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const LpGrad
   // elements that are read as kFloor: p = 0 beside exponents y of up to `reach`, and
   // a + b y has to be finite for their product to be 0
   const float reach = fmaf(-1.5f * kFloor, q.c, fabsf(q.l2));
-  const bool plain = !q.zero && within_floor(q.m, q.c) && fmaf(fabsf(q.b), reach, fabsf(q.a)) < 0.5f * FLT_MAX;
+  const bool plain = !q.zero && fabsf(q.m) <= a.limit && fmaf(fabsf(q.b), reach, fabsf(q.a)) < 0.5f * FLT_MAX;
   const uint64_t nm2 = pair_of(-q.m, -q.m), c2 = pair_of(q.c, q.c), nl2 = pair_of(-q.l2, -q.l2), a2 = pair_of(q.a, q.a),
                  b2 = pair_of(q.b, q.b);
   for (int32_t p = first; p < row.pieces; p += U * stride) {
@@ -743,6 +746,7 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob(const void* d_logits, int32_t lo
     a.vocab = (int32_t)vocab;
     a.top = (int32_t)topk;
     a.temperature = temperature;
+    a.limit = floor_limit(exp2_scale(temperature));
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const cudaError_t e = logits_fp32 ? (topk ? launch_rows<float, true>(a, n, cs) : launch_rows<float, false>(a, n, cs))
                                       : (topk ? launch_rows<uint16_t, true>(a, n, cs) : launch_rows<uint16_t, false>(a, n, cs));
@@ -787,6 +791,7 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, i
     a.ldd = ldd;
     a.vocab = (int32_t)vocab;
     a.temperature = temperature;
+    a.limit = floor_limit(exp2_scale(temperature));
     // Small CTAs, so that many rows are under way (8192 x 1000 fp32: 9.3 us with 64
     // threads, 11 with 128, 16 with 256; 8192 x 4000 43, 41 and 43).  A load round is
     // four pieces a thread.  CTAs of up to five rounds once that leaves many times
