@@ -113,6 +113,8 @@ struct AdArgs {
   uint32_t ldc16;  // cache row stride in units of 16 bytes
   int32_t batch, hq, hkv, group, sub, page, page_shift, max_len;
   float softmax_scale;
+  int64_t n_tickets, n_parts;  // the workspace's counters and floats
+  uint32_t* err;               // debug builds' store checks
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -232,6 +234,7 @@ __device__ __forceinline__ void add_scaled(float4& a, float f, float4 v) {
 
 // outputs d .. d + 3 of a head from its sums; a head without keys gives zeros
 __device__ __forceinline__ void finish(const AdArgs& a, int b, int h, int D, int d, float4 acc, float l, float m, float sv) {
+  if (!dcheck(b < a.batch && h >= 0 && h < a.hq && d + 4 <= D, a.err)) return;
   const float f = l == 0.0f ? 0.0f : sv / l;
   *reinterpret_cast<uint2*>(a.out + b * a.ldo + (int64_t)h * D + d) = make_uint2(bf16x2_rn(acc.x * f, acc.y * f), bf16x2_rn(acc.z * f, acc.w * f));
   if (a.lse && d == 0) a.lse[(int64_t)b * a.hq + h] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
@@ -281,7 +284,8 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
   // sequences without keys: zeros, spread over the CTAs
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;
-    for (int i = tid; i < a.hq * H; i += kAdThreads) a.out[b * a.ldo + i] = 0;
+    for (int i = tid; i < a.hq * H; i += kAdThreads)
+      if (dcheck(i < a.ldo, a.err)) a.out[b * a.ldo + i] = 0;
     if (a.lse)
       for (int i = tid; i < a.hq; i += kAdThreads) a.lse[(int64_t)b * a.hq + i] = -INFINITY;
   }
@@ -585,6 +589,7 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
         finish(a, b, h_item + wi * P * a.group + h, H, d, acc, ll, mm, sv);
       } else {
         float* to = part + wi * F::kPart;
+        if (!dcheck(to >= a.parts && to + F::kPart <= a.parts + a.n_parts && h >= 0 && h < 8 * NT, a.err)) continue;
         *reinterpret_cast<float4*>(to + h * H + d) = acc;
         if (d == 0) {
           to[8 * NT * H + h] = mm;
@@ -616,7 +621,8 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
       for (;;) {
         __threadfence();
         __syncthreads();
-        if (tid == 0) {
+        if (tid == 0 && !dcheck(ticket >= a.tickets && ticket < a.tickets + a.n_tickets, a.err)) last = 0;
+        else if (tid == 0) {
           last = count == 1 || atomicAdd(ticket, 1u) == (uint32_t)(count - 1);
           if (last) *ticket = 0u;  // ready for the next call
         }
@@ -680,6 +686,7 @@ __global__ void __launch_bounds__(kAdThreads, F::kCtas) attn_decode_kernel(const
               finish(a, b, h_item + wi * P * a.group + h, H, d, acc, head_l[slot], head_m[slot], sv);
             } else {
               float* to = part_of(from) + wi * F::kPart;
+              if (!dcheck(to >= a.parts && to + F::kPart <= a.parts + a.n_parts && h >= 0 && h < 8 * NT, a.err)) continue;
               *reinterpret_cast<float4*>(to + h * H + d) = acc;
               if (d == 0) {
                 to[8 * NT * H + h] = head_m[slot];
@@ -737,15 +744,22 @@ auto with_form(int64_t batch, int64_t kv_heads, int64_t group, int64_t head_dim,
 // The workspace starts with the items' counters: an area of one size for every
 // shape, so that one workspace can serve several (partials never land on counters).
 constexpr int kAdMaxCtas = 4;
-int64_t ticket_bytes() { return ((int64_t)sm_count() * kAdMaxCtas * 3 * 4 + 255) / 256 * 256; }
+int64_t ticket_count() { return (int64_t)sm_count() * kAdMaxCtas * 3; }
+int64_t ticket_bytes() { return (ticket_count() * 4 + 255) / 256 * 256; }
 
 template <class F>
-cudaError_t launch_decode(AdArgs a, void* workspace, cudaStream_t stream) {
+cudaError_t launch_decode(AdArgs a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   a.hkv /= F::P;
   a.sub = (F::P * a.group + 8 * F::NT - 1) / (8 * F::NT);
   static_assert(F::kCtas <= kAdMaxCtas);
   a.tickets = static_cast<uint32_t*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes());
+  a.n_tickets = ticket_count();
+  a.n_parts = ((int64_t)workspace_bytes - ticket_bytes()) / 4;
+#ifdef FP8RL_DEBUG  // only the store checks look at it
+  a.err = device_error_word();
+  if (!a.err) return cudaErrorUnknown;
+#endif
   const size_t smem = ad_smem<F>() + ((size_t)a.batch + 1) * 8;
   // the attribute lives in the context: set once per device and context, for the largest batch
   static std::atomic<uint64_t> ready[64];
@@ -830,7 +844,7 @@ extern "C" FP8RL_API fp8rl_status fp8rl_attn_decode(const void* q_bf16, int64_t 
   a.max_len = (int32_t)(max_blocks * block_size);
   a.softmax_scale = softmax_scale;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = with_form(batch, kv_heads, a.group, head_dim, [&](auto f) { return launch_decode<decltype(f)>(a, d_workspace, cs); });
+  const cudaError_t e = with_form(batch, kv_heads, a.group, head_dim, [&](auto f) { return launch_decode<decltype(f)>(a, d_workspace, workspace_bytes, cs); });
   if (e != cudaSuccess) {
     cudaGetLastError();
     return FP8RL_ERR_CUDA;

@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         const float inv = 1.0f / ml.y;
         const int32_t pos = it.pos0 + x * (kApTile / a.pack) + row / a.pack, head = it.head0 + row % a.pack;
         const int64_t token = (int64_t)it.start + pos;
-        const bool store = pos < it.len && dcheck(token < a.total, a.err);
+        const bool store = pos < it.len && dcheck(token < a.total && head < a.hq, a.err);
         uint16_t* dst = a.out + token * a.ldo + (int64_t)head * D;
         // (the second words are those of an item's second 128 positions: the second tile's)
         const uint32_t* words = marks + ((i - 1) % kApItems) * kApMarks;

@@ -318,6 +318,8 @@ struct LpArgs {
   int64_t ld;
   int32_t vocab, top;
   float temperature, limit;
+  int64_t rows;
+  uint32_t* err;  // debug builds' store checks
 };
 
 // grid (cluster, rows), clusters of gridDim.x CTAs: a CTA takes the pieces
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(T) logprob_kernel(const LpArgs a) {
   const int rank = blockIdx.x, ranks = gridDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t t = a.tokens[r];
   if (t < 0 || t >= a.vocab) {  // no token: the whole cluster leaves
-    if (rank == 0) {
+    if (rank == 0 && dcheck(r < a.rows, a.err)) {
       if (tid == 0) {
         a.lp[r] = 0.0f;
         a.entropy[r] = 0.0f;
@@ -510,12 +512,13 @@ __global__ void __launch_bounds__(T) logprob_kernel(const LpArgs a) {
     const bool none = all.m == -INFINITY && all.s == 0.0f;
     const float ln_s = logf(all.s);
     auto log_prob = [&](float v) { return none ? -INFINITY : (v - all.m) / a.temperature - ln_s; };
-    if (lane == 0) {
+    const bool in = dcheck(r < a.rows, a.err);
+    if (lane == 0 && in) {
       a.lp[r] = log_prob(xt);
       a.entropy[r] = none ? 0.0f : ln_s - kLn2 * (all.w / all.s);
       a.stats[r] = make_float2(all.m, ln_s);
     }
-    if (TOP && lane < a.top) {
+    if (TOP && lane < a.top && in) {
       a.top_ids[r * a.top + lane] = (int32_t) ~(uint32_t)list;
       a.top_lp[r * a.top + lane] = log_prob(from_ordered((uint32_t)(list >> 32)));
     }
@@ -537,6 +540,7 @@ struct LpGradArgs {
   int64_t ldx, ldd;
   int32_t vocab;
   float temperature, limit;
+  uint32_t* err;  // debug builds' store checks
 };
 
 // dx_j = p (a + b log2 p) with a = -(g + g_H H) / T and b = -g_H ln 2 / T;
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const LpGrad
       float v;
       if (sizeof(In) == 2) v = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(x)[j]);
       else v = reinterpret_cast<const float*>(x)[j];
-      store1<In>(dx + j, q.zero ? 0.0f : grad_of(q, v, j));
+      if (dcheck(j >= 0 && j < a.vocab, a.err)) store1<In>(dx + j, q.zero ? 0.0f : grad_of(q, v, j));
     }
     return;
   }
@@ -649,7 +653,8 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const LpGrad
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = sizeof(In) == 2 ? bf16x2_rn(d[(2 * e) % N], d[(2 * e + 1) % N]) : __float_as_uint(d[e]);
-        __stcs(reinterpret_cast<uint4*>(dx + j0), make_uint4(w[0], w[1], w[2], w[3]));
+        if (dcheck(j0 >= 0 && j0 + N <= a.vocab, a.err))
+          __stcs(reinterpret_cast<uint4*>(dx + j0), make_uint4(w[0], w[1], w[2], w[3]));
       } else {
         for (int e = 0; e < N; ++e) {
           const int32_t j = j0 + e;
@@ -657,7 +662,7 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const LpGrad
           float v;
           if (sizeof(In) == 2) v = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(x)[j]);
           else v = reinterpret_cast<const float*>(x)[j];
-          store1<In>(dx + j, q.zero ? 0.0f : grad_of(q, v, j));
+          if (dcheck(j >= 0 && j < a.vocab, a.err)) store1<In>(dx + j, q.zero ? 0.0f : grad_of(q, v, j));
         }
       }
     }
@@ -669,6 +674,17 @@ int sm_count() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 152;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
   return n;
+}
+
+// the word that debug builds' store checks report to (release builds have none)
+bool check_word(uint32_t** err) {
+#ifdef FP8RL_DEBUG
+  *err = device_error_word();
+  return *err != nullptr;
+#else
+  *err = nullptr;
+  return true;
+#endif
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -731,6 +747,8 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob(const void* d_logits, int32_t lo
   if (!aligned(d_logits, logits_fp32 ? 4 : 2) || !aligned(d_tokens, 4) || !aligned(d_lp, 4) || !aligned(d_entropy, 4) ||
       !aligned(d_stats, 8) || !aligned(d_top_ids, 4) || !aligned(d_top_lp, 4))
     return FP8RL_ERR_ALIGNMENT;
+  uint32_t* err = nullptr;
+  if (!check_word(&err)) return FP8RL_ERR_CUDA;
   const size_t size = logits_fp32 ? 4 : 2;
   for (int64_t r0 = 0; r0 < rows; r0 += kMaxRows) {
     const int64_t n = std::min(kMaxRows, rows - r0);
@@ -747,6 +765,8 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob(const void* d_logits, int32_t lo
     a.top = (int32_t)topk;
     a.temperature = temperature;
     a.limit = floor_limit(exp2_scale(temperature));
+    a.rows = n;
+    a.err = err;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const cudaError_t e = logits_fp32 ? (topk ? launch_rows<float, true>(a, n, cs) : launch_rows<float, false>(a, n, cs))
                                       : (topk ? launch_rows<uint16_t, true>(a, n, cs) : launch_rows<uint16_t, false>(a, n, cs));
@@ -776,6 +796,8 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, i
   if (!aligned(d_logits, size) || !aligned(d_dlogits, size) || !aligned(d_tokens, 4) || !aligned(d_stats, 8) ||
       !aligned(d_entropy, 4) || !aligned(d_grad_lp, 4) || !aligned(d_grad_entropy, 4))
     return FP8RL_ERR_ALIGNMENT;
+  uint32_t* err = nullptr;
+  if (!check_word(&err)) return FP8RL_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   for (int64_t r0 = 0; r0 < rows; r0 += kMaxRows) {
     const int64_t n = std::min(kMaxRows, rows - r0);
@@ -792,6 +814,7 @@ extern "C" FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, i
     a.vocab = (int32_t)vocab;
     a.temperature = temperature;
     a.limit = floor_limit(exp2_scale(temperature));
+    a.err = err;
     // Small CTAs, so that many rows are under way (8192 x 1000 fp32: 9.3 us with 64
     // threads, 11 with 128, 16 with 256; 8192 x 4000 43, 41 and 43).  A load round is
     // four pieces a thread.  CTAs of up to five rounds once that leaves many times

@@ -50,11 +50,16 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ void store8_bf16(uint16_t* row, int32_t c, int32_t k, const float (&v)[8]) {
+__device__ __forceinline__ void store8_bf16(uint16_t* row, int32_t c, int32_t k, const float (&v)[8], uint32_t* err) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = bf16x2_rn(v[2 * i], v[2 * i + 1]);
-  if (c < k) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (c < k && dcheck(c + 8 <= k, err)) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename S>
+__device__ __forceinline__ void store_scale(const NormArgs& a, int32_t group, int64_t row, S s) {
+  if (dcheck(group >= 0 && group * (int64_t)kBlock < a.k && row < a.m, a.err)) static_cast<S*>(a.scale)[group * a.m + row] = s;
 }
 
 __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_kernel
     if (a.h) {
       uint16_t* hr = a.h + row * a.ldh;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) store8_bf16(hr, (tid + j * T) * 8, a.k, h[j]);
+      for (int j = 0; j < NP; ++j) store8_bf16(hr, (tid + j * T) * 8, a.k, h[j], a.err);
     }
     ss = row_sum<T>(ss, part[turn]);
     const float rms = rsqrtf(ss / (float)a.k + a.eps);
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_kernel
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           code[i] = e4m3x2(h[j][4 * i] * f, h[j][4 * i + 1] * f) | (e4m3x2(h[j][4 * i + 2] * f, h[j][4 * i + 3] * f) << 16);
-        if ((tid & 15) == 0) static_cast<uint8_t*>(a.scale)[(int64_t)(c / kBlock) * a.m + row] = (uint8_t)(e2 + 127);
+        if ((tid & 15) == 0) store_scale(a, c / kBlock, row, (uint8_t)(e2 + 127));
       } else {
         const float s = scale_fp32(amax), r = __frcp_rn(s);
         float y[8];
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_kernel
         for (int e = 0; e < 8; ++e) y[e] = s >= kFastDivMinScale ? div_by_scale(h[j][e], s, r) : __fdiv_rn(h[j][e], s);
 #pragma unroll
         for (int i = 0; i < 2; ++i) code[i] = e4m3x2(y[4 * i], y[4 * i + 1]) | (e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
-        if ((tid & 15) == 0) static_cast<float*>(a.scale)[(int64_t)(c / kBlock) * a.m + row] = s;
+        if ((tid & 15) == 0) store_scale(a, c / kBlock, row, s);
       }
       if (dcheck(c + 8 <= a.k, a.err)) *reinterpret_cast<uint2*>(qr + c) = make_uint2(code[0], code[1]);
     }
@@ -211,8 +216,8 @@ __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_any_ke
         for (int i = 0; i < 2; ++i) {
           const uint32_t v = bf16x2_rn(h[j][2 * i], h[j][2 * i + 1]);
           const int32_t c = column(j, 2 * i);
-          if (c < a.k) hr[c] = (uint16_t)v;
-          if (c + 32 < a.k) hr[c + 32] = (uint16_t)(v >> 16);
+          if (c < a.k && dcheck(c >= 0 && row < a.m, a.err)) hr[c] = (uint16_t)v;
+          if (c + 32 < a.k && dcheck(c >= 0 && row < a.m, a.err)) hr[c + 32] = (uint16_t)(v >> 16);
         }
     }
     ss = row_sum<T>(ss, part[turn]);
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_any_ke
         const float f = exp2_neg(e2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) code[i] = e4m3x2(h[j][2 * i] * f, h[j][2 * i + 1] * f);
-        if (lane == 0) static_cast<uint8_t*>(a.scale)[(int64_t)group * a.m + row] = (uint8_t)(e2 + 127);
+        if (lane == 0) store_scale(a, group, row, (uint8_t)(e2 + 127));
       } else {
         const float s = scale_fp32(amax), r = __frcp_rn(s);
         float y[4];
@@ -245,13 +250,13 @@ __global__ void __launch_bounds__(T, kNormThreadsPerSm / T) rmsnorm_quant_any_ke
         for (int i = 0; i < 4; ++i) y[i] = s >= kFastDivMinScale ? div_by_scale(h[j][i], s, r) : __fdiv_rn(h[j][i], s);
 #pragma unroll
         for (int i = 0; i < 2; ++i) code[i] = e4m3x2(y[2 * i], y[2 * i + 1]);
-        if (lane == 0) static_cast<float*>(a.scale)[(int64_t)group * a.m + row] = s;
+        if (lane == 0) store_scale(a, group, row, s);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int32_t c = column(j, 2 * i);
-        if (c < a.k) qr[c] = (uint8_t)code[i];
-        if (c + 32 < a.k) qr[c + 32] = (uint8_t)(code[i] >> 8);
+        if (c < a.k && dcheck(c >= 0 && row < a.m, a.err)) qr[c] = (uint8_t)code[i];
+        if (c + 32 < a.k && dcheck(c >= 0 && row < a.m, a.err)) qr[c + 32] = (uint8_t)(code[i] >> 8);
       }
     }
   }
