@@ -170,10 +170,8 @@ __device__ __forceinline__ uint32_t absmax_u4(uint32_t acc, uint4 v) {
 constexpr uint32_t kErrTimeout = 1u;
 constexpr uint32_t kErrDeviceCheck = 2u;
 
-// Debug builds (compiled with FP8RL_DEBUG): the kernels (but those of the KV
-// append and calibration, the MoE plan, dispatch and combine, and the TIS weights)
-// check the index of each global store against its buffer before storing; a
-// failed check sets
+// Debug builds (compiled with FP8RL_DEBUG): the kernels check the index of
+// each global store against its buffer before storing; a failed check sets
 // kErrDeviceCheck in the device error word and the store is skipped (no
 // trap).  Release builds compile the checks away.
 __device__ __forceinline__ bool dcheck(bool ok, uint32_t* err) {
