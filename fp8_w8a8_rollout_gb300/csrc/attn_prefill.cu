@@ -9,8 +9,10 @@
 // Compute-bound (4 d flop per query-key pair and head): both products run on
 // tcgen05 with fp32 accumulators in TMEM.  GB300, 32 query and 8 KV heads of
 // 128: 8192 tokens 324 us alone (1.70 PFLOP/s, 0.89 of the measured burst rate)
-// and 355 back to back (the power limit); 24 packed prompts of up to 2048, 32
-// and 4 heads, 179 us (1.23 PFLOP/s).  What is left: a tile's softmax
+// and 352 back to back (the power limit); 24 packed prompts of up to 2048, 32
+// and 4 heads, 192 to 199 us back to back (1.11 to 1.15 PFLOP/s; 180 by the
+// device, one call alone).  With heads of 64, where the softmax weighs twice as
+// much against the products, 278 and 152 us (0.99 and 0.73).  What is left: a tile's softmax
 // (about 1.4 us) and its products (0.55 us) take turns, and the two tiles
 // hide most of one another's, not all.  One CTA per SM walks work items; an
 // item is two tiles of 128 query rows of one KV head.  A tile's rows are
@@ -43,8 +45,8 @@
 // range first; CTAs take them in snake order, which evens the causal lengths
 // out; a warp of its own reads it and hands the items to the others.  The
 // kernel's size matters: at 73 KB of code, waits spelled out at every site, a
-// fifth of the issue slots' stalls were instruction fetches (8192 tokens 334 us,
-// packed prompts 190; at 55 KB 324 and 174).  Every wait is bounded.
+// fifth of the issue slots' stalls were instruction fetches (one call alone, 8192
+// tokens 334 us, packed prompts 190; at 55 KB 324 and 174).  Every wait is bounded.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>

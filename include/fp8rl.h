@@ -649,7 +649,8 @@ FP8RL_API fp8rl_status fp8rl_attn_prefill(const void* q_bf16, int64_t ldq, const
  *                   its counters zero); one of the largest size serves several shapes.  One call
  *                   at a time per workspace.
  * Codes enter the products exactly; scores, softmax statistics and sums are
- * fp32, the probabilities are rounded to f16, the output once to bf16.  The
+ * fp32, the probabilities are rounded to f16 (11 bits down to 2^-25 of the largest,
+ * steps of 2^-35 of it below), the output once to bf16.  The
  * table and the lengths are device data and are not read on the host: a key
  * whose cache row falls outside [0, num_slots) (a table entry of -1) is left
  * out, and nothing is read for it.  A sequence without keys gives zeros and
