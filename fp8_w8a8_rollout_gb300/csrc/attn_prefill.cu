@@ -12,7 +12,7 @@
 // and 352 back to back (the power limit); 24 packed prompts of up to 2048, 32
 // and 4 heads, 192 to 199 us back to back (1.11 to 1.15 PFLOP/s; 180 by the
 // device, one call alone).  With heads of 64, where the softmax weighs twice as
-// much against the products, 278 and 152 us (0.99 and 0.73).  What is left: a tile's softmax
+// much against the products, 274 and 148 us (1.00 and 0.74).  What is left: a tile's softmax
 // (about 1.4 us) and its products (0.55 us) take turns, and the two tiles
 // hide most of one another's, not all.  One CTA per SM walks work items; an
 // item is two tiles of 128 query rows of one KV head.  A tile's rows are
@@ -661,6 +661,10 @@ __global__ void __launch_bounds__(kApThreads, 1)
     const uint32_t ts = tmem + lanes + C::kTmemS + 128 * x, to = tmem + lanes + C::kTmemO + 128 * x;
     const float c = a.softmax_scale * kLog2e;
     const uint64_t c2 = f32x2(c, c);
+    // While a row's scores are all -inf its p is 0: the reference is tested for that,
+    // or starts finite.  The two differ in the code's layout alone: 8192 tokens of 32 / 8 heads
+    // of 64 274 us tested, 282 started finite; heads of 128 327 and 322.
+    constexpr bool kRefTested = D == 64;
     uint32_t s_seen = 0, o_seen = 0;
     bool alive = true;
     Item it;
@@ -668,7 +672,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
       const int32_t n = it.n(x);
       if (n == 0) continue;
       const int32_t first = it.pos0 + x * (kApTile / a.pack), pos = first + row / a.pack;
-      float mc = -INFINITY;  // reference maximum times c
+      float mc = kRefTested ? -INFINITY : -FLT_MAX;  // reference maximum times c
       uint64_t l2[4];        // the row's sum, in eight strands
 #pragma unroll
       for (int i = 0; i < 4; ++i) l2[i] = f32x2(0.0f, 0.0f);
@@ -700,7 +704,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         };
         // P of a quarter into TMEM, and its sum into l2
         auto exponentials = [&](int q) {
-          const float ref = mc == -INFINITY ? 0.0f : mc;  // scores of -inf alone so far: p = 0
+          const float ref = kRefTested && mc == -INFINITY ? 0.0f : mc;
           const uint64_t nm2 = f32x2(-ref, -ref);
           uint32_t p[16];
 #pragma unroll
@@ -825,7 +829,10 @@ __global__ void __launch_bounds__(kApThreads, 1)
           }
         }
         if (store && a.lse) a.lse[token * a.hq + head] = fmaf(ml.x, kLn2, logf(ml.y));
-        if (store && taken_out) add_taken_out<D>(a, it, words, pos, head, ml.x, dst);
+        if (taken_out) {
+          if (store) add_taken_out<D>(a, it, words, pos, head, ml.x, dst);
+          __syncwarp();
+        }
       }
     }
   }
