@@ -9,7 +9,9 @@ loudly when the library has not been built.
 
 The convenience helpers below them (``quant_weight``, ``quant_act``,
 ``gemm``, ``grouped_gemm``, ``quant_weights_batched``) allocate the outputs
-with torch and call the same entry points.
+with torch and call the same entry points.  With a ``stream`` given, outputs
+still come from torch's current stream (keep them until the other one is done
+with them); what a helper makes for the call alone belongs to the given one.
 """
 from __future__ import annotations
 
@@ -783,12 +785,6 @@ class _NoBackward(torch.autograd.Function):
         raise RuntimeError(f"{ctx.name} has no backward pass; call it under torch.no_grad() or on detached tensors")
 
 
-def _no_backward(name, outputs, *inputs):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
-        return _NoBackward.apply(name, tuple(outputs), *inputs)
-    return outputs
-
-
 def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
                   fmt=SCALE_FP32, out=None, stream=None):
     """(q uint8 [m, k], scale [ceil(k/128), m], h bf16 [m, k]): the RMS norm of
@@ -817,8 +813,8 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
         ldq, ldh = _ld(q, m, k), 0 if h is None else _ld(h, m, k)
     fp8rl_rmsnorm_quant(x.data_ptr(), _ld(x, m, k), residual, 0 if residual is None else _ld(residual, m, k),
                         weight.data_ptr(), eps, m, k, h, ldh, q.data_ptr(), ldq, s.data_ptr(), fmt, stream)
-    if h is not None:
-        h, = _no_backward("rmsnorm_quant", (h,), x, weight, residual)
+    if h is not None and torch.is_grad_enabled() and (x.requires_grad or (residual is not None and residual.requires_grad)):
+        h, = _NoBackward.apply("rmsnorm_quant", (h,), x, residual)
     return q, s, h
 
 
@@ -897,7 +893,9 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: AttnPl
                        _ld(v, tokens, hkv * d), plan.data.data_ptr(), plan.data.numel(), plan.batch, tokens, hq, hkv, d,
                        d ** -0.5 if softmax_scale is None else softmax_scale, out[0].data_ptr(), hq * d,
                        out[1].data_ptr(), stream)
-    return _no_backward("attn_prefill", out, q, k, v)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        out = _NoBackward.apply("attn_prefill", out, q, k, v)
+    return out
 
 
 def attn_decode_workspace(q_heads: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
@@ -949,7 +947,9 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
                       slots, block_table.data_ptr(), _ld(block_table, batch, blocks), blocks, block_size, lens.data_ptr(),
                       scales.data_ptr(), d ** -0.5 if softmax_scale is None else softmax_scale, out[0].data_ptr(), hq * d,
                       out[1].data_ptr(), workspace.data_ptr(), workspace.nbytes, stream)
-    return _no_backward("attn_decode", out, q)
+    if torch.is_grad_enabled() and q.requires_grad:
+        out = _NoBackward.apply("attn_decode", out, q)
+    return out
 
 
 def _check_logits(logits: torch.Tensor, tokens: torch.Tensor):
