@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -37,6 +38,9 @@ __all__ = [
     "fp8rl_attn_prefill_plan_size", "fp8rl_attn_prefill_plan", "fp8rl_attn_prefill", "attn_prefill_plan", "attn_prefill", "AttnPlan",
     "fp8rl_rmsnorm_quant", "rmsnorm_quant", "fp8rl_attn_decode_workspace_size", "fp8rl_attn_decode",
     "attn_decode_workspace", "attn_decode", "fp8rl_logprob", "fp8rl_logprob_backward", "logprobs", "logprobs_backward",
+    "fp8rl_sample", "sample", "fp8rl_rotary", "fp8rl_rotary_kv_append", "rotary_freqs", "RotaryFreqs", "rotary", "rotary_kv_append",
+    "fp8rl_kv_reserve_workspace_size", "fp8rl_kv_reserve", "fp8rl_kv_fork", "fp8rl_kv_compact_workspace_size", "fp8rl_kv_compact",
+    "KvCaches", "kv_reserve", "kv_fork", "kv_compact",
     "fp8rl_e4m3_encode", "fp8rl_debug_set", "fp8rl_sync_status", "fp8rl_status_string", "fp8rl_version",
     "quant_weight", "quant_weights_batched", "quant_act", "gemm", "grouped_gemm", "HostWeightSync",
     "CanaryError", "canaries_enabled", "check_canaries",
@@ -122,6 +126,17 @@ def load_library(build_if_missing: bool = False):
                                   ctypes.c_float, vp, i64, vp, vp, ctypes.c_size_t, vp],
             "fp8rl_logprob": [vp, i32, i64, i64, i64, ctypes.c_float, vp, vp, vp, vp, i64, vp, vp, vp],
             "fp8rl_logprob_backward": [vp, i32, i64, i64, i64, ctypes.c_float, vp, vp, vp, vp, vp, vp, i64, vp],
+            "fp8rl_sample": [vp, i32, i64, i64, i64, vp, ctypes.c_float, i64, ctypes.c_float, ctypes.c_float, vp, vp, vp, vp,
+                             vp, vp, vp, vp, vp],
+            "fp8rl_rotary": [vp, i64, i64, vp, i64, i64, i64, i64, vp, i64, vp, i64, i64, i32, i32, vp, i64, vp, i64, vp],
+            "fp8rl_rotary_kv_append": [vp, i64, i64, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp, i64, i64, i32, vp, i64, vp, i64,
+                                       vp, vp, vp, i64, i64, vp, vp],
+            "fp8rl_kv_reserve_workspace_size": [i64, i64, i64],
+            "fp8rl_kv_reserve": [vp, i64, i64, i64, i64, vp, vp, i64, vp, vp, i64, vp, vp, vp, i32, i64, i64, vp,
+                                 ctypes.c_size_t, vp],
+            "fp8rl_kv_fork": [vp, i64, i64, i64, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp],
+            "fp8rl_kv_compact_workspace_size": [i64],
+            "fp8rl_kv_compact": [vp, i64, i64, i64, i64, vp, vp, i64, vp, vp, i32, i64, i64, vp, ctypes.c_size_t, vp],
             "fp8rl_debug_set": [i32, i64],
             "fp8rl_sync_status": [vp],
             "fp8rl_status_string": [st],
@@ -137,6 +152,8 @@ def load_library(build_if_missing: bool = False):
         lib.fp8rl_tis_workspace_size.restype = ctypes.c_size_t
         lib.fp8rl_attn_prefill_plan_size.restype = ctypes.c_size_t
         lib.fp8rl_attn_decode_workspace_size.restype = ctypes.c_size_t
+        lib.fp8rl_kv_reserve_workspace_size.restype = ctypes.c_size_t
+        lib.fp8rl_kv_compact_workspace_size.restype = ctypes.c_size_t
         lib.fp8rl_version.restype = i32
         _lib = lib
         return lib
@@ -371,6 +388,63 @@ def fp8rl_logprob_backward(d_logits, logits_fp32, rows, vocab, ld, temperature, 
                                               _p(d_stats), _p(d_entropy), _p(d_grad_lp), _p(d_grad_entropy),
                                               _p(d_dlogits), ldd, _stream(stream)),
         "fp8rl_logprob_backward")
+
+
+def fp8rl_sample(d_logits, logits_fp32, rows, vocab, ld, d_uniform, temperature, top_k, top_p, min_p, d_temperature, d_top_k,
+                 d_top_p, d_min_p, d_tokens, d_lp, d_lp_kept, d_kept, stream=None) -> None:
+    _ok(load_library().fp8rl_sample(_p(d_logits), logits_fp32, rows, vocab, ld, _p(d_uniform), temperature, top_k, top_p, min_p,
+                                    _p(d_temperature), _p(d_top_k), _p(d_top_p), _p(d_min_p), _p(d_tokens), _p(d_lp),
+                                    _p(d_lp_kept), _p(d_kept), _stream(stream)),
+        "fp8rl_sample")
+
+
+def fp8rl_rotary(q_bf16, ldq, q_heads, k_bf16, ldk, kv_heads, tokens, head_dim, d_freqs, pairs, d_positions, ldp, axes,
+                 interleaved, inverse, q_out, ldqo, k_out, ldko, stream=None) -> None:
+    _ok(load_library().fp8rl_rotary(_p(q_bf16), ldq, q_heads, _p(k_bf16), ldk, kv_heads, tokens, head_dim, _p(d_freqs), pairs,
+                                    _p(d_positions), ldp, axes, interleaved, inverse, _p(q_out), ldqo, _p(k_out), ldko,
+                                    _stream(stream)),
+        "fp8rl_rotary")
+
+
+def fp8rl_rotary_kv_append(q_bf16, ldq, q_heads, k_bf16, ldk, v_bf16, ldv, kv_heads, tokens, head_dim, d_freqs, pairs,
+                           d_positions, ldp, axes, interleaved, q_out, ldqo, k_out, ldko, d_slot_mapping, k_cache, v_cache,
+                           ld_cache, num_slots, d_scales, stream=None) -> None:
+    _ok(load_library().fp8rl_rotary_kv_append(_p(q_bf16), ldq, q_heads, _p(k_bf16), ldk, _p(v_bf16), ldv, kv_heads, tokens,
+                                              head_dim, _p(d_freqs), pairs, _p(d_positions), ldp, axes, interleaved, _p(q_out),
+                                              ldqo, _p(k_out), ldko, _p(d_slot_mapping), _p(k_cache), _p(v_cache), ld_cache,
+                                              num_slots, _p(d_scales), _stream(stream)),
+        "fp8rl_rotary_kv_append")
+
+
+def fp8rl_kv_reserve_workspace_size(rows, total_tokens, block_size) -> int:
+    return int(load_library().fp8rl_kv_reserve_workspace_size(rows, total_tokens, block_size))
+
+
+def fp8rl_kv_reserve(d_block_table, ldt, rows, max_blocks, block_size, d_lens, d_refs, pages, d_cu_seqlens, d_count, total_tokens,
+                     d_slots, d_info, caches, n_caches, width, ld_cache, d_workspace, workspace_bytes, stream=None) -> None:
+    _ok(load_library().fp8rl_kv_reserve(_p(d_block_table), ldt, rows, max_blocks, block_size, _p(d_lens), _p(d_refs), pages,
+                                        _p(d_cu_seqlens), _p(d_count), total_tokens, _p(d_slots), _p(d_info), caches, n_caches,
+                                        width, ld_cache, _p(d_workspace), workspace_bytes, _stream(stream)),
+        "fp8rl_kv_reserve")
+
+
+def fp8rl_kv_fork(d_block_table, ldt, rows, max_blocks, block_size, d_lens, d_parent, new_rows, d_new_table, ld_new, d_new_lens,
+                  d_refs, pages, stream=None) -> None:
+    _ok(load_library().fp8rl_kv_fork(_p(d_block_table), ldt, rows, max_blocks, block_size, _p(d_lens), _p(d_parent), new_rows,
+                                     _p(d_new_table), ld_new, _p(d_new_lens), _p(d_refs), pages, _stream(stream)),
+        "fp8rl_kv_fork")
+
+
+def fp8rl_kv_compact_workspace_size(pages) -> int:
+    return int(load_library().fp8rl_kv_compact_workspace_size(pages))
+
+
+def fp8rl_kv_compact(d_block_table, ldt, rows, max_blocks, block_size, d_lens, d_refs, pages, d_used, caches, n_caches, width,
+                     ld_cache, d_workspace, workspace_bytes, stream=None) -> None:
+    _ok(load_library().fp8rl_kv_compact(_p(d_block_table), ldt, rows, max_blocks, block_size, _p(d_lens), _p(d_refs), pages,
+                                        _p(d_used), caches, n_caches, width, ld_cache, _p(d_workspace), workspace_bytes,
+                                        _stream(stream)),
+        "fp8rl_kv_compact")
 
 
 def fp8rl_grouped_gemm_blockscaled(xq, x_scale, wq, w_scale, d_offsets, num_experts, rows, n, k,
@@ -1038,6 +1112,337 @@ def logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: torch.T
     fp8rl_logprob_backward(logits, int(logits.dtype == torch.float32), rows, vocab, _ld(logits, rows, vocab), temperature,
                            tokens, stats, entropy, grad_lp, grad_entropy, out, _ld(out, rows, vocab), stream)
     return out
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, stream=None):
+    """(tokens int32, lp fp32, lp_kept fp32, kept int32, each [rows]): a token
+    drawn from each row of logits (bf16 or fp32 [rows, vocab]) with the random
+    numbers uniform (fp64 [rows], in [0, 1); another number, -1 say, marks a row
+    without a draw: token -1, zeros).  temperature, top_p, min_p are numbers or fp32
+    [rows] tensors, top_k a number or an int32 [rows] tensor; top_k 0, top_p 1 and
+    min_p 0 cut nothing off, temperature 0 takes the most likely token.  lp is the
+    token's log probability at the temperature (what logprobs gives it), lp_kept its
+    log probability among the kept tokens.  No gradient comes from a draw: take lp's
+    from logprobs."""
+    if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be a 2-D bf16 or fp32 tensor with unit column stride")
+    rows, vocab = logits.shape
+    values, arrays = [], []
+    for name, v, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
+                           ("min_p", min_p, torch.float32)):
+        if isinstance(v, torch.Tensor):
+            if v.dtype != dtype or v.shape != (rows,) or not v.is_contiguous():
+                raise ValueError(f"{name} must be a number or a contiguous {dtype} [rows] tensor")
+            arrays.append(v)
+            values.append(1)
+        else:
+            arrays.append(None)
+            values.append(v)
+    _check_cuda(logits, uniform, *arrays, *(out or ()))
+    if uniform.dtype != torch.float64 or uniform.shape != (rows,) or not uniform.is_contiguous():
+        raise ValueError("uniform must be a contiguous fp64 [rows] tensor")
+    specs = (((rows,), torch.int32), ((rows,), torch.float32), ((rows,), torch.float32), ((rows,), torch.int32))
+    if out is None:
+        out = tuple(_outs(specs, logits.device))
+    else:
+        if len(out) != 4:
+            raise ValueError("out must hold 4 tensors")
+        for t, (shape, dtype), name in zip(out, specs, ("tokens", "lp", "lp_kept", "kept")):
+            _check_out(t, shape, dtype, name)
+    fp8rl_sample(logits.data_ptr(), int(logits.dtype == torch.float32), rows, vocab, _ld(logits, rows, vocab), uniform.data_ptr(),
+                 *values, *arrays, *out, stream)
+    if torch.is_grad_enabled() and logits.requires_grad:
+        out = (out[0], *_NoBackward.apply("sample", out[1:3], logits), out[3])
+    return out
+
+
+class RotaryFreqs:
+    """The frequencies of rotary positions, laid out for the kernels (rotary_freqs):
+    one per model."""
+
+    def __init__(self, data, rotary_dim, axes):
+        self.data, self.rotary_dim, self.axes = data, rotary_dim, axes
+
+
+def rotary_freqs(rotary_dim: int, theta: float = 10000.0, sections=None, inv_freq=None, axis=None, device=None) -> RotaryFreqs:
+    """Frequencies of rotary_dim // 2 pairs: theta ** (-2 i / rotary_dim) radians a
+    position, or the given ones (inv_freq: numbers, fp64 where they are exact, for
+    scaled positions).  With several axes, sections is how many pairs each takes, one
+    after the other ((16, 24, 24): time, height, width), or axis each pair's own
+    (any order)."""
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    pairs = rotary_dim // 2
+    if inv_freq is None:
+        if not theta > 0:
+            raise ValueError("theta must be positive")
+        inv_freq = [theta ** (-i / pairs) for i in range(pairs)]
+    else:
+        inv_freq = [float(f) for f in inv_freq]
+    if sections is not None and axis is not None:
+        raise ValueError("sections or axis, not both")
+    if sections is not None:
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    axis = [0] * pairs if axis is None else [int(a) for a in axis]
+    if len(inv_freq) != pairs or len(axis) != pairs or any(a < 0 for a in axis) or not all(map(math.isfinite, inv_freq)):
+        raise ValueError("one finite frequency and one axis for each of the rotary_dim // 2 pairs")
+    axes = len(sections) if sections is not None else max(axis, default=0) + 1
+    turns = []
+    for f in inv_freq:
+        part = math.fmod(f / (2 * math.pi), 1.0)
+        turns.append((int(math.ldexp(part, 64)) + (1 << 63)) % (1 << 64) - (1 << 63))  # as a signed word
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return RotaryFreqs(torch.tensor([turns, axis], dtype=torch.int64).to(device), rotary_dim, axes)
+
+
+def _rotary_args(q, k, positions, freqs):
+    """(tokens, q_heads, kv_heads, head_dim, positions [axes, tokens])."""
+    _check_heads(q, "q")
+    if k is not None:
+        _check_heads(k, "k")
+        if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+            raise ValueError("k must be [tokens, kv_heads, head_dim] with q's tokens and head_dim")
+    tokens, hq, d = q.shape
+    if positions.dim() == 1:
+        positions = positions[None]
+    if positions.dtype != torch.int32 or positions.shape != (freqs.axes, tokens) or (positions.stride(1) != 1 and tokens > 1):
+        raise ValueError("positions must be an int32 [tokens] or [axes, tokens] tensor with the frequencies' axes and unit column stride")
+    if freqs.rotary_dim > d:
+        raise ValueError("rotary_dim must not exceed head_dim")
+    return tokens, hq, 0 if k is None else k.shape[1], d, positions
+
+
+def _row_ld(t, tokens, width):
+    """The row stride of [tokens, heads, d] (a tensor without elements has none that counts)."""
+    return _ld(t, tokens, width) if t is not None and t.numel() else width
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, freqs: RotaryFreqs, interleaved: bool = False,
+           inverse: bool = False, out=None, stream=None):
+    """(q, k) turned by their positions: q [tokens, q_heads, d] and k [tokens,
+    kv_heads, d] (bf16; column ranges of one projection's output are fine; k may be
+    None), positions int32 [tokens], or [axes, tokens] for frequencies of several
+    axes.  `out` is such a pair and may be (q, k) itself.  inverse=True turns back,
+    which is the backward pass; with q or k that require a gradient it runs under
+    autograd (on the current stream of the backward pass)."""
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        if out is not None:
+            raise ValueError("rotary with a gradient allocates its outputs")
+        return _Rotary.apply(q, k, positions, freqs, interleaved, inverse, stream)
+    return _rotary(q, k, positions, freqs, interleaved, inverse, out, stream)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, freqs, interleaved, inverse, stream):
+        ctx.save_for_backward(positions, freqs.data)
+        ctx.plan = (freqs.rotary_dim, freqs.axes, interleaved, inverse)
+        ctx.set_materialize_grads(False)
+        return _rotary(q.detach(), None if k is None else k.detach(), positions, freqs, interleaved, inverse, None, stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_q, grad_k):
+        positions, data = ctx.saved_tensors
+        rotary_dim, axes, interleaved, inverse = ctx.plan
+        freqs = RotaryFreqs(data, rotary_dim, axes)
+        grads = [None if g is None else _heads_of(g) for g in (grad_q, grad_k)]
+        if grads[0] is not None:
+            grads = _rotary(grads[0], grads[1], positions, freqs, interleaved, not inverse, None, None)
+        elif grads[1] is not None:
+            grads = (None, _rotary(grads[1], None, positions, freqs, interleaved, not inverse, None, None)[0])
+        return (*grads, None, None, None, None, None)
+
+
+def _heads_of(g):
+    """A gradient as the kernels read heads: as it lies, or copied."""
+    _, heads, d = g.shape
+    _, by_head, by_column = g.stride()
+    return g if (by_column == 1 or d <= 1) and (by_head == d or heads <= 1) and (g.stride(0) >= heads * d or g.shape[0] <= 1) else g.contiguous()
+
+
+def _rotary(q, k, positions, freqs, interleaved, inverse, out, stream):
+    _check_cuda(q, k, positions, freqs.data, *(out or ()))
+    tokens, hq, hkv, d, positions = _rotary_args(q, k, positions, freqs)
+    if out is None:
+        q_out, k_out = _outs((((tokens, hq, d), torch.bfloat16), None if k is None else ((tokens, hkv, d), torch.bfloat16)), q.device)
+    else:
+        q_out, k_out = out
+        for name, t, like in (("out[0]", q_out, q), ("out[1]", k_out, k)):
+            if (t is None) != (like is None):
+                raise ValueError("out must be a pair like (q, k)")
+            if t is not None:
+                _check_heads(t, name)
+                if t.shape != like.shape:
+                    raise ValueError(f"{name} must have its input's shape")
+    fp8rl_rotary(q.data_ptr(), _row_ld(q, tokens, hq * d), hq, k, _row_ld(k, tokens, hkv * d), hkv, tokens, d, freqs.data.data_ptr(),
+                 freqs.rotary_dim // 2, positions.data_ptr(), _row_ld(positions, freqs.axes, tokens), freqs.axes, int(interleaved),
+                 int(inverse), q_out.data_ptr(), _row_ld(q_out, tokens, hq * d), k_out, _row_ld(k_out, tokens, hkv * d), stream)
+    return q_out, k_out
+
+
+def rotary_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, freqs: RotaryFreqs,
+                     slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
+                     interleaved: bool = False, keys: bool = False, out=None, stream=None):
+    """rotary of q and k with kv_append of the turned keys and of v, in one launch:
+    (q [tokens, q_heads, d], turned k or None).  The caches ([num_slots, kv_heads *
+    d] uint8) get the codes in rows slot_mapping (int32 [tokens]; a slot outside the
+    cache, -1 for padding, is skipped).  keys=True gives the turned keys in bf16 as
+    well (attention over the prompt itself).  `out` is such a pair and may be (q,
+    k).  No backward pass: one that reaches the outputs raises."""
+    _check_cuda(q, k, v, positions, freqs.data, slot_mapping, k_cache, v_cache, scales, *(out or ()))
+    tokens, hq, hkv, d, positions = _rotary_args(q, k, positions, freqs)
+    _check_heads(v, "v")
+    if v.shape != k.shape:
+        raise ValueError("v must have k's shape")
+    slots, width = k_cache.shape
+    ldc = _ld(k_cache, slots, width)
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8 or k_cache.stride(1) != 1 or v_cache.stride(1) != 1 or width != hkv * d:
+        raise ValueError("the caches must be uint8 [num_slots, kv_heads * head_dim] tensors with unit column stride")
+    if v_cache.shape != k_cache.shape or _ld(v_cache, slots, width) != ldc:
+        raise ValueError("k_cache and v_cache must have one shape and stride")
+    if slot_mapping.dtype != torch.int32 or slot_mapping.shape != (tokens,) or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int32 [tokens] tensor")
+    if scales.dtype != torch.float32 or scales.numel() < 2 or not scales.is_contiguous():
+        raise ValueError("scales must hold the fp32 K and V scales")
+    if out is None:
+        q_out, k_out = _outs((((tokens, hq, d), torch.bfloat16), ((tokens, hkv, d), torch.bfloat16) if keys else None), q.device)
+    else:
+        q_out, k_out = out
+        for name, t, like in (("out[0]", q_out, q), ("out[1]", k_out, k)):
+            if t is None and like is k:
+                continue
+            _check_heads(t, name)
+            if t.shape != like.shape:
+                raise ValueError(f"{name} must have its input's shape")
+    fp8rl_rotary_kv_append(q.data_ptr(), _row_ld(q, tokens, hq * d), hq, k.data_ptr(), _row_ld(k, tokens, hkv * d), v.data_ptr(),
+                           _row_ld(v, tokens, hkv * d), hkv, tokens, d, freqs.data.data_ptr(), freqs.rotary_dim // 2,
+                           positions.data_ptr(), _row_ld(positions, freqs.axes, tokens), freqs.axes, int(interleaved),
+                           q_out.data_ptr(), _row_ld(q_out, tokens, hq * d), k_out, _row_ld(k_out, tokens, hkv * d),
+                           slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ldc, slots, scales.data_ptr(), stream)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        if k_out is None:
+            q_out, = _NoBackward.apply("rotary_kv_append", (q_out,), q, k, v)
+        else:
+            q_out, k_out = _NoBackward.apply("rotary_kv_append", (q_out, k_out), q, k, v)
+    return q_out, k_out
+
+
+class KvCaches:
+    """The caches that share one table of pages (K and V of every layer, each uint8
+    [num_slots, width] of one shape and stride), listed once for kv_reserve and
+    kv_compact."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        for t in self.tensors:
+            if t.dtype != torch.uint8 or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+                raise ValueError("the caches must be uint8 [num_slots, width] tensors with unit column stride")
+        first = self.tensors[0] if self.tensors else None
+        self.slots, self.width = first.shape if self.tensors else (None, 0)
+        self.ld = _ld(first, self.slots, self.width) if self.tensors else 0
+        if any(t.shape != first.shape or _ld(t, *t.shape) != self.ld or t.device != first.device for t in self.tensors):
+            raise ValueError("the caches must have one shape, stride and device")
+        self.pointers = (ctypes.c_void_p * max(1, len(self.tensors)))(*(t.data_ptr() for t in self.tensors))
+
+
+def _page_args(block_table, lens, refs, block_size, caches):
+    """The caches' handle and sizes: (caches, rows, max_blocks, ldt, pages)."""
+    caches = caches if isinstance(caches, KvCaches) else KvCaches(caches)
+    _check_cuda(block_table, lens, refs, *caches.tensors[:1])
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table must be an int32 [rows, max_blocks] tensor with unit column stride")
+    rows, blocks = block_table.shape
+    if lens.dtype != torch.int32 or lens.shape != (rows,) or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous int32 [rows] tensor")
+    if refs.dtype != torch.int32 or refs.dim() != 1 or not refs.is_contiguous():
+        raise ValueError("refs must be a contiguous int32 [pages] tensor")
+    if caches.slots is not None and refs.numel() * block_size > caches.slots:
+        raise ValueError("the caches must hold every page: pages * block_size rows")
+    return caches, rows, blocks, _ld(block_table, rows, blocks), refs.numel()
+
+
+def kv_reserve(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, block_size: int, caches=(), count=None,
+               cu_seqlens=None, total_tokens: int | None = None, workspace: torch.Tensor | None = None, out=None, stream=None):
+    """(slots int32, info int32 [2]): room for new tokens in the rows of a paged
+    cache; block_table (int32 [rows, max_blocks]), lens (int32 [rows]) and refs (int32
+    [pages]: rows that hold each page) are updated.  slots are the cache rows of the
+    new tokens, for kv_append or rotary_kv_append.  Decode: a token for each row (slots
+    [rows]), with count (int32 [rows], 0 or 1) for some; prompts: row r's new tokens
+    are cu_seqlens[r] .. cu_seqlens[r + 1] of total_tokens (slots [total_tokens]).
+    Entries that a row does not ask for are -1, and so are those of a row that is
+    refused (pages run out, or its table is full; it stays as it was).  info: pages
+    free after the call, rows refused.  A last page that other rows hold too is
+    copied first, in all `caches` (KvCaches, or a list of tensors)."""
+    caches, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, caches)
+    _check_cuda(count, cu_seqlens, workspace, *(out or ()))
+    if count is not None and (count.dtype != torch.int32 or count.shape != (rows,) or not count.is_contiguous()):
+        raise ValueError("count must be a contiguous int32 [rows] tensor")
+    if cu_seqlens is None:
+        total_tokens = rows if total_tokens is None else total_tokens
+    elif cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (rows + 1,) or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 [rows + 1] tensor")
+    elif total_tokens is None:
+        raise ValueError("cu_seqlens needs total_tokens")
+    need = fp8rl_kv_reserve_workspace_size(rows, total_tokens, block_size)
+    if workspace is None:
+        with _on(stream, refs.device):
+            workspace = torch.empty(max(need, 64), dtype=torch.uint8, device=refs.device)
+    if out is None:
+        out = tuple(_outs((((total_tokens,), torch.int32), ((2,), torch.int32)), refs.device))
+    else:
+        _check_out(out[0], (total_tokens,), torch.int32, "slots")
+        _check_out(out[1], (2,), torch.int32, "info")
+    fp8rl_kv_reserve(block_table.data_ptr(), ldt, rows, blocks, block_size, lens.data_ptr(), refs.data_ptr(), pages, cu_seqlens, count,
+                     total_tokens, out[0].data_ptr(), out[1].data_ptr(), caches.pointers, len(caches.tensors), caches.width, caches.ld,
+                     workspace.data_ptr(), workspace.nbytes, stream)
+    return out
+
+
+def kv_fork(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, parent: torch.Tensor, block_size: int, out=None,
+            stream=None):
+    """(block_table int32 [n, max_blocks], lens int32 [n]): row i holds, shared, the
+    pages of old row parent[i] (int32 [n]); -1 gives an empty row.  The old rows give
+    up theirs (refs is updated): one call forks prompts, frees rows that have ended
+    and reorders the others.  `out` may be (block_table, lens) itself; then a row
+    with parent[i] != i takes its pages from a row that stays (parent[p] == p), or is
+    empty."""
+    _, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, _NO_CACHES)
+    _check_cuda(parent, *(out or ()))
+    if parent.dtype != torch.int32 or parent.dim() != 1 or not parent.is_contiguous():
+        raise ValueError("parent must be a contiguous int32 [rows] tensor")
+    n = parent.numel()
+    if out is None:
+        out = tuple(_outs((((n, blocks), torch.int32), ((n,), torch.int32)), refs.device))
+    else:
+        _check_out(out[0], (n, blocks), torch.int32, "block_table", rows=True)
+        _check_out(out[1], (n,), torch.int32, "lens")
+    fp8rl_kv_fork(block_table.data_ptr(), ldt, rows, blocks, block_size, lens.data_ptr(), parent.data_ptr(), n, out[0].data_ptr(),
+                  _ld(out[0], n, blocks), out[1].data_ptr(), refs.data_ptr(), pages, stream)
+    return out
+
+
+def kv_compact(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, block_size: int, caches,
+               workspace: torch.Tensor | None = None, out=None, stream=None):
+    """int32 [1], the number n of pages in use: the used pages move to numbers below
+    n, contents (in all `caches`), refs and block_table with them, so that the caches'
+    rows from n * block_size on are free for something else."""
+    caches, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, caches)
+    _check_cuda(workspace, out)
+    need = fp8rl_kv_compact_workspace_size(pages)
+    if workspace is None:
+        with _on(stream, refs.device):
+            workspace = torch.empty(max(need, 64), dtype=torch.uint8, device=refs.device)
+    if out is None:
+        out = _out((1,), torch.int32, refs.device)
+    else:
+        _check_out(out, (1,), torch.int32, "out")
+    fp8rl_kv_compact(block_table.data_ptr(), ldt, rows, blocks, block_size, lens.data_ptr(), refs.data_ptr(), pages, out.data_ptr(),
+                     caches.pointers, len(caches.tensors), caches.width, caches.ld, workspace.data_ptr(), workspace.nbytes, stream)
+    return out
+
+
+_NO_CACHES = KvCaches(())
 
 
 class HostWeightSync:

@@ -38,7 +38,9 @@
  *     is synchronised.
  *   - Overlapped launches: fp8rl_quant_act_group, fp8rl_rmsnorm_quant,
  *     fp8rl_attn_prefill, fp8rl_attn_decode, fp8rl_logprob,
- *     fp8rl_logprob_backward and the GEMMs at decode
+ *     fp8rl_logprob_backward, fp8rl_sample, fp8rl_rotary,
+ *     fp8rl_rotary_kv_append, fp8rl_kv_reserve, fp8rl_kv_fork,
+ *     fp8rl_kv_compact and the GEMMs at decode
  *     sizes (dense, m <= 64, and up to 128 for the narrow shapes that debug
  *     key 10 lists; fp8rl_gemm_act_quant at m <= 16) are launched
  *     with programmatic stream serialisation, and let the next kernel of the
@@ -711,6 +713,166 @@ FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, int32_t logi
                                               int64_t ld, float temperature, const int32_t* d_tokens,
                                               const float* d_stats, const float* d_entropy, const float* d_grad_lp,
                                               const float* d_grad_entropy, void* d_dlogits, int64_t ldd, void* stream);
+
+/*
+ * A token drawn from each row of logits ("Method steps", step 3: the engine's
+ * rollout generation), from a random number u that the caller gives.  With m = max x,
+ * w_j = exp((x_j - m) / T) (0 below 2^-100) and S = sum w_j, tokens are ordered by
+ * (logit, lower id first; -0 equals 0) and a prefix is kept: of the logits above -inf the
+ * first top_k (0: all); of these the shortest prefix whose mass is at least top_p
+ * times theirs (1 or more: all); of these the ones with x_j >= m + T ln(min_p) (0: all).
+ * With W the mass kept, the token is the lowest id j with
+ *   (sum of w_i over the kept ids i <= j) > u W,
+ * and lp = (x_j - m) / T - ln S (the log probability that fp8rl_logprob gives it),
+ * lp_kept = (x_j - m) / T - ln W.
+ *   d_logits    device, bf16 (logits_fp32 = 0) or fp32 (1) [rows][vocab], row stride ld elements
+ *   d_uniform   device, fp64 [rows]; a u outside [0, 1) (or NaN) marks a row without a draw: it is
+ *               not read, its token is -1, the other outputs 0
+ *   temperature, top_k, top_p, min_p   of all rows, where the array of the same name is null
+ *   d_temperature, d_top_p, d_min_p    device, fp32 [rows], or null;  d_top_k device, int32 [rows], or null:
+ *               of each row.  T = 0 takes the most likely token (lp as at T = 1).  A row with a
+ *               negative, infinite or NaN T, or a NaN top_p or min_p, has no draw.  A top_p of
+ *               0 or less keeps one token, a top_k of 0 or less all, a min_p above 1 counts as 1.
+ *   d_tokens    device, int32 [rows] out
+ *   d_lp, d_lp_kept   device, fp32 [rows] out, or null
+ *   d_kept      device, int32 [rows] out: how many tokens are kept; or null
+ * A row of -inf alone gives token -1 and -inf, one with a NaN or +inf token -1 and
+ * NaN; both keep 0.  Temperatures outside [1e-30, 1e30] count as the nearer end.
+ * Weights and sums are carried to about 2^-43 of the sum, in an order that the
+ * sizes and the rows' place in a 16-byte piece fix: the same bits on every run, and the
+ * token of exact arithmetic but where u W lies that near a border.  One launch per
+ * 65535 rows; no workspace.  Launched with programmatic stream serialisation.
+ * Errors: INVALID_ARG (null pointers, negative rows, vocab < 1, ld < vocab; of the scalars that are used:
+ *         T negative or not finite, top_k < 0, top_p not positive, min_p outside [0, 1]), SHAPE
+ *         (vocab > 2^30), ALIGNMENT (element alignment), CUDA.
+ */
+FP8RL_API fp8rl_status fp8rl_sample(const void* d_logits, int32_t logits_fp32, int64_t rows, int64_t vocab, int64_t ld,
+                                    const double* d_uniform, float temperature, int64_t top_k, float top_p, float min_p,
+                                    const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                                    const float* d_min_p, int32_t* d_tokens, float* d_lp, float* d_lp_kept,
+                                    int32_t* d_kept, void* stream);
+
+/*
+ * Rotary positions of queries and keys, with one or several axes (text: one; images and video: time,
+ * height, width).  Pair i of a head turns by the angle p f_i, p the token's position on
+ * the pair's axis: (a, b) -> (a cos - b sin, a sin + b cos); with inverse = 1 by -p f_i, the
+ * backward pass (the gradient of the unturned heads from that of the turned ones).
+ * Angles are exact to 2^-32 of a turn at every position, the products are fp32
+ * and rounded once ("Where Rounding Happens Matters": the rotation stays in fp32).
+ *   q_bf16     device, bf16 [tokens][q_heads * head_dim], row stride ldq (a column range of the qkv
+ *              linear's output: nothing needs to be copied apart)
+ *   k_bf16     device, bf16 [tokens][kv_heads * head_dim], row stride ldk; kv_heads may be 0, so may q_heads
+ *   d_freqs    device, int64 [2][pairs]: f_i / (2 pi) modulo 1 as a 64-bit binary fraction (times 2^64), then the
+ *              pair's axis (a pair with an axis outside [0, axes) does not turn)
+ *   pairs      of a head; 2 * pairs <= head_dim, the elements behind stay as they are
+ *   d_positions device, int32 [axes][tokens], row stride ldp >= tokens
+ *   interleaved  0: pair i is elements i and pairs + i;  1: elements 2 i and 2 i + 1
+ *   q_out, k_out device, bf16, row strides ldqo, ldko; may be q_bf16, k_bf16 themselves (with their
+ *              row strides), no other overlap
+ * Heads with head_dim a multiple of 16 and pairs a multiple of 8, in rows of 16-byte alignment, take the
+ * vector path; any layout is accepted.  Launched with programmatic stream serialisation.
+ * Errors: INVALID_ARG (null pointers, negative sizes, short strides, flags other than 0 and 1, axes < 1),
+ *         SHAPE (head_dim > 1024, more than 8192 heads, 64 axes or 2^31 tokens), ALIGNMENT (element
+ *         alignment), CUDA.
+ */
+FP8RL_API fp8rl_status fp8rl_rotary(const void* q_bf16, int64_t ldq, int64_t q_heads, const void* k_bf16, int64_t ldk,
+                                    int64_t kv_heads, int64_t tokens, int64_t head_dim, const int64_t* d_freqs,
+                                    int64_t pairs, const int32_t* d_positions, int64_t ldp, int64_t axes,
+                                    int32_t interleaved, int32_t inverse, void* q_out, int64_t ldqo, void* k_out,
+                                    int64_t ldko, void* stream);
+
+/*
+ * fp8rl_rotary joined with fp8rl_kv_append, in one launch: q is turned, the turned keys and
+ * the values are quantised with the calibrated scales into the cache rows that the slots
+ * name.  The key's code is that of the fp32 product (one rounding; fp8rl_kv_append of fp8rl_rotary's
+ * bf16 keys rounds twice), the value's exactly fp8rl_kv_append's.
+ *   v_bf16     device, bf16 [tokens][kv_heads * head_dim], row stride ldv
+ *   k_out      the turned keys in bf16 as well (attention over the prompt itself); or null
+ *   d_slot_mapping, k_cache, v_cache, ld_cache, num_slots, d_scales   as fp8rl_kv_append: a token whose slot is
+ *              outside [0, num_slots) is turned and not stored; two tokens of one slot leave either's codes
+ * Other arguments and errors as fp8rl_rotary; kv_heads >= 1.
+ */
+FP8RL_API fp8rl_status fp8rl_rotary_kv_append(const void* q_bf16, int64_t ldq, int64_t q_heads, const void* k_bf16,
+                                              int64_t ldk, const void* v_bf16, int64_t ldv, int64_t kv_heads,
+                                              int64_t tokens, int64_t head_dim, const int64_t* d_freqs, int64_t pairs,
+                                              const int32_t* d_positions, int64_t ldp, int64_t axes, int32_t interleaved,
+                                              void* q_out, int64_t ldqo, void* k_out, int64_t ldko,
+                                              const int32_t* d_slot_mapping, void* k_cache, void* v_cache,
+                                              int64_t ld_cache, int64_t num_slots, const float* d_scales, void* stream);
+
+/*
+ * The pages of the E4M3 KV cache.  A page is block_size cache rows of every cache it is kept in
+ * (K and V of each layer); the book-keeping is three device arrays that the calls below
+ * keep in step:
+ *   d_block_table  int32 [rows][max_blocks], row stride ldt: as fp8rl_attn_decode reads it
+ *   d_lens         int32 [rows]: tokens of each row; a row of n holds its first ceil(n / block_size)
+ *                  entries, later ones say nothing
+ *   d_refs         int32 [pages]: how many rows hold each page; 0 is free
+ * An empty cache is lengths and counts of 0.  Entries outside [0, pages) stand for no page.
+ *   caches         HOST array of n_caches device pointers, read during the call only: E4M3
+ *                  [pages * block_size][ld_cache], `width` bytes of each row in use; may be empty
+ * All launch with programmatic stream serialisation; results do not depend on timing.
+ *
+ * fp8rl_kv_reserve makes room for new tokens, in the rows' order: row r gets count[r] more, from
+ * position lens[r] on, in new pages (the lowest-numbered free ones) behind its own.  Where its last
+ * page is not full and other rows hold it too, the row first gets a copy of its own
+ * (copy on write; the last holder of all gets one too if all write in one call).  lens, table and
+ * counts are updated.  A row is refused, and left as it was, when it would pass
+ * max_blocks, or when the pages that it and the rows ahead of it ask for are more than are
+ * free at the start of the call.
+ *   d_cu_seqlens   device, int32 [rows + 1]: row r's new tokens are entries [d_cu_seqlens[r], d_cu_seqlens[r + 1]) of
+ *                  d_slots, not overlapping, clamped to [0, total_tokens]; null: total_tokens / rows entries each
+ *   d_count        device, int32 [rows]: how many of its entries a row asks for, clamped to [0, entries]; null: all
+ *   d_slots        device, int32 [total_tokens] out: the cache row of each new token (what fp8rl_kv_append
+ *                  takes), -1 for entries that the row did not ask for or was refused; entries of no row are not written
+ *   d_info         device, int32 [2] out: pages free after the call, rows refused; or null
+ *   d_workspace    device scratch of fp8rl_kv_reserve_workspace_size() bytes, 16-byte aligned, no initial
+ *                  contents; one call at a time per buffer
+ * Errors: INVALID_ARG (null pointers, negative sizes, short strides, block_size < 1, total_tokens no multiple of
+ *         rows without d_cu_seqlens, workspace too small), SHAPE (rows > 8192, more than 2^31 - 1 cache rows or
+ *         tokens a row, a page of 2^31 bytes), ALIGNMENT (element alignment; workspace 16), CUDA.
+ */
+FP8RL_API size_t fp8rl_kv_reserve_workspace_size(int64_t rows, int64_t total_tokens, int64_t block_size);
+FP8RL_API fp8rl_status fp8rl_kv_reserve(int32_t* d_block_table, int64_t ldt, int64_t rows, int64_t max_blocks,
+                                        int64_t block_size, int32_t* d_lens, int32_t* d_refs, int64_t pages,
+                                        const int32_t* d_cu_seqlens, const int32_t* d_count, int64_t total_tokens,
+                                        int32_t* d_slots, int32_t* d_info, void* const* caches, int32_t n_caches,
+                                        int64_t width, int64_t ld_cache, void* d_workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/*
+ * New rows from old ones: new row i holds the pages (shared, not copied) and the length
+ * of old row d_parent[i]; a parent outside [0, rows) gives an empty row.  The old rows give up what
+ * they held, so one call forks a prompt for several answers, frees the rows that have ended,
+ * keeps and reorders the others.
+ *   d_parent      device, int32 [new_rows]
+ *   d_new_table   device, int32 [new_rows][max_blocks] out, row stride ld_new; entries past a row's pages are -1
+ *   d_new_lens    device, int32 [new_rows] out
+ * Both may be d_block_table and d_lens themselves (new_rows = rows, ld_new = ldt; no other
+ * overlap).  Then rows with d_parent[i] = i are not touched, and the parent of any other row has to be one of
+ * those: a row whose parent is not becomes empty.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT as above, CUDA.
+ */
+FP8RL_API fp8rl_status fp8rl_kv_fork(const int32_t* d_block_table, int64_t ldt, int64_t rows, int64_t max_blocks,
+                                     int64_t block_size, const int32_t* d_lens, const int32_t* d_parent,
+                                     int64_t new_rows, int32_t* d_new_table, int64_t ld_new, int32_t* d_new_lens,
+                                     int32_t* d_refs, int64_t pages, void* stream);
+
+/*
+ * Moves the used pages to the lowest numbers: with n pages in use, the k-th used page numbered n or
+ * more goes to the k-th free one below n, contents, counts and table entries with it.  The tails of the caches
+ * from row n * block_size on are then free for other uses.
+ *   d_used        device, int32 [1] out: n
+ *   d_workspace   device scratch of fp8rl_kv_compact_workspace_size() bytes, 16-byte aligned, no initial
+ *                 contents; one call at a time per buffer
+ * Every table that holds pages of these caches has to be the one given.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT as above, CUDA.
+ */
+FP8RL_API size_t fp8rl_kv_compact_workspace_size(int64_t pages);
+FP8RL_API fp8rl_status fp8rl_kv_compact(int32_t* d_block_table, int64_t ldt, int64_t rows, int64_t max_blocks,
+                                        int64_t block_size, const int32_t* d_lens, int32_t* d_refs, int64_t pages,
+                                        int32_t* d_used, void* const* caches, int32_t n_caches, int64_t width,
+                                        int64_t ld_cache, void* d_workspace, size_t workspace_bytes, void* stream);
 
 /* Static, NUL-terminated name of a status code. */
 FP8RL_API const char* fp8rl_status_string(fp8rl_status s);
