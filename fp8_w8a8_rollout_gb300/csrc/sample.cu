@@ -10,17 +10,28 @@
 // The answer is a whole number that a comparison of sums decides.  A sum that is off by
 // e S gives another token for a share of about 2 e u's for each token heavier than
 // that: with fp32 sums (e = 10^-7) a few per cent of the draws from a flat row of 150 000.
-// So weights and sums are carried to about 2^-43, as pairs of fp32 numbers: the
-// exponent t = (m - x) log2(e) / T as a pair; 2^-t from a table of 2^-(i / 256) and
-// a polynomial of the rest, whose first term is a pair too; lanes' sums as pairs,
-// everything above them in fp64.  The order of all sums is fixed.
+// Two kernels see to it.
 //
-// A cluster takes a row, a CTA a contiguous share of it, a warp a contiguous share of
-// that, so that sums by place in the row fall out: the token is found by descending
-// from CTAs to warps to parts of a warp's share to pieces.  The cut of
-// top-k and top-p is found by histograms of 1024 bins over the values (counts, or masses
-// as 13-bit fractions of the bin's heaviest), refined until the bin with the cut holds
-// one value or at most 256 elements, which are sorted.
+// sample_kernel takes each row in one pass, as the log probabilities do: exponentials
+// in fp32 against the running maximum, each thread's sum with a bound of its error.
+// Where nothing is cut off, the token is found by descending from the sums of warps
+// (each has a contiguous share of the row) to parts of one and to pieces, and
+// stands if u W is further from both its borders than the sums can be wrong.  Where something
+// is cut off, the thread maxima give a bound below which nothing is kept (the k-th
+// largest; or so many of the largest that their masses alone reach p S), the few
+// elements above it are collected, sorted, weighed exactly, cut and drawn from.  A row
+// that cannot be decided so (a draw on a border, more elements than the list
+// holds, temperatures or maxima out of range) is marked for
+//
+// sample_exact_kernel, which follows at once and passes by all other rows.  There
+// weights and sums are carried to about 2^-43, as pairs of fp32 numbers: the exponent
+// t = (m - x) log2(e) / T as a pair; 2^-t from a table of 2^-(i / 256) and a polynomial
+// of the rest, whose first term is a pair too.  The cut of top-k and top-p is found by
+// histograms of 1024 bins over the values (counts, or masses as 13-bit fractions of the
+// bin's heaviest), refined until the bin with the cut holds one value or at most 256
+// elements, which are sorted.
+//
+// The order of all sums is fixed.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -32,13 +43,13 @@
 namespace fp8rl {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kUnroll = 2;
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the exact kernel
+constexpr int kUnroll = 4;
 constexpr int kBins = 1024;
 constexpr int kList = 256;  // elements that are sorted, one a thread
 constexpr int kMaxCluster = 8;
-constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
 constexpr float kReach = 100.0f;  // weights below 2^-100 count as 0
+constexpr int32_t kUndecided = -2;  // the token of a row that is left to the exact kernel
 
 // ------------------------------------------------------------------ weights
 
@@ -49,7 +60,7 @@ struct Exp2Table {
 constexpr Exp2Table make_table() {
   Exp2Table t{};
   for (int i = 0; i < 256; ++i) {
-    const double y = -kLn2 * i / 256;
+    const double y = -0.69314718055994530942 * i / 256;
     double sum = 1.0, term = 1.0;
     for (int n = 1; n < 30; ++n) {
       term *= y / n;
@@ -70,12 +81,64 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t both(float v) { return pair_of(v, v); }
 
+// A number as a pair of fp32 numbers, about 48 bits
+struct Pair {
+  float h = 0.0f, l = 0.0f;
+};
+__device__ __forceinline__ Pair normal(float h, float l) {  // |h| >= |l|
+  const float s = h + l;
+  return Pair{s, l - (s - h)};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const float s = a.h + b.h, t = s - a.h;
+  return normal(s, (a.h - (s - t)) + (b.h - t) + (a.l + b.l));
+}
+__device__ __forceinline__ Pair operator-(Pair a, Pair b) { return a + Pair{-b.h, -b.l}; }
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  const float p = __fmul_rn(a.h, b.h);  // (not to be joined with the sum)
+  return normal(p, fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h));
+}
+__device__ __forceinline__ bool operator<(Pair a, Pair b) { return a.h < b.h || (a.h == b.h && a.l < b.l); }
+__device__ __forceinline__ bool operator<=(Pair a, Pair b) { return !(b < a); }
+__device__ __forceinline__ Pair pair_from(double v) {
+  const float h = (float)v;
+  return Pair{h, (float)(v - (double)h)};
+}
+__device__ __forceinline__ Pair shuffle_up(Pair a, int d) {
+  return Pair{__shfl_up_sync(0xffffffffu, a.h, d), __shfl_up_sync(0xffffffffu, a.l, d)};
+}
+__device__ __forceinline__ Pair shuffle(Pair a, int lane) {
+  return Pair{__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
+}
+// the sum over the lanes up to and with this one
+__device__ __forceinline__ Pair scan_lanes(Pair a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Pair o = shuffle_up(a, d);
+    if (lane >= d) a = o + a;
+  }
+  return a;
+}
+// ln of a sum of at least 1
+__device__ __forceinline__ float log_of(Pair s) { return s.h < 2.0f ? log1pf((s.h - 1.0f) + s.l) : logf(s.h); }
+
 // what a row's weights go by
 struct Scale {
   float m;       // the maximum
   float hi, lo;  // log2(e) / T as a pair
   float cut;     // elements below have weight 0
 };
+
+__device__ __forceinline__ Scale scale_of(float m, float temperature) {
+  constexpr float kLow = 1.92596299e-8f;  // log2(e) = kLog2e + kLow
+  Scale s;
+  s.m = m;
+  s.hi = __fdiv_rn(kLog2e, temperature);
+  s.lo = __fdiv_rn(fmaf(-s.hi, temperature, kLog2e) + kLow, temperature);
+  s.cut = fmaxf(m - kReach * kLn2 * temperature, -FLT_MAX);
+  return s;
+}
 
 // The weights of two elements, each hi + lo.  With d = m - x (exact as a pair) and t = d c
 // (a pair), k = round(256 t) and the rest r: 2^-t = 2^-(k >> 8) 2^-((k & 255) / 256) e^g,
@@ -122,11 +185,11 @@ struct Sum {
     h = s;
     l = add2(l, add2(e, vl));
   }
-  __device__ __forceinline__ double value() const {
+  __device__ __forceinline__ Pair value() const {
     float a, b, c, d;
     ptx::f32x2_unpack(h, a, b);
     ptx::f32x2_unpack(l, c, d);
-    return ((double)a + (double)b) + ((double)c + (double)d);
+    return normal(a, c) + normal(b, d);
   }
 };
 
@@ -134,7 +197,7 @@ struct Sum {
 
 // what threads, warps and CTAs add up: sums, a maximum, a minimum, counts
 struct alignas(16) Part {
-  double a = 0.0, b = 0.0;
+  Pair a, b;
   float most = -INFINITY, least = INFINITY;
   uint32_t n = 0, k = 0;
 };
@@ -156,8 +219,8 @@ __device__ __forceinline__ Part merge_lanes(Part v) {
 #pragma unroll
   for (int d = L / 2; d > 0; d >>= 1) {
     Part o;
-    o.a = __shfl_xor_sync(0xffffffffu, v.a, d);
-    o.b = __shfl_xor_sync(0xffffffffu, v.b, d);
+    o.a = Pair{__shfl_xor_sync(0xffffffffu, v.a.h, d), __shfl_xor_sync(0xffffffffu, v.a.l, d)};
+    o.b = Pair{__shfl_xor_sync(0xffffffffu, v.b.h, d), __shfl_xor_sync(0xffffffffu, v.b.l, d)};
     o.most = __shfl_xor_sync(0xffffffffu, v.most, d);
     o.least = __shfl_xor_sync(0xffffffffu, v.least, d);
     o.n = __shfl_xor_sync(0xffffffffu, v.n, d);
@@ -171,13 +234,11 @@ struct Shared {
   float2 table[256];
   uint32_t hist[kBins];
   uint64_t list[kList], sorted[kList];
-  double mass[kList];
+  Pair mass[kList];
   Part warp[kWarps];       // the last gather's sums of this CTA's warps
   Part mine[2];            // of this CTA, read by the others (two take turns)
   Part all[kMaxCluster];   // of every CTA
-  double part[kWarps];
-  uint64_t scan[kWarps];
-  Scale scale;
+  Pair part[kWarps];
   float border;            // min-p's
   int32_t n_list, bin, last;
 };
@@ -338,10 +399,10 @@ struct Team {
 
   // Narrows `keep` to its first k elements (by count), or to the shortest prefix with mass >= target of `whole`.
   // Every CTA of the cluster comes to the same decisions, from the same sums.
-  __device__ void select(const Scale& s, Keep& keep, bool by_count, uint32_t k, double target, double whole) {
+  __device__ void select(const Scale& s, Keep& keep, bool by_count, uint32_t k, Pair target, Pair whole) {
     // bins over (hi - x) * pre * scale; a bin is `step` wide in t
     float hi = s.m, lo = -FLT_MAX, pre = 1.0f, scale = 16.0f * s.hi, step = 1.0f / 16.0f;
-    double above = 0.0;    // mass and number of what lies above the range
+    Pair above;            // mass and number of what lies above the range
     uint32_t n_above = 0;
     for (;;) {
       auto place = [&](float x, int32_t j, float& f) {  // the bin, or -1
@@ -369,42 +430,61 @@ struct Team {
       else __syncthreads();
       // the cluster's bins, four a thread
       uint32_t c[4] = {0, 0, 0, 0};
-      float4 many = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (uint32_t r = 0; r < ranks; ++r) {
         const float4 v = ptx::ld_dsmem_f32x4(ptx::mapa_shared(ptx::smem_u32(&sh.hist[4 * threadIdx.x]), r));
         const uint32_t w[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] += w[i];
-        many.x += (float)w[0], many.y += (float)w[1], many.z += (float)w[2], many.w += (float)w[3];
+        for (int i = 0; i < 4; ++i) {
+          c[i] += w[i];
+          f[i] += (float)w[i];
+        }
       }
-      // the first bin in which the running sum reaches what is asked for (masses: nearly)
+      // the first bin in which the running sum reaches what is asked for (counts exactly, masses nearly)
       const float t0 = (s.m - hi) * s.hi;
-      float f[4] = {many.x, many.y, many.z, many.w};
+      uint32_t n_run = 0, n_own = 0;
+      float f_run = 0.0f, f_own = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] *= ex2(fmaxf(-t0 - (float)(4 * threadIdx.x + i) * step, -120.0f)) * (1.0f / 8192.0f);
-      double own = by_count ? (double)c[0] + c[1] + c[2] + c[3] : (double)f[0] + f[1] + f[2] + f[3], run = own;
+      for (int i = 0; i < 4; ++i) {
+        f[i] *= ex2(fmaxf(-t0 - (float)(4 * threadIdx.x + i) * step, -120.0f));
+        n_own += c[i];
+        f_own += f[i];
+      }
+      n_run = n_own, f_run = f_own;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, run, d);
-        if (lane >= d) run += o;
+        const uint32_t n = __shfl_up_sync(0xffffffffu, n_run, d);
+        const float o = __shfl_up_sync(0xffffffffu, f_run, d);
+        if (lane >= d) {
+          n_run += n;
+          f_run += o;
+        }
       }
-      if (lane == 31) sh.part[warp] = run;
+      if (lane == 31) {
+        sh.warp[warp].n = n_run;
+        sh.warp[warp].most = f_run;
+      }
       __syncthreads();
-      run -= own;
-      double sum = 0.0;
+      n_run -= n_own;
+      f_run -= f_own;
+      float f_all = 0.0f;
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) run += sh.part[w];
-        sum += sh.part[w];
+        if (w < warp) {
+          n_run += sh.warp[w].n;
+          f_run += sh.warp[w].most;
+        }
+        f_all += sh.warp[w].most;
       }
       // (the masses are up to 2^-13 small: as shares of their own sum, head and tail are good to that)
-      const double want = by_count ? (double)(k - n_above) : (target - above) / whole * sum;
+      const float share = (target - above).h / whole.h * f_all;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (c[i] == 0) continue;
         const int b = 4 * threadIdx.x + i;
         atomicMax(&sh.last, b);
-        run += by_count ? (double)c[i] : (double)f[i];
-        if (run >= want) atomicMin(&sh.bin, b);
+        n_run += c[i];
+        f_run += f[i];
+        if (by_count ? n_run >= k - n_above : f_run >= share) atomicMin(&sh.bin, b);
       }
       __syncthreads();
       int bin = min(sh.bin, sh.last);
@@ -450,7 +530,7 @@ struct Team {
         t = gather(p);
         if (by_count) break;
         // the histogram's masses are not exact: step to the neighbour until the cut lies inside
-        const bool below = above + t.a >= target && t.n > 0;
+        const bool below = target <= above + t.a && t.n > 0;
         const bool past = above + t.a + t.b < target;
         if (below && way <= 0 && bin > 0) {
           way = -1;
@@ -463,7 +543,7 @@ struct Team {
         }
       }
       if (t.k == 0) return;  // nothing further down: all of `keep` stays
-      above += t.a;
+      above = above + t.a;
       n_above += t.n;
       if (t.k > (uint32_t)kList && t.most > t.least) {  // a closer look at the bin
         hi = t.most;
@@ -478,11 +558,15 @@ struct Team {
       if (t.k > (uint32_t)kList) {  // many of one value
         uint32_t need = by_count ? k - n_above : 1;
         if (!by_count) {
-          const double w = t.b / t.k;
-          double n = w > 0.0 ? ceil((target - above) / w) : 1.0;
-          n = fmin(fmax(n, 1.0), (double)t.k);
-          if (n > 1.0 && above + (n - 1.0) * w >= target) n -= 1.0;
-          need = (uint32_t)n;
+          uint64_t h, l;  // the first n with above + n w >= target
+          weights(s, sh.table, t.most, -INFINITY, h, l);
+          float h0, l0, none;
+          ptx::f32x2_unpack(h, h0, none);
+          ptx::f32x2_unpack(l, l0, none);
+          const double w = (double)h0 + (double)l0, left = (double)(target - above).h + (double)(target - above).l;
+          const double n = w > 0.0 ? ceil(left / w) : 1.0;
+          need = (uint32_t)fmin(fmax(n, 1.0), (double)t.k);
+          if (need > 1 && (double)(need - 1) * w >= left) --need;
         }
         need = max(1u, min(need, t.k));
         const int32_t j = need == t.k ? INT_MAX : nth_equal(t.most, keep, need);
@@ -529,26 +613,22 @@ struct Team {
           float h0, l0, rest;
           ptx::f32x2_unpack(h, h0, rest);
           ptx::f32x2_unpack(l, l0, rest);
-          sh.mass[threadIdx.x] = (double)h0 + (double)l0;
+          sh.mass[threadIdx.x] = normal(h0, l0);
         } else {
-          sh.mass[threadIdx.x] = 0.0;
+          sh.mass[threadIdx.x] = Pair{};
         }
         if (threadIdx.x == 0) sh.bin = n - 1;
         __syncthreads();
         if (warp == 0) {
           constexpr int kEach = kList / 32;
-          double sum = 0.0;
-          for (int i = 0; i < kEach; ++i) sum += sh.mass[lane * kEach + i];
-          double incl = sum;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const double o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
-          }
-          double part = above + (incl - sum);
+          Pair sum;
+          for (int i = 0; i < kEach; ++i) sum = sum + sh.mass[lane * kEach + i];
+          Pair ahead = shuffle_up(scan_lanes(sum), 1);
+          if (lane == 0) ahead = Pair{};
+          Pair part = above + ahead;
           for (int i = 0; i < kEach; ++i) {
-            part += sh.mass[lane * kEach + i];
-            if (part >= target) {
+            part = part + sh.mass[lane * kEach + i];
+            if (target <= part) {
               atomicMin(&sh.bin, lane * kEach + i);
               break;
             }
@@ -591,161 +671,744 @@ __device__ __forceinline__ void report(const SampleArgs& a, int64_t r, int32_t t
   if (a.kept) a.kept[r] = kept;
 }
 
-// ln of a sum of at least 1
-__device__ __forceinline__ float log_of(double s) { return s < 2.0 ? log1pf((float)(s - 1.0)) : logf((float)s); }
+// what one row is drawn with; false: no draw
+struct Draw {
+  double u;
+  float temperature, top_p, min_p;
+  int64_t k;
+  __device__ __forceinline__ bool load(const SampleArgs& a, int64_t r) {
+    u = a.uniform[r];
+    temperature = a.temperature ? a.temperature[r] : a.t;
+    top_p = a.top_p ? a.top_p[r] : a.p;
+    min_p = a.min_p ? a.min_p[r] : a.q;
+    k = a.top_k ? a.top_k[r] : a.k;
+    if (!(u >= 0.0 && u < 1.0) || !(temperature >= 0.0f && temperature <= FLT_MAX) || isnan(top_p) || isnan(min_p)) return false;
+    if (temperature == 0.0f) {
+      temperature = 1.0f;
+      k = 1;
+    }
+    if (top_p <= 0.0f) k = 1;
+    temperature = fminf(fmaxf(temperature, 1e-30f), 1e30f);
+    return true;
+  }
+  // T ln(min_p), and the smallest kept value
+  __device__ __forceinline__ double reach() const { return (double)temperature * log((double)fminf(min_p, 1.0f)); }
+};
+__device__ __forceinline__ float border_of(float m, double reach) { return __double2float_ru((double)m + reach); }
+
+// ------------------------------------------------------------------ one pass
+
+constexpr int kCap = 1024;    // elements that a row's cut is made among
+constexpr int kMassBins = 128;  // of the thread maxima, a quarter of a power of two each
+constexpr float kStep = 0x1p-24f;  // an fp32 operation's largest relative error
+
+// a warp's share of a row: sums against its maximum m
+struct WarpStat {
+  float m;
+  Pair s;            // sum of w
+  float err, wt;     // a bound of s's error so far; sum of w t (t <= 0: exponents in base 2)
+  uint32_t masked;   // elements of -inf
+  uint32_t pad[2];
+};
+static_assert(sizeof(WarpStat) == 32, "read as 8 words");
+
+template <bool CUT, int T>
+struct PassShared {
+  WarpStat warp[T / 32];
+  float bound;             // of this CTA's share: at least its part of the first k lies at or above
+  // of the whole row, after the pass
+  Pair total, left;
+  float m, err, tau;
+  uint32_t finite;
+  int owner, owner_warp;
+  Pair part[T / 32];
+};
+template <int T>
+struct CutShared {
+  float2 table[256];
+  float most[T];           // thread maxima
+  uint32_t bins[kMassBins];
+  uint64_t list[kCap];     // this CTA's finds
+  uint64_t key[kCap];      // rank 0: all of them, sorted
+  Pair w[kCap];
+  Pair part[T / 32];
+  double reach;
+  int16_t cand[T];
+  int hits, cands, last_bin, below[2], n_border, token;
+};
+
+// keys sorted, the largest first; n a power of two, the whole block
+template <int T>
+__device__ void sort_down(uint64_t* key, int n) {
+  for (int k = 2; k <= n; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < n / 2; i += T) {
+        const int a = 2 * i - (i & (j - 1)), b = a + j;
+        const uint64_t x = key[a], y = key[b];
+        if ((x < y) == ((a & k) == 0)) {
+          key[a] = y;
+          key[b] = x;
+        }
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// The running sums of w[0 .. n): a thread takes kCap / T entries in a row and shows each to
+// f(i, sum before, sum with); returns the whole sum
+template <int T, typename F>
+__device__ Pair sums_of(const Pair* w, int n, Pair* part, F f) {
+  constexpr int E = kCap / T;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i0 = threadIdx.x * E;
+  Pair own;
+  for (int i = i0; i < min(n, i0 + E); ++i) own = own + w[i];
+  const Pair incl = scan_lanes(own);
+  Pair sum = shuffle_up(incl, 1);
+  if (lane == 0) sum = Pair{};
+  __syncthreads();
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  Pair all;
+  for (int i = 0; i < T / 32; ++i) {
+    if (i == warp) sum = all + sum;
+    all = all + part[i];
+  }
+  for (int i = i0; i < min(n, i0 + E); ++i) {
+    const Pair with = sum + w[i];
+    f(i, sum, with);
+    sum = with;
+  }
+  return all;
+}
 
 // grid (cluster, rows)
+template <typename In, bool CUT, int T>
+__global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
+  constexpr int N = Row<In>::N, U = 4, W = T / 32;
+  __shared__ __align__(16) unsigned char smem[sizeof(PassShared<CUT, T>)];
+  __shared__ __align__(16) unsigned char cut_smem[CUT ? sizeof(CutShared<T>) : 16];
+  auto& sh = *reinterpret_cast<PassShared<CUT, T>*>(smem);
+  auto& cs = *reinterpret_cast<CutShared<T>*>(cut_smem);
+  ptx::grid_dep_launch_dependents();
+  ptx::grid_dep_wait();
+  const int64_t r = blockIdx.y;
+  const int rank = blockIdx.x, ranks = gridDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Draw draw;
+  if (!draw.load(a, r)) {  // the whole cluster leaves
+    if (rank == 0 && tid == 0) report(a, r, -1, 0.0f, 0.0f, 0);
+    return;
+  }
+  const float c = exp2_scale(draw.temperature), limit = floor_limit(c);
+  const Row<In> row(static_cast<const In*>(a.x) + r * a.ld, a.vocab);
+  const int32_t cta = (row.pieces + ranks - 1) / ranks, each = (cta + W - 1) / W;
+  auto share = [&](int rk, int w, int32_t& p0, int32_t& p1) {  // the pieces of a warp
+    const int32_t c0 = min(row.pieces, rk * cta), c1 = min(row.pieces, c0 + cta);
+    p0 = min(c1, c0 + w * each);
+    p1 = min(c1, p0 + each);
+  };
+  int32_t w0, w1;
+  share(rank, warp, w0, w1);
+  if (CUT) {
+    for (int i = tid; i < 256; i += T) cs.table[i] = kExp2.v[i];
+    for (int i = tid; i < kMassBins; i += T) cs.bins[i] = 0;
+    if (tid == 0) {
+      cs.hits = cs.cands = 0;
+      cs.last_bin = INT_MAX;
+      cs.below[0] = cs.below[1] = cs.n_border = 0;
+      cs.token = -1;
+      if (draw.min_p > 0.0f && rank == 0) cs.reach = draw.reach();
+    }
+  }
+
+  // the pass: this thread's sums against its own maximum
+  float m = -INFINITY, err = 0.0f, wt = 0.0f;
+  Sum sum;
+  uint64_t wt2 = 0;
+  uint32_t masked = 0;
+  const uint64_t c2 = both(c);
+  for (int32_t p0 = w0; p0 < w1; p0 += 32 * U) {
+    uint4 u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) u[i] = p0 + 32 * i + lane < w1 ? row.load(p0 + 32 * i + lane) : absent<In>();
+    const float big = largest<In>(u);
+    if (big > m) {
+      // (all sums so far times a power: one rounding of the exponential and of the product)
+      const float d = m == -INFINITY ? 0.0f : fmaxf((m - big) * c, kTinyExp2), f = m == -INFINITY ? 0.0f : ex2(d);
+      float h0, h1, l0, l1;
+      ptx::f32x2_unpack(sum.h, h0, h1);
+      ptx::f32x2_unpack(sum.l, l0, l1);
+      float t0, t1;
+      ptx::f32x2_unpack(wt2, t0, t1);
+      wt = f * fmaf(d, h0 + h1, wt + t0 + t1);
+      wt2 = 0;
+      err = f * fmaf(6.0f * kStep, h0 + h1, err);
+      sum.h = pair_of(h0 * f, h1 * f);
+      sum.l = pair_of(l0 * f, l1 * f);
+      m = big;
+    }
+    if (fabsf(m) <= limit) {
+      const uint64_t nm2 = both(-m);
+      uint64_t s[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        uint64_t v[N / 2], p2[N / 2];
+        floored_pairs<In>(u[i], v);
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          const uint64_t y = pair_mul(add2(v[e], nm2), c2);
+          float y0, y1;
+          ptx::f32x2_unpack(y, y0, y1);
+          p2[e] = pair_of(ex2(y0), ex2(y1));
+          wt2 = pair_fma(p2[e], y, wt2);
+        }
+        s[i] = add2(p2[0], p2[1]);
+        if (N == 8) s[i] = add2(s[i], add2(p2[N / 2 - 2], p2[N / 2 - 1]));
+      }
+      sum.add(add2(add2(s[0], s[1]), add2(s[2], s[3])), 0);
+    } else {
+      // a maximum out of range (left to the exact kernel), or -inf alone; NaN marks the sum
+      float bad = 0.0f;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float v[N];
+        values<In>(u[i], v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) bad = isnan(v[e]) ? v[e] : bad;
+      }
+      sum.add(both(bad), 0);
+      if (m > -INFINITY) err = INFINITY;
+    }
+    // elements of -inf, where there are any
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < U; ++i) any |= least_is_masked<In>(u[i]);
+    if (any) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float v[N];
+        values<In>(u[i], v);
+        const int32_t j0 = (p0 + 32 * i + lane) * N - row.off;
+        if (p0 + 32 * i + lane < w1) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) masked += v[e] == -INFINITY && j0 + e >= 0 && j0 + e < a.vocab;
+        }
+      }
+    }
+  }
+  {
+    float h0, h1, l0, l1;
+    ptx::f32x2_unpack(sum.h, h0, h1);
+    ptx::f32x2_unpack(sum.l, l0, l1);
+    Pair s = Pair{h0, l0} + Pair{h1, l1};
+    ptx::f32x2_unpack(wt2, h0, h1);
+    wt += h0 + h1;
+    const float own = m;
+    if (CUT) cs.most[tid] = m;
+    // the warp's, against the warp's maximum
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float d = own == -INFINITY ? 0.0f : fmaxf((own - m) * c, kTinyExp2), f = own == -INFINITY ? 0.0f : ex2(d);
+    wt = f * fmaf(d, s.h, wt);
+    err = f * fmaf(16.0f * kStep, s.h, err);  // this exponential, those of the sum and the additions
+    s = Pair{s.h * f, s.l * f};
+    s = scan_lanes(s);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+      err += __shfl_xor_sync(0xffffffffu, err, k);
+      wt += __shfl_xor_sync(0xffffffffu, wt, k);
+    }
+    masked = __reduce_add_sync(0xffffffffu, masked);
+    if (lane == 31) sh.warp[warp] = WarpStat{m, s, err, wt, masked, {}};
+  }
+  const bool by_rank = CUT && draw.k > 0 && draw.k <= kCap;
+  if (CUT) {
+    // Each CTA gives the first ceil(k / CTAs) of its threads' maxima; the least of these bounds is one of the
+    // k-th largest element.  The upper half of the ordered number: a lower bound.
+    float bound = -INFINITY;
+    if (by_rank) {
+      const int want = (int)((draw.k + ranks - 1) / ranks);
+      const uint32_t own = max(ordered(cs.most[tid]) >> 16, 1u);
+      uint32_t lo = 0;
+      if (want <= T) {
+        for (int b = 15; b >= 0; --b) {
+          const uint32_t mid = lo | 1u << b;
+          if (__syncthreads_count(own >= mid) >= want) lo = mid;
+        }
+      }
+      bound = lo >= 0x80u ? from_ordered(lo << 16) : -INFINITY;  // (below: -inf)
+    }
+    if (tid == 0) sh.bound = bound;
+  }
+  if (ranks > 1) ptx::cluster_sync();
+  else __syncthreads();
+
+  // the row's sums, in every CTA: lane i has the shares 2 i and 2 i + 1
+  if (warp == 0) {
+    WarpStat st[2];
+    float tau = INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = 2 * lane + i;
+      st[i] = WarpStat{-INFINITY, {}, 0.0f, 0.0f, 0, {}};
+      if (e < ranks * W) {
+        const uint32_t at = ptx::mapa_shared(ptx::smem_u32(&sh.warp[e % W]), e / W);
+        const float4 x = ptx::ld_dsmem_f32x4(at), y = ptx::ld_dsmem_f32x4(at + 16);
+        st[i] = WarpStat{x.x, {x.y, x.z}, x.w, y.x, __float_as_uint(y.y), {}};
+      }
+    }
+    if (CUT && lane < ranks) tau = __uint_as_float(ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&sh.bound), lane)));
+    float top = fmaxf(st[0].m, st[1].m);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      tau = fminf(tau, __shfl_xor_sync(0xffffffffu, tau, d));
+    }
+    err = wt = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float d = st[i].m == -INFINITY ? 0.0f : fmaxf((st[i].m - top) * c, kTinyExp2), f = st[i].m == -INFINITY ? 0.0f : ex2(d);
+      wt += f * fmaf(d, st[i].s.h, st[i].wt);
+      err += f * fmaf(6.0f * kStep, st[i].s.h, st[i].err);
+      st[i].s = Pair{st[i].s.h * f, st[i].s.l * f};
+    }
+    masked = __reduce_add_sync(0xffffffffu, st[0].masked + st[1].masked);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+      err += __shfl_xor_sync(0xffffffffu, err, k);
+      wt += __shfl_xor_sync(0xffffffffu, wt, k);
+    }
+    const Pair incl = scan_lanes(st[0].s + st[1].s), total = shuffle(incl, 31);
+    // exponents: x - m, log2(e) / T and their product are rounded
+    err = fmaf(2.6f * kStep, fabsf(wt), err);
+    Pair before = shuffle_up(incl, 1);
+    if (lane == 0) before = Pair{};
+    const Pair goal = pair_from(draw.u) * total, middle = before + st[0].s;
+    int at = st[0].s.h > 0.0f && before <= goal ? 2 * lane : -1;
+    Pair start = before;
+    if (st[1].s.h > 0.0f && middle <= goal) {
+      at = 2 * lane + 1;
+      start = middle;
+    }
+    const uint32_t can = __ballot_sync(0xffffffffu, at >= 0);
+    const int from = can ? 31 - __clz(can) : 0;
+    at = __shfl_sync(0xffffffffu, at, from);
+    start = shuffle(start, from);
+    if (lane == 0) {
+      sh.total = total;
+      sh.left = goal - start;
+      sh.m = top;
+      sh.err = err;
+      sh.tau = tau;
+      sh.finite = (uint32_t)a.vocab - masked;
+      sh.owner = at < 0 ? 0 : at / W;
+      sh.owner_warp = at < 0 ? 0 : at % W;
+    }
+  }
+  __syncthreads();
+  const Pair total = sh.total;
+  m = sh.m;
+  err = sh.err;
+  const uint32_t finite = sh.finite;
+  const int64_t k = draw.k;
+  const bool by_k = CUT && k > 0 && k < (int64_t)finite, by_p = CUT && draw.top_p < 1.0f && draw.top_p > 0.0f,
+             by_q = CUT && draw.min_p > 0.0f;
+  const bool odd = isnan(total.h) || !(fabsf(m) <= limit);  // NaN, infinities, -inf alone, out of range
+  if (odd) {
+    if (rank == 0 && tid == 0) {
+      if (isnan(total.h) || m == INFINITY) report(a, r, -1, NAN, NAN, 0);
+      else if (m == -INFINITY) report(a, r, -1, -INFINITY, -INFINITY, 0);
+      else report(a, r, kUndecided, 0.0f, 0.0f, 0);
+    }
+  } else if (!by_k && !by_p && !by_q) {
+    if (rank == sh.owner) {
+      int32_t a0, a1;
+      share(rank, sh.owner_warp, a0, a1);
+      const int32_t some = (a1 - a0 + W - 1) / W;
+      const int32_t b0 = min(a1, a0 + warp * some), b1 = min(a1, b0 + some);
+      const uint64_t nm2 = both(-m);
+      auto exponentials = [&](uint4 u, float (&p)[N]) {
+        uint64_t v[N / 2];
+        floored_pairs<In>(u, v);
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          float y0, y1;
+          ptx::f32x2_unpack(pair_mul(add2(v[e], nm2), c2), y0, y1);
+          p[2 * e] = ex2(y0);
+          p[2 * e + 1] = ex2(y1);
+        }
+      };
+      auto sum_of = [&](const float (&p)[N]) {
+        const float s = (p[0] + p[1]) + (p[2] + p[3]);
+        return N == 8 ? s + ((p[N - 4] + p[N - 3]) + (p[N - 2] + p[N - 1])) : s;
+      };
+      Pair mass;
+      for (int32_t p0 = b0; p0 < b1; p0 += 32 * U) {
+        uint4 u[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) u[i] = p0 + 32 * i + lane < b1 ? row.load(p0 + 32 * i + lane) : absent<In>();
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          float p[N];
+          exponentials(u[i], p);
+          mass = mass + Pair{sum_of(p), 0.0f};
+        }
+      }
+      mass = scan_lanes(mass);
+      if (lane == 31) sh.part[warp] = mass;
+      __syncthreads();
+      Pair left = sh.left, start, run;
+      int mine = 0;
+      for (int i = 0; i < W; ++i) {
+        const Pair v = sh.part[i];
+        if (v.h > 0.0f && run <= left) {
+          mine = i;
+          start = run;
+        }
+        run = run + v;
+      }
+      left = left - start;
+      if (mine == warp) {
+        // pieces in the row's order, 32 at a time; rest: what is left of u W ahead of them
+        Pair rest = left;
+        float under = -1.0f, over = -1.0f, x = 0.0f;
+        int32_t token = kUndecided;
+        for (int32_t p0 = b0; p0 < b1 && rest.h >= 0.0f; p0 += 32) {
+          const uint4 u = p0 + lane < b1 ? row.load(p0 + lane) : absent<In>();
+          float p[N], v[N];
+          exponentials(u, p);
+          values<In>(u, v);
+          const float own = sum_of(p);
+          float incl = own;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const float o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+          }
+          float before = incl - own;
+          const uint32_t can = __ballot_sync(0xffffffffu, own > 0.0f && before <= rest.h);
+          if (can) {
+            int32_t j = 0;
+            float lo = 0.0f, hi = 0.0f, xj = 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              if (p[e] > 0.0f && before <= rest.h) {
+                j = (p0 + lane) * N - row.off + e;
+                xj = v[e];
+                lo = rest.h - before;
+                hi = before + p[e] - rest.h;
+              }
+              before += p[e];
+            }
+            const int from = 31 - __clz(can);
+            token = __shfl_sync(0xffffffffu, j, from);
+            x = __shfl_sync(0xffffffffu, xj, from);
+            under = __shfl_sync(0xffffffffu, lo, from);
+            over = __shfl_sync(0xffffffffu, hi, from);
+          }
+          rest = rest - Pair{__shfl_sync(0xffffffffu, incl, 31), 0.0f};
+        }
+        if (lane == 0) {
+          // both the sum ahead of the token and u W may be off by err, the last steps' by theirs
+          const float margin = fmaf(2.0f, err, 24.0f * kStep * total.h);
+          if (under >= margin && over >= margin) {
+            const float y = (x - m) / draw.temperature, lp = y - log_of(total);
+            report(a, r, token, lp, lp, (int32_t)finite);
+          } else {
+            report(a, r, kUndecided, 0.0f, 0.0f, 0);
+          }
+        }
+      }
+    }
+  } else if (CUT) {
+    // what may be kept: at or above tau, the border, and the last bin of the thread maxima that reach top_p's mass
+    const float tau = by_k ? sh.tau : -INFINITY;
+    const float c4 = 4.0f * c;
+    int last_bin = INT_MAX;
+    if (by_p && !by_k) {
+      for (int q = 0; q < ranks; ++q) {
+        const float v = __uint_as_float(ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&cs.most[tid]), q)));
+        const float t = (m - v) * c4;
+        if (t < (float)kMassBins) atomicAdd(&cs.bins[(int)t], (uint32_t)(ex2(-0.25f * t) * 0x1.fff8p+19f));
+      }
+      __syncthreads();
+      if (warp == 0) {
+        uint32_t n[4], own = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          n[i] = cs.bins[4 * lane + i];
+          own += n[i];
+        }
+        uint32_t incl = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += o;
+        }
+        uint32_t run = incl - own;
+        const float want = draw.top_p * (total.h + 2.0f * err) * 0x1p+20f * (1.0f + 8.0f * kStep);
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          uint32_t upto = run;
+          for (int e = 0; e <= i; ++e) upto += n[e];
+          if (__uint2float_rd(upto) >= want) atomicMin(&cs.last_bin, 4 * lane + i);
+        }
+      }
+      __syncthreads();
+      last_bin = cs.last_bin;
+    }
+    const bool flat = by_p && !by_k && last_bin == INT_MAX;  // not even all maxima reach it
+    const float border = by_q ? border_of(m, ranks > 1 ? __hiloint2double((int)ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&cs.reach), 0) + 4),
+                                                                           (int)ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&cs.reach), 0)))
+                                                       : cs.reach)
+                              : -INFINITY;
+    const bool possible = a.vocab <= kCap || (!flat && (!by_k || (by_rank && tau > -INFINITY)));
+    const float least = fmaxf(tau, by_p ? -INFINITY : border);  // (top_p's mass counts what min_p cuts off)
+    auto may = [&](float v) {
+      return v > -INFINITY && v >= least && (last_bin == INT_MAX || (m - v) * c4 < (float)(last_bin + 1));
+    };
+    if (possible) {
+      // the elements of the threads whose maxima may be kept, spread over all threads
+      if (may(cs.most[tid])) cs.cand[atomicAdd(&cs.cands, 1)] = (int16_t)tid;
+      __syncthreads();
+      const int32_t rounds = (each + 31) / 32, items = cs.cands * rounds;
+      for (int32_t f = tid; f < items; f += T) {
+        const int who = cs.cand[f / rounds];
+        int32_t b0, b1;
+        share(rank, who >> 5, b0, b1);
+        const int32_t p = b0 + (who & 31) + 32 * (f % rounds);
+        if (p >= b1) continue;
+        float v[N];
+        values<In>(row.load(p), v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          if (!may(v[e])) continue;
+          const int at = atomicAdd(&cs.hits, 1);
+          if (at < kCap) cs.list[at] = (uint64_t)ordered(v[e]) << 32 | (uint32_t) ~(p * N - row.off + e);
+        }
+      }
+    }
+    if (ranks > 1) ptx::cluster_sync();
+    else __syncthreads();
+    if (rank == 0) {
+      int n = 0;
+      bool whole = possible;
+      for (int q = 0; q < ranks; ++q) {
+        const int h = (int)ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&cs.hits), q));
+        if (n + h <= kCap && h <= kCap) {
+          for (int i = tid; i < h; i += T) {
+            const uint32_t at = ptx::mapa_shared(ptx::smem_u32(&cs.list[i]), q);
+            cs.key[n + i] = (uint64_t)ptx::ld_dsmem_u32(at + 4) << 32 | ptx::ld_dsmem_u32(at);
+          }
+          n += h;
+        } else {
+          whole = false;
+        }
+      }
+      if (!whole || n < 1) {
+        if (tid == 0) report(a, r, kUndecided, 0.0f, 0.0f, 0);
+      } else {
+        int n2 = 2;
+        while (n2 < n) n2 *= 2;
+        for (int i = n + tid; i < n2; i += T) cs.key[i] = 0;
+        sort_down<T>(cs.key, n2);
+        const Scale s = scale_of(m, draw.temperature);
+        for (int i = tid; i < n; i += T) {
+          uint64_t h, l;
+          float h0, l0, none;
+          const float x = from_ordered((uint32_t)(cs.key[i] >> 32));
+          weights(s, cs.table, x, -INFINITY, h, l);
+          ptx::f32x2_unpack(h, h0, none);
+          ptx::f32x2_unpack(l, l0, none);
+          cs.w[i] = normal(h0, l0);
+          if (x >= border) atomicAdd(&cs.n_border, 1);
+        }
+        __syncthreads();
+        const int n_k = by_k ? (int)min((int64_t)n, k) : n;
+        int n_kept = n_k;
+        bool sure = true;
+        if (by_p) {
+          // how many sums lie below top_p's share (of the sum known to err: below its least and its largest)
+          Pair low = total + Pair{-err, 0.0f}, high = total + Pair{err, 0.0f};
+          if (by_k || n == (int)finite) low = high = sums_of<T>(cs.w, n_k, cs.part, [](int, Pair, Pair) {});
+          const Pair p{draw.top_p, 0.0f};
+          low = p * low;
+          high = p * high;
+          sums_of<T>(cs.w, n_k, cs.part, [&](int, Pair, Pair with) {
+            if (with < low) atomicAdd(&cs.below[0], 1);
+            if (with < high) atomicAdd(&cs.below[1], 1);
+          });
+          __syncthreads();
+          sure = cs.below[0] == cs.below[1] && cs.below[1] < n_k;
+          n_kept = min(n_kept, cs.below[0] + 1);
+        }
+        n_kept = min(n_kept, cs.n_border);
+        if (!sure) {
+          if (tid == 0) report(a, r, kUndecided, 0.0f, 0.0f, 0);
+        } else {
+          // the kept ones in the row's order, with their place among the sorted
+          n2 = 2;
+          while (n2 < n_kept) n2 *= 2;
+          for (int i = tid; i < n2; i += T) cs.list[i] = i < n_kept ? cs.key[i] << 32 | (uint32_t)i : 0;
+          sort_down<T>(cs.list, n2);
+          // (sorted keys low words are ~index: the largest first is the lowest index first)
+          const Pair mass = sums_of<T>(cs.w, n_kept, cs.part, [](int, Pair, Pair) {});
+          constexpr int E = kCap / T;
+          Pair w[E];
+#pragma unroll
+          for (int i = 0; i < E; ++i) w[i] = tid * E + i < n_kept ? cs.w[(uint32_t)cs.list[tid * E + i]] : Pair{};
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (tid * E + i < n_kept) cs.w[tid * E + i] = w[i];
+          __syncthreads();
+          const Pair goal = pair_from(draw.u) * mass;
+          sums_of<T>(cs.w, n_kept, cs.part, [&](int i, Pair before, Pair) {
+            if (cs.w[i].h > 0.0f && before <= goal) atomicMax(&cs.token, i);
+          });
+          __syncthreads();
+          if (tid == 0) {
+            const uint64_t key = cs.list[max(cs.token, 0)];
+            const float x = from_ordered((uint32_t)(cs.key[(uint32_t)key] >> 32)), y = (x - m) / draw.temperature;
+            report(a, r, (int32_t) ~(uint32_t)(key >> 32), y - log_of(total), y - log_of(mass), n_kept);
+          }
+        }
+      }
+    }
+  }
+  if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's shared memory
+}
+
+// ------------------------------------------------------------------ exact
+
+// grid (cluster, clusters): the rows that the pass has left
 template <typename In>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads) sample_exact_kernel(const SampleArgs a) {
   __shared__ __align__(16) unsigned char smem[sizeof(Shared)];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   constexpr int N = Row<In>::N;
   ptx::grid_dep_launch_dependents();
   ptx::grid_dep_wait();
-  const int64_t r = blockIdx.y;
   const uint32_t rank = blockIdx.x, ranks = gridDim.x;
-  const double u = a.uniform[r];
-  float temperature = a.temperature ? a.temperature[r] : a.t;
-  float top_p = a.top_p ? a.top_p[r] : a.p, min_p = a.min_p ? a.min_p[r] : a.q;
-  int64_t k = a.top_k ? a.top_k[r] : a.k;
-  // no draw for this row: the whole cluster leaves
-  if (!(u >= 0.0 && u < 1.0) || !(temperature >= 0.0f && temperature <= FLT_MAX) || isnan(top_p) || isnan(min_p)) {
-    if (rank == 0 && threadIdx.x == 0) report(a, r, -1, 0.0f, 0.0f, 0);
-    return;
-  }
-  if (temperature == 0.0f) {
-    temperature = 1.0f;
-    k = 1;
-  }
-  if (top_p <= 0.0f) k = 1;
-  temperature = fminf(fmaxf(temperature, 1e-30f), 1e30f);
-  for (int i = threadIdx.x; i < 256; i += kThreads) sh.table[i] = kExp2.v[i];
-
-  Team<In> team(sh, static_cast<const In*>(a.x) + r * a.ld, a.vocab, rank, ranks);
-  Part p;
-  team.each(team.w0, team.w1, [&](float (&v)[N], int32_t) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      p.most = max_nan(p.most, v[e]);
-      p.n += v[e] > -INFINITY;
+  bool first = true;
+  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+    if (__ldcg(a.tokens + r) != kUndecided) continue;
+    if (first) {
+      for (int i = threadIdx.x; i < 256; i += kThreads) sh.table[i] = kExp2.v[i];
+      first = false;
     }
-  });
-  p = team.gather(p);
-  const float m = p.most;
-  const uint32_t finite = p.n;
-  if (!(m <= FLT_MAX && m >= -FLT_MAX)) {  // NaN or +inf; -inf alone
-    const float lp = m == -INFINITY ? -INFINITY : NAN;
-    if (rank == 0 && threadIdx.x == 0) report(a, r, -1, lp, lp, 0);
-    if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's sums
-    return;
-  }
-  if (threadIdx.x == 0) {
-    const double c = kLog2e / (double)temperature;
-    Scale s;
-    s.m = m;
-    s.hi = (float)c;
-    s.lo = (float)(c - (double)s.hi);
-    s.cut = fmaxf(__double2float_ru((double)m - (double)kReach * kLn2 * (double)temperature), -FLT_MAX);
-    sh.scale = s;
-    sh.border = min_p > 0.0f ? __double2float_ru((double)m + (double)temperature * log((double)fminf(min_p, 1.0f))) : -INFINITY;
-  }
-  __syncthreads();
-  const Scale s = sh.scale;
-
-  // all weights; then the cut, and the kept ones
-  Keep keep;
-  p = team.gather(team.mass(s, keep, team.w0, team.w1));
-  const double total = p.a;
-  const bool by_k = k > 0 && k < (int64_t)finite, by_p = top_p < 1.0f && top_p > 0.0f;
-  if (by_k) team.select(s, keep, true, (uint32_t)k, 0.0, 0.0);
-  if (by_p) {
-    const double all = by_k ? team.gather(team.mass(s, keep, team.w0, team.w1)).a : total;
-    team.select(s, keep, false, 0, (double)top_p * all, all);
-  }
-  keep.border = sh.border;
-  if (by_k || by_p || keep.border > -INFINITY) p = team.gather(team.mass(s, keep, team.w0, team.w1));
-  const double mass = p.a;
-  const int32_t kept = (int32_t)p.n;
-
-  // the last CTA, warp, part and piece with a mass of its own whose predecessors' mass is at most u W
-  double left = u * mass;
-  auto descend = [&](int n, auto mass_of) {
-    int at = 0;
-    double sum = 0.0, start = 0.0;
-    for (int i = 0; i < n; ++i) {
-      const double v = mass_of(i);
-      if (v > 0.0 && sum <= left) {
-        at = i;
-        start = sum;
+    Draw draw;
+    draw.load(a, r);
+    Team<In> team(sh, static_cast<const In*>(a.x) + r * a.ld, a.vocab, rank, ranks);
+    Part p;
+    team.each(team.w0, team.w1, [&](float (&v)[N], int32_t) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        p.most = fmaxf(p.most, v[e]);
+        p.n += v[e] > -INFINITY;
       }
-      sum += v;
+    });
+    p = team.gather(p);
+    const float m = p.most;
+    const uint32_t finite = p.n;
+    const Scale s = scale_of(m, draw.temperature);
+    if (threadIdx.x == 0) sh.border = draw.min_p > 0.0f ? border_of(m, draw.reach()) : -INFINITY;
+
+    // all weights; then the cut, and the kept ones
+    Keep keep;
+    p = team.gather(team.mass(s, keep, team.w0, team.w1));
+    const Pair total = p.a;
+    const bool by_k = draw.k > 0 && draw.k < (int64_t)finite, by_p = draw.top_p < 1.0f && draw.top_p > 0.0f;
+    if (by_k) team.select(s, keep, true, (uint32_t)draw.k, Pair{}, Pair{1.0f, 0.0f});
+    if (by_p) {
+      const Pair all = by_k ? team.gather(team.mass(s, keep, team.w0, team.w1)).a : total;
+      team.select(s, keep, false, 0, Pair{draw.top_p, 0.0f} * all, all);
     }
-    left -= start;
-    return at;
-  };
-  const int owner = descend((int)ranks, [&](int i) { return sh.all[i].a; });
-  if (owner == (int)rank) {
-    const int w = descend(kWarps, [&](int i) { return sh.warp[i].a; });
-    int32_t a0, a1;
-    team.share(rank, w, a0, a1);
-    const int32_t each = (a1 - a0 + kWarps - 1) / kWarps;
-    const int32_t b0 = min(a1, a0 + team.warp * each), b1 = min(a1, b0 + each);
-    const Part part = merge_lanes<32>(team.mass(s, keep, b0, b1));
-    if (team.lane == 0) sh.part[team.warp] = part.a;
-    __syncthreads();
-    const int mine = descend(kWarps, [&](int i) { return sh.part[i]; });
-    if (mine == team.warp) {
-      int32_t token = -1;
-      float x = 0.0f;
-      double sum = 0.0;
-      for (int32_t p0 = b0; p0 < b1 && sum <= left; p0 += 32) {
-        float v[N];
-        values<In>(p0 + team.lane < b1 ? team.row.load(p0 + team.lane) : absent<In>(), v);
-        const int32_t j0 = (p0 + team.lane) * N - team.row.off;
-        double w_of[N], own = 0.0;
-#pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          uint64_t h, l;
-          weights(s, sh.table, keep(v[e], j0 + e) ? v[e] : -INFINITY, keep(v[e + 1], j0 + e + 1) ? v[e + 1] : -INFINITY, h, l);
-          float h0, h1, l0, l1;
-          ptx::f32x2_unpack(h, h0, h1);
-          ptx::f32x2_unpack(l, l0, l1);
-          w_of[e] = (double)h0 + (double)l0;
-          w_of[e + 1] = (double)h1 + (double)l1;
-          own += w_of[e] + w_of[e + 1];
+    keep.border = sh.border;
+    if (by_k || by_p || keep.border > -INFINITY) p = team.gather(team.mass(s, keep, team.w0, team.w1));
+    const Pair mass = p.a;
+    const int32_t kept = (int32_t)p.n;
+
+    // the last CTA, warp, part and piece with a mass of its own whose predecessors' mass is at most u W
+    Pair left = pair_from(draw.u) * mass;
+    auto descend = [&](int n, auto mass_of) {
+      int at = 0;
+      Pair sum, start;
+      for (int i = 0; i < n; ++i) {
+        const Pair v = mass_of(i);
+        if (v.h > 0.0f && sum <= left) {
+          at = i;
+          start = sum;
         }
-        double incl = own;
+        sum = sum + v;
+      }
+      left = left - start;
+      return at;
+    };
+    const int owner = descend((int)ranks, [&](int i) { return sh.all[i].a; });
+    if (owner == (int)rank) {
+      const int w = descend(kWarps, [&](int i) { return sh.warp[i].a; });
+      int32_t a0, a1;
+      team.share(rank, w, a0, a1);
+      const int32_t each = (a1 - a0 + kWarps - 1) / kWarps;
+      const int32_t b0 = min(a1, a0 + team.warp * each), b1 = min(a1, b0 + each);
+      const Part part = merge_lanes<32>(team.mass(s, keep, b0, b1));
+      if (team.lane == 0) sh.part[team.warp] = part.a;
+      __syncthreads();
+      const int mine = descend(kWarps, [&](int i) { return sh.part[i]; });
+      if (mine == team.warp) {
+        int32_t token = -1;
+        float x = 0.0f;
+        Pair sum;
+        for (int32_t p0 = b0; p0 < b1 && sum <= left; p0 += 32) {
+          float v[N];
+          values<In>(p0 + team.lane < b1 ? team.row.load(p0 + team.lane) : absent<In>(), v);
+          const int32_t j0 = (p0 + team.lane) * N - team.row.off;
+          Pair w_of[N], own;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const double o = __shfl_up_sync(0xffffffffu, incl, d);
-          if (team.lane >= d) incl += o;
-        }
-        double before = sum + (incl - own);
-        const uint32_t can = __ballot_sync(0xffffffffu, own > 0.0 && before <= left);
-        int32_t j = -1;
-        float xj = 0.0f;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          if (w_of[e] > 0.0 && before <= left) {
-            j = j0 + e;
-            xj = v[e];
+          for (int e = 0; e < N; e += 2) {
+            uint64_t h, l;
+            weights(s, sh.table, keep(v[e], j0 + e) ? v[e] : -INFINITY, keep(v[e + 1], j0 + e + 1) ? v[e + 1] : -INFINITY, h, l);
+            float h0, h1, l0, l1;
+            ptx::f32x2_unpack(h, h0, h1);
+            ptx::f32x2_unpack(l, l0, l1);
+            w_of[e] = normal(h0, l0);
+            w_of[e + 1] = normal(h1, l1);
+            own = own + w_of[e];
+            own = own + w_of[e + 1];
           }
-          before += w_of[e];
+          const Pair incl = scan_lanes(own);
+          Pair before = shuffle_up(incl, 1);
+          if (team.lane == 0) before = Pair{};
+          before = sum + before;
+          const uint32_t can = __ballot_sync(0xffffffffu, own.h > 0.0f && before <= left);
+          int32_t j = -1;
+          float xj = 0.0f;
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            if (w_of[e].h > 0.0f && before <= left) {
+              j = j0 + e;
+              xj = v[e];
+            }
+            before = before + w_of[e];
+          }
+          if (can) {
+            const int from = 31 - __clz(can);
+            token = __shfl_sync(0xffffffffu, j, from);
+            x = __shfl_sync(0xffffffffu, xj, from);
+          }
+          sum = sum + shuffle(incl, 31);
         }
-        if (can) {
-          const int from = 31 - __clz(can);
-          token = __shfl_sync(0xffffffffu, j, from);
-          x = __shfl_sync(0xffffffffu, xj, from);
+        if (team.lane == 0) {
+          const float y = (x - m) / draw.temperature;
+          report(a, r, token, y - log_of(total), y - log_of(mass), kept);
         }
-        sum += __shfl_sync(0xffffffffu, incl, 31);
-      }
-      if (team.lane == 0) {
-        const float y = (x - m) / temperature;
-        report(a, r, token, y - log_of(total), y - log_of(mass), kept);
       }
     }
+    if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's shared memory
+    else __syncthreads();
   }
-  if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's shared memory
 }
 
 int sm_count() {
@@ -771,15 +1434,11 @@ bool check_word(uint32_t** err) {
 constexpr int64_t kMaxRows = 65535;             // grid y
 constexpr int64_t kMaxVocab = (int64_t)1 << 30;  // 32-bit element and piece numbers
 
-template <typename In>
-cudaError_t launch_sample(const SampleArgs& a, int64_t rows, cudaStream_t stream) {
-  // few rows are split over a cluster, down to a load round per CTA
-  const int64_t want = 4 * (int64_t)sm_count(), round = (int64_t)kThreads * kUnroll * Row<In>::N;
-  int cluster = 1;
-  while (cluster < kMaxCluster && rows * cluster < want && (int64_t)a.vocab > cluster * round) cluster *= 2;
+template <typename K>
+cudaError_t launch(K kernel, const SampleArgs& a, int cluster, int64_t rows, int threads, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster, (unsigned)rows);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -789,7 +1448,28 @@ cudaError_t launch_sample(const SampleArgs& a, int64_t rows, cudaStream_t stream
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<In>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename In>
+cudaError_t launch_sample(const SampleArgs& a, int64_t rows, cudaStream_t stream) {
+  const bool cut = a.temperature || a.top_k || a.top_p || a.min_p || a.k > 0 || a.p < 1.0f || a.q > 0.0f || a.t == 0.0f;
+  const int64_t pieces = ((int64_t)a.vocab + Row<In>::N - 1) / Row<In>::N;
+  cudaError_t e;
+  if (pieces <= 256) {
+    e = cut ? launch(sample_kernel<In, true, 64>, a, 1, rows, 64, stream) : launch(sample_kernel<In, false, 64>, a, 1, rows, 64, stream);
+  } else {
+    // few rows are split over a cluster, down to a load round per CTA
+    const int64_t want = 7 * (int64_t)sm_count() / 2, round = (int64_t)kThreads * 4;
+    int cluster = 1;
+    while (cluster < kMaxCluster && rows * cluster < want && pieces > cluster * round) cluster *= 2;
+    e = cut ? launch(sample_kernel<In, true, 256>, a, cluster, rows, 256, stream)
+            : launch(sample_kernel<In, false, 256>, a, cluster, rows, 256, stream);
+  }
+  if (e != cudaSuccess) return e;
+  int cluster = 1;
+  while (cluster < kMaxCluster && pieces > (int64_t)cluster * kThreads * kUnroll) cluster *= 2;
+  return launch(sample_exact_kernel<In>, a, cluster, std::min<int64_t>(rows, std::max(1, 2 * sm_count() / cluster)), kThreads, stream);
 }
 
 }  // namespace
