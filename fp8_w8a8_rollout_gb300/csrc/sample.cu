@@ -43,10 +43,13 @@
 namespace fp8rl {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the exact kernel
-constexpr int kUnroll = 4;
+constexpr int kThreads = 512, kWarps = kThreads / 32;  // of the exact kernel
+constexpr int kUnroll = 2;
 constexpr int kBins = 1024;
-constexpr int kList = 256;  // elements that are sorted, one a thread
+constexpr int kBinades = 12;                           // of bf16 values that have bins of their own
+constexpr int kValues = 2 * 128 * kBinades + 2;        // (+ the ones nearer to 0, + the ones below)
+constexpr int kList = 256;  // elements that are sorted, at most one a thread
+static_assert(kList <= kThreads && kBins % kThreads == 0, "threads take list entries and bins by their number");
 constexpr int kMaxCluster = 8;
 constexpr float kReach = 100.0f;  // weights below 2^-100 count as 0
 constexpr int32_t kUndecided = -2;  // the token of a row that is left to the exact kernel
@@ -103,6 +106,10 @@ __device__ __forceinline__ bool operator<=(Pair a, Pair b) { return !(b < a); }
 __device__ __forceinline__ Pair pair_from(double v) {
   const float h = (float)v;
   return Pair{h, (float)(v - (double)h)};
+}
+__device__ __forceinline__ Pair pair_from(uint32_t n) {  // n < 2^31
+  const float h = (float)n;
+  return Pair{h, (float)((int32_t)n - (int32_t)h)};
 }
 __device__ __forceinline__ Pair shuffle_up(Pair a, int d) {
   return Pair{__shfl_up_sync(0xffffffffu, a.h, d), __shfl_up_sync(0xffffffffu, a.l, d)};
@@ -232,7 +239,7 @@ __device__ __forceinline__ Part merge_lanes(Part v) {
 
 struct Shared {
   float2 table[256];
-  uint32_t hist[kBins];
+  uint32_t hist[(kValues + 3) / 4 * 4];
   uint64_t list[kList], sorted[kList];
   Pair mass[kList];
   Part warp[kWarps];       // the last gather's sums of this CTA's warps
@@ -241,6 +248,8 @@ struct Shared {
   Pair part[kWarps];
   float border;            // min-p's
   int32_t n_list, bin, last;
+  uint32_t ahead;          // elements, and mass, ahead of `bin`
+  Pair ahead_mass;
 };
 
 // kept: at or above `border`, and above `x` or equal to it at an index up to j
@@ -352,6 +361,217 @@ struct Team {
     return p;
   }
 
+  // The same of this warp's pieces, a contiguous run of them for each lane
+  __device__ __forceinline__ int32_t run() const { return (w1 - w0 + 31) / 32; }
+  __device__ Part mass_of_run(const Scale& s, const Keep& keep) const {
+    Sum sum;
+    uint32_t n = 0;
+    const int32_t a = w0 + lane * run();
+    for (int32_t i = 0; i < run(); ++i) {
+      const int32_t j0 = (a + i) * N - row.off;
+      float v[N];
+      values<In>(a + i < w1 ? row.load(a + i) : absent<In>(), v);
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (keep(v[e], j0 + e)) {
+          ++n;
+          any = true;
+        } else {
+          v[e] = -INFINITY;
+        }
+      }
+      if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        uint64_t h, l;
+        weights(s, sh.table, v[e], v[e + 1], h, l);
+        sum.add(h, l);
+      }
+    }
+    Part p;
+    p.a = sum.value();
+    p.n = n;
+    return p;
+  }
+
+  // Top-k and top-p of bf16 rows by the values themselves: every value in 12 binades has a bin that
+  // counts it, so a bin's mass is its count times one weight and a cut needs no second look.
+  // False where a cut falls among the values nearer to 0 than that (or far below): nothing is changed then.
+  __device__ bool by_value(const Scale& s, Keep& keep, uint32_t k, float top_p, Pair& total) {
+    constexpr int kEach = (kValues + kThreads - 1) / kThreads, kTiny = 128 * kBinades, kRest = kValues - 1;
+    // the binades below the largest magnitude that matters
+    const float far = fmaxf(fabsf(s.m), s.hi > 0.0f ? 64.0f / s.hi - s.m : 0.0f);
+    const int32_t lowest = max(0, (int32_t)((__float_as_uint(fminf(far, FLT_MAX)) >> 23) - (kBinades - 1))) << 7;  // its upper 16 bits
+    auto place = [&](float x) {
+      const uint32_t b = __float_as_uint(x) >> 16;
+      const int32_t g = (int32_t)(b & 0x7FFFu) - lowest;  // magnitudes in steps of bf16
+      if (g < 0 || (b & 0x7FFFu) == 0) return kTiny;  // (zeros of both signs together)
+      if (b >> 15) return g < kTiny ? kTiny + 1 + g : kRest;
+      return kTiny - 1 - g;  // (no value is above the maximum's binade)
+    };
+    auto value_at = [&](int b) {
+      const uint32_t g = (uint32_t)(b < kTiny ? kTiny - 1 - b : b - kTiny - 1) + (uint32_t)lowest;
+      return __uint_as_float((b < kTiny ? g : g | 0x8000u) << 16);
+    };
+    for (int i = threadIdx.x; i < kValues; i += kThreads) sh.hist[i] = 0;
+    __syncthreads();
+    each(w0, w1, [&](float (&v)[N], int32_t) {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (v[e] > -INFINITY) atomicAdd(&sh.hist[place(v[e])], 1u);
+    });
+    if (ranks > 1) ptx::cluster_sync();
+    else __syncthreads();
+    uint32_t count[kEach], n_own = 0;
+    Pair mass[kEach], own;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int b = threadIdx.x * kEach + i;
+      count[i] = 0;
+      if (b < kValues)
+        for (uint32_t r = 0; r < ranks; ++r) count[i] += ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&sh.hist[b]), r));
+      mass[i] = Pair{};
+      if (count[i] > 0 && b != kTiny && b != kRest) {
+        uint64_t h, l;
+        weights(s, sh.table, value_at(b), -INFINITY, h, l);
+        float h0, l0, none;
+        ptx::f32x2_unpack(h, h0, none);
+        ptx::f32x2_unpack(l, l0, none);
+        mass[i] = normal(h0, l0) * pair_from(count[i]);
+      }
+      n_own += count[i];
+    }
+    // the tiny ones' mass, exactly
+    Part tiny;
+    each(w0, w1, [&](float (&v)[N], int32_t) {
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (v[e] > -INFINITY && place(v[e]) == kTiny) any = true;
+        else v[e] = -INFINITY;
+      }
+      if (!__any_sync(0xffffffffu, any)) return;
+      Sum sum;
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        uint64_t h, l;
+        weights(s, sh.table, v[e], v[e + 1], h, l);
+        sum.add(h, l);
+      }
+      tiny.a = tiny.a + sum.value();
+    });
+    tiny = gather(tiny);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (threadIdx.x * kEach + i == kTiny) mass[i] = tiny.a;
+      own = own + mass[i];
+    }
+    // counts and masses ahead of this thread's bins
+    uint32_t n_run = n_own;
+    Pair run = scan_lanes(own);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, n_run, d);
+      if (lane >= d) n_run += o;
+    }
+    if (lane == 31) {
+      sh.part[warp] = run;
+      sh.warp[warp].k = n_run;
+    }
+    run = shuffle_up(run, 1);
+    if (lane == 0) run = Pair{};
+    n_run -= n_own;
+    __syncthreads();
+    Pair all;
+    uint32_t finite = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) {
+        run = all + run;
+        n_run += finite;
+      }
+      all = all + sh.part[w];
+      finite += sh.warp[w].k;
+    }
+    total = all;
+    // (a bin, and how many of it are kept)
+    int bin = -1;
+    uint32_t need = 0, have = 0;
+    auto found = [&](auto reached) {  // the first bin at whose end `reached` holds; every thread hears of it
+      if (threadIdx.x == 0) sh.bin = INT_MAX;
+      __syncthreads();
+      uint32_t n = n_run;
+      Pair m = run;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (count[i] == 0) continue;
+        n += count[i];
+        m = m + mass[i];
+        if (reached(n, m)) {
+          atomicMin(&sh.bin, (int)threadIdx.x * kEach + i);
+          break;
+        }
+      }
+      __syncthreads();
+      const int b = sh.bin;
+      if (b / kEach == (int)threadIdx.x) {
+        n = n_run;
+        m = run;
+        for (int i = 0; i < b % kEach; ++i) {
+          n += count[i];
+          m = m + mass[i];
+        }
+        sh.ahead = n;
+        sh.ahead_mass = m;
+        sh.last = (int)count[b % kEach];
+      }
+      __syncthreads();
+      return b;
+    };
+    Pair mass_k = all;
+    if (k > 0) {
+      bin = found([&](uint32_t n, Pair) { return n >= k; });
+      if (bin == kTiny || bin == kRest) return false;
+      need = k - sh.ahead;
+      have = (uint32_t)sh.last;
+      uint64_t h, l;
+      weights(s, sh.table, value_at(bin), -INFINITY, h, l);
+      float h0, l0, none;
+      ptx::f32x2_unpack(h, h0, none);
+      ptx::f32x2_unpack(l, l0, none);
+      mass_k = sh.ahead_mass + normal(h0, l0) * pair_from(need);
+    }
+    if (top_p < 1.0f) {
+      const Pair target = Pair{top_p, 0.0f} * mass_k;
+      const int b = found([&](uint32_t, Pair m) { return target <= m; });
+      if (b == kTiny || b == kRest) return false;
+      if (b < kValues && (bin < 0 || b <= bin)) {  // (no bin: rounding; all of them, or the first k)
+        const uint32_t most = b == bin ? need : (uint32_t)sh.last;
+        uint64_t h, l;
+        weights(s, sh.table, value_at(b), -INFINITY, h, l);
+        float h0, l0, none;
+        ptx::f32x2_unpack(h, h0, none);
+        ptx::f32x2_unpack(l, l0, none);
+        need = first_reaching(target - sh.ahead_mass, normal(h0, l0), most);
+        bin = b;
+        have = (uint32_t)sh.last;
+      }
+    }
+    if (bin < 0) return true;
+    keep.x = value_at(bin);
+    keep.j = need >= have ? INT_MAX : nth_equal(keep.x, keep, need);
+    return true;
+  }
+
+  // the smallest n in [1, most] with n w >= left
+  static __device__ uint32_t first_reaching(Pair left, Pair w, uint32_t most) {
+    const double a = (double)left.h + (double)left.l, b = (double)w.h + (double)w.l;
+    const double n = b > 0.0 ? ceil(a / b) : 1.0;
+    uint32_t need = (uint32_t)fmin(fmax(n, 1.0), (double)most);
+    if (need > 1 && (double)(need - 1) * b >= a) --need;
+    return need;
+  }
+
   // The index of the need-th element (from 1) with value x among the kept, in the row's order
   __device__ int32_t nth_equal(float x, const Keep& keep, uint32_t need) {
     Part p;
@@ -428,25 +648,23 @@ struct Team {
       });
       if (ranks > 1) ptx::cluster_sync();
       else __syncthreads();
-      // the cluster's bins, four a thread
-      uint32_t c[4] = {0, 0, 0, 0};
-      float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (uint32_t r = 0; r < ranks; ++r) {
-        const float4 v = ptx::ld_dsmem_f32x4(ptx::mapa_shared(ptx::smem_u32(&sh.hist[4 * threadIdx.x]), r));
-        const uint32_t w[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
+      // the cluster's bins, some a thread
+      constexpr int kEach = kBins / kThreads;
+      uint32_t c[kEach];
+      float f[kEach];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          c[i] += w[i];
-          f[i] += (float)w[i];
-        }
+      for (int i = 0; i < kEach; ++i) {
+        c[i] = 0;
+        for (uint32_t r = 0; r < ranks; ++r) c[i] += ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&sh.hist[kEach * threadIdx.x + i]), r));
+        f[i] = (float)c[i];
       }
       // the first bin in which the running sum reaches what is asked for (counts exactly, masses nearly)
       const float t0 = (s.m - hi) * s.hi;
       uint32_t n_run = 0, n_own = 0;
       float f_run = 0.0f, f_own = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] *= ex2(fmaxf(-t0 - (float)(4 * threadIdx.x + i) * step, -120.0f));
+      for (int i = 0; i < kEach; ++i) {
+        f[i] *= ex2(fmaxf(-t0 - (float)(kEach * threadIdx.x + i) * step, -120.0f));
         n_own += c[i];
         f_own += f[i];
       }
@@ -478,9 +696,9 @@ struct Team {
       // (the masses are up to 2^-13 small: as shares of their own sum, head and tail are good to that)
       const float share = (target - above).h / whole.h * f_all;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kEach; ++i) {
         if (c[i] == 0) continue;
-        const int b = 4 * threadIdx.x + i;
+        const int b = kEach * threadIdx.x + i;
         atomicMax(&sh.last, b);
         n_run += c[i];
         f_run += f[i];
@@ -563,10 +781,7 @@ struct Team {
           float h0, l0, none;
           ptx::f32x2_unpack(h, h0, none);
           ptx::f32x2_unpack(l, l0, none);
-          const double w = (double)h0 + (double)l0, left = (double)(target - above).h + (double)(target - above).l;
-          const double n = w > 0.0 ? ceil(left / w) : 1.0;
-          need = (uint32_t)fmin(fmax(n, 1.0), (double)t.k);
-          if (need > 1 && (double)(need - 1) * w >= left) --need;
+          need = first_reaching(target - above, normal(h0, l0), t.k);
         }
         need = max(1u, min(need, t.k));
         const int32_t j = need == t.k ? INT_MAX : nth_equal(t.most, keep, need);
@@ -614,22 +829,22 @@ struct Team {
           ptx::f32x2_unpack(h, h0, rest);
           ptx::f32x2_unpack(l, l0, rest);
           sh.mass[threadIdx.x] = normal(h0, l0);
-        } else {
+        } else if (threadIdx.x < kList) {
           sh.mass[threadIdx.x] = Pair{};
         }
         if (threadIdx.x == 0) sh.bin = n - 1;
         __syncthreads();
         if (warp == 0) {
-          constexpr int kEach = kList / 32;
+          constexpr int kEntries = kList / 32;
           Pair sum;
-          for (int i = 0; i < kEach; ++i) sum = sum + sh.mass[lane * kEach + i];
+          for (int i = 0; i < kEntries; ++i) sum = sum + sh.mass[lane * kEntries + i];
           Pair ahead = shuffle_up(scan_lanes(sum), 1);
           if (lane == 0) ahead = Pair{};
           Pair part = above + ahead;
-          for (int i = 0; i < kEach; ++i) {
-            part = part + sh.mass[lane * kEach + i];
+          for (int i = 0; i < kEntries; ++i) {
+            part = part + sh.mass[lane * kEntries + i];
             if (target <= part) {
-              atomicMin(&sh.bin, lane * kEach + i);
+              atomicMin(&sh.bin, lane * kEntries + i);
               break;
             }
           }
@@ -781,6 +996,92 @@ __device__ Pair sums_of(const Pair* w, int n, Pair* part, F f) {
     sum = with;
   }
   return all;
+}
+
+// the sum of the block's values up to and with this thread's, and of all
+template <int T>
+__device__ __forceinline__ Pair block_sums(Pair v, Pair* part, Pair& all) {
+  constexpr int W = T / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Pair incl = scan_lanes(v);
+  __syncthreads();  // the sums before have been read
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  Pair w = part[lane % W];
+#pragma unroll
+  for (int d = 1; d < W; d <<= 1) {
+    const Pair o = shuffle_up(w, d);
+    if (lane >= d) w = o + w;
+  }
+  all = shuffle(w, W - 1);
+  const Pair ahead = shuffle(w, (warp + 31) & 31);
+  return warp > 0 ? ahead + incl : incl;
+}
+
+// The draw from a list of at most one element a thread (rank 0's cs.key, in any order): `n_k` of them are the
+// first k, `exact`: the list's masses are what top_p goes by (else the sum, known to err).
+template <int T>
+__device__ void draw_from_few(const SampleArgs& a, int64_t r, CutShared<T>& cs, const Draw& draw, const Scale& s, int n, int n_k,
+                              bool by_p, bool exact, Pair total, float err, float border) {
+  const int tid = threadIdx.x;
+  if (tid == 0 && (n & 1)) cs.key[n] = 0;
+  __syncthreads();
+  // by value: each counts the ones ahead of it
+  const uint64_t mine = tid < n ? cs.key[tid] : 0;
+  int place = 0;
+  for (int i = 0; i < n; i += 2) {
+    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&cs.key[i]);
+    place += (two.x > mine) + (two.y > mine);
+  }
+  if (tid < n) cs.list[place] = mine;
+  __syncthreads();
+  const uint64_t key = tid < n ? cs.list[tid] : 0;
+  const float x = from_ordered((uint32_t)(key >> 32));
+  Pair w;
+  if (tid < n) {
+    uint64_t h, l;
+    weights(s, cs.table, x, -INFINITY, h, l);
+    float h0, l0, none;
+    ptx::f32x2_unpack(h, h0, none);
+    ptx::f32x2_unpack(l, l0, none);
+    w = normal(h0, l0);
+  }
+  Pair all;
+  const Pair upto = block_sums<T>(tid < n_k ? w : Pair{}, cs.part, all);
+  int n_kept = n_k;
+  if (by_p) {
+    // how many sums lie below top_p's share (of the sum known to err: below its least and its largest)
+    const Pair low = exact ? all : total + Pair{-err, 0.0f}, high = exact ? all : total + Pair{err, 0.0f}, p{draw.top_p, 0.0f};
+    const int n_low = __syncthreads_count(tid < n_k && upto < p * low);
+    const int n_high = exact ? n_low : __syncthreads_count(tid < n_k && upto < p * high);
+    if (n_low != n_high || n_high >= n_k) {
+      if (tid == 0) report(a, r, kUndecided, 0.0f, 0.0f, 0);
+      return;
+    }
+    n_kept = n_low + 1;
+  }
+  n_kept = min(n_kept, __syncthreads_count(tid < n && x >= border));
+  // in the row's order
+  const bool kept = tid < n_kept;
+  place = 0;
+  for (int i = 0; i < n_kept; ++i) place += (uint32_t)cs.list[i] > (uint32_t)key;  // (low words: ~index)
+  if (kept) {
+    cs.w[place] = w;
+    cs.key[place] = key;
+  }
+  __syncthreads();
+  w = kept ? cs.w[tid] : Pair{};
+  Pair mass;
+  const Pair with = block_sums<T>(w, cs.part, mass);
+  const Pair goal = pair_from(draw.u) * mass;
+  // the last one with a mass whose predecessors' mass is at most u W
+  if (kept && w.h > 0.0f && with - w <= goal) atomicMax(&cs.token, tid);
+  __syncthreads();
+  if (tid == 0) {
+    const uint64_t won = cs.key[max(cs.token, 0)];
+    const float y = (from_ordered((uint32_t)(won >> 32)) - s.m) / draw.temperature;
+    report(a, r, (int32_t) ~(uint32_t)won, y - log_of(total), y - log_of(mass), n_kept);
+  }
 }
 
 // grid (cluster, rows)
@@ -1209,11 +1510,14 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
       if (!whole || n < 1) {
         if (tid == 0) report(a, r, kUndecided, 0.0f, 0.0f, 0);
       } else {
+        const Scale s = scale_of(m, draw.temperature);
+        if (n <= T) {
+          draw_from_few<T>(a, r, cs, draw, s, n, by_k ? (int)min((int64_t)n, k) : n, by_p, by_k || n == (int)finite, total, err, border);
+        } else {
         int n2 = 2;
         while (n2 < n) n2 *= 2;
         for (int i = n + tid; i < n2; i += T) cs.key[i] = 0;
         sort_down<T>(cs.key, n2);
-        const Scale s = scale_of(m, draw.temperature);
         for (int i = tid; i < n; i += T) {
           uint64_t h, l;
           float h0, l0, none;
@@ -1274,6 +1578,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
             report(a, r, (int32_t) ~(uint32_t)(key >> 32), y - log_of(total), y - log_of(mass), n_kept);
           }
         }
+        }
       }
     }
   }
@@ -1314,23 +1619,39 @@ __global__ void __launch_bounds__(kThreads) sample_exact_kernel(const SampleArgs
     const uint32_t finite = p.n;
     const Scale s = scale_of(m, draw.temperature);
     if (threadIdx.x == 0) sh.border = draw.min_p > 0.0f ? border_of(m, draw.reach()) : -INFINITY;
+    __syncthreads();
 
-    // all weights; then the cut, and the kept ones
+    // the cut, and the mass of what is kept (and of all)
     Keep keep;
-    p = team.gather(team.mass(s, keep, team.w0, team.w1));
-    const Pair total = p.a;
     const bool by_k = draw.k > 0 && draw.k < (int64_t)finite, by_p = draw.top_p < 1.0f && draw.top_p > 0.0f;
-    if (by_k) team.select(s, keep, true, (uint32_t)draw.k, Pair{}, Pair{1.0f, 0.0f});
-    if (by_p) {
-      const Pair all = by_k ? team.gather(team.mass(s, keep, team.w0, team.w1)).a : total;
-      team.select(s, keep, false, 0, Pair{draw.top_p, 0.0f} * all, all);
+    Pair total;
+    bool summed = false;
+    if (by_k || by_p) {
+      summed = sizeof(In) == 2 && team.by_value(s, keep, by_k ? (uint32_t)draw.k : 0, by_p ? draw.top_p : 1.0f, total);
+      if (!summed) {
+        total = team.gather(team.mass(s, keep, team.w0, team.w1)).a;
+        summed = true;
+        if (by_k) team.select(s, keep, true, (uint32_t)draw.k, Pair{}, Pair{1.0f, 0.0f});
+        if (by_p) {
+          const Pair all = by_k ? team.gather(team.mass(s, keep, team.w0, team.w1)).a : total;
+          team.select(s, keep, false, 0, Pair{draw.top_p, 0.0f} * all, all);
+        }
+      }
     }
-    keep.border = sh.border;
-    if (by_k || by_p || keep.border > -INFINITY) p = team.gather(team.mass(s, keep, team.w0, team.w1));
+    const float border = sh.border;
+    if (border > -INFINITY && !summed) {
+      total = team.gather(team.mass(s, keep, team.w0, team.w1)).a;
+      summed = true;
+    }
+    keep.border = border;
+    p = team.mass_of_run(s, keep);
+    const Pair own = p.a;  // of this lane's run
+    p = team.gather(p);
     const Pair mass = p.a;
     const int32_t kept = (int32_t)p.n;
+    if (!summed) total = mass;
 
-    // the last CTA, warp, part and piece with a mass of its own whose predecessors' mass is at most u W
+    // the last CTA, warp, lane and element with a mass of its own whose predecessors' mass is at most u W
     Pair left = pair_from(draw.u) * mass;
     auto descend = [&](int n, auto mass_of) {
       int at = 0;
@@ -1347,63 +1668,42 @@ __global__ void __launch_bounds__(kThreads) sample_exact_kernel(const SampleArgs
       return at;
     };
     const int owner = descend((int)ranks, [&](int i) { return sh.all[i].a; });
-    if (owner == (int)rank) {
-      const int w = descend(kWarps, [&](int i) { return sh.warp[i].a; });
-      int32_t a0, a1;
-      team.share(rank, w, a0, a1);
-      const int32_t each = (a1 - a0 + kWarps - 1) / kWarps;
-      const int32_t b0 = min(a1, a0 + team.warp * each), b1 = min(a1, b0 + each);
-      const Part part = merge_lanes<32>(team.mass(s, keep, b0, b1));
-      if (team.lane == 0) sh.part[team.warp] = part.a;
-      __syncthreads();
-      const int mine = descend(kWarps, [&](int i) { return sh.part[i]; });
-      if (mine == team.warp) {
-        int32_t token = -1;
-        float x = 0.0f;
-        Pair sum;
-        for (int32_t p0 = b0; p0 < b1 && sum <= left; p0 += 32) {
-          float v[N];
-          values<In>(p0 + team.lane < b1 ? team.row.load(p0 + team.lane) : absent<In>(), v);
-          const int32_t j0 = (p0 + team.lane) * N - team.row.off;
-          Pair w_of[N], own;
-#pragma unroll
-          for (int e = 0; e < N; e += 2) {
-            uint64_t h, l;
-            weights(s, sh.table, keep(v[e], j0 + e) ? v[e] : -INFINITY, keep(v[e + 1], j0 + e + 1) ? v[e + 1] : -INFINITY, h, l);
-            float h0, h1, l0, l1;
-            ptx::f32x2_unpack(h, h0, h1);
-            ptx::f32x2_unpack(l, l0, l1);
-            w_of[e] = normal(h0, l0);
-            w_of[e + 1] = normal(h1, l1);
-            own = own + w_of[e];
-            own = own + w_of[e + 1];
-          }
-          const Pair incl = scan_lanes(own);
-          Pair before = shuffle_up(incl, 1);
-          if (team.lane == 0) before = Pair{};
-          before = sum + before;
-          const uint32_t can = __ballot_sync(0xffffffffu, own.h > 0.0f && before <= left);
-          int32_t j = -1;
-          float xj = 0.0f;
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            if (w_of[e].h > 0.0f && before <= left) {
-              j = j0 + e;
-              xj = v[e];
-            }
-            before = before + w_of[e];
-          }
-          if (can) {
-            const int from = 31 - __clz(can);
-            token = __shfl_sync(0xffffffffu, j, from);
-            x = __shfl_sync(0xffffffffu, xj, from);
-          }
-          sum = sum + shuffle(incl, 31);
+    if (owner == (int)rank && descend(kWarps, [&](int i) { return sh.warp[i].a; }) == team.warp) {
+      Pair before = shuffle_up(scan_lanes(own), 1);
+      if (team.lane == 0) before = Pair{};
+      const uint32_t lanes = __ballot_sync(0xffffffffu, own.h > 0.0f && before <= left);
+      const int from = lanes ? 31 - __clz(lanes) : 0;
+      left = left - shuffle(before, from);
+      // that lane's elements, one a lane
+      const int32_t first_j = (team.w0 + from * team.run()) * N - team.row.off, some = team.run() * N;
+      int32_t token = -1;
+      float x = 0.0f;
+      Pair sum;
+      for (int32_t e0 = 0; e0 < some && sum <= left; e0 += 32) {
+        const int32_t j = first_j + e0 + team.lane;
+        float v = -INFINITY;
+        if (e0 + team.lane < some && j >= 0 && j < a.vocab) {
+          if (sizeof(In) == 2) v = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(team.row.x)[j]);
+          else v = reinterpret_cast<const float*>(team.row.x)[j];
         }
-        if (team.lane == 0) {
-          const float y = (x - m) / draw.temperature;
-          report(a, r, token, y - log_of(total), y - log_of(mass), kept);
+        uint64_t h, l;
+        weights(s, sh.table, keep(v, j) ? v : -INFINITY, -INFINITY, h, l);
+        float h0, l0, none;
+        ptx::f32x2_unpack(h, h0, none);
+        ptx::f32x2_unpack(l, l0, none);
+        const Pair w = normal(h0, l0), incl = scan_lanes(w);
+        Pair ahead = shuffle_up(incl, 1);
+        if (team.lane == 0) ahead = Pair{};
+        const uint32_t can = __ballot_sync(0xffffffffu, w.h > 0.0f && sum + ahead <= left);
+        if (can) {
+          token = __shfl_sync(0xffffffffu, j, 31 - __clz(can));
+          x = __shfl_sync(0xffffffffu, v, 31 - __clz(can));
         }
+        sum = sum + shuffle(incl, 31);
+      }
+      if (team.lane == 0) {
+        const float y = (x - m) / draw.temperature;
+        report(a, r, token, y - log_of(total), y - log_of(mass), kept);
       }
     }
     if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's shared memory
