@@ -159,9 +159,9 @@ struct Team {
       turn ^= 1;
     }
     __syncthreads();
-    Part t = sh.all[0];
-    for (uint32_t r = 1; r < ranks; ++r) t = merge(t, sh.all[r]);
-    return t;
+    Part t;
+    if ((lane & (kMaxCluster - 1)) < (int)ranks) t = sh.all[lane & (kMaxCluster - 1)];
+    return merge_lanes<kMaxCluster>(t);
   }
 
   // mass and number of the kept elements of the pieces [a, b), this lane's part
@@ -329,15 +329,18 @@ struct Team {
     if (lane == 0) run = Pair{};
     n_run -= n_own;
     __syncthreads();
-    Pair all;
-    uint32_t n_all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) {
-        run = all + run;
-        n_run += n_all;
-      }
-      all = all + sh.part[w];
-      n_all += sh.scan[w];
+    const Pair upto = scan_lanes(lane < kWarps ? sh.part[lane] : Pair{});
+    uint32_t n_upto = lane < kWarps ? sh.scan[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < kWarps; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, n_upto, d);
+      if (lane >= d) n_upto += o;
+    }
+    const Pair all = shuffle(upto, kWarps - 1), ahead = shuffle(upto, (warp + 31) & 31);
+    const uint32_t n_ahead = __shfl_sync(0xffffffffu, n_upto, (warp + 31) & 31);
+    if (warp > 0) {
+      run = ahead + run;
+      n_run += n_ahead;
     }
     total = all;
     auto found = [&](auto reached) {  // the first bin at whose end `reached` holds; every thread hears of it
@@ -770,44 +773,31 @@ __global__ void __launch_bounds__(T, RESIDENT) sample_exact_kernel(const SampleA
 
     // the last CTA, warp, lane and element with a mass of its own whose predecessors' mass is at most u W
     const Pair goal = pair_from(draw.u) * mass;
-    Pair sum;         // of what lies ahead: the mass without ties, and the number of those
+    Pair sum;  // of what lies ahead: the mass without ties, and the number of those
     uint32_t n = 0;
-    auto descend = [&](int count, auto part) {
-      int at = 0;
-      Pair run = sum;
-      uint32_t n_run = n;
-      for (int i = 0; i < count; ++i) {
-        const Part v = part(i);
-        const Pair before = ties.mass(run, n_run), next_run = run + v.a;
-        if (before < ties.mass(next_run, n_run + v.k) && before <= goal) {
-          at = i;
-          sum = run;
-          n = n_run;
-        }
-        run = next_run;
-        n_run += v.k;
-      }
-      return at;
-    };
-    const int owner = descend((int)ranks, [&](int i) { return sh.all[i]; });
-    if (owner == (int)rank && descend(T / 32, [&](int i) { return sh.warp[i]; }) == team.warp) {
-      auto scan = [&](uint32_t v) {  // the sum over the lanes ahead
-        uint32_t x = v;
+    auto descend = [&](const Part& v) {  // lane i has the i-th of the places to choose from
+      const Pair incl = scan_lanes(v.a);
+      Pair ahead = shuffle_up(incl, 1);
+      if (team.lane == 0) ahead = Pair{};
+      uint32_t n_incl = v.k;
+      if (CUT) {
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t o = __shfl_up_sync(0xffffffffu, x, d);
-          if (team.lane >= d) x += o;
+          const uint32_t o = __shfl_up_sync(0xffffffffu, n_incl, d);
+          if (team.lane >= d) n_incl += o;
         }
-        return x - v;
-      };
-      Pair ahead = shuffle_up(scan_lanes(own.a), 1);
-      if (team.lane == 0) ahead = Pair{};
-      const uint32_t n_ahead = CUT ? scan(own.k) : 0;
-      Pair before = ties.mass(sum + ahead, n + n_ahead);
-      const uint32_t lanes = __ballot_sync(0xffffffffu, before < ties.mass(sum + ahead + own.a, n + n_ahead + own.k) && before <= goal);
-      const int from = lanes ? 31 - __clz(lanes) : 0;
-      sum = sum + shuffle(ahead, from);
-      n += __shfl_sync(0xffffffffu, n_ahead, from);
+      }
+      // (from `ahead`, not from the scan's next sum, which may round otherwise: an empty place adds nothing)
+      const Pair before = ties.mass(sum + ahead, n + n_incl - v.k), after = ties.mass(sum + ahead + v.a, n + n_incl);
+      const uint32_t can = __ballot_sync(0xffffffffu, before < after && before <= goal);
+      const int at = can ? 31 - __clz(can) : 0;
+      sum = sum + shuffle(ahead, at);
+      n += __shfl_sync(0xffffffffu, n_incl - v.k, at);
+      return at;
+    };
+    const int owner = descend(team.lane < (int)ranks ? sh.all[team.lane] : Part{});
+    if (owner == (int)rank && descend(team.lane < T / 32 ? sh.warp[team.lane] : Part{}) == team.warp) {
+      const int from = descend(own);
       // that lane's elements, one a lane
       const int32_t first_j = (team.w0 + from * team.run()) * N - team.row.off, some = team.run() * N;
       int32_t token = -1;
@@ -819,20 +809,23 @@ __global__ void __launch_bounds__(T, RESIDENT) sample_exact_kernel(const SampleA
           if (sizeof(In) == 2) v = bf16_lo((uint32_t) reinterpret_cast<const uint16_t*>(team.row.x)[j]);
           else v = reinterpret_cast<const float*>(team.row.x)[j];
         }
+        Part one;
         const bool in = keep(v, j);
-        const uint32_t tie = CUT && !in && ties(v);
-        const Pair w = weight(s, sh.table, in ? v : -INFINITY), incl = scan_lanes(w);
-        ahead = shuffle_up(incl, 1);
+        one.a = weight(s, sh.table, in ? v : -INFINITY);
+        one.k = CUT && !in && ties(v);
+        const Pair incl = scan_lanes(one.a);
+        Pair ahead = shuffle_up(incl, 1);
         if (team.lane == 0) ahead = Pair{};
-        const uint32_t t_ahead = CUT ? scan(tie) : 0;
-        before = ties.mass(sum + ahead, n + t_ahead);
-        const uint32_t can = __ballot_sync(0xffffffffu, before < ties.mass(sum + incl, n + t_ahead + tie) && before <= goal);
+        const uint32_t tied = __ballot_sync(0xffffffffu, one.k != 0);
+        const uint32_t t_ahead = __popc(tied & ((1u << team.lane) - 1));
+        const Pair before = ties.mass(sum + ahead, n + t_ahead);
+        const uint32_t can = __ballot_sync(0xffffffffu, before < ties.mass(sum + ahead + one.a, n + t_ahead + one.k) && before <= goal);
         if (can) {
           token = __shfl_sync(0xffffffffu, j, 31 - __clz(can));
           x = __shfl_sync(0xffffffffu, v, 31 - __clz(can));
         }
         sum = sum + shuffle(incl, 31);
-        n += __shfl_sync(0xffffffffu, t_ahead + tie, 31);
+        n += __popc(tied);
         if (goal < ties.mass(sum, n)) break;
       }
       if (team.lane == 0) {
@@ -848,10 +841,13 @@ __global__ void __launch_bounds__(T, RESIDENT) sample_exact_kernel(const SampleA
 template <typename In, bool CUT, int T, int RESIDENT>
 cudaError_t launch_exact(const SampleArgs& a, cudaStream_t stream) {
   const int64_t pieces = ((int64_t)a.vocab + Row<In>::N - 1) / Row<In>::N;
+  // Small clusters lose less time between a row's passes, large ones have a row done sooner: as many CTAs as
+  // three resident waves take if all rows were left (a share of them is).
+  const int sms = sm_count();
   int cluster = 1;
-  while (cluster < kMaxCluster && pieces > (int64_t)cluster * T) cluster *= 2;
+  while (cluster < kMaxCluster && pieces > (int64_t)cluster * T && (!CUT || a.rows * cluster < 3 * sms)) cluster *= 2;
   return launch_clusters(sample_exact_kernel<In, CUT, T, RESIDENT>, a, cluster,
-                         std::min<int64_t>(a.rows, std::max(1, RESIDENT * sm_count() / cluster)), T, stream);
+                         std::min<int64_t>(a.rows, std::max(1, RESIDENT * sms / cluster)), T, stream);
 }
 
 }  // namespace
