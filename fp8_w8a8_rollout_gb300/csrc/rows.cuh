@@ -143,14 +143,24 @@ __device__ __forceinline__ void floored_pairs(uint4 u, uint64_t (&v)[Row<In>::N 
   }
 }
 
-// whether a piece holds an element of -inf (or, bf16, a NaN beside one: a caller looks closer)
-template <typename In>
-__device__ __forceinline__ bool least_is_masked(uint4 u) {
+// whether some pieces hold an element of -inf (NaN left out)
+template <typename In, int U>
+__device__ __forceinline__ bool holds_masked(const uint4 (&u)[U]) {
   if (sizeof(In) == 2) {
-    const uint32_t m = min_bf16x2(min_bf16x2(u.x, u.y), min_bf16x2(u.z, u.w));
-    return (m & 0xFFFFu) == 0xFF80u || (m >> 16) == 0xFF80u;
+    uint32_t m = min_bf16x2(min_bf16x2(u[0].x, u[0].y), min_bf16x2(u[0].z, u[0].w));
+#pragma unroll
+    for (int i = 1; i < U; ++i) {
+      m = min_bf16x2(m, min_bf16x2(u[i].x, u[i].y));
+      m = min_bf16x2(m, min_bf16x2(u[i].z, u[i].w));
+    }
+    return fminf(bf16_lo(m), bf16_hi(m)) == -INFINITY;
   }
-  return fminf(fminf(__uint_as_float(u.x), __uint_as_float(u.y)), fminf(__uint_as_float(u.z), __uint_as_float(u.w))) == -INFINITY;
+  float m = INFINITY;
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+    m = fminf(m, fminf(fminf(__uint_as_float(u[i].x), __uint_as_float(u[i].y)),
+                       fminf(__uint_as_float(u[i].z), __uint_as_float(u[i].w))));
+  return m == -INFINITY;
 }
 
 // the largest value of some pieces (NaN left out)

@@ -42,17 +42,19 @@ namespace {
 
 // ------------------------------------------------------------------ one pass
 
+constexpr int kStages = 2;    // of a lane's ring
 constexpr int kCap = 1024;    // elements that a row's cut is made among
 constexpr int kMassBins = 128;  // of the thread maxima, a quarter of a power of two each
 constexpr float kStep = 0x1p-24f;  // an fp32 operation's largest relative error
+constexpr float kSlope = 2.6f, kMoved = 2.4f;  // of the error's bound: kSlope kMoved > 6
 
 // a warp's share of a row: sums against its maximum m
 struct WarpStat {
   float m;
   Pair s;            // sum of w
-  float err, wt;     // a bound of s's error so far; sum of w t (t <= 0: exponents in base 2)
+  float wt;          // sum of w t (t <= 0: exponents in base 2), and what stands for moves of the maximum
   uint32_t masked;   // elements of -inf
-  uint32_t pad[2];
+  uint32_t pad[3];
 };
 static_assert(sizeof(WarpStat) == 32, "read as 8 words");
 
@@ -67,14 +69,17 @@ struct PassShared {
   int owner, owner_warp;
   Pair part[T / 32];
 };
+// the lists of a cut, in the memory of the pass's ring
+struct Lists {
+  uint64_t list[kCap];  // this CTA's finds
+  uint64_t key[kCap];   // rank 0: all of them, sorted
+  Pair w[kCap];
+};
 template <int T>
 struct CutShared {
   float2 table[256];
-  float most[T];           // thread maxima
+  float most[T];  // thread maxima
   uint32_t bins[kMassBins];
-  uint64_t list[kCap];     // this CTA's finds
-  uint64_t key[kCap];      // rank 0: all of them, sorted
-  Pair w[kCap];
   Pair part[T / 32];
   double reach;
   int16_t cand[T];
@@ -147,24 +152,24 @@ __device__ __forceinline__ Pair block_sums(Pair v, Pair* part, Pair& all) {
   return warp > 0 ? ahead + incl : incl;
 }
 
-// The draw from a list of at most one element a thread (rank 0's cs.key, in any order): `n_k` of them are the
+// The draw from a list of at most one element a thread (rank 0's keys, in any order): `n_k` of them are the
 // first k, `exact`: the list's masses are what top_p goes by (else the sum, known to err).
 template <int T>
-__device__ void draw_from_few(const SampleArgs& a, int64_t r, CutShared<T>& cs, const Draw& draw, const Scale& s, int n, int n_k,
+__device__ void draw_from_few(const SampleArgs& a, int64_t r, CutShared<T>& cs, Lists& lists, const Draw& draw, const Scale& s, int n, int n_k,
                               bool by_p, bool exact, Pair total, float err, float border, int finite) {
   const int tid = threadIdx.x;
-  if (tid == 0 && (n & 1)) cs.key[n] = 0;
+  if (tid == 0 && (n & 1)) lists.key[n] = 0;
   __syncthreads();
   // by value: each counts the ones ahead of it
-  const uint64_t mine = tid < n ? cs.key[tid] : 0;
+  const uint64_t mine = tid < n ? lists.key[tid] : 0;
   int place = 0;
   for (int i = 0; i < n; i += 2) {
-    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&cs.key[i]);
+    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&lists.key[i]);
     place += (two.x > mine) + (two.y > mine);
   }
-  if (tid < n) cs.list[place] = mine;
+  if (tid < n) lists.list[place] = mine;
   __syncthreads();
-  const uint64_t key = tid < n ? cs.list[tid] : 0;
+  const uint64_t key = tid < n ? lists.list[tid] : 0;
   const float x = from_ordered((uint32_t)(key >> 32));
   Pair w;
   if (tid < n) {
@@ -188,13 +193,13 @@ __device__ void draw_from_few(const SampleArgs& a, int64_t r, CutShared<T>& cs, 
   // in the row's order
   const bool kept = tid < n_kept;
   place = 0;
-  for (int i = 0; i < n_kept; ++i) place += (uint32_t)cs.list[i] > (uint32_t)key;  // (low words: ~index)
+  for (int i = 0; i < n_kept; ++i) place += (uint32_t)lists.list[i] > (uint32_t)key;  // (low words: ~index)
   if (kept) {
-    cs.w[place] = w;
-    cs.key[place] = key;
+    lists.w[place] = w;
+    lists.key[place] = key;
   }
   __syncthreads();
-  w = kept ? cs.w[tid] : Pair{};
+  w = kept ? lists.w[tid] : Pair{};
   Pair mass;
   const Pair with = block_sums<T>(w, cs.part, mass);
   const Pair goal = pair_from(draw.u) * mass;
@@ -202,7 +207,7 @@ __device__ void draw_from_few(const SampleArgs& a, int64_t r, CutShared<T>& cs, 
   if (kept && w.h > 0.0f && with - w <= goal) atomicMax(&cs.token, tid);
   __syncthreads();
   if (tid == 0) {
-    const uint64_t won = cs.key[max(cs.token, 0)];
+    const uint64_t won = lists.key[max(cs.token, 0)];
     const float y = (from_ordered((uint32_t)(won >> 32)) - s.m) / draw.temperature;
     report(a, r, (int32_t) ~(uint32_t)won, y - log_of(total), y - log_of(mass), n_kept);
   }
@@ -212,8 +217,13 @@ __device__ void draw_from_few(const SampleArgs& a, int64_t r, CutShared<T>& cs, 
 template <typename In, bool CUT, int T>
 __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
   constexpr int N = Row<In>::N, U = 4, W = T / 32;
+  // each lane's own ring of pieces: the next rounds are under way while one is summed
+  constexpr int kRing = kStages * U * T * (int)sizeof(uint4);
+  __shared__ __align__(16) unsigned char ring_smem[CUT && kRing < (int)sizeof(Lists) ? sizeof(Lists) : kRing];
   __shared__ __align__(16) unsigned char smem[sizeof(PassShared<CUT, T>)];
   __shared__ __align__(16) unsigned char cut_smem[CUT ? sizeof(CutShared<T>) : 16];
+  Lists& lists = *reinterpret_cast<Lists*>(ring_smem);
+  uint4* ring = reinterpret_cast<uint4*>(ring_smem) + threadIdx.x;
   auto& sh = *reinterpret_cast<PassShared<CUT, T>*>(smem);
   auto& cs = *reinterpret_cast<CutShared<T>*>(cut_smem);
   ptx::grid_dep_launch_dependents();
@@ -248,27 +258,47 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
   }
 
   // the pass: this thread's sums against its own maximum
-  float m = -INFINITY, err = 0.0f, wt = 0.0f;
+  float m = -INFINITY, wt = 0.0f;
   Sum sum;
   uint64_t wt2 = 0;
   uint32_t masked = 0;
   const uint64_t c2 = both(c);
-  for (int32_t p0 = w0; p0 < w1; p0 += 32 * U) {
-    uint4 u[U];
+  const int32_t inner = w0 == 0 && row.off > 0 ? 0 : min(w1, (row.off + a.vocab) / N);  // (the first piece may lack elements too)
+  auto request = [&](int32_t p0, int stage) {  // a round of whole pieces
+    if (p0 + 32 * U <= inner) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) u[i] = p0 + 32 * i + lane < w1 ? row.load(p0 + 32 * i + lane) : absent<In>();
+      for (int i = 0; i < U; ++i)
+        ptx::cp_async_16(ptx::smem_u32(ring + (stage * U + i) * T), row.x + ((p0 + 32 * i + lane) * N - row.off));
+    }
+    ptx::cp_async_commit();
+  };
+  static_assert(kStages == 2, "one round behind the one that is summed");
+  request(w0, 0);
+  request(w0 + 32 * U, 1);
+  int stage = 0;
+  for (int32_t p0 = w0; p0 < w1; p0 += 32 * U, stage ^= 1) {
+    uint4 u[U];
+    ptx::cp_async_wait<1>();
+    if (p0 + 32 * U <= inner) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) u[i] = ring[(stage * U + i) * T];
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i) u[i] = p0 + 32 * i + lane < w1 ? row.load(p0 + 32 * i + lane) : absent<In>();
+    }
     const float big = largest<In>(u);
+    request(p0 + 64 * U, stage);  // (all of the stage has been read for `big`)
     if (big > m) {
-      // (all sums so far times a power: one rounding of the exponential and of the product)
+      // All sums so far times a power: the exponential's and the product's rounding, up to 6 kStep of them, which
+      // kMoved stands for in wt.
       const float d = m == -INFINITY ? 0.0f : fmaxf((m - big) * c, kTinyExp2), f = m == -INFINITY ? 0.0f : ex2(d);
       float h0, h1, l0, l1;
       ptx::f32x2_unpack(sum.h, h0, h1);
       ptx::f32x2_unpack(sum.l, l0, l1);
       float t0, t1;
       ptx::f32x2_unpack(wt2, t0, t1);
-      wt = f * fmaf(d, h0 + h1, wt + t0 + t1);
+      wt = f * fmaf(d - kMoved, h0 + h1, wt + t0 + t1);
       wt2 = 0;
-      err = f * fmaf(6.0f * kStep, h0 + h1, err);
       sum.h = pair_of(h0 * f, h1 * f);
       sum.l = pair_of(l0 * f, l1 * f);
       m = big;
@@ -303,13 +333,9 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
         for (int e = 0; e < N; ++e) bad = isnan(v[e]) ? v[e] : bad;
       }
       sum.add(both(bad), 0);
-      if (m > -INFINITY) err = INFINITY;
     }
     // elements of -inf, where there are any
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < U; ++i) any |= least_is_masked<In>(u[i]);
-    if (any) {
+    if (holds_masked<In>(u)) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         float v[N];
@@ -322,6 +348,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
       }
     }
   }
+  ptx::cp_async_wait<0>();  // (the ring's memory has other uses)
   {
     float h0, h1, l0, l1;
     ptx::f32x2_unpack(sum.h, h0, h1);
@@ -335,17 +362,13 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float d = own == -INFINITY ? 0.0f : fmaxf((own - m) * c, kTinyExp2), f = own == -INFINITY ? 0.0f : ex2(d);
-    wt = f * fmaf(d, s.h, wt);
-    err = f * fmaf(16.0f * kStep, s.h, err);  // this exponential, those of the sum and the additions
+    wt = f * fmaf(d - kMoved, s.h, wt);
     s = Pair{s.h * f, s.l * f};
     s = scan_lanes(s);
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) {
-      err += __shfl_xor_sync(0xffffffffu, err, k);
-      wt += __shfl_xor_sync(0xffffffffu, wt, k);
-    }
+    for (int k = 16; k > 0; k >>= 1) wt += __shfl_xor_sync(0xffffffffu, wt, k);
     masked = __reduce_add_sync(0xffffffffu, masked);
-    if (lane == 31) sh.warp[warp] = WarpStat{m, s, err, wt, masked, {}};
+    if (lane == 31) sh.warp[warp] = WarpStat{m, s, wt, masked, {}};
   }
   const bool by_rank = CUT && draw.k > 0 && draw.k <= kCap;
   if (CUT) {
@@ -376,11 +399,11 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = 2 * lane + i;
-      st[i] = WarpStat{-INFINITY, {}, 0.0f, 0.0f, 0, {}};
+      st[i] = WarpStat{-INFINITY, {}, 0.0f, 0, {}};
       if (e < ranks * W) {
         const uint32_t at = ptx::mapa_shared(ptx::smem_u32(&sh.warp[e % W]), e / W);
-        const float4 x = ptx::ld_dsmem_f32x4(at), y = ptx::ld_dsmem_f32x4(at + 16);
-        st[i] = WarpStat{x.x, {x.y, x.z}, x.w, y.x, __float_as_uint(y.y), {}};
+        const float4 x = ptx::ld_dsmem_f32x4(at);
+        st[i] = WarpStat{x.x, {x.y, x.z}, x.w, ptx::ld_dsmem_u32(at + 16), {}};
       }
     }
     if (CUT && lane < ranks) tau = __uint_as_float(ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&sh.bound), lane)));
@@ -390,23 +413,20 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       tau = fminf(tau, __shfl_xor_sync(0xffffffffu, tau, d));
     }
-    err = wt = 0.0f;
+    wt = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float d = st[i].m == -INFINITY ? 0.0f : fmaxf((st[i].m - top) * c, kTinyExp2), f = st[i].m == -INFINITY ? 0.0f : ex2(d);
-      wt += f * fmaf(d, st[i].s.h, st[i].wt);
-      err += f * fmaf(6.0f * kStep, st[i].s.h, st[i].err);
+      wt += f * fmaf(d - kMoved, st[i].s.h, st[i].wt);
       st[i].s = Pair{st[i].s.h * f, st[i].s.l * f};
     }
     masked = __reduce_add_sync(0xffffffffu, st[0].masked + st[1].masked);
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) {
-      err += __shfl_xor_sync(0xffffffffu, err, k);
-      wt += __shfl_xor_sync(0xffffffffu, wt, k);
-    }
+    for (int k = 16; k > 0; k >>= 1) wt += __shfl_xor_sync(0xffffffffu, wt, k);
     const Pair incl = scan_lanes(st[0].s + st[1].s), total = shuffle(incl, 31);
-    // exponents: x - m, log2(e) / T and their product are rounded
-    err = fmaf(2.6f * kStep, fabsf(wt), err);
+    // What the sum may be off by: its exponentials (4 kStep each) and their sums four deep; and of each exponent
+    // x - m, log2(e) / T and their product are rounded, 3.3 kStep ln 2 times the exponent (and a share for wt itself).
+    const float err = kStep * fmaf(kSlope, fabsf(wt), 9.0f * total.h);
     Pair before = shuffle_up(incl, 1);
     if (lane == 0) before = Pair{};
     const Pair goal = pair_from(draw.u) * total, middle = before + st[0].s;
@@ -435,7 +455,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
   if (ranks > 1) ptx::cluster_arrive();  // this CTA has read the others' sums
   const Pair total = sh.total;
   m = sh.m;
-  err = sh.err;
+  const float err = sh.err;
   const uint32_t finite = sh.finite;
   const int64_t k = draw.k;
   const bool by_k = CUT && k > 0 && k < (int64_t)finite, by_p = CUT && draw.top_p < 1.0f && draw.top_p > 0.0f,
@@ -613,7 +633,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
         for (int e = 0; e < N; ++e) {
           if (!may(v[e])) continue;
           const int at = atomicAdd(&cs.hits, 1);
-          if (at < kCap) cs.list[at] = (uint64_t)ordered(v[e]) << 32 | (uint32_t) ~(p * N - row.off + e);
+          if (at < kCap) lists.list[at] = (uint64_t)ordered(v[e]) << 32 | (uint32_t) ~(p * N - row.off + e);
         }
       }
     }
@@ -641,8 +661,8 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
             if (i >= end) q = e + 1, start = end;
           }
           if (i < n) {
-            const uint32_t at = ptx::mapa_shared(ptx::smem_u32(&cs.list[i - start]), q);
-            cs.key[i] = (uint64_t)ptx::ld_dsmem_u32(at + 4) << 32 | ptx::ld_dsmem_u32(at);
+            const uint32_t at = ptx::mapa_shared(ptx::smem_u32(&lists.list[i - start]), q);
+            lists.key[i] = (uint64_t)ptx::ld_dsmem_u32(at + 4) << 32 | ptx::ld_dsmem_u32(at);
           }
         }
       }
@@ -654,15 +674,15 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
       } else {
         const Scale s = scale_of(m, draw.temperature);
         if (n <= T) {
-          draw_from_few<T>(a, r, cs, draw, s, n, by_k ? (int)min((int64_t)n, k) : n, by_p, by_k || n == (int)finite, total, err, border, (int)finite);
+          draw_from_few<T>(a, r, cs, lists, draw, s, n, by_k ? (int)min((int64_t)n, k) : n, by_p, by_k || n == (int)finite, total, err, border, (int)finite);
         } else {
         int n2 = 2;
         while (n2 < n) n2 *= 2;
-        for (int i = n + tid; i < n2; i += T) cs.key[i] = 0;
-        sort_down<T>(cs.key, n2);
+        for (int i = n + tid; i < n2; i += T) lists.key[i] = 0;
+        sort_down<T>(lists.key, n2);
         for (int i = tid; i < n; i += T) {
-          const float x = from_ordered((uint32_t)(cs.key[i] >> 32));
-          cs.w[i] = weight(s, cs.table, x);
+          const float x = from_ordered((uint32_t)(lists.key[i] >> 32));
+          lists.w[i] = weight(s, cs.table, x);
           if (x >= border) atomicAdd(&cs.n_border, 1);
         }
         __syncthreads();
@@ -672,11 +692,11 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
         if (by_p) {
           // how many sums lie below top_p's share (of the sum known to err: below its least and its largest)
           Pair low = total + Pair{-err, 0.0f}, high = total + Pair{err, 0.0f};
-          if (by_k || n == (int)finite) low = high = sums_of<T>(cs.w, n_k, cs.part, [](int, Pair, Pair) {});
+          if (by_k || n == (int)finite) low = high = sums_of<T>(lists.w, n_k, cs.part, [](int, Pair, Pair) {});
           const Pair p{draw.top_p, 0.0f};
           low = p * low;
           high = p * high;
-          sums_of<T>(cs.w, n_k, cs.part, [&](int, Pair, Pair with) {
+          sums_of<T>(lists.w, n_k, cs.part, [&](int, Pair, Pair with) {
             if (with < low) atomicAdd(&cs.below[0], 1);
             if (with < high) atomicAdd(&cs.below[1], 1);
           });
@@ -691,27 +711,27 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
           // the kept ones in the row's order, with their place among the sorted
           n2 = 2;
           while (n2 < n_kept) n2 *= 2;
-          for (int i = tid; i < n2; i += T) cs.list[i] = i < n_kept ? cs.key[i] << 32 | (uint32_t)i : 0;
-          sort_down<T>(cs.list, n2);
+          for (int i = tid; i < n2; i += T) lists.list[i] = i < n_kept ? lists.key[i] << 32 | (uint32_t)i : 0;
+          sort_down<T>(lists.list, n2);
           // (sorted keys low words are ~index: the largest first is the lowest index first)
-          const Pair mass = sums_of<T>(cs.w, n_kept, cs.part, [](int, Pair, Pair) {});
+          const Pair mass = sums_of<T>(lists.w, n_kept, cs.part, [](int, Pair, Pair) {});
           constexpr int E = kCap / T;
           Pair w[E];
 #pragma unroll
-          for (int i = 0; i < E; ++i) w[i] = tid * E + i < n_kept ? cs.w[(uint32_t)cs.list[tid * E + i]] : Pair{};
+          for (int i = 0; i < E; ++i) w[i] = tid * E + i < n_kept ? lists.w[(uint32_t)lists.list[tid * E + i]] : Pair{};
           __syncthreads();
 #pragma unroll
           for (int i = 0; i < E; ++i)
-            if (tid * E + i < n_kept) cs.w[tid * E + i] = w[i];
+            if (tid * E + i < n_kept) lists.w[tid * E + i] = w[i];
           __syncthreads();
           const Pair goal = pair_from(draw.u) * mass;
-          sums_of<T>(cs.w, n_kept, cs.part, [&](int i, Pair before, Pair) {
-            if (cs.w[i].h > 0.0f && before <= goal) atomicMax(&cs.token, i);
+          sums_of<T>(lists.w, n_kept, cs.part, [&](int i, Pair before, Pair) {
+            if (lists.w[i].h > 0.0f && before <= goal) atomicMax(&cs.token, i);
           });
           __syncthreads();
           if (tid == 0) {
-            const uint64_t key = cs.list[max(cs.token, 0)];
-            const float x = from_ordered((uint32_t)(cs.key[(uint32_t)key] >> 32)), y = (x - m) / draw.temperature;
+            const uint64_t key = lists.list[max(cs.token, 0)];
+            const float x = from_ordered((uint32_t)(lists.key[(uint32_t)key] >> 32)), y = (x - m) / draw.temperature;
             report(a, r, (int32_t) ~(uint32_t)(key >> 32), y - log_of(total), y - log_of(mass), n_kept);
           }
         }
