@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -1127,17 +1128,13 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
     if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be a 2-D bf16 or fp32 tensor with unit column stride")
     rows, vocab = logits.shape
-    values, arrays = [], []
-    for name, v, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
-                           ("min_p", min_p, torch.float32)):
+    values, arrays = [temperature, top_k, top_p, min_p], [None] * 4
+    for i, v in enumerate(values):
         if isinstance(v, torch.Tensor):
+            dtype = torch.int32 if i == 1 else torch.float32
             if v.dtype != dtype or v.shape != (rows,) or not v.is_contiguous():
-                raise ValueError(f"{name} must be a number or a contiguous {dtype} [rows] tensor")
-            arrays.append(v)
-            values.append(1)
-        else:
-            arrays.append(None)
-            values.append(v)
+                raise ValueError(f"{('temperature', 'top_k', 'top_p', 'min_p')[i]} must be a number or a contiguous {dtype} [rows] tensor")
+            values[i], arrays[i] = 1, v
     _check_cuda(logits, uniform, *arrays, *(out or ()))
     if uniform.dtype != torch.float64 or uniform.shape != (rows,) or not uniform.is_contiguous():
         raise ValueError("uniform must be a contiguous fp64 [rows] tensor")
@@ -1214,7 +1211,7 @@ def _rotary_args(q, k, positions, freqs):
 
 def _row_ld(t, tokens, width):
     """The row stride of [tokens, heads, d] (a tensor without elements has none that counts)."""
-    return _ld(t, tokens, width) if t is not None and t.numel() else width
+    return t.stride(0) if t is not None and tokens > 1 and width else width
 
 
 def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, freqs: RotaryFreqs, interleaved: bool = False,
@@ -1346,10 +1343,25 @@ class KvCaches:
         self.pointers = (ctypes.c_void_p * max(1, len(self.tensors)))(*(t.data_ptr() for t in self.tensors))
 
 
-def _page_args(block_table, lens, refs, block_size, caches):
+@functools.lru_cache(maxsize=256)
+def _page_workspace(rows, total_tokens, block_size, pages):
+    """Workspace bytes of kv_reserve (pages None) or kv_compact."""
+    return max(64, fp8rl_kv_reserve_workspace_size(rows, total_tokens, block_size) if pages is None else
+               fp8rl_kv_compact_workspace_size(pages))
+
+
+def _workspace(nbytes, device, stream):
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with _on(stream, device):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _page_args(block_table, lens, refs, block_size, caches, *more):
     """The caches' handle and sizes: (caches, rows, max_blocks, ldt, pages)."""
-    caches = caches if isinstance(caches, KvCaches) else KvCaches(caches)
-    _check_cuda(block_table, lens, refs, *caches.tensors[:1])
+    if not isinstance(caches, KvCaches):
+        caches = KvCaches(caches)
+    _check_cuda(block_table, lens, refs, *caches.tensors[:1], *more)
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
         raise ValueError("block_table must be an int32 [rows, max_blocks] tensor with unit column stride")
     rows, blocks = block_table.shape
@@ -1357,9 +1369,10 @@ def _page_args(block_table, lens, refs, block_size, caches):
         raise ValueError("lens must be a contiguous int32 [rows] tensor")
     if refs.dtype != torch.int32 or refs.dim() != 1 or not refs.is_contiguous():
         raise ValueError("refs must be a contiguous int32 [pages] tensor")
-    if caches.slots is not None and refs.numel() * block_size > caches.slots:
+    pages = refs.numel()
+    if caches.slots is not None and pages * block_size > caches.slots:
         raise ValueError("the caches must hold every page: pages * block_size rows")
-    return caches, rows, blocks, _ld(block_table, rows, blocks), refs.numel()
+    return caches, rows, blocks, _ld(block_table, rows, blocks), pages
 
 
 def kv_reserve(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, block_size: int, caches=(), count=None,
@@ -1374,8 +1387,7 @@ def kv_reserve(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
     refused (pages run out, or its table is full; it stays as it was).  info: pages
     free after the call, rows refused.  A last page that other rows hold too is
     copied first, in all `caches` (KvCaches, or a list of tensors)."""
-    caches, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, caches)
-    _check_cuda(count, cu_seqlens, workspace, *(out or ()))
+    caches, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, caches, count, cu_seqlens, workspace, *(out or ()))
     if count is not None and (count.dtype != torch.int32 or count.shape != (rows,) or not count.is_contiguous()):
         raise ValueError("count must be a contiguous int32 [rows] tensor")
     if cu_seqlens is None:
@@ -1384,10 +1396,8 @@ def kv_reserve(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
         raise ValueError("cu_seqlens must be a contiguous int32 [rows + 1] tensor")
     elif total_tokens is None:
         raise ValueError("cu_seqlens needs total_tokens")
-    need = fp8rl_kv_reserve_workspace_size(rows, total_tokens, block_size)
     if workspace is None:
-        with _on(stream, refs.device):
-            workspace = torch.empty(max(need, 64), dtype=torch.uint8, device=refs.device)
+        workspace = _workspace(_page_workspace(rows, total_tokens, block_size, None), refs.device, stream)
     if out is None:
         out = tuple(_outs((((total_tokens,), torch.int32), ((2,), torch.int32)), refs.device))
     else:
@@ -1407,8 +1417,7 @@ def kv_fork(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, p
     and reorders the others.  `out` may be (block_table, lens) itself; then a row
     with parent[i] != i takes its pages from a row that stays (parent[p] == p), or is
     empty."""
-    _, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, _NO_CACHES)
-    _check_cuda(parent, *(out or ()))
+    _, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, _NO_CACHES, parent, *(out or ()))
     if parent.dtype != torch.int32 or parent.dim() != 1 or not parent.is_contiguous():
         raise ValueError("parent must be a contiguous int32 [rows] tensor")
     n = parent.numel()
@@ -1427,12 +1436,9 @@ def kv_compact(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
     """int32 [1], the number n of pages in use: the used pages move to numbers below
     n, contents (in all `caches`), refs and block_table with them, so that the caches'
     rows from n * block_size on are free for something else."""
-    caches, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, caches)
-    _check_cuda(workspace, out)
-    need = fp8rl_kv_compact_workspace_size(pages)
+    caches, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, caches, workspace, out)
     if workspace is None:
-        with _on(stream, refs.device):
-            workspace = torch.empty(max(need, 64), dtype=torch.uint8, device=refs.device)
+        workspace = _workspace(_page_workspace(0, 0, block_size, pages), refs.device, stream)
     if out is None:
         out = _out((1,), torch.int32, refs.device)
     else:

@@ -15,7 +15,7 @@
 //            free one before n.
 //
 // Each is one planning kernel: a CTA, or a cluster of 8 once there is much to count,
-// whose threads own runs of pages; ranks come from one scan over the threads and an
+// whose warps own runs of pages; ranks come from a scan over the warps and an
 // exchange over the cluster, so the result does not depend on timing (reference counts
 // are sums of integers).  Its latency bounds it (about 4 dependent loads).  The
 // pages' contents are copied by a second kernel, which starts while the plan
@@ -36,6 +36,7 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyCtasPerSm = 8;
 constexpr int kMaxCaches = 256;    // a launch's, by value
 constexpr int64_t kMaxRows = 8192;
+constexpr int kFewPages = 8;       // new pages of a row that one thread hands out
 constexpr int kHeader = 16;        // ints of the workspace ahead of the lists
 
 struct Copy {  // a page's first `rows` cache rows
@@ -91,31 +92,61 @@ __device__ __forceinline__ void sync_all(uint32_t ranks) {
   else ptx::cluster_sync();  // (its release and acquire cover global memory too)
 }
 
-// f(page, count) of the run [p0, p1) of pages, four at a time where they are aligned
-template <typename F>
-__device__ __forceinline__ void each_page(const int32_t* refs, int32_t p0, int32_t p1, bool vec, F f) {
-  if (!vec) {
-    for (int32_t p = p0; p < p1; ++p) f(p, refs[p]);
-    return;
+// the sum over the block's warps before this one, and of all, from one value a warp
+__device__ __forceinline__ uint64_t warps_scan(uint64_t v, uint64_t* sums, uint64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();  // `sums` may still be read from the scan before
+  if (lane == 0) sums[warp] = v;
+  __syncthreads();
+  uint64_t w = sums[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += y;
   }
-  int32_t p = p0;
-#pragma unroll 4
-  for (; p + 4 <= p1; p += 4) {
-    const int4 v = *reinterpret_cast<const int4*>(refs + p);
-    f(p, v.x);
-    f(p + 1, v.y);
-    f(p + 2, v.z);
-    f(p + 3, v.w);
-  }
-  for (; p < p1; ++p) f(p, refs[p]);
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const uint64_t ahead = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return warp > 0 ? ahead : 0;
 }
 
-// the run of pages of this thread among the cluster's (a multiple of 8: whole 32-byte sectors)
+// the pages of this warp among the cluster's: a run of whole 128s
 __device__ __forceinline__ void own_run(int32_t pages, uint32_t ranks, uint32_t rank, int32_t& p0, int32_t& p1) {
-  const int64_t threads = (int64_t)ranks * kPlanThreads;
-  const int64_t run = ((pages + threads - 1) / threads + 7) / 8 * 8;
-  p0 = (int32_t)min((int64_t)pages, run * ((int64_t)rank * kPlanThreads + threadIdx.x));
+  const int64_t warps = (int64_t)ranks * 32;
+  const int64_t run = ((pages + warps - 1) / warps + 127) / 128 * 128;
+  p0 = (int32_t)min((int64_t)pages, run * ((int64_t)rank * 32 + (threadIdx.x >> 5)));
   p1 = (int32_t)min((int64_t)pages, (int64_t)p0 + run);
+}
+
+// f(page, counts of it and the three behind it) of the warp's run [p0, p1), lane by lane; behind the run: `none`
+template <typename F>
+__device__ __forceinline__ void each_four(const int32_t* refs, int32_t p0, int32_t p1, bool vec, int32_t none, F f) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int32_t q = p0; q < p1; q += 128) {
+    const int32_t p = q + 4 * lane;
+    int4 c = make_int4(none, none, none, none);
+    if (vec && p + 4 <= p1) {
+      c = *reinterpret_cast<const int4*>(refs + p);
+    } else {
+      if (p < p1) c.x = refs[p];
+      if (p + 1 < p1) c.y = refs[p + 1];
+      if (p + 2 < p1) c.z = refs[p + 2];
+      if (p + 3 < p1) c.w = refs[p + 3];
+    }
+    f(p, c);
+  }
+}
+
+// the sum of the lanes before this one
+__device__ __forceinline__ uint32_t lanes_before(uint32_t v, uint32_t& total) {
+  uint32_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if ((int)(threadIdx.x & 31) >= d) x += y;
+  }
+  total = __shfl_sync(0xffffffffu, x, 31);
+  return x - v;
 }
 
 // ------------------------------------------------------------------ reserve
@@ -183,18 +214,21 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
   const int tid = threadIdx.x;
   if (tid == 0) freed = 0;
 
-  // the free pages of this thread's run
-  int32_t p0, p1, mine = 0;
+  // the free pages of this warp's run
+  int32_t p0, p1;
+  uint32_t mine = 0;
   own_run(a.pages, ranks, rank, p0, p1);
-  each_page(a.refs, p0, p1, a.vec, [&](int32_t, int32_t c) { mine += c == 0; });
+  each_four(a.refs, p0, p1, a.vec, 1, [&](int32_t, int4 c) { mine += (c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0); });
+  mine = __reduce_add_sync(0xffffffffu, mine);
   uint64_t cta_free, n_free;
-  const uint64_t before = block_scan((uint64_t)mine, sums, cta_free);
+  const uint64_t before = warps_scan(mine, sums, cta_free);
   const uint64_t rank_before = cluster_scan(cta_free, &slot[0], ranks, n_free);
   const uint64_t avail = min(n_free, (uint64_t)a.list_cap);
 
-  // what the rows need, in their order: every CTA the same (the high word counts copies)
-  uint64_t first = 0;  // of the tile
-  uint64_t wanted = 0, taken = 0, refused = 0;
+  // what the rows need, in their order: every CTA the same
+  uint64_t first = 0;              // pages asked for by the tiles before
+  uint64_t copies = 0, taken = 0, refused = 0;
+  bool many = false;               // a row that takes more pages than a thread should hand out
   for (int32_t r0 = 0; r0 < a.rows; r0 += kPlanThreads) {
     const int32_t r = r0 + tid;
     RowNeed n{};
@@ -202,42 +236,51 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
     n.fits = true;
     if (r < a.rows) n = need_of(a, r);
     uint64_t tile;
-    const uint64_t at = (first + block_scan((uint64_t)n.need, sums, tile));
+    const uint64_t at = first + block_scan((uint64_t)n.need, sums, tile);
     first += tile;
     const bool served = n.fits && (n.need == 0 || at + (uint64_t)n.need <= avail);
-    // copies, then pages given and rows refused (for the report)
-    uint64_t tile_copies, tile_taken;
-    const uint64_t copy_at = wanted + block_scan(served && n.last >= 0 ? 1 : 0, sums, tile_copies);
-    block_scan(served ? (uint64_t)n.need : (uint64_t)1 << 32, sums, tile_taken);
-    wanted += tile_copies;
-    taken += tile_taken & 0xffffffffu;
-    refused += tile_taken >> 32;
+    many |= served && n.need > kFewPages;
+    // copies (16 bits), rows refused (16 bits), pages given
+    const uint64_t report = (served && n.last >= 0 ? 1u : 0u) | (uint64_t)!served << 16 | (served ? (uint64_t)n.need << 32 : 0);
+    const uint64_t before_row = block_scan(report, sums, tile);
     if (r < a.rows && rank == 0 && dcheck((int64_t)at + n.need <= a.list_cap || !served, a.err)) {
       // (the third is the row's place in the list)
-      a.row[r] = make_int4(n.len, served ? n.count : 0, (int32_t)min(at, (uint64_t)INT_MAX), served && n.last >= 0 ? (int32_t)copy_at : -1);
+      a.row[r] = make_int4(n.len, served ? n.count : 0, (int32_t)min(at, (uint64_t)INT_MAX),
+                           served && n.last >= 0 ? (int32_t)(copies + (before_row & 0xffffu)) : -1);
     }
+    copies += tile & 0xffffu;
+    refused += tile >> 16 & 0xffffu;
+    taken += tile >> 32;
   }
   const uint64_t end = first;  // pages that the rows ask for
 
   // the lowest free pages, as many as may be handed out
   uint64_t rank_at = rank_before + before;
   if (mine > 0 && rank_at < end) {
-    each_page(a.refs, p0, p1, a.vec, [&](int32_t p, int32_t c) {
-      if (c == 0) {
-        if (rank_at < end && rank_at < (uint64_t)a.list_cap && dcheck(rank_at < (uint64_t)a.list_cap, a.err)) a.list[rank_at] = p;
-        ++rank_at;
+    each_four(a.refs, p0, p1, a.vec, 1, [&](int32_t p, int4 c) {
+      if (rank_at >= end) return;  // (all lanes alike)
+      const int32_t v[4] = {c.x, c.y, c.z, c.w};
+      uint32_t total;
+      uint64_t at = rank_at + lanes_before((c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0), total);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (v[i] != 0) continue;
+        if (at < end && at < (uint64_t)a.list_cap && dcheck(at < (uint64_t)a.list_cap, a.err)) a.list[at] = p + i;
+        ++at;
       }
+      rank_at += total;
     });
   }
   sync_all(ranks);  // nobody reads the counts, the rows' lengths and last pages from here on
 
-  // a warp per row: its pages
-  const int lane = tid & 31;
-  for (int32_t r = rank * 32 + (tid >> 5); r < a.rows; r += (int32_t)ranks * 32) {
+  // the rows' pages: a thread per row, and a warp for each that takes many
+  many = __syncthreads_or(many);
+  auto hand_out = [&](int32_t r, int lane, int lanes) {
     const int4 info = a.row[r];
     const int32_t len = info.x, given = info.y, copy_at = info.w;
-    if (given == 0) continue;
+    if (given == 0) return;
     const int32_t held = blocks_of(len, a.block), after = blocks_of(len + given, a.block);
+    if (many && (after - held + (copy_at >= 0) > kFewPages) != (lanes > 1)) return;
     int32_t* row = a.table + r * a.ldt;
     int32_t at = info.z;
     if (copy_at >= 0) {  // the shared last page's copy
@@ -252,7 +295,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
         }
       }
     }
-    for (int32_t j = held + lane; j < after; j += 32) {
+    for (int32_t j = held + lane; j < after; j += lanes) {
       const int32_t p = a.list[at + j - held];
       if (dcheck(p >= 0 && p < a.pages && j < a.cols, a.err)) {
         a.refs[p] = 1;
@@ -260,12 +303,15 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
       }
     }
     if (lane == 0 && dcheck(r < a.rows, a.err)) a.lens[r] = len + given;
-  }
+  };
+  for (int32_t r = (int32_t)rank * kPlanThreads + tid; r < a.rows; r += (int32_t)ranks * kPlanThreads) hand_out(r, 0, 1);
+  if (many)
+    for (int32_t r = (int32_t)rank * 32 + (tid >> 5); r < a.rows; r += (int32_t)ranks * 32) hand_out(r, tid & 31, 32);
   __syncthreads();
   uint64_t all_freed;
   cluster_scan((uint64_t)freed, &slot[1], ranks, all_freed);  // (with one CTA the barrier above is the one needed)
   if (rank == 0 && tid == 0) {
-    a.header[0] = (int32_t)wanted;
+    a.header[0] = (int32_t)copies;
     if (a.info) {
       a.info[0] = (int32_t)(n_free - taken + all_freed);
       a.info[1] = (int32_t)refused;
@@ -362,30 +408,60 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
   ptx::grid_dep_launch_dependents();
   ptx::grid_dep_wait();
   const uint32_t ranks = gridDim.x, rank = blockIdx.x;
-  int32_t p0, p1, mine = 0;
+  int32_t p0, p1;
+  uint32_t mine = 0;
   own_run(a.pages, ranks, rank, p0, p1);
-  each_page(a.refs, p0, p1, a.vec, [&](int32_t, int32_t c) { mine += c > 0; });
+  each_four(a.refs, p0, p1, a.vec, 0, [&](int32_t, int4 c) { mine += (c.x > 0) + (c.y > 0) + (c.z > 0) + (c.w > 0); });
+  mine = __reduce_add_sync(0xffffffffu, mine);
   uint64_t cta, all;
-  block_scan((uint64_t)mine, sums, cta);
+  warps_scan(mine, sums, cta);
   cluster_scan(cta, &slot[0], ranks, all);
   const int32_t n = (int32_t)all;
   // holes before n (low word) and used pages past it (high word): as many of one as of the other
-  uint64_t both = 0;
-  each_page(a.refs, p0, p1, a.vec, [&](int32_t p, int32_t c) { both += p < n ? (uint64_t)(c <= 0) : (uint64_t)(c > 0) << 32; });
-  uint64_t at = block_scan(both, sums, cta);
+  uint32_t holes = 0, movers = 0;
+  each_four(a.refs, p0, p1, a.vec, 0, [&](int32_t p, int4 c) {
+    const int32_t v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p + i < p1) {
+        holes += p + i < n && v[i] <= 0;
+        movers += p + i >= n && v[i] > 0;
+      }
+    }
+  });
+  holes = __reduce_add_sync(0xffffffffu, holes);
+  movers = __reduce_add_sync(0xffffffffu, movers);
+  uint64_t at = warps_scan((uint64_t)movers << 32 | holes, sums, cta);
   at += cluster_scan(cta, &slot[1], ranks, all);
   uint32_t hole = (uint32_t)at, mover = (uint32_t)(at >> 32);
   const int32_t moves = (int32_t)(all >> 32);
-  if (both != 0 || p1 > n) {
-    each_page(a.refs, p0, p1, a.vec, [&](int32_t p, int32_t c) {
-      if (p >= n && c <= 0 && dcheck(p < a.pages, a.err)) a.to[p] = p;  // (no row holds it, or the counts are wrong)
-      if (p < n ? c > 0 : c <= 0) return;
-      const uint32_t k = p < n ? hole++ : mover++;
-      if (!dcheck((int32_t)k <= a.pages / 2, a.err)) return;
-      if (p < n) a.copies[k].dst = p;
-      else a.copies[k].src = p;
-    });
-  }
+  each_four(a.refs, p0, p1, a.vec, 0, [&](int32_t p, int4 c) {
+    const int32_t v[4] = {c.x, c.y, c.z, c.w};
+    // (a run may lie on both sides of n)
+    uint32_t here = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p + i < p1) here += p + i < n ? (v[i] <= 0 ? 1u : 0u) : (v[i] > 0 ? 0x10000u : 0u);
+    }
+    uint32_t total;
+    const uint32_t ahead = lanes_before(here, total);
+    uint32_t h = hole + (ahead & 0xffffu), m = mover + (ahead >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p + i >= p1) continue;
+      if (p + i < n) {
+        if (v[i] <= 0 && dcheck((int32_t)h <= a.pages / 2, a.err)) a.copies[h].dst = p + i;
+        h += v[i] <= 0;
+      } else if (v[i] > 0) {
+        if (dcheck((int32_t)m <= a.pages / 2, a.err)) a.copies[m].src = p + i;
+        ++m;
+      } else if (dcheck(p + i < a.pages, a.err)) {
+        a.to[p + i] = p + i;  // (no row holds it, or the counts are wrong)
+      }
+    }
+    hole += total & 0xffffu;
+    mover += total >> 16;
+  });
   if (rank == 0 && threadIdx.x == 0) {
     a.header[0] = moves;
     a.header[1] = n;

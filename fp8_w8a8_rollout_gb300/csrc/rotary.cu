@@ -28,7 +28,7 @@ namespace fp8rl {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotAhead = 4;         // heads a thread loads before it turns the first
+constexpr int kRotAhead = 2;  // heads a thread loads before it turns the first
 constexpr int64_t kMaxHeadDim = 1024;
 
 struct RotArgs {
@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t codes4(const float* x, float s, float r) {
 // A unit is 16 elements of a head: 8 pairs, or 16 elements behind the rotated part.
 // Thread = (token of the tile, unit, share of the heads).
 template <bool APPEND, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const RotArgs a) {
   extern __shared__ float4 smem4[];
   float* cs = reinterpret_cast<float*>(smem4);  // [tile][2][pairs]: cosines, sines
   ptx::grid_dep_launch_dependents();

@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
     if (p0 + 32 * U <= inner) {
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        ptx::cp_async_16(ptx::smem_u32(ring + (stage * U + i) * T), row.x + ((p0 + 32 * i + lane) * N - row.off));
+        cp_async_16(ptx::smem_u32(ring + (stage * U + i) * T), row.x + ((p0 + 32 * i + lane) * N - row.off));
     }
     ptx::cp_async_commit();
   };
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
     }
   }
   __syncthreads();
-  if (ranks > 1) ptx::cluster_arrive();  // this CTA has read the others' sums
+  if (ranks > 1) cluster_arrive();  // this CTA has read the others' sums
   const Pair total = sh.total;
   m = sh.m;
   const float err = sh.err;
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
       }
     }
   } else if (CUT) {
-    if (ranks > 1) ptx::cluster_wait();
+    if (ranks > 1) cluster_wait();
     // what may be kept: at or above tau, the border, and the last bin of the thread maxima that reach top_p's mass
     const float tau = by_k ? sh.tau : -INFINITY;
     const float c4 = 4.0f * c;
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
       }
     }
   }
-  if (ranks > 1 && (odd || !cut)) ptx::cluster_wait();  // the others have read this CTA's sums
+  if (ranks > 1 && (odd || !cut)) cluster_wait();  // the others have read this CTA's sums
 }
 
 constexpr int64_t kMaxRows = 65535;             // grid y

@@ -223,6 +223,16 @@ struct Draw {
 };
 __device__ __forceinline__ float border_of(float m, double reach) { return __double2float_ru((double)m + reach); }
 
+// A cluster barrier in two halves: a CTA that only has to outlive the others' reads of its
+// shared memory waits at its end
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// 16-byte asynchronous global -> shared copy past L1
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // the rows that the pass has left (sample_exact.cu)
 cudaError_t launch_sample_exact(const SampleArgs& a, bool fp32, bool cut, cudaStream_t stream);
 
