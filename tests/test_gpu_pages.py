@@ -328,3 +328,47 @@ def test_pages_past_2_31_bytes():
     assert int(fp8rl.kv_compact(table2, lens2, refs, page, [cache])) == 2
     assert table2[:, 0].tolist() == [1, 0]
     assert torch.equal(cache[:2 * page], content)
+
+
+def test_odd_places_and_strides():
+    # arrays that start anywhere and a table that is a part of a wider one
+    page, pages, rows, cols = 16, 70, 5, 6
+    base = torch.zeros(pages + 3, dtype=torch.int32, device="cuda")
+    wide = torch.full((rows, cols + 3), -7, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(rows + 1, dtype=torch.int32, device="cuda")[1:]
+    table, refs = wide[:, 1:cols + 1], base[1:pages + 1]
+    table.fill_(-1)
+    pool = torch.randint(0, 255, (pages * page + 1, 96), device="cuda", dtype=torch.int64).to(torch.uint8)
+    cache = pool[:, 1:65]  # no 16-byte pieces
+    before = pool.clone()
+    cu = torch.tensor([0, 20, 20, 20, 20, 20], dtype=torch.int32, device="cuda")
+    slots, info = fp8rl.kv_reserve(table, lens, refs, page, [cache], cu_seqlens=cu, total_tokens=20)
+    assert slots.tolist() == list(range(20)) and info.tolist() == [pages - 2, 0]
+    fp8rl.kv_fork(table, lens, refs, torch.tensor([0, 0, -1, 0, -1], dtype=torch.int32, device="cuda"), page, out=(table, lens))
+    slots, info = fp8rl.kv_reserve(table, lens, refs, page, [cache], count=torch.tensor([0, 1, 1, 1, 0], dtype=torch.int32, device="cuda"))
+    assert slots.tolist() == [-1, 2 * page + 4, 3 * page, 4 * page + 4, -1] and info.tolist() == [pages - 5, 0]
+    assert torch.equal(cache[2 * page:2 * page + 4], before[page:page + 4, 1:65])
+    fp8rl.kv_fork(table, lens, refs, torch.tensor([-1, 1, -1, -1, -1], dtype=torch.int32, device="cuda"), page, out=(table, lens))
+    used = fp8rl.kv_compact(table, lens, refs, page, [cache])
+    assert int(used) == 2 and table[1].tolist()[:2] == [0, 1] and refs.tolist() == [1, 1] + [0] * (pages - 2)
+    assert torch.equal(cache[page:page + 4], before[page:page + 4, 1:65])
+    assert base[0] == 0 and not base[pages + 1:].any() and (wide[:, 0] == -7).all() and (wide[:, cols + 1:] == -7).all()
+    assert torch.equal(pool[:, 0], before[:, 0]) and torch.equal(pool[:, 65:], before[:, 65:])
+
+
+def test_two_streams_at_once():
+    models = [Model(40, 12, 16, 400, 256, 4, seed=i) for i in range(2)]
+    for m in models:
+        m.prompts([21] + [0] * 39)
+        m.fork([0] * 40)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(30):
+        for m, s in zip(models, streams):
+            with torch.cuda.stream(s):
+                fp8rl.kv_reserve(*m.dev, m.page, m.handle)
+    torch.cuda.synchronize()
+    for m in models:
+        for _ in range(30):
+            m.reserve([1] * 40)
+        m.same()

@@ -253,3 +253,32 @@ def test_streams_and_graphs():
         fp8rl.rotary(q, k, pos, freqs, out=out)
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_rows_far_into_memory():
+    # element offsets past 2^31
+    tokens, ld = 3, 1 << 30
+    base = torch.empty(3 * ld, dtype=torch.bfloat16, device="cuda")
+    q = base.as_strided((tokens, 2, 128), (ld, 128, 1))
+    src, _, _ = qkv(tokens, 2, 1, 128, 1)
+    q.copy_(src)
+    freqs, inv, axis = plan(128, 1.0, 1)
+    pos = positions_of(tokens, 1, 100)
+    near(fp8rl.rotary(q, None, pos, freqs)[0], *ref(src, pos, inv, axis, False))
+
+
+def test_gradient_of_strided_and_shared_inputs():
+    # q and k are views of one projection: its gradient gathers both; a backward pass of a sum (an expanded gradient)
+    tokens, d = 9, 64
+    x = torch.randn(tokens, 5 * d, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).bfloat16().requires_grad_()
+    freqs, inv, axis = plan(d, 1.0, 1)
+    pos = positions_of(tokens, 1, 100)
+    h = x.view(tokens, 5, d)
+    q, k = fp8rl.rotary(h[:, :3], h[:, 3:], pos, freqs)
+    (q.sum() + 2 * k.sum()).backward()
+    g = torch.ones(tokens, 5, d, dtype=torch.bfloat16, device="cuda")
+    g[:, 3:] = 2
+    near(x.grad.view(tokens, 5, d), *ref(g, pos, inv, axis, False, True))
+    # back and forth: the rotation undoes itself but for two roundings to bf16
+    back = fp8rl.rotary(q.detach(), None, pos, freqs, inverse=True)[0]
+    assert ((back - h[:, :3]).abs().max() <= 2.0 ** -6 * h.abs().max()).item()

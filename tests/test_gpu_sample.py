@@ -261,3 +261,55 @@ def test_a_row_far_into_memory():
     src, u = make(3, vocab, torch.bfloat16, 4)
     rows.copy_(src)
     check(rows, u, 0.9, 0, 0.9)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_vocabulary_of_a_million(dtype):
+    x, u = make(3, 1200007, dtype, 21, spread=1.5)
+    for k, p in ((0, 1.0), (40, 1.0), (0, 0.9)):
+        check(x, u, 1.0, k, p)
+
+
+def test_more_rows_than_a_grid_has():
+    rows, vocab = 70001, 8  # (rows of whole 16-byte pieces: the same bits wherever they lie)
+    x, u = make(rows, vocab, torch.float32, 22)
+    u[69000:69010] = -1
+    token, lp, lp_kept, kept = fp8rl.sample(x, u, 1.0, 3)
+    some = [0, 1, 65534, 65535, 65536, 68999, 69000, 69009, 69010, 70000]
+    at = torch.tensor(some, device="cuda")
+    want = fp8rl.sample(x[at].contiguous(), u[at], 1.0, 3)
+    for a, b in zip((token, lp, lp_kept, kept), want):
+        assert torch.equal(a[at], b)
+    on = u >= 0
+    assert ((token >= 0) == on).all() and (kept[on] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_tokens_alone(dtype):
+    # the C call without its optional outputs
+    x, u = make(40, 9001, dtype, 23, spread=1.0)
+    for k, p in ((0, 1.0), (30, 0.9), (0, 0.9)):
+        want = fp8rl.sample(x, u, 1.0, k, p)
+        token = torch.full((40,), -9, dtype=torch.int32, device="cuda")
+        fp8rl.fp8rl_sample(x, int(dtype == torch.float32), 40, 9001, x.stride(0), u, 1.0, k, p, 0.0, None, None, None, None, token, None,
+                           None, None)
+        assert torch.equal(token, want[0])
+
+
+def test_two_streams_at_once():
+    x, u = make(64, 32001, torch.bfloat16, 24)
+    y, v = make(64, 32001, torch.float32, 25)
+    want = fp8rl.sample(x, u, 1.0, 0, 0.9), fp8rl.sample(y, v)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        pair = []
+        for s, (a, b, p) in zip(streams, ((x, u, 0.9), (y, v, 1.0))):
+            with torch.cuda.stream(s):
+                pair.append(fp8rl.sample(a, b, 1.0, 0, p))
+        got.append(pair)
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert all(torch.equal(c, d) for c, d in zip(a, b))
