@@ -18,7 +18,6 @@ namespace fp8rl {
 namespace sampling {
 namespace {
 
-constexpr int kUnroll = 2;
 constexpr int kBins = 1024;
 constexpr int kBinades = 15;                     // of bf16 values that have bins of their own
 constexpr int kValues = 2 * 128 * kBinades + 2;  // (+ the ones nearer to 0, + the ones below)
@@ -100,7 +99,8 @@ struct Ties {
 
 template <typename In, int T>
 struct Team {
-  static constexpr int N = Row<In>::N, kThreads = T, kWarps = T / 32;
+  static constexpr int N = Row<In>::N, kWarps = T / 32;
+  static constexpr int kUnroll = T > 256 ? 3 : 2;  // pieces a lane loads before it uses the first
   static_assert(kList <= T && kBins % T == 0 && kValueBins % T == 0, "threads take list entries and bins by their number");
   Shared<T>& sh;
   const Row<In> row;
@@ -281,20 +281,27 @@ struct Team {
     Part tiny;
     tiny.a = sum.value();
     tiny = gather(tiny);  // (and the counts are there)
+    // each CTA adds up its part of the bins, in the place that no other reads; then all read the sums
+    const int part = kValueBins / (int)ranks;
+    if (ranks > 1) {
+      for (int i = threadIdx.x; i < part; i += T) {
+        const uint32_t at = ptx::smem_u32(&sh.hist[rank * part + i]);
+        uint32_t n = 0;
+        for (uint32_t r = 0; r < ranks; ++r) n += ptx::ld_dsmem_u32(ptx::mapa_shared(at, r));
+        sh.hist[rank * part + i] = n;
+      }
+      ptx::cluster_sync();
+    }
     uint32_t count[kEach], n_own = 0;
     Pair mass[kEach], own;
+    const uint32_t bins = ptx::mapa_shared(ptx::smem_u32(&sh.hist[kEach * threadIdx.x]), kEach * threadIdx.x / part);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) count[i] = 0;
-    for (uint32_t r = 0; r < ranks; ++r) {
-      const uint32_t at = ptx::mapa_shared(ptx::smem_u32(&sh.hist[kEach * threadIdx.x]), r);
-#pragma unroll
-      for (int i = 0; i < kEach; i += 4) {
-        const float4 c = ptx::ld_dsmem_f32x4(at + 4 * i);
-        count[i] += __float_as_uint(c.x);
-        count[i + 1] += __float_as_uint(c.y);
-        count[i + 2] += __float_as_uint(c.z);
-        count[i + 3] += __float_as_uint(c.w);
-      }
+    for (int i = 0; i < kEach; i += 4) {
+      const float4 c = ptx::ld_dsmem_f32x4(bins + 4 * i);
+      count[i] = __float_as_uint(c.x);
+      count[i + 1] = __float_as_uint(c.y);
+      count[i + 2] = __float_as_uint(c.z);
+      count[i + 3] = __float_as_uint(c.w);
     }
 #pragma unroll
     for (int i = 0; i < kEach; i += 2) {
@@ -346,33 +353,29 @@ struct Team {
     auto found = [&](auto reached) {  // the first bin at whose end `reached` holds; every thread hears of it
       if (threadIdx.x == 0) sh.bin = INT_MAX;
       __syncthreads();
-      uint32_t n = n_run;
+      int mine = -1;
+      uint32_t n = n_run, in = 0;
       Pair m = run;
+      if (n_own > 0 && !reached(n_run, run) && reached(n_run + n_own, run + own)) {  // (one thread, roundings aside)
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        if (count[i] == 0) continue;
-        n += count[i];
-        m = m + mass[i];
-        if (reached(n, m)) {
-          atomicMin(&sh.bin, (int)threadIdx.x * kEach + i);
-          break;
+        for (int i = 0; i < kEach; ++i) {
+          if (mine >= 0 || count[i] == 0) continue;
+          in = count[i];
+          if (reached(n + in, m + mass[i])) {
+            mine = threadIdx.x * kEach + i;
+          } else {
+            n += in;
+            m = m + mass[i];
+          }
         }
+        if (mine >= 0) atomicMin(&sh.bin, mine);
       }
       __syncthreads();
       const int b = sh.bin;
-      if (b / kEach == (int)threadIdx.x) {
-        n = n_run;
-        m = run;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          if (i == b % kEach) {
-            sh.ahead = n;
-            sh.ahead_mass = m;
-            sh.last = (int)count[i];
-          }
-          n += count[i];
-          m = m + mass[i];
-        }
+      if (b == mine) {
+        sh.ahead = n;
+        sh.ahead_mass = m;
+        sh.last = (int)in;
       }
       __syncthreads();
       return b;
@@ -406,13 +409,16 @@ struct Team {
     return true;
   }
 
-  // the smallest n in [1, most] with n w >= left
+  // the smallest n in [1, most] with n w >= left: an fp32 quotient, corrected by its remainder
   static __device__ uint32_t first_reaching(Pair left, Pair w, uint32_t most) {
-    const double a = (double)left.h + (double)left.l, b = (double)w.h + (double)w.l;
-    const double n = b > 0.0 ? ceil(a / b) : 1.0;
-    uint32_t need = (uint32_t)fmin(fmax(n, 1.0), (double)most);
-    if (need > 1 && (double)(need - 1) * b >= a) --need;
-    return need;
+    if (!(w.h > 0.0f) || most <= 1) return 1;
+    float n = fminf(fmaxf(floorf(left.h / w.h), 1.0f), (float)most);
+    const Pair rest = left - w * pair_from((uint32_t)n);
+    int32_t at = (int32_t)n + (int32_t)floorf(rest.h / w.h);
+    at = max(1, min(at, (int32_t)most));
+    while (at < (int32_t)most && w * pair_from((uint32_t)at) < left) ++at;
+    while (at > 1 && left <= w * pair_from((uint32_t)(at - 1))) --at;
+    return (uint32_t)at;
   }
 
   // The index of the need-th element (from 1) with value x among the kept, in the row's order
@@ -473,7 +479,7 @@ struct Team {
         f = (hi - x) * pre * scale;
         return f < (float)(kBins - 1) ? (int)f : kBins - 1;
       };
-      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
+      for (int i = threadIdx.x; i < kBins; i += T) sh.hist[i] = 0;
       if (threadIdx.x == 0) {
         sh.bin = INT_MAX;
         sh.last = 0;
@@ -492,7 +498,7 @@ struct Team {
       if (ranks > 1) ptx::cluster_sync();
       else __syncthreads();
       // the cluster's bins, some a thread
-      constexpr int kEach = kBins / kThreads;
+      constexpr int kEach = kBins / T;
       uint32_t c[kEach];
       float f[kEach];
 #pragma unroll
