@@ -72,6 +72,7 @@ struct Shared {
   Pair part[T / 32];
   float border;            // min-p's
   int32_t n_list, bin, last;
+  int32_t row, nearest[T / 32];
   uint32_t scan[T / 32];
   uint32_t ahead;          // elements, and mass, ahead of `bin`
   Pair ahead_mass;
@@ -704,6 +705,54 @@ struct Team {
 
 // ------------------------------------------------------------------ kernel
 
+// The next row for this cluster: from `start` on, the first one still undecided that it gets hold of (a row is
+// taken by writing kTaken over its mark), -1: none within the next `cover`.  All of the cluster call it; `cursor` is
+// rank 0's place.  Rows are few and fall where they fall: with each cluster keeping to rows of its own, the 128 or
+// so of 1024 x 151936 took 50 us, five rows one behind the other somewhere.
+constexpr int32_t kTaken = -3;
+template <int T>
+__device__ int64_t next_row(const SampleArgs& a, Shared<T>& sh, uint32_t rank, uint32_t ranks, int32_t start, int32_t cover, int32_t& cursor) {
+  constexpr int kLook = 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = (int32_t)a.rows;
+  int32_t row = -1;
+  if (rank == 0) {
+    while (cursor < cover) {
+      int32_t nearest = INT_MAX;
+#pragma unroll
+      for (int i = kLook - 1; i >= 0; --i) {
+        const int32_t at = cursor + i * T + (int32_t)threadIdx.x;
+        if (at >= cover) continue;
+        const int32_t r = start + at < rows ? start + at : start + at - rows;
+        if (__ldcg(a.tokens + r) == kUndecided) nearest = at;
+      }
+      nearest = __reduce_min_sync(0xffffffffu, nearest);
+      __syncthreads();  // the look before has been read
+      if (lane == 0) sh.nearest[warp] = nearest;
+      __syncthreads();
+      nearest = __reduce_min_sync(0xffffffffu, lane < T / 32 ? sh.nearest[lane] : INT_MAX);
+      if (nearest == INT_MAX) {
+        cursor += kLook * T;
+        continue;
+      }
+      cursor = nearest + 1;
+      const int32_t r = start + nearest < rows ? start + nearest : start + nearest - rows;
+      if (threadIdx.x == 0) sh.row = atomicCAS(a.tokens + r, kUndecided, kTaken) == kUndecided ? r : -1;
+      __syncthreads();
+      row = sh.row;
+      if (row >= 0) break;
+    }
+    if (row < 0) {
+      __syncthreads();
+      if (threadIdx.x == 0) sh.row = -1;
+    }
+  }
+  if (ranks > 1) {
+    ptx::cluster_sync();
+    return (int32_t)ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&sh.row), 0));
+  }
+  return row;
+}
+
 // grid (cluster, clusters): the rows that the pass has left.  CUT: something may be cut off
 template <typename In, bool CUT, int T, int RESIDENT>
 __global__ void __launch_bounds__(T, RESIDENT) sample_exact_kernel(const SampleArgs a) {
@@ -714,8 +763,14 @@ __global__ void __launch_bounds__(T, RESIDENT) sample_exact_kernel(const SampleA
   ptx::grid_dep_wait();
   const uint32_t rank = blockIdx.x, ranks = gridDim.x;
   bool first = true;
-  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    if (__ldcg(a.tokens + r) != kUndecided) continue;
+  const int32_t share = (int32_t)((a.rows + gridDim.y - 1) / gridDim.y), start = (int32_t)min(a.rows - 1, (int64_t)blockIdx.y * share);
+  const int32_t cover = (int32_t)min(a.rows, max((int64_t)16 * share, (int64_t)8192));
+  int32_t cursor = 0;
+  const bool own = a.rows <= (int64_t)gridDim.y;  // a row to each cluster: nothing to agree on
+  if (own && __ldcg(a.tokens + blockIdx.y) != kUndecided) return;
+  for (;;) {
+    const int64_t r = own ? (first ? (int64_t)blockIdx.y : -1) : next_row<T>(a, sh, rank, ranks, start, cover, cursor);
+    if (r < 0) break;
     if (first) {
       for (int i = threadIdx.x; i < 256; i += T) sh.table[i] = kExp2.v[i];
       first = false;
@@ -771,8 +826,8 @@ __global__ void __launch_bounds__(T, RESIDENT) sample_exact_kernel(const SampleA
       }
       keep.border = ties.border = border;
     }
-    const Part own = team.template mass_of_run<!CUT>(s, keep, ties);  // of this lane's run
-    p = team.gather(own);
+    const Part mine = team.template mass_of_run<!CUT>(s, keep, ties);  // of this lane's run
+    p = team.gather(mine);
     const Pair mass = ties.mass(p.a, p.k);
     const int32_t kept = CUT ? (int32_t)(p.n + min(p.k, ties.need)) : (int32_t)finite;
     if (!summed) total = mass;
@@ -803,7 +858,7 @@ __global__ void __launch_bounds__(T, RESIDENT) sample_exact_kernel(const SampleA
     };
     const int owner = descend(team.lane < (int)ranks ? sh.all[team.lane] : Part{});
     if (owner == (int)rank && descend(team.lane < T / 32 ? sh.warp[team.lane] : Part{}) == team.warp) {
-      const int from = descend(own);
+      const int from = descend(mine);
       // that lane's elements, one a lane
       const int32_t first_j = (team.w0 + from * team.run()) * N - team.row.off, some = team.run() * N;
       int32_t token = -1;
@@ -842,6 +897,7 @@ __global__ void __launch_bounds__(T, RESIDENT) sample_exact_kernel(const SampleA
     if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's shared memory
     else __syncthreads();
   }
+  if (ranks > 1 && !own) ptx::cluster_sync();  // the others have read that there is no row
 }
 
 template <typename In, bool CUT, int T, int RESIDENT>
