@@ -23,15 +23,16 @@
 // that cannot be decided so (a draw on a border, more elements than the list
 // holds, temperatures or maxima out of range) is marked for
 //
-// sample_exact_kernel, which follows at once and passes by all other rows.  There
-// weights and sums are carried to about 2^-43, as pairs of fp32 numbers: the exponent
-// t = (m - x) log2(e) / T as a pair; 2^-t from a table of 2^-(i / 256) and a polynomial
-// of the rest, whose first term is a pair too.  The cut of top-k and top-p is found by
-// histograms of 1024 bins over the values (counts, or masses as 13-bit fractions of the
-// bin's heaviest), refined until the bin with the cut holds one value or at most 256
-// elements, which are sorted.
+// sample_exact_kernel (sample_exact.cu), which follows at once and passes by all other rows.
 //
 // The order of all sums is fixed.
+//
+// Bound by HBM for many rows, by the chain of waits for few.  The exponentials' pass asks
+// 10 instructions an element: 1024 x 151936 bf16 takes 70 us (4.4 TB/s), and the
+// exact kernel 28 for the 128 or so draws of so many that fall among tokens lighter than 10^-5; with
+// top-50 and top-p 104 us.  Pieces come through a ring in shared memory, two
+// rounds ahead of each lane (without: 127 us for both kernels, 120 so).  16 rows: 8 us
+// where nothing is cut off, 16 with top-50, 14 with min-p.
 #include <algorithm>
 
 #include "sample.cuh"
@@ -58,7 +59,7 @@ struct WarpStat {
 };
 static_assert(sizeof(WarpStat) == 32, "read as 8 words");
 
-template <bool CUT, int T>
+template <int T>
 struct PassShared {
   WarpStat warp[T / 32];
   float bound;             // of this CTA's share: at least its part of the first k lies at or above
@@ -213,6 +214,67 @@ __device__ void draw_from_few(const SampleArgs& a, int64_t r, CutShared<T>& cs, 
   }
 }
 
+// The same from up to kCap elements
+template <int T>
+__device__ void draw_from_many(const SampleArgs& a, int64_t r, CutShared<T>& cs, Lists& lists, const Draw& draw, const Scale& s, int n, int n_k,
+                               bool by_p, bool exact, Pair total, float err, float border, int finite) {
+  const int tid = threadIdx.x;
+  int n2 = 2;
+  while (n2 < n) n2 *= 2;
+  for (int i = n + tid; i < n2; i += T) lists.key[i] = 0;
+  sort_down<T>(lists.key, n2);
+  for (int i = tid; i < n; i += T) {
+    const float x = from_ordered((uint32_t)(lists.key[i] >> 32));
+    lists.w[i] = weight(s, cs.table, x);
+    if (x >= border) atomicAdd(&cs.n_border, 1);
+  }
+  __syncthreads();
+  int n_kept = n_k;
+  if (by_p) {
+    Pair low = total + Pair{-err, 0.0f}, high = total + Pair{err, 0.0f};
+    if (exact) low = high = sums_of<T>(lists.w, n_k, cs.part, [](int, Pair, Pair) {});
+    const Pair p{draw.top_p, 0.0f};
+    low = p * low;
+    high = p * high;
+    sums_of<T>(lists.w, n_k, cs.part, [&](int, Pair, Pair with) {
+      if (with < low) atomicAdd(&cs.below[0], 1);
+      if (with < high) atomicAdd(&cs.below[1], 1);
+    });
+    __syncthreads();
+    if (cs.below[0] != cs.below[1] || cs.below[1] >= n_k) {
+      if (tid == 0) report(a, r, kUndecided, s.m, 0.0f, finite);
+      return;
+    }
+    n_kept = cs.below[0] + 1;
+  }
+  n_kept = min(n_kept, cs.n_border);
+  // the kept ones in the row's order (low words: ~index), with their place among the sorted
+  n2 = 2;
+  while (n2 < n_kept) n2 *= 2;
+  for (int i = tid; i < n2; i += T) lists.list[i] = i < n_kept ? lists.key[i] << 32 | (uint32_t)i : 0;
+  sort_down<T>(lists.list, n2);
+  const Pair mass = sums_of<T>(lists.w, n_kept, cs.part, [](int, Pair, Pair) {});
+  constexpr int E = kCap / T;
+  Pair w[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) w[i] = tid * E + i < n_kept ? lists.w[(uint32_t)lists.list[tid * E + i]] : Pair{};
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (tid * E + i < n_kept) lists.w[tid * E + i] = w[i];
+  __syncthreads();
+  const Pair goal = pair_from(draw.u) * mass;
+  sums_of<T>(lists.w, n_kept, cs.part, [&](int i, Pair before, Pair) {
+    if (lists.w[i].h > 0.0f && before <= goal) atomicMax(&cs.token, i);
+  });
+  __syncthreads();
+  if (tid == 0) {
+    const uint64_t key = lists.list[max(cs.token, 0)];
+    const float y = (from_ordered((uint32_t)(lists.key[(uint32_t)key] >> 32)) - s.m) / draw.temperature;
+    report(a, r, (int32_t) ~(uint32_t)(key >> 32), y - log_of(total), y - log_of(mass), n_kept);
+  }
+}
+
 // grid (cluster, rows)
 template <typename In, bool CUT, int T>
 __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
@@ -220,11 +282,11 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
   // each lane's own ring of pieces: the next rounds are under way while one is summed
   constexpr int kRing = kStages * U * T * (int)sizeof(uint4);
   __shared__ __align__(16) unsigned char ring_smem[CUT && kRing < (int)sizeof(Lists) ? sizeof(Lists) : kRing];
-  __shared__ __align__(16) unsigned char smem[sizeof(PassShared<CUT, T>)];
+  __shared__ __align__(16) unsigned char smem[sizeof(PassShared<T>)];
   __shared__ __align__(16) unsigned char cut_smem[CUT ? sizeof(CutShared<T>) : 16];
   Lists& lists = *reinterpret_cast<Lists*>(ring_smem);
   uint4* ring = reinterpret_cast<uint4*>(ring_smem) + threadIdx.x;
-  auto& sh = *reinterpret_cast<PassShared<CUT, T>*>(smem);
+  auto& sh = *reinterpret_cast<PassShared<T>*>(smem);
   auto& cs = *reinterpret_cast<CutShared<T>*>(cut_smem);
   ptx::grid_dep_launch_dependents();
   ptx::grid_dep_wait();
@@ -673,69 +735,10 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
         if (tid == 0) report(a, r, kUndecided, m, 0.0f, (int32_t)finite);
       } else {
         const Scale s = scale_of(m, draw.temperature);
-        if (n <= T) {
-          draw_from_few<T>(a, r, cs, lists, draw, s, n, by_k ? (int)min((int64_t)n, k) : n, by_p, by_k || n == (int)finite, total, err, border, (int)finite);
-        } else {
-        int n2 = 2;
-        while (n2 < n) n2 *= 2;
-        for (int i = n + tid; i < n2; i += T) lists.key[i] = 0;
-        sort_down<T>(lists.key, n2);
-        for (int i = tid; i < n; i += T) {
-          const float x = from_ordered((uint32_t)(lists.key[i] >> 32));
-          lists.w[i] = weight(s, cs.table, x);
-          if (x >= border) atomicAdd(&cs.n_border, 1);
-        }
-        __syncthreads();
         const int n_k = by_k ? (int)min((int64_t)n, k) : n;
-        int n_kept = n_k;
-        bool sure = true;
-        if (by_p) {
-          // how many sums lie below top_p's share (of the sum known to err: below its least and its largest)
-          Pair low = total + Pair{-err, 0.0f}, high = total + Pair{err, 0.0f};
-          if (by_k || n == (int)finite) low = high = sums_of<T>(lists.w, n_k, cs.part, [](int, Pair, Pair) {});
-          const Pair p{draw.top_p, 0.0f};
-          low = p * low;
-          high = p * high;
-          sums_of<T>(lists.w, n_k, cs.part, [&](int, Pair, Pair with) {
-            if (with < low) atomicAdd(&cs.below[0], 1);
-            if (with < high) atomicAdd(&cs.below[1], 1);
-          });
-          __syncthreads();
-          sure = cs.below[0] == cs.below[1] && cs.below[1] < n_k;
-          n_kept = min(n_kept, cs.below[0] + 1);
-        }
-        n_kept = min(n_kept, cs.n_border);
-        if (!sure) {
-          if (tid == 0) report(a, r, kUndecided, m, 0.0f, (int32_t)finite);
-        } else {
-          // the kept ones in the row's order, with their place among the sorted
-          n2 = 2;
-          while (n2 < n_kept) n2 *= 2;
-          for (int i = tid; i < n2; i += T) lists.list[i] = i < n_kept ? lists.key[i] << 32 | (uint32_t)i : 0;
-          sort_down<T>(lists.list, n2);
-          // (sorted keys low words are ~index: the largest first is the lowest index first)
-          const Pair mass = sums_of<T>(lists.w, n_kept, cs.part, [](int, Pair, Pair) {});
-          constexpr int E = kCap / T;
-          Pair w[E];
-#pragma unroll
-          for (int i = 0; i < E; ++i) w[i] = tid * E + i < n_kept ? lists.w[(uint32_t)lists.list[tid * E + i]] : Pair{};
-          __syncthreads();
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (tid * E + i < n_kept) lists.w[tid * E + i] = w[i];
-          __syncthreads();
-          const Pair goal = pair_from(draw.u) * mass;
-          sums_of<T>(lists.w, n_kept, cs.part, [&](int i, Pair before, Pair) {
-            if (lists.w[i].h > 0.0f && before <= goal) atomicMax(&cs.token, i);
-          });
-          __syncthreads();
-          if (tid == 0) {
-            const uint64_t key = lists.list[max(cs.token, 0)];
-            const float x = from_ordered((uint32_t)(lists.key[(uint32_t)key] >> 32)), y = (x - m) / draw.temperature;
-            report(a, r, (int32_t) ~(uint32_t)(key >> 32), y - log_of(total), y - log_of(mass), n_kept);
-          }
-        }
-        }
+        const bool exact = by_k || n == (int)finite;
+        if (n <= T) draw_from_few<T>(a, r, cs, lists, draw, s, n, n_k, by_p, exact, total, err, border, (int)finite);
+        else draw_from_many<T>(a, r, cs, lists, draw, s, n, n_k, by_p, exact, total, err, border, (int)finite);
       }
     }
   }
@@ -766,8 +769,9 @@ cudaError_t launch_sample(const SampleArgs& a, int64_t rows, cudaStream_t stream
   if (pieces <= 256) {
     e = cut ? launch_clusters(sample_kernel<In, true, 64>, a, 1, rows, 64, stream) : launch_clusters(sample_kernel<In, false, 64>, a, 1, rows, 64, stream);
   } else {
-    // few rows are split over a cluster, down to a load round per CTA
-    const int64_t want = 7 * (int64_t)sm_count() / 2, round = 256 * 4;
+    // Few rows are split over a cluster, down to a load round per CTA, until there are five CTAs for two SMs
+    // (256 rows with the top 50: 39 us on clusters of two, 45 on four, 60 on one CTA).
+    const int64_t want = 5 * (int64_t)sm_count() / 2, round = 256 * 4;
     int cluster = 1;
     while (cluster < kMaxCluster && rows * cluster < want && pieces > cluster * round) cluster *= 2;
     e = cut ? launch_clusters(sample_kernel<In, true, 256>, a, cluster, rows, 256, stream)

@@ -8,8 +8,12 @@
 // (counts, or masses as 13-bit fractions of the bin's heaviest), refined until the bin
 // with the cut holds one value or at most 256 elements, which are sorted.
 //
-// Bound by latency: a row takes a handful of passes over its share (the first from L2, the
-// others from L1), each followed by an exchange over the cluster.
+// Bound by latency: a row takes one to four passes over its share (the first from L2, the
+// others from L1), each followed by an exchange over the cluster of about 2 us.  A row of
+// 151936 bf16 takes 14 us where nothing is cut off (one pass, whose weights are 4 us of
+// fp32 arithmetic), 33 with top-p: counting the values 5, their sums and weights 4, the
+// cut 4, the kept ones' mass by place 9.  Where nothing is cut off four CTAs share an SM
+// (64 registers: 1024 x 151936 136 us for both kernels, 199 with one of 512 threads).
 #include <algorithm>
 
 #include "sample.cuh"
