@@ -285,7 +285,6 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
   __shared__ __align__(16) unsigned char smem[sizeof(PassShared<T>)];
   __shared__ __align__(16) unsigned char cut_smem[CUT ? sizeof(CutShared<T>) : 16];
   Lists& lists = *reinterpret_cast<Lists*>(ring_smem);
-  uint4* ring = reinterpret_cast<uint4*>(ring_smem) + threadIdx.x;
   auto& sh = *reinterpret_cast<PassShared<T>*>(smem);
   auto& cs = *reinterpret_cast<CutShared<T>*>(cut_smem);
   ptx::grid_dep_launch_dependents();
@@ -326,24 +325,27 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
   uint32_t masked = 0;
   const uint64_t c2 = both(c);
   const int32_t inner = w0 == 0 && row.off > 0 ? 0 : min(w1, (row.off + a.vocab) / N);  // (the first piece may lack elements too)
-  auto request = [&](int32_t p0, int stage) {  // a round of whole pieces
+  constexpr uint32_t kStage = U * T * sizeof(uint4);
+  static_assert(kStages == 2 && (kStage & (kStage - 1)) == 0, "one round behind the one that is summed, told apart by a bit");
+  const uint32_t ring = ptx::smem_u32(ring_smem) + 16 * tid;
+  const uint4* next = reinterpret_cast<const uint4*>(row.x + (w0 * N - row.off)) + lane;  // the piece that is requested next
+  uint32_t stage = 0;
+  auto request = [&](int32_t p0, uint32_t to) {  // a round of whole pieces
     if (p0 + 32 * U <= inner) {
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        cp_async_16(ptx::smem_u32(ring + (stage * U + i) * T), row.x + ((p0 + 32 * i + lane) * N - row.off));
+      for (int i = 0; i < U; ++i) cp_async_16(ring + to + 16 * T * i, next + 32 * i);
     }
+    next += 32 * U;
     ptx::cp_async_commit();
   };
-  static_assert(kStages == 2, "one round behind the one that is summed");
   request(w0, 0);
-  request(w0 + 32 * U, 1);
-  int stage = 0;
-  for (int32_t p0 = w0; p0 < w1; p0 += 32 * U, stage ^= 1) {
+  request(w0 + 32 * U, kStage);
+  for (int32_t p0 = w0; p0 < w1; p0 += 32 * U, stage ^= kStage) {
     uint4 u[U];
     ptx::cp_async_wait<1>();
     if (p0 + 32 * U <= inner) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) u[i] = ring[(stage * U + i) * T];
+      for (int i = 0; i < U; ++i) u[i] = ld_shared_16(ring + stage + 16 * T * i);
     } else {
 #pragma unroll
       for (int i = 0; i < U; ++i) u[i] = p0 + 32 * i + lane < w1 ? row.load(p0 + 32 * i + lane) : absent<In>();

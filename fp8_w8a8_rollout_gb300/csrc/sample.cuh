@@ -107,7 +107,9 @@ __device__ __forceinline__ Scale scale_of(float m, float temperature) {
   return s;
 }
 
-// The weights of two elements, each hi + lo.  With d = m - x (exact as a pair) and t = d c
+// The weights of two elements, each hi + lo: a table-driven exponential (P. T. P. Tang, "Table-driven
+// implementation of the exponential function in IEEE floating-point arithmetic", ACM TOMS 15(2), 1989) in pairs
+// of numbers (T. J. Dekker, "A floating-point technique for extending the available precision", 1971).  With d = m - x (exact as a pair) and t = d c
 // (a pair), k = round(256 t) and the rest r: 2^-t = 2^-(k >> 8) 2^-((k & 255) / 256) e^g,
 // g = -r ln 2, |g| < 0.0014.  e^g - 1 = g + g^2 (1/2 + g/6) with g a pair: the
 // terms left out are below 2^-42.
@@ -231,6 +233,12 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // 16-byte asynchronous global -> shared copy past L1
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
 }
 
 // the rows that the pass has left (sample_exact.cu)
