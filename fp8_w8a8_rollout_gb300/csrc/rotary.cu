@@ -70,9 +70,10 @@ __device__ __forceinline__ float2 turn_of(const RotArgs& a, int32_t t, int32_t i
 }
 
 // the IEEE quotient x / s, r = RN(1 / s), of values whose codes do not saturate (the
-// others stop at 1024, so that x r does not overflow in between)
+// others stop at 1024, so that x r does not overflow in between; a NaN stays one)
 __device__ __forceinline__ float quotient(float x, float s, float r) {
-  x = fminf(fmaxf(x, -1024.0f * s), 1024.0f * s);
+  const float most = 1024.0f * s;
+  x = fabsf(x) > most ? copysignf(most, x) : x;
   return s >= kFastDivMinScale ? div_by_scale(x, s, r) : __fdiv_rn(x, s);
 }
 __device__ __forceinline__ uint32_t codes4(const float* x, float s, float r) {

@@ -282,3 +282,47 @@ def test_gradient_of_strided_and_shared_inputs():
     # back and forth: the rotation undoes itself but for two roundings to bf16
     back = fp8rl.rotary(q.detach(), None, pos, freqs, inverse=True)[0]
     assert ((back - h[:, :3]).abs().max() <= 2.0 ** -6 * h.abs().max()).item()
+
+
+@pytest.mark.parametrize("d", [128, 6])  # the vector path, any layout
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_keeps_nan(d, interleaved):
+    # a NaN in a pair makes both its elements NaN, in bf16 and as a code; what is infinite saturates
+    q, k, v = (x.contiguous() for x in qkv(5, 2, 2, d, 3))
+    freqs, inv, axis = plan(d, 1.0, 1)
+    pos = positions_of(5, 1, 50) + 1
+    k[1, 0, 0] = v[2, 1, 1] = float("nan")
+    k[3, 1, 1], v[4, 0, 0] = float("inf"), -float("inf")
+    at = torch.arange(5, device="cuda", dtype=torch.int32)
+    caches = [torch.zeros(5, 2 * d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    _, yk = fp8rl.rotary_kv_append(q, k, v, pos, freqs, at, *caches, torch.full((2,), 0.01, device="cuda"), interleaved=interleaved, keys=True)
+    codes = caches[0].view(5, 2, d)
+    want, _ = ref(k, pos, inv, axis, interleaved)
+    assert torch.equal(yk.isnan(), want.isnan()) and int(want.isnan().sum()) == 2
+    assert torch.equal((codes & 0x7F) == 0x7F, want.isnan())
+    far = want.abs() == float("inf")
+    assert int(far.sum()) == 2 and torch.equal(codes[far], torch.where(want[far] > 0, 0x7E, 0xFE).to(torch.uint8))
+    k_ref, v_ref = (torch.zeros_like(c) for c in caches)
+    fp8rl.kv_append(k.flatten(1), v.flatten(1), at, k_ref, v_ref, torch.full((2,), 0.01, device="cuda"))
+    assert torch.equal(caches[1], v_ref)
+
+
+def test_captured_backward_pass():
+    tokens, hq, hkv, d = 40, 4, 2, 128
+    freqs, _, _ = plan(d, 1.0, 1)
+    pos = positions_of(tokens, 1, 500)
+    q0, k0, _ = (x.contiguous() for x in qkv(tokens, hq, hkv, d, 1))
+    gq, gk = (torch.randn_like(x) for x in (q0, k0))
+    q, k = (torch.zeros_like(x).requires_grad_() for x in (q0, k0))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        yq, yk = fp8rl.rotary(q, k, pos, freqs)
+        grads = torch.autograd.grad((yq, yk), (q, k), (gq, gk))
+    with torch.no_grad():
+        q.copy_(q0), k.copy_(k0)
+    for _ in range(2):
+        graph.replay()
+        want = fp8rl.rotary(q0, k0, pos, freqs)
+        back = fp8rl.rotary(gq, gk, pos, freqs, inverse=True)
+        assert all(torch.equal(x, y) for x, y in zip((yq, yk, *grads), (*want, *back)))
+        gq.neg_()
