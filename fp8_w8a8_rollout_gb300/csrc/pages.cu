@@ -204,6 +204,12 @@ __device__ __forceinline__ RowNeed need_of(const ReserveArgs& a, int32_t r) {
   return n;
 }
 
+// the cache row of a position, or -1 where the table names no page
+__device__ __forceinline__ int32_t slot_of(const ReserveArgs& a, int64_t r, int64_t pos) {
+  const int32_t p = a.table[r * a.ldt + pos / a.block];
+  return p >= 0 && p < a.pages ? p * a.block + (int32_t)(pos % a.block) : -1;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const ReserveArgs a) {
   __shared__ uint64_t sums[32];
   __shared__ uint64_t slot[2];
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
       const int4 info = a.row[lo];
       const int64_t i = t - a.cu[lo], pos = info.x + i;
       int32_t s = -1;
-      if (i < info.y) s = a.table[lo * a.ldt + pos / a.block] * a.block + (int32_t)(pos % a.block);
+      if (i < info.y) s = slot_of(a, lo, pos);
       if (dcheck(t < a.total, a.err)) a.slots[t] = s;
     }
   } else {
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
       const int4 info = a.row[r];
       const int64_t pos = info.x + i;
       int32_t s = -1;
-      if (i < info.y) s = a.table[r * a.ldt + pos / a.block] * a.block + (int32_t)(pos % a.block);
+      if (i < info.y) s = slot_of(a, r, pos);
       if (dcheck(t < a.total, a.err)) a.slots[t] = s;
     }
   }

@@ -372,3 +372,18 @@ def test_two_streams_at_once():
         for _ in range(30):
             m.reserve([1] * 40)
         m.same()
+
+
+@pytest.mark.parametrize("entry", [-1, -7, 9, 2 ** 31 - 1, -2 ** 31, 2 ** 28])
+def test_a_table_entry_that_is_no_page_has_no_slots(entry):
+    # the tokens behind it on the same page have none either; those on the next page do
+    m = Model(2, 3, 16, 9, 32, 1)
+    m.prompts([13, 5])
+    table, lens, refs = m.dev
+    table[0, 0] = entry
+    slots, info = fp8rl.kv_reserve(table, lens, refs, 16, m.handle, total_tokens=8)
+    assert slots.tolist() == [-1, -1, -1, 32, 21, 22, 23, 24] and info.tolist() == [6, 0]
+    table[0, 1] = entry
+    cu = torch.tensor([0, 2, 3], dtype=torch.int32, device="cuda")
+    slots, info = fp8rl.kv_reserve(table, lens, refs, 16, m.handle, cu_seqlens=cu, total_tokens=3)
+    assert slots.tolist() == [-1, -1, 25] and info.tolist() == [6, 0]
