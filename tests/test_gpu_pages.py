@@ -387,3 +387,20 @@ def test_a_table_entry_that_is_no_page_has_no_slots(entry):
     cu = torch.tensor([0, 2, 3], dtype=torch.int32, device="cuda")
     slots, info = fp8rl.kv_reserve(table, lens, refs, 16, m.handle, cu_seqlens=cu, total_tokens=3)
     assert slots.tolist() == [-1, -1, 25] and info.tolist() == [6, 0]
+
+
+@pytest.mark.parametrize("width,ld", [(32, 32), (33, 40)])
+def test_many_copies_at_once(width, ld):
+    # several copies a CTA: runs of one page that begin and end anywhere, then moves of pages that differ
+    m = Model(140, 4, 8, 700, width, 64, ld=ld)
+    m.prompts([3 + 5 * (r % 5) for r in range(24)] + [0] * 116)
+    parent, r = [], 0
+    while len(parent) < 140:
+        parent += [r % 24] * (1 + r % 9)
+        r += 1
+    m.fork(parent[:140])
+    m.step([1] * 140)
+    m.step([7] * 140, width=7)
+    m.fork([r if r % 3 else -1 for r in range(140)])
+    m.step([r % 4 for r in range(140)], width=3)
+    m.compact()
