@@ -738,10 +738,13 @@ FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, int32_t logi
  *   d_kept      device, int32 [rows] out: how many tokens are kept; or null
  * A row of -inf alone gives token -1 and -inf, one with a NaN or +inf token -1 and
  * NaN; both keep 0.  Temperatures outside [1e-30, 1e30] count as the nearer end.
- * Weights and sums are carried to about 2^-43 of the sum, in an order that the
- * sizes and the rows' place in a 16-byte piece fix: the same bits on every run, and the
- * token of exact arithmetic but where u W lies that near a border.  One launch per
- * 65535 rows; no workspace.  Launched with programmatic stream serialisation.
+ * The token and the kept ones are those of weights and sums known to about 2^-43 of the sum (or of
+ * fp32 ones whose error bound reaches no border): the token of exact arithmetic but where u W
+ * lies that near a border.  lp and lp_kept are off by at most about 2^-18 besides their rounding.  The order of
+ * all sums is fixed by the sizes and the rows' place in a 16-byte piece: the same bits on every run.
+ * Two launches per 65535 rows, the second one for rows that the first leaves open (they are marked in
+ * the outputs in between, which are complete when the call's work is); no workspace.  Launched
+ * with programmatic stream serialisation.
  * Errors: INVALID_ARG (null pointers, negative rows, vocab < 1, ld < vocab; of the scalars that are used:
  *         T negative or not finite, top_k < 0, top_p not positive, min_p outside [0, 1]), SHAPE
  *         (vocab > 2^30), ALIGNMENT (element alignment), CUDA.
@@ -757,7 +760,7 @@ FP8RL_API fp8rl_status fp8rl_sample(const void* d_logits, int32_t logits_fp32, i
  * height, width).  Pair i of a head turns by the angle p f_i, p the token's position on
  * the pair's axis: (a, b) -> (a cos - b sin, a sin + b cos); with inverse = 1 by -p f_i, the
  * backward pass (the gradient of the unturned heads from that of the turned ones).
- * Angles are exact to 2^-32 of a turn at every position, the products are fp32
+ * Angles are known to 2^-26 of a turn at every position (fp32 half turns of an exact product), the products are fp32
  * and rounded once ("Where Rounding Happens Matters": the rotation stays in fp32).
  *   q_bf16     device, bf16 [tokens][q_heads * head_dim], row stride ldq (a column range of the qkv
  *              linear's output: nothing needs to be copied apart)
@@ -824,7 +827,8 @@ FP8RL_API fp8rl_status fp8rl_rotary_kv_append(const void* q_bf16, int64_t ldq, i
  *                  d_slots, not overlapping, clamped to [0, total_tokens]; null: total_tokens / rows entries each
  *   d_count        device, int32 [rows]: how many of its entries a row asks for, clamped to [0, entries]; null: all
  *   d_slots        device, int32 [total_tokens] out: the cache row of each new token (what fp8rl_kv_append
- *                  takes), -1 for entries that the row did not ask for or was refused; entries of no row are not written
+ *                  takes), -1 for entries that the row did not ask for or was refused, or whose page is none; entries of
+ *                  no row are not written
  *   d_info         device, int32 [2] out: pages free after the call, rows refused; or null
  *   d_workspace    device scratch of fp8rl_kv_reserve_workspace_size() bytes, 16-byte aligned, no initial
  *                  contents; one call at a time per buffer
