@@ -16,7 +16,9 @@
 // in fp32 against the running maximum, each thread's sum with a bound of its error.
 // Where nothing is cut off, the token is found by descending from the sums of warps
 // (each has a contiguous share of the row) to parts of one and to pieces, and
-// stands if u W is further from both its borders than the sums can be wrong.  Where something
+// stands if u W is further from both its borders than the sums can be wrong (what the shares before, behind and
+// at it may be off by, each with its factor: 40 of 1024 rows stay open, with twice the whole
+// sum's bound 128).  Where something
 // is cut off, the thread maxima give a bound below which nothing is kept (the k-th
 // largest; or so many of the largest that their masses alone reach p S), the few
 // elements above it are collected, sorted, weighed exactly, cut and drawn from.  A row
@@ -29,9 +31,9 @@
 //
 // Bound by HBM for many rows, by the chain of waits for few.  The exponentials' pass asks
 // 10 instructions an element: 1024 x 151936 bf16 takes 70 us (4.4 TB/s), and the
-// exact kernel 28 for the 128 or so draws of so many that fall among tokens lighter than 10^-5; with
+// exact kernel 28 for the 40 or so draws of so many that fall among the lightest tokens; with
 // top-50 and top-p 104 us.  Pieces come through a ring in shared memory, two
-// rounds ahead of each lane (without: 127 us for both kernels, 120 so).  16 rows: 8 us
+// rounds ahead of each lane (without: 127 us for both kernels, 120 so).  16 rows: 11 us
 // where nothing is cut off, 16 with top-50, 14 with min-p.
 #include <algorithm>
 
@@ -65,7 +67,7 @@ struct PassShared {
   float bound;             // of this CTA's share: at least its part of the first k lies at or above
   // of the whole row, after the pass
   Pair total, left;
-  float m, err, tau;
+  float m, err, margin, tau;
   uint32_t finite;
   int owner, owner_warp;
   Pair part[T / 32];
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
     }
     if (tid == 0) sh.bound = bound;
   }
-  if (ranks > 1) ptx::cluster_sync();
+  if (ranks > 1) cluster_sync();
   else __syncthreads();
 
   // the row's sums, in every CTA: lane i has the shares 2 i and 2 i + 1
@@ -477,20 +479,25 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       tau = fminf(tau, __shfl_xor_sync(0xffffffffu, tau, d));
     }
-    wt = 0.0f;
+    // What each sum may be off by: its exponentials (4 kStep each) and their sums four deep; and of each exponent
+    // x - m, log2(e) / T and their product are rounded, 3.3 kStep ln 2 times the exponent (and a share for wt itself).
+    float off[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float d = st[i].m == -INFINITY ? 0.0f : fmaxf((st[i].m - top) * c, kTinyExp2), f = st[i].m == -INFINITY ? 0.0f : ex2(d);
-      wt += f * fmaf(d - kMoved, st[i].s.h, st[i].wt);
-      st[i].s = Pair{st[i].s.h * f, st[i].s.l * f};
+      const float s = st[i].s.h;
+      st[i].s = Pair{s * f, st[i].s.l * f};
+      off[i] = kStep * fmaf(kSlope, fabsf(f * fmaf(d - kMoved, s, st[i].wt)), 9.0f * st[i].s.h);
     }
     masked = __reduce_add_sync(0xffffffffu, st[0].masked + st[1].masked);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) wt += __shfl_xor_sync(0xffffffffu, wt, k);
     const Pair incl = scan_lanes(st[0].s + st[1].s), total = shuffle(incl, 31);
-    // What the sum may be off by: its exponentials (4 kStep each) and their sums four deep; and of each exponent
-    // x - m, log2(e) / T and their product are rounded, 3.3 kStep ln 2 times the exponent (and a share for wt itself).
-    const float err = kStep * fmaf(kSlope, fabsf(wt), 9.0f * total.h);
+    float off_upto = off[0] + off[1];
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const float o = __shfl_up_sync(0xffffffffu, off_upto, k);
+      if (lane >= k) off_upto += o;
+    }
+    const float err = __shfl_sync(0xffffffffu, off_upto, 31);
     Pair before = shuffle_up(incl, 1);
     if (lane == 0) before = Pair{};
     const Pair goal = pair_from(draw.u) * total, middle = before + st[0].s;
@@ -502,6 +509,13 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
     }
     const uint32_t can = __ballot_sync(0xffffffffu, at >= 0);
     const int from = can ? 31 - __clz(can) : 0;
+    // By how much u W, less the sum ahead of a token in that warp's share, may be off.  With e what each weight is
+    // off by it is the sum of (1 - u) e over the shares before, of u e over those behind; the share itself is summed anew
+    // as far as the token: (1 + u) e, and 24 steps for what follows in fp32 there (the pairs: 2^-40).
+    const float u = (float)draw.u, own = at & 1 ? off[1] : off[0], ahead = off_upto - off[0] - off[1] + (at & 1 ? off[0] : 0.0f);
+    float margin = fmaf(1.0f - u, ahead, u * fmaxf(err - ahead - own, 0.0f));
+    margin += fmaf(1.0f + u, own, 24.0f * kStep * (at & 1 ? st[1].s.h : st[0].s.h));
+    margin = __shfl_sync(0xffffffffu, fmaf(margin, 1.0f + 0x1p-10f, 0x1p-38f * total.h + 0x1p-20f * err), from);
     at = __shfl_sync(0xffffffffu, at, from);
     start = shuffle(start, from);
     if (lane == 0) {
@@ -509,6 +523,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
       sh.left = goal - start;
       sh.m = top;
       sh.err = err;
+      sh.margin = margin;
       sh.tau = tau;
       sh.finite = (uint32_t)a.vocab - masked;
       sh.owner = at < 0 ? 0 : at / W;
@@ -621,8 +636,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
           rest = rest - Pair{__shfl_sync(0xffffffffu, incl, 31), 0.0f};
         }
         if (lane == 0) {
-          // both the sum ahead of the token and u W may be off by err, the last steps' by theirs
-          const float margin = fmaf(2.0f, err, 24.0f * kStep * total.h);
+          const float margin = sh.margin;
           if (under >= margin && over >= margin) {
             const float y = (x - m) / draw.temperature, lp = y - log_of(total);
             report(a, r, token, lp, lp, (int32_t)finite);
@@ -701,7 +715,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
         }
       }
     }
-    if (ranks > 1) ptx::cluster_sync();
+    if (ranks > 1) cluster_sync();
     else __syncthreads();
     int n = 0;
     bool whole = possible;
@@ -731,7 +745,7 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
         }
       }
     }
-    if (ranks > 1) ptx::cluster_sync();  // rank 0 has read the others' finds: they are done
+    if (ranks > 1) cluster_sync();  // rank 0 has read the others' finds: they are done
     if (rank == 0) {
       if (!whole || n < 1) {
         if (tid == 0) report(a, r, kUndecided, m, 0.0f, (int32_t)finite);

@@ -227,8 +227,13 @@ __device__ __forceinline__ float border_of(float m, double reach) { return __dou
 
 // A cluster barrier in two halves: a CTA that only has to outlive the others' reads of its
 // shared memory waits at its end
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// (not .aligned: the lanes may come from code that some of them ran alone)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
 
 // 16-byte asynchronous global -> shared copy past L1
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {

@@ -156,7 +156,7 @@ struct Team {
       if (lane == 0) (ranks > 1 ? sh.mine[turn] : sh.all[0]) = v;
     }
     if (ranks > 1) {
-      ptx::cluster_sync();
+      cluster_sync();
       if (threadIdx.x < ranks * 8) {
         const uint32_t r = threadIdx.x >> 3, w = threadIdx.x & 7;
         reinterpret_cast<uint32_t*>(&sh.all[r])[w] = ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&sh.mine[turn]), r) + 4 * w);
@@ -295,7 +295,7 @@ struct Team {
         for (uint32_t r = 0; r < ranks; ++r) n += ptx::ld_dsmem_u32(ptx::mapa_shared(at, r));
         sh.hist[rank * part + i] = n;
       }
-      ptx::cluster_sync();
+      cluster_sync();
     }
     uint32_t count[kEach], n_own = 0;
     Pair mass[kEach], own;
@@ -500,7 +500,7 @@ struct Team {
           if (q) atomicAdd(&sh.hist[b], q);
         }
       });
-      if (ranks > 1) ptx::cluster_sync();
+      if (ranks > 1) cluster_sync();
       else __syncthreads();
       // the cluster's bins, some a thread
       constexpr int kEach = kBins / T;
@@ -662,7 +662,7 @@ struct Team {
         key = (uint64_t)ptx::ld_dsmem_u32(from + 4) << 32 | ptx::ld_dsmem_u32(from);
         sh.sorted[threadIdx.x] = key;
       }
-      if (ranks > 1) ptx::cluster_sync();
+      if (ranks > 1) cluster_sync();
       else __syncthreads();
       int32_t at = 0;
       for (int32_t i = 0; i < n; ++i) at += sh.sorted[i] > key;
@@ -751,7 +751,7 @@ __device__ int64_t next_row(const SampleArgs& a, Shared<T>& sh, uint32_t rank, u
     }
   }
   if (ranks > 1) {
-    ptx::cluster_sync();
+    cluster_sync();
     return (int32_t)ptx::ld_dsmem_u32(ptx::mapa_shared(ptx::smem_u32(&sh.row), 0));
   }
   return row;
@@ -898,10 +898,10 @@ __global__ void __launch_bounds__(T, RESIDENT) sample_exact_kernel(const SampleA
         report(a, r, token, y - log_of(total), y - log_of(mass), kept);
       }
     }
-    if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's shared memory
+    if (ranks > 1) cluster_sync();  // the others have read this CTA's shared memory
     else __syncthreads();
   }
-  if (ranks > 1 && !own) ptx::cluster_sync();  // the others have read that there is no row
+  if (ranks > 1 && !own) cluster_sync();  // the others have read that there is no row
 }
 
 template <typename In, bool CUT, int T, int RESIDENT>
