@@ -15,6 +15,7 @@ larger maximum, which meet shrinking shares of S) + 2^-22 t (its exponent t in b
 mass of a row where something is cut off is exact to 2^-40."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -313,3 +314,37 @@ def test_two_streams_at_once():
     for pair in got:
         for a, b in zip(pair, want):
             assert all(torch.equal(c, d) for c, d in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab,rows", [(151936, 24), (151936, 320), (151936, 1300), (4001, 320), (1500, 320)])
+@pytest.mark.parametrize("t,k,p", [(1.0, 0, 1.0), (0.6, 0, 1.0), (1.0, 300, 0.9), (1.0, 0, 0.9)])
+@pytest.mark.parametrize("spread", [1.0, 4.0])
+def test_draws_next_to_a_border(dtype, vocab, rows, t, k, p, spread):
+    """u beside borders between tokens, 2^-34 to 2^-19 to both sides: what fp32 sums cannot tell apart, can just tell,
+    and can.  The borders are known to 2^-45 (extended sums of 64-bit weights).  The draws' weights are off by up to
+    2^-41.6 each; a lane's sum of n pairs by n roundings, 2^-25 each, of a low part that n roundings have made
+    (n 2^-50 of the sum as they come, n <= 150: 2^-42.8); u is held to 2^-48.  So a token may be the
+    neighbour of the one it should be where u W lies within 2^-40 W of a border (of any: light tokens have many)."""
+    x, _ = make(1, vocab, dtype, vocab + rows, spread=spread)
+    rng = np.random.default_rng(vocab + rows)
+    y = x[0].double().cpu().numpy()
+    w = np.exp((y - y.max()) / f32(t)).astype(np.longdouble)
+    order = np.argsort(-y, kind="stable")
+    order = order[:k] if k else order
+    mass = np.cumsum(w[order])
+    order = order[:int(np.searchsorted(mass, f32(p) * mass[-1])) + 1] if p < 1 else order
+    kept = np.zeros(vocab, dtype=bool)
+    kept[order] = True
+    upto = np.cumsum(np.where(kept, w, 0))
+    # borders of any token, and of tokens as they are drawn
+    at = np.concatenate([rng.choice(order, rows // 2), np.searchsorted(upto, rng.random(rows - rows // 2) * upto[-1], side="right")])
+    off = np.array([s * 2.0 ** -e for e in (34, 30, 27, 25, 23, 22, 21, 20, 19) for s in (-1, 1)])
+    u = np.clip((upto[at] / upto[-1]).astype(np.float64) + off[np.arange(rows) % len(off)], 0.0, LAST_U)
+    want = np.searchsorted(upto, u.astype(np.longdouble) * upto[-1], side="right")
+    token, _, _, n = fp8rl.sample(x.repeat(rows, 1), torch.tensor(u, device="cuda"), t, k, p)
+    assert (n == len(order)).all()
+    token, goal, near = token.cpu().numpy(), u.astype(np.longdouble) * upto[-1], np.longdouble(2.0) ** -40 * upto[-1]
+    ahead = np.concatenate([np.zeros(1, dtype=upto.dtype), upto])[token]
+    assert kept[token].all() and (ahead <= goal + near).all() and (goal - near <= upto[token]).all()
+    assert (token == want).mean() >= 0.99
