@@ -1384,7 +1384,8 @@ def kv_reserve(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
     [rows]), with count (int32 [rows], 0 or 1) for some; prompts: row r's new tokens
     are cu_seqlens[r] .. cu_seqlens[r + 1] of total_tokens (slots [total_tokens]).
     Entries that a row does not ask for are -1, and so are those of a row that is
-    refused (pages run out, or its table is full; it stays as it was).  info: pages
+    refused (pages run out, or its table is full; it stays as it was) and, of a padded
+    batch, those of no row (in slots of `out` these stay as they were).  info: pages
     free after the call, rows refused.  A last page that other rows hold too is
     copied first, in all `caches` (KvCaches, or a list of tensors)."""
     caches, rows, blocks, ldt, pages = _page_args(block_table, lens, refs, block_size, caches, count, cu_seqlens, workspace, *(out or ()))
@@ -1400,6 +1401,9 @@ def kv_reserve(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
         workspace = _workspace(_page_workspace(rows, total_tokens, block_size, None), refs.device, stream)
     if out is None:
         out = tuple(_outs((((total_tokens,), torch.int32), ((2,), torch.int32)), refs.device))
+        if cu_seqlens is not None:  # (the kernel leaves entries of no row as they are; no append may take them for slots)
+            with _on(stream, refs.device):
+                out[0].fill_(-1)
     else:
         _check_out(out[0], (total_tokens,), torch.int32, "slots")
         _check_out(out[1], (2,), torch.int32, "info")

@@ -1,0 +1,47 @@
+"""The pages of the cache where a batch has gaps or no rows, and where a page is as
+large as it can be: against the rules of the book-keeping."""
+import pytest
+import torch
+
+import fp8_w8a8_rollout_gb300 as fp8rl
+
+pytestmark = pytest.mark.gpu
+
+
+def pool(rows, cols, pages):
+    return (torch.full((rows, cols), -1, dtype=torch.int32, device="cuda"), torch.zeros(rows, dtype=torch.int32, device="cuda"),
+            torch.zeros(pages, dtype=torch.int32, device="cuda"))
+
+
+def ints(*values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("ends,total", [((3, 13, 13, 20), 32), ((0, 10, 10, 17), 17), ((0, 0, 0, 0), 9), ((5, 5, 25, 30), 31)])
+@pytest.mark.parametrize("on_side", [False, True])
+def test_entries_of_no_row_store_nothing(ends, total, on_side):
+    # a padded batch of prompts: what the allocator hands out again is full of slots of earlier calls
+    page, pages, hkv, d = 16, 12, 2, 64
+    table, lens, refs = pool(3, 4, pages)
+    caches = [torch.full((pages * page, hkv * d), 0x55, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    side = torch.cuda.Stream() if on_side else None
+    for _ in range(4):
+        old = [torch.full((total,), pages * page - 1, dtype=torch.int32, device="cuda") for _ in range(8)]
+        del old
+        table.fill_(-1), lens.zero_(), refs.zero_()
+        torch.cuda.synchronize()
+        slots, info = fp8rl.kv_reserve(table, lens, refs, page, caches, cu_seqlens=ints(*ends), total_tokens=total, stream=side)
+        torch.cuda.synchronize()
+        want, at = [-1] * total, 0
+        for r in range(3):
+            for i in range(ends[r + 1] - ends[r]):
+                want[ends[r] + i] = (at + i // page) * page + i % page
+            at += -(-(ends[r + 1] - ends[r]) // page)
+        assert slots.tolist() == want and info.tolist() == [pages - at, 0]
+    g = torch.Generator("cuda").manual_seed(1)
+    q, k, v = (torch.randn(total, h, d, generator=g, device="cuda").bfloat16() for h in (4, hkv, hkv))
+    fp8rl.rotary_kv_append(q, k, v, torch.zeros(total, dtype=torch.int32, device="cuda"), fp8rl.rotary_freqs(d), slots, *caches,
+                           torch.full((2,), 0.01, device="cuda"))
+    rest = torch.ones(pages * page, dtype=torch.bool, device="cuda")
+    rest[slots[slots >= 0].long()] = False
+    assert all((c[rest] == 0x55).all() for c in caches)
