@@ -1410,6 +1410,10 @@ def kv_reserve(block_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
     fp8rl_kv_reserve(block_table.data_ptr(), ldt, rows, blocks, block_size, lens.data_ptr(), refs.data_ptr(), pages, cu_seqlens, count,
                      total_tokens, out[0].data_ptr(), out[1].data_ptr(), caches.pointers, len(caches.tensors), caches.width, caches.ld,
                      workspace.data_ptr(), workspace.nbytes, stream)
+    if rows == 0:  # (that launches nothing: info is a row's without a table or tokens, whatever its length)
+        workspace = _workspace(_page_workspace(1, 0, block_size, None), refs.device, stream)
+        fp8rl_kv_reserve(None, 0, 1, 0, block_size, out[1].data_ptr(), refs.data_ptr(), pages, None, None, 0, None, out[1].data_ptr(),
+                         None, 0, 0, 0, workspace.data_ptr(), workspace.nbytes, stream)
     return out
 
 

@@ -829,7 +829,8 @@ FP8RL_API fp8rl_status fp8rl_rotary_kv_append(const void* q_bf16, int64_t ldq, i
  *   d_slots        device, int32 [total_tokens] out: the cache row of each new token (what fp8rl_kv_append
  *                  takes), -1 for entries that the row did not ask for or was refused, or whose page is none; entries of
  *                  no row are not written (where an append takes all entries of a padded batch, they are to be -1 before)
- *   d_info         device, int32 [2] out: pages free after the call, rows refused; or null
+ *   d_info         device, int32 [2] out: pages free after the call, rows refused; or null.  With rows = 0 nothing is
+ *                  launched, nothing written
  *   d_workspace    device scratch of fp8rl_kv_reserve_workspace_size() bytes, 16-byte aligned, no initial
  *                  contents; one call at a time per buffer
  * Errors: INVALID_ARG (null pointers, negative sizes, short strides, block_size < 1, total_tokens no multiple of

@@ -45,3 +45,18 @@ def test_entries_of_no_row_store_nothing(ends, total, on_side):
     rest = torch.ones(pages * page, dtype=torch.bool, device="cuda")
     rest[slots[slots >= 0].long()] = False
     assert all((c[rest] == 0x55).all() for c in caches)
+
+
+@pytest.mark.parametrize("pages,free", [(5, 5), (0, 0), (70001, 69997)])
+def test_an_empty_batch_reports_the_free_pages(pages, free):
+    table, lens, refs = pool(0, 4, pages)
+    refs[:pages - free] = 2
+    for more in ({}, {"cu_seqlens": ints(0), "total_tokens": 3}, {"out": (torch.empty(0, dtype=torch.int32, device="cuda"), ints(7, 7))},
+                 {"stream": torch.cuda.Stream()}, {"workspace": torch.empty(4096, dtype=torch.uint8, device="cuda")}):
+        old = [torch.full((2,), -9, dtype=torch.int32, device="cuda") for _ in range(8)]
+        del old
+        torch.cuda.synchronize()
+        slots, info = fp8rl.kv_reserve(table, lens, refs, 16, **more)
+        torch.cuda.synchronize()
+        assert info.tolist() == [free, 0] and slots.tolist() == [-1] * more.get("total_tokens", 0)
+    assert int(refs.sum()) == 2 * (pages - free)
