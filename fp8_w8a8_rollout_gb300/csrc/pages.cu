@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
       }
       if (a.rows == 0 || t < a.cu[lo] || t >= a.cu[lo + 1]) continue;  // of no row
       const int4 info = a.row[lo];
-      const int64_t i = t - a.cu[lo], pos = info.x + i;
+      const int64_t i = t - max(0, a.cu[lo]), pos = info.x + i;  // (ranges are clamped to the entries)
       int32_t s = -1;
       if (i < info.y) s = slot_of(a, lo, pos);
       if (dcheck(t < a.total, a.err)) a.slots[t] = s;

@@ -824,7 +824,7 @@ FP8RL_API fp8rl_status fp8rl_rotary_kv_append(const void* q_bf16, int64_t ldq, i
  * max_blocks, or when the pages that it and the rows ahead of it ask for are more than are
  * free at the start of the call.
  *   d_cu_seqlens   device, int32 [rows + 1]: row r's new tokens are entries [d_cu_seqlens[r], d_cu_seqlens[r + 1]) of
- *                  d_slots, not overlapping, clamped to [0, total_tokens]; null: total_tokens / rows entries each
+ *                  d_slots, ascending, clamped to [0, total_tokens]; null: total_tokens / rows entries each
  *   d_count        device, int32 [rows]: how many of its entries a row asks for, clamped to [0, entries]; null: all
  *   d_slots        device, int32 [total_tokens] out: the cache row of each new token (what fp8rl_kv_append
  *                  takes), -1 for entries that the row did not ask for or was refused, or whose page is none; entries of

@@ -60,3 +60,14 @@ def test_an_empty_batch_reports_the_free_pages(pages, free):
         torch.cuda.synchronize()
         assert info.tolist() == [free, 0] and slots.tolist() == [-1] * more.get("total_tokens", 0)
     assert int(refs.sum()) == 2 * (pages - free)
+
+
+def test_ranges_that_begin_ahead_of_the_entries():
+    # clamped to the entries there are: the first of them is the row's first new token
+    table, lens, refs = pool(2, 4, 10)
+    lens[0] = 5
+    table[0, 0], refs[0] = 0, 1
+    slots, info = fp8rl.kv_reserve(table, lens, refs, 16, cu_seqlens=ints(-3, 4, 9), total_tokens=7)
+    assert slots.tolist() == [5, 6, 7, 8, 16, 17, 18] and info.tolist() == [8, 0] and lens.tolist() == [9, 3]
+    slots, _ = fp8rl.kv_reserve(table, lens, refs, 16, count=ints(2, 1), cu_seqlens=ints(-2 ** 31, 3, 2 ** 31 - 1), total_tokens=5)
+    assert slots.tolist() == [9, 10, -1, 19, -1] and lens.tolist() == [11, 4]
