@@ -556,9 +556,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
       for (int k = 0; k < kRun; ++k) good = good && to[k] >= 0 && to[k] < a.pages;
       if (!dcheck(good, a.err)) continue;
       const P* src = base + (int64_t)c.src * a.block * ld;
-      const int32_t pieces = (int32_t)(c.rows * per_row);
-      auto place = [&](int32_t i) { return per_row == ld ? (int64_t)i : (i / per_row) * ld + i % per_row; };
-      for (int32_t i = threadIdx.x; i < pieces; i += U * kCopyThreads) {
+      const uint32_t pieces = (uint32_t)(c.rows * per_row);  // (below 2^31, so that a thread's last numbers, past them, do not wrap)
+      auto place = [&](uint32_t i) { return per_row == ld ? (int64_t)i : (i / per_row) * ld + i % per_row; };
+      for (uint32_t i = threadIdx.x; i < pieces; i += U * kCopyThreads) {
         P v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)

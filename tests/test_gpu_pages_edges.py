@@ -71,3 +71,22 @@ def test_ranges_that_begin_ahead_of_the_entries():
     assert slots.tolist() == [5, 6, 7, 8, 16, 17, 18] and info.tolist() == [8, 0] and lens.tolist() == [9, 3]
     slots, _ = fp8rl.kv_reserve(table, lens, refs, 16, count=ints(2, 1), cu_seqlens=ints(-2 ** 31, 3, 2 ** 31 - 1), total_tokens=5)
     assert slots.tolist() == [9, 10, -1, 19, -1] and lens.tolist() == [11, 4]
+
+
+@pytest.mark.parametrize("width", [2 ** 31 - 1, 2 ** 31 - 1024])
+def test_a_page_as_large_as_it_can_be(width):
+    # byte numbers within a page end at 2^31: odd widths go byte by byte, others by 16-byte pieces
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    cache = torch.zeros(3, width, dtype=torch.uint8, device="cuda")
+    g = torch.Generator("cuda").manual_seed(1)
+    cache[2, :4096] = torch.randint(1, 255, (4096,), generator=g, device="cuda", dtype=torch.int64).to(torch.uint8)
+    cache[2, -4096:] = torch.randint(1, 255, (4096,), generator=g, device="cuda", dtype=torch.int64).to(torch.uint8)
+    cache[2, width // 2] = 7
+    cache[1] = 9
+    table, lens, refs = ints(2, -1, 1, -1).view(2, 2), ints(1, 1), ints(0, 1, 1)
+    assert int(fp8rl.kv_compact(table, lens, refs, 1, [cache])) == 2
+    assert table[:, 0].tolist() == [0, 1] and refs.tolist() == [1, 1, 0]
+    assert torch.equal(cache[0], cache[2]) and bool((cache[1] == 9).all())
+    del cache
+    torch.cuda.empty_cache()
