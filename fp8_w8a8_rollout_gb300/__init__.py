@@ -1161,10 +1161,33 @@ class RotaryFreqs:
         self.data, self.rotary_dim, self.axes = data, rotary_dim, axes
 
 
+@functools.lru_cache(maxsize=None)
+def _pi(bits: int) -> int:
+    """pi in units of 2^-bits, off by less than one of them (Machin's formula, in integers)."""
+    def arctan_of_one_over(n):
+        term = total = (1 << bits + 32) // n
+        k = 1
+        while term:
+            term //= -n * n  # (rounds down: off by a unit a term at most)
+            k += 2
+            total += term // k
+        return total
+    return 4 * (4 * arctan_of_one_over(5) - arctan_of_one_over(239)) >> 32
+
+
+def _turns(f: float) -> int:
+    """f / (2 pi) in units of 2^-64, to the nearest: from f's own digits and as many of
+    pi (the fp64 quotient is off by 2^-54 of a turn, 2^-23 at position 2^31)."""
+    n, d = f.as_integer_ratio()
+    bits = 128 + max(0, n.bit_length() - d.bit_length())
+    n, d = n << 64 + bits, d * 2 * _pi(bits)
+    return (2 * n + d) // (2 * d)
+
+
 def rotary_freqs(rotary_dim: int, theta: float = 10000.0, sections=None, inv_freq=None, axis=None, device=None) -> RotaryFreqs:
     """Frequencies of rotary_dim // 2 pairs: theta ** (-2 i / rotary_dim) radians a
-    position, or the given ones (inv_freq: numbers, fp64 where they are exact, for
-    scaled positions).  With several axes, sections is how many pairs each takes, one
+    position (in fp64), or the given ones (inv_freq: numbers, fp64 where they are exact,
+    for scaled positions).  With several axes, sections is how many pairs each takes, one
     after the other ((16, 24, 24): time, height, width), or axis each pair's own
     (any order)."""
     if rotary_dim < 0 or rotary_dim % 2:
@@ -1184,10 +1207,7 @@ def rotary_freqs(rotary_dim: int, theta: float = 10000.0, sections=None, inv_fre
     if len(inv_freq) != pairs or len(axis) != pairs or any(a < 0 for a in axis) or not all(map(math.isfinite, inv_freq)):
         raise ValueError("one finite frequency and one axis for each of the rotary_dim // 2 pairs")
     axes = len(sections) if sections is not None else max(axis, default=0) + 1
-    turns = []
-    for f in inv_freq:
-        part = math.fmod(f / (2 * math.pi), 1.0)
-        turns.append((int(math.ldexp(part, 64)) + (1 << 63)) % (1 << 64) - (1 << 63))  # as a signed word
+    turns = [(_turns(float(f)) + (1 << 63)) % (1 << 64) - (1 << 63) for f in inv_freq]  # as signed words
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     return RotaryFreqs(torch.tensor([turns, axis], dtype=torch.int64).to(device), rotary_dim, axes)
 

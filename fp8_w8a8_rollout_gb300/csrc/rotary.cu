@@ -10,8 +10,8 @@
 // Angles of far positions lose their digits in fp32 (p f of 10^5 is known to
 // 0.008), so a frequency is held as the 64-bit binary fraction F of a turn per
 // position.  p F modulo 2^64 is the angle's fraction of a turn, exact for every
-// 32-bit position but for F's rounding, 2^-65 of a turn a position; its
-// upper 32 bits go to sincospi.  The product is rotated in fp32 and rounded once:
+// 32-bit position but for F's rounding, 2^-65 of a turn a position (2^-34 at the
+// last one); its upper 32 bits go to sincospi as fp32 half turns, 2^-26 of a turn.  The product is rotated in fp32 and rounded once:
 // to bf16, or (keys of the append) to the E4M3 code of the IEEE quotient by the
 // cache's scale.
 //

@@ -760,8 +760,9 @@ FP8RL_API fp8rl_status fp8rl_sample(const void* d_logits, int32_t logits_fp32, i
  * height, width).  Pair i of a head turns by the angle p f_i, p the token's position on
  * the pair's axis: (a, b) -> (a cos - b sin, a sin + b cos); with inverse = 1 by -p f_i, the
  * backward pass (the gradient of the unturned heads from that of the turned ones).
- * Angles are known to 2^-26 of a turn at every position (fp32 half turns of an exact product), the products are fp32
- * and rounded once ("Where Rounding Happens Matters": the rotation stays in fp32).
+ * Angles are known to 1.02 x 2^-26 of a turn at every position (the product's upper 32 bits as an fp32 half turn; 2^-34 at
+ * most comes from d_freqs, where that is rounded to the nearest), the products are fp32 and rounded once ("Where
+ * Rounding Happens Matters": the rotation stays in fp32).
  *   q_bf16     device, bf16 [tokens][q_heads * head_dim], row stride ldq (a column range of the qkv
  *              linear's output: nothing needs to be copied apart)
  *   k_bf16     device, bf16 [tokens][kv_heads * head_dim], row stride ldk; kv_heads may be 0, so may q_heads
