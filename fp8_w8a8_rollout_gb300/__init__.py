@@ -1239,7 +1239,7 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, fre
     """(q, k) turned by their positions: q [tokens, q_heads, d] and k [tokens,
     kv_heads, d] (bf16; column ranges of one projection's output are fine; k may be
     None), positions int32 [tokens], or [axes, tokens] for frequencies of several
-    axes.  `out` is such a pair and may be (q, k) itself.  inverse=True turns back,
+    axes (one row expanded over them, too).  `out` is such a pair and may be (q, k) itself.  inverse=True turns back,
     which is the backward pass; with q or k that require a gradient it runs under
     autograd (on the current stream of the backward pass)."""
     if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):

@@ -267,7 +267,7 @@ bool check_word(uint32_t** err) {
 fp8rl_status check(const RotArgs& a, int64_t tokens, int64_t hq, int64_t hkv, int64_t d, int64_t pairs, int64_t axes,
                    int32_t interleaved, bool* none) {
   *none = false;
-  if (tokens < 0 || hq < 0 || hkv < 0 || hq + hkv < 1 || d < 1 || pairs < 0 || 2 * pairs > d || axes < 1 || a.ldp < tokens ||
+  if (tokens < 0 || hq < 0 || hkv < 0 || hq + hkv < 1 || d < 1 || pairs < 0 || 2 * pairs > d || axes < 1 || (a.ldp < tokens && a.ldp != 0) ||
       (interleaved != 0 && interleaved != 1))
     return FP8RL_ERR_INVALID_ARG;
   if (d > kMaxHeadDim || hq > 8192 || hkv > 8192 || tokens >= (int64_t)1 << 31 || axes > 64) return FP8RL_ERR_SHAPE;

@@ -769,7 +769,7 @@ FP8RL_API fp8rl_status fp8rl_sample(const void* d_logits, int32_t logits_fp32, i
  *   d_freqs    device, int64 [2][pairs]: f_i / (2 pi) modulo 1 as a 64-bit binary fraction (times 2^64), then the
  *              pair's axis (a pair with an axis outside [0, axes) does not turn)
  *   pairs      of a head; 2 * pairs <= head_dim, the elements behind stay as they are
- *   d_positions device, int32 [axes][tokens], row stride ldp >= tokens
+ *   d_positions device, int32 [axes][tokens], row stride ldp >= tokens, or 0: all axes share one row (text)
  *   interleaved  0: pair i is elements i and pairs + i;  1: elements 2 i and 2 i + 1
  *   q_out, k_out device, bf16, row strides ldqo, ldko; may be q_bf16, k_bf16 themselves (with their
  *              row strides), no other overlap

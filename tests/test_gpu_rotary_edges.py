@@ -1,0 +1,30 @@
+"""Rotary positions at the ends of their ranges: positions that several axes share,
+as many tokens as a call takes, keys past the cache's scale."""
+import pytest
+import torch
+
+import fp8_w8a8_rollout_gb300 as fp8rl
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 37])
+@pytest.mark.parametrize("d", [128, 6])  # the vector path, any layout
+def test_positions_that_all_axes_share(tokens, d):
+    # text among images: one row of positions, expanded over the axes
+    g = torch.Generator("cuda").manual_seed(tokens)
+    q, k, v = (torch.randn(tokens, h, d, generator=g, device="cuda").bfloat16() for h in (4, 2, 2))
+    freqs = fp8rl.rotary_freqs(d, sections=(d // 2 - 2, 1, 1))
+    pos = torch.randint(0, 5000, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    shared, apart = pos.expand(3, -1), pos.repeat(3, 1)
+    want = fp8rl.rotary(q, k, apart, freqs)
+    assert all(torch.equal(a, b) for a, b in zip(fp8rl.rotary(q, k, shared, freqs), want))
+    caches = [[torch.zeros(tokens, 2 * d, dtype=torch.uint8, device="cuda") for _ in range(2)] for _ in range(2)]
+    at = torch.arange(tokens, device="cuda", dtype=torch.int32)
+    got = [fp8rl.rotary_kv_append(q, k, v, p, freqs, at, *c, torch.ones(2, device="cuda"))[0] for p, c in zip((shared, apart), caches)]
+    assert torch.equal(*got) and all(torch.equal(a, b) for a, b in zip(*caches))
+    x, y = (q.clone().requires_grad_() for _ in range(2))
+    fp8rl.rotary(x, None, shared, freqs)[0].sum().backward()
+    fp8rl.rotary(y, None, apart, freqs)[0].sum().backward()
+    assert torch.equal(x.grad, y.grad)
