@@ -305,7 +305,7 @@ fp8rl_status launch(RotArgs& a, int32_t interleaved, cudaStream_t stream) {
     const int32_t units = a.d / 16;
     a.tile = 1;
     while (a.tile < 8 && 2 * a.tile * units <= kRotThreads && (int64_t)a.tokens > (int64_t)2 * a.tile * 4 * sm_count()) a.tile *= 2;
-    cfg.gridDim = dim3((unsigned)((a.tokens + a.tile - 1) / a.tile));
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.tokens + a.tile - 1) / a.tile));  // (2^31 - 1 tokens: the sum is past 32 bits)
     cfg.dynamicSmemBytes = (size_t)a.tile * 2 * a.pairs * sizeof(float);
     e = interleaved ? cudaLaunchKernelEx(&cfg, rotary_kernel<APPEND, true>, a) : cudaLaunchKernelEx(&cfg, rotary_kernel<APPEND, false>, a);
   } else {

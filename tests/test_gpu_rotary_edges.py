@@ -28,3 +28,23 @@ def test_positions_that_all_axes_share(tokens, d):
     fp8rl.rotary(x, None, shared, freqs)[0].sum().backward()
     fp8rl.rotary(y, None, apart, freqs)[0].sum().backward()
     assert torch.equal(x.grad, y.grad)
+
+
+def test_as_many_tokens_as_a_call_takes():
+    tokens, d = 2 ** 31 - 1, 16
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB")
+    q = torch.zeros(tokens, 1, d, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(tokens, dtype=torch.int32, device="cuda")
+    g = torch.Generator("cuda").manual_seed(1)
+    freqs = fp8rl.rotary_freqs(d)
+    ends = (slice(0, 33), slice(tokens // 2, tokens // 2 + 33), slice(tokens - 33, tokens))
+    want = []
+    for s in ends:
+        q[s] = torch.randn(33, 1, d, generator=g, device="cuda").bfloat16()
+        pos[s] = torch.randint(0, 1000, (33,), generator=g, device="cuda", dtype=torch.int32)
+        want.append(fp8rl.rotary(q[s].clone(), None, pos[s].clone(), freqs)[0])
+    fp8rl.rotary(q, None, pos, freqs, out=(q, None))
+    assert all(torch.equal(q[s], w) for s, w in zip(ends, want))
+    del q, pos
+    torch.cuda.empty_cache()
