@@ -23,6 +23,7 @@
 // 65536 tokens 198 us (6.8 TB/s), 8192 29; with the append 65536 tokens 237 us (6.2 TB/s; the
 // quotients' instructions), 4001 16.3, 16 tokens 3.0.
 #include <algorithm>
+#include <cfloat>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -72,12 +73,12 @@ __device__ __forceinline__ float2 turn_of(const RotArgs& a, int32_t t, int32_t i
   return cs;
 }
 
-// the IEEE quotient x / s, r = RN(1 / s), of values whose codes do not saturate (the
-// others stop at 1024, so that x r does not overflow in between; a NaN stays one)
+// the IEEE quotient x / s, r = RN(1 / s), of values whose codes do not saturate; 1024 stands for those of the
+// others, infinities among them (s past 2^118 too, where 1024 s would be infinite).  A NaN stays one
 __device__ __forceinline__ float quotient(float x, float s, float r) {
-  const float most = 1024.0f * s;
-  x = fabsf(x) > most ? copysignf(most, x) : x;
-  return s >= kFastDivMinScale ? div_by_scale(x, s, r) : __fdiv_rn(x, s);
+  const float most = fminf(1024.0f * s, FLT_MAX);
+  const float q = s >= kFastDivMinScale ? div_by_scale(x, s, r) : __fdiv_rn(x, s);
+  return fabsf(x) > most ? copysignf(1024.0f, x) : q;
 }
 __device__ __forceinline__ uint32_t codes4(const float* x, float s, float r) {
   return e4m3x2(quotient(x[0], s, r), quotient(x[1], s, r)) | e4m3x2(quotient(x[2], s, r), quotient(x[3], s, r)) << 16;

@@ -48,3 +48,22 @@ def test_as_many_tokens_as_a_call_takes():
     assert all(torch.equal(q[s], w) for s, w in zip(ends, want))
     del q, pos
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("d", [128, 6])  # the vector path, any layout
+@pytest.mark.parametrize("scale", [5e35, 7.5e35, 0.01])
+def test_keys_that_are_infinite_saturate_at_every_scale(d, scale):
+    # 1024 scales are past fp32's range from 3.3e35 on (the largest bf16 calibrates to 7.6e35)
+    k = torch.zeros(4, 1, d, dtype=torch.bfloat16, device="cuda")
+    k[0, 0, 0], k[1, 0, 1], k[2, 0, 0], k[2, 0, d // 2], k[3, 0, 0] = INF, -INF, 3e38, -3e38, 208 * scale
+    pos = torch.tensor([0, 0, 1, 0], dtype=torch.int32, device="cuda")
+    freqs = fp8rl.rotary_freqs(d, inv_freq=[0.7853981633974483] * (d // 2))  # (an eighth of a turn: sums of both halves)
+    caches = [torch.zeros(4, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    # a turn by 0 would meet 0 x infinity in the pair's other element
+    fp8rl.rotary_kv_append(k, k, k, pos, freqs, torch.arange(4, device="cuda", dtype=torch.int32), *caches,
+                           torch.tensor([scale, 1.0], device="cuda"))
+    codes = caches[0].cpu()
+    assert int(codes[0, 0]) == 0x7E and int(codes[1, 1]) == 0xFE
+    assert int(codes[3, 0]) == int(torch.tensor(208.0).to(torch.float8_e4m3fn).view(torch.uint8))
+    # (3e38 + 3e38) / sqrt(2) is infinite in fp32
+    assert int(codes[2, 0]) == 0x7E
