@@ -479,15 +479,17 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       tau = fminf(tau, __shfl_xor_sync(0xffffffffu, tau, d));
     }
-    // What each sum may be off by: its exponentials (4 kStep each) and their sums four deep; and of each exponent
-    // x - m, log2(e) / T and their product are rounded, 3.3 kStep ln 2 times the exponent (and a share for wt itself).
+    // What each sum may be off by: its exponentials (4 kStep each) and their sums four deep, and the n rounds' own
+    // sum (n^2 2^-53 where all are equal: a step from 2^14 rounds on); and of each exponent x - m, log2(e) / T and
+    // their product are rounded, 3.3 kStep ln 2 times the exponent (and a share for wt itself).
+    const float rounds = (float)((each + 32 * U - 1) / (32 * U)), steps = fmaf(rounds * 0x1p-14f, rounds * 0x1p-14f, 9.0f);
     float off[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float d = st[i].m == -INFINITY ? 0.0f : fmaxf((st[i].m - top) * c, kTinyExp2), f = st[i].m == -INFINITY ? 0.0f : ex2(d);
       const float s = st[i].s.h;
       st[i].s = Pair{s * f, st[i].s.l * f};
-      off[i] = kStep * fmaf(kSlope, fabsf(f * fmaf(d - kMoved, s, st[i].wt)), 9.0f * st[i].s.h);
+      off[i] = kStep * fmaf(kSlope, fabsf(f * fmaf(d - kMoved, s, st[i].wt)), steps * st[i].s.h);
     }
     masked = __reduce_add_sync(0xffffffffu, st[0].masked + st[1].masked);
     const Pair incl = scan_lanes(st[0].s + st[1].s), total = shuffle(incl, 31);

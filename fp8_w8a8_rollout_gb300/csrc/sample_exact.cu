@@ -1,5 +1,5 @@
 // sample_exact.cu -- the draws that sampling's pass leaves open: weights and sums to
-// about 2^-43.  (sample.cu says what is computed and why twice.)
+// 2^-40, as a rule 2^-44.  (sample.cu says what is computed and why twice.)
 //
 // A cluster takes a row, a CTA a contiguous share of it, a warp a contiguous share of
 // that and a lane a contiguous run of pieces, so that sums by place in the row fall
@@ -126,9 +126,13 @@ struct Team {
     b = min(c1, a + each);
   }
 
-  // f(values, index of the first) of the pieces [a, b), lane by lane; elements of no piece are -inf
-  template <typename F>
-  __device__ __forceinline__ void each(int32_t a, int32_t b, F f) const {
+  // f(values, index of the first) of the pieces [a, b), lane by lane, and then() after a few; elements of no piece
+  // are -inf
+  struct Nothing {
+    __device__ __forceinline__ void operator()() const {}
+  };
+  template <typename F, typename G = Nothing>
+  __device__ __forceinline__ void each(int32_t a, int32_t b, F f, G then = G{}) const {
     for (int32_t p0 = a; p0 < b; p0 += 32 * kUnroll) {
       uint4 u[kUnroll];
 #pragma unroll
@@ -142,6 +146,7 @@ struct Team {
         values<In>(u[i], v);
         f(v, (p0 + 32 * i + lane) * N - row.off);
       }
+      then();
     }
   }
 
@@ -171,7 +176,7 @@ struct Team {
 
   // mass and number of the kept elements of the pieces [a, b), this lane's part
   __device__ Part mass(const Scale& s, const Keep& keep, int32_t a, int32_t b) const {
-    Sum sum;
+    LongSum sum;
     uint32_t n = 0;
     each(a, b, [&](float (&v)[N], int32_t j0) {
       bool any = false;
@@ -191,7 +196,7 @@ struct Team {
         weights(s, sh.table, v[e], v[e + 1], h, l);
         sum.add(h, l);
       }
-    });
+    }, [&] { sum.fold(); });
     Part p;
     p.a = sum.value();
     p.n = n;
@@ -203,7 +208,7 @@ struct Team {
   __device__ __forceinline__ int32_t run() const { return (w1 - w0 + 31) / 32; }
   template <bool ALL>
   __device__ Part mass_of_run(const Scale& s, const Keep& keep, const Ties& ties) const {
-    Sum sum;
+    LongSum sum;
     Part p;
     const int32_t a = w0 + lane * run();
     for (int32_t i0 = 0; i0 < run(); i0 += kUnroll) {
@@ -236,6 +241,7 @@ struct Team {
           sum.add(h, l);
         }
       }
+      sum.fold();
     }
     p.a = sum.value();
     return p;
@@ -263,7 +269,7 @@ struct Team {
     for (int i = threadIdx.x; i < kValueBins; i += T) sh.hist[i] = 0;
     __syncthreads();
     // counts, and the tiny ones' mass
-    Sum sum;
+    LongSum sum;
     each(w0, w1, [&](float (&v)[N], int32_t) {
       bool any = false;
 #pragma unroll
@@ -282,7 +288,7 @@ struct Team {
         weights(s, sh.table, v[e], v[e + 1], h, l);
         sum.add(h, l);
       }
-    });
+    }, [&] { sum.fold(); });
     Part tiny;
     tiny.a = sum.value();
     tiny = gather(tiny);  // (and the counts are there)
@@ -565,7 +571,7 @@ struct Team {
       Part t;
       for (int way = 0;;) {
         Part p;
-        Sum sa, sb;
+        LongSum sa, sb;
         each(w0, w1, [&](float (&v)[N], int32_t j0) {
           bool any = false;
           bool in[N];
@@ -596,6 +602,9 @@ struct Team {
             sb.add(pair_of(in[e] ? h0 : 0.0f, in[e + 1] ? h1 : 0.0f), pair_of(in[e] ? l0 : 0.0f, in[e + 1] ? l1 : 0.0f));
             sa.add(pair_of(in[e] ? 0.0f : h0, in[e + 1] ? 0.0f : h1), pair_of(in[e] ? 0.0f : l0, in[e + 1] ? 0.0f : l1));
           }
+        }, [&] {
+          sa.fold();
+          sb.fold();
         });
         p.a = sa.value();
         p.b = sb.value();

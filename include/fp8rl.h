@@ -738,7 +738,7 @@ FP8RL_API fp8rl_status fp8rl_logprob_backward(const void* d_logits, int32_t logi
  *   d_kept      device, int32 [rows] out: how many tokens are kept; or null
  * A row of -inf alone gives token -1 and -inf, one with a NaN or +inf token -1 and
  * NaN; both keep 0.  Temperatures outside [1e-30, 1e30] count as the nearer end.
- * The token and the kept ones are those of weights and sums known to about 2^-43 of the sum (or of
+ * The token and the kept ones are those of weights and sums known to 2^-40 of the sum (to 2^23 logits; or of
  * fp32 ones whose error bound reaches no border): the token of exact arithmetic but where u W
  * lies that near a border.  lp and lp_kept are off by at most about 2^-18 besides their rounding.  The order of
  * all sums is fixed by the sizes and the rows' place in a 16-byte piece: the same bits on every run.
