@@ -5,7 +5,7 @@
 // that and a lane a contiguous run of pieces, so that sums by place in the row fall
 // out and the token is found by descending through them.  The cut of top-k and top-p: by
 // counts of the values themselves (bf16), or by histograms of 1024 bins over the values
-// (counts, or masses as 13-bit fractions of the bin's heaviest), refined until the bin
+// (counts, or masses as fractions of the bin's heaviest, of up to 13 bits), refined until the bin
 // with the cut holds one value or at most 256 elements, which are sorted.
 //
 // Bound by latency: a row takes one to four passes over its share (the first from L2, the
@@ -484,6 +484,9 @@ struct Team {
     float hi = s.m, lo = -FLT_MAX, pre = 1.0f, scale = 16.0f * s.hi, step = 1.0f / 16.0f;
     Pair above;            // mass and number of what lies above the range
     uint32_t n_above = 0;
+    // a bin adds up to `unit` an element: 13 bits, or as many as leave the sum of all of the row's below 2^32 (rows from
+    // 2^19 on; a bin that wrapped misplaced the cut's first guess: 4.7 ms where 0.15 do)
+    const float unit = (float)(8192u >> max(0, 32 - __clz(row.vocab) - 19));
     for (;;) {
       auto place = [&](float x, int32_t j, float& f) {  // the bin, or -1
         if (!(x <= hi && x >= lo && keep(x, j))) return -1;
@@ -502,7 +505,7 @@ struct Team {
           float f;
           const int b = place(v[e], j0 + e, f);
           if (b < 0) continue;
-          const uint32_t q = by_count ? 1u : (uint32_t)(ex2(fmaxf(((float)b - f) * step, -64.0f)) * 8192.0f);
+          const uint32_t q = by_count ? 1u : (uint32_t)(ex2(fmaxf(((float)b - f) * step, -64.0f)) * unit);
           if (q) atomicAdd(&sh.hist[b], q);
         }
       });
@@ -553,7 +556,7 @@ struct Team {
         }
         f_all += sh.warp[w].most;
       }
-      // (the masses are up to 2^-13 small: as shares of their own sum, head and tail are good to that)
+      // (the masses are up to 1 / unit small: as shares of their own sum, head and tail are good to that)
       const float share = (target - above).h / whole.h * f_all;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {

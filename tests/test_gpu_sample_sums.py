@@ -1,5 +1,6 @@
 """Sampling from long rows of equal weights: the exact kernel's sums, and how it finds
 a cut among them."""
+import math
 
 import numpy as np
 import pytest
@@ -31,3 +32,50 @@ def test_borders_between_long_runs_of_equal_weights(vocab, rows):
     token, _, _, kept = fp8rl.sample(x, torch.tensor(u, device="cuda"), 1.0, 0, 1.0, 1e-6)
     assert (kept == vocab).all()
     assert int((token.cpu().numpy() != np.where(side < 0, half - 1, half)).sum()) == 0
+
+
+def time_of(x, u, top_p):
+    out = fp8rl.sample(x, u, 1.0, 0, top_p)
+    best = math.inf
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        fp8rl.sample(x, u, 1.0, 0, top_p, out=out)
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best, out
+
+
+def two_values(n, rows=1):
+    """50 logits of 0, n of -10: each of the latter is 2^-0.83 / 16 = 7902 / 8192 of its bin's heaviest."""
+    x = torch.full((rows, 50 + n), -10.0, device="cuda")
+    x[:, 1000:1050] = 0.0
+    return x
+
+
+def test_a_cut_behind_more_elements_than_32_bits_of_mass_hold():
+    # 543530 x 7902 is 2^32 and 4764 more: a bin that wraps looks empty, and the cut is then sought bin by bin (230 of
+    # them, a pass each).  The tokens are the same either way; the time is not.
+    u = torch.tensor([0.9], device="cuda", dtype=torch.float64)
+    fits, _ = time_of(two_values(500000), u, 0.9)
+    n = 543530
+    took, (token, lp, lp_kept, kept) = time_of(two_values(n), u, 0.9)
+    w = math.exp(-10.0)
+    want = math.ceil((0.9 * (50 + n * w) - 50) / w)  # of the light ones, the lowest ids first
+    assert abs(int(kept) - 50 - want) <= 1  # (top_p is fp32: 2^-25 of the mass is 0.04 of a token)
+    goal, light = 0.9 * (50 + (int(kept) - 50) * w), (0.9 * (50 + (int(kept) - 50) * w) - 50) / w
+    assert abs(int(token) - (50 + math.floor(light))) <= 1 and goal > 50
+    assert took <= 4 * fits, (took, fits)
+
+
+@pytest.mark.parametrize("vocab", [1 << 20, (1 << 21) + 77])
+@pytest.mark.parametrize("top_p", [0.3, 0.95])
+def test_flat_rows_of_millions(vocab, top_p):
+    x = torch.full((2, vocab), 1.5, device="cuda")
+    u = torch.tensor([0.25, 1 - 2.0 ** -53], device="cuda", dtype=torch.float64)
+    token, _, lp_kept, kept = fp8rl.sample(x, u, 1.0, 0, top_p)
+    p = torch.tensor(top_p).double().item()
+    n = math.ceil(p * vocab)
+    assert kept.tolist() == [n, n] and token.tolist() == [math.floor(0.25 * n), n - 1]
+    assert (lp_kept + math.log(n)).abs().max() <= 2.0 ** -21 * math.log(n)
