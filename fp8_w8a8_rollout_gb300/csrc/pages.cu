@@ -263,17 +263,18 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
   const uint64_t end = first;  // pages that the rows ask for
 
   // the lowest free pages, as many as may be handed out
+  const uint64_t handed = min(end, avail);
   uint64_t rank_at = rank_before + before;
-  if (mine > 0 && rank_at < end) {
+  if (mine > 0 && rank_at < handed) {
     each_four(a.refs, p0, p1, a.vec, 1, [&](int32_t p, int4 c) {
-      if (rank_at >= end) return;  // (all lanes alike)
+      if (rank_at >= handed) return;  // (all lanes alike)
       const int32_t v[4] = {c.x, c.y, c.z, c.w};
       uint32_t total;
       uint64_t at = rank_at + lanes_before((c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0), total);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (v[i] != 0) continue;
-        if (at < end && at < (uint64_t)a.list_cap && dcheck(at < (uint64_t)a.list_cap, a.err)) a.list[at] = p + i;
+        if (at < handed && dcheck(at < (uint64_t)a.list_cap && p + i < a.pages, a.err)) a.list[at] = p + i;
         ++at;
       }
       rank_at += total;
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
       const int32_t fresh = a.list[at++];
       if (lane == 0) {
         const int32_t old = row[held - 1];
-        if (atomicSub(a.refs + old, 1) == 1) atomicAdd(&freed, 1);
-        if (dcheck(fresh >= 0 && fresh < a.pages && copy_at < a.rows, a.err)) {
+        if (dcheck(fresh >= 0 && fresh < a.pages && old >= 0 && old < a.pages && held <= a.cols && copy_at < a.rows, a.err)) {
+          if (atomicSub(a.refs + old, 1) == 1) atomicAdd(&freed, 1);
           a.refs[fresh] = 1;
           row[held - 1] = fresh;
           a.copies[copy_at] = Copy{old, fresh, len % a.block, 0};
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
         row[j] = p;
       }
     }
-    if (lane == 0 && dcheck(r < a.rows, a.err)) a.lens[r] = len + given;
+    if (lane == 0 && dcheck(after <= a.cols, a.err)) a.lens[r] = len + given;
   };
   for (int32_t r = (int32_t)rank * kPlanThreads + tid; r < a.rows; r += (int32_t)ranks * kPlanThreads) hand_out(r, 0, 1);
   if (many)
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
   __syncthreads();
   uint64_t all_freed;
   cluster_scan((uint64_t)freed, &slot[1], ranks, all_freed);  // (with one CTA the barrier above is the one needed)
-  if (rank == 0 && tid == 0) {
+  if (rank == 0 && tid == 0 && dcheck(copies <= (uint64_t)a.rows && taken <= avail, a.err)) {
     a.header[0] = (int32_t)copies;
     if (a.info) {
       a.info[0] = (int32_t)(n_free - taken + all_freed);
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
       const int64_t i = t - max(0, a.cu[lo]), pos = info.x + i;  // (ranges are clamped to the entries)
       int32_t s = -1;
       if (i < info.y) s = slot_of(a, lo, pos);
-      if (dcheck(t < a.total, a.err)) a.slots[t] = s;
+      if (dcheck(i >= 0 && s < (int64_t)a.pages * a.block, a.err)) a.slots[t] = s;
     }
   } else {
     for (int64_t t = (int64_t)rank * kPlanThreads + tid; t < a.total; t += (int64_t)ranks * kPlanThreads) {
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
       const int64_t pos = info.x + i;
       int32_t s = -1;
       if (i < info.y) s = slot_of(a, r, pos);
-      if (dcheck(t < a.total, a.err)) a.slots[t] = s;
+      if (dcheck(r < a.rows && s < (int64_t)a.pages * a.block, a.err)) a.slots[t] = s;
     }
   }
   if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's slot
@@ -392,10 +393,10 @@ __global__ void __launch_bounds__(128) fork_kernel(const ForkArgs a) {
         page = a.in[p * a.ld_in + j];
         if (!stays && page >= 0 && page < a.pages) atomicAdd(a.refs + page, 1);
       }
-      if (dcheck(j < a.cols, a.err)) a.out[r * a.ld_out + j] = page;
+      if (dcheck(j < a.ld_out && held <= a.cols, a.err)) a.out[r * a.ld_out + j] = page;
     }
   }
-  if (threadIdx.x == 0 && r < a.rows_out && dcheck(r < a.rows_out, a.err)) a.lens_out[r] = new_len;
+  if (threadIdx.x == 0 && r < a.rows_out && dcheck(held <= a.cols, a.err)) a.lens_out[r] = new_len;
 }
 
 // ------------------------------------------------------------------ compact
@@ -463,14 +464,14 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
       } else if (v[i] > 0) {
         if (dcheck((int32_t)m <= a.pages / 2, a.err)) a.copies[m].src = p + i;
         ++m;
-      } else if (dcheck(p + i < a.pages, a.err)) {
+      } else if (dcheck(p >= 0 && p + i < a.pages, a.err)) {
         a.to[p + i] = p + i;  // (no row holds it, or the counts are wrong)
       }
     }
     hole += total & 0xffffu;
     mover += total >> 16;
   });
-  if (rank == 0 && threadIdx.x == 0) {
+  if (rank == 0 && threadIdx.x == 0 && dcheck(moves <= a.pages / 2 && moves <= n && n <= a.pages, a.err)) {
     a.header[0] = moves;
     a.header[1] = n;
     if (a.used) a.used[0] = n;
@@ -478,9 +479,9 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
   sync_all(ranks);  // nobody counts from here on
   for (int32_t k = rank * kPlanThreads + threadIdx.x; k < moves; k += (int32_t)ranks * kPlanThreads) {
     Copy& c = a.copies[k];
-    c.rows = a.block;
     const int32_t src = c.src, dst = c.dst;
-    if (dcheck(src >= n && src < a.pages && dst >= 0 && dst < n, a.err)) {
+    if (dcheck(k <= a.pages / 2 && src >= n && src < a.pages && dst >= 0 && dst < n, a.err)) {
+      c.rows = a.block;
       a.to[src] = dst;
       a.refs[dst] = a.refs[src];
       a.refs[src] = 0;
@@ -516,7 +517,7 @@ __device__ __forceinline__ void follow(const CopyArgs& a) {
     if (j * a.block >= len) continue;  // (entries past a row's pages say nothing)
     int32_t* at = a.table + r * a.ldt + j;
     const int32_t p = *at;
-    if (p >= n && p < a.pages && dcheck(r < a.rows, a.err)) *at = a.to[p];
+    if (p >= n && p < a.pages && dcheck(j < a.ldt && a.to[p] >= 0 && a.to[p] <= p, a.err)) *at = a.to[p];
   }
 }
 

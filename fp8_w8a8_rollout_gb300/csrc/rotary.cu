@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const RotArgs a
     if (APPEND && (key || value) && slot >= 0) {
       const float sc = key ? sk : sv;
       uint8_t* code = (key ? a.kc : a.vc) + slot * a.ldc + (int64_t)(h - (key ? a.hq : keys)) * a.d;
-      if (dcheck(slot < a.num_slots, a.err)) {
+      if (dcheck(slot < a.num_slots && (int64_t)(h - (key ? a.hq : keys) + 1) * a.d <= a.ldc, a.err)) {
         code[c0] = (uint8_t)e4m3x2(__fdiv_rn(y0, sc), 0.0f);
         if (turned) code[c1] = (uint8_t)e4m3x2(__fdiv_rn(y1, sc), 0.0f);
       }

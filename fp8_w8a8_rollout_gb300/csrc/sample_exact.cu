@@ -752,7 +752,7 @@ __device__ int64_t next_row(const SampleArgs& a, Shared<T>& sh, uint32_t rank, u
       }
       cursor = nearest + 1;
       const int32_t r = start + nearest < rows ? start + nearest : start + nearest - rows;
-      if (threadIdx.x == 0) sh.row = atomicCAS(a.tokens + r, kUndecided, kTaken) == kUndecided ? r : -1;
+      if (threadIdx.x == 0) sh.row = dcheck(r >= 0 && r < rows, a.err) && atomicCAS(a.tokens + r, kUndecided, kTaken) == kUndecided ? r : -1;
       __syncthreads();
       row = sh.row;
       if (row >= 0) break;
