@@ -69,6 +69,12 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* sums, uint6
 }
 static_assert(kPlanThreads == 32 * 32, "block_scan takes 32 warps");
 
+// The cluster's barrier, not .aligned: lanes come to it from code that some of them ran alone (one that stores, loops of
+// different lengths), and an aligned barrier that a warp's lanes do not reach together is undefined
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // this CTA's place in the sum over the cluster's CTAs
 __device__ __forceinline__ uint64_t cluster_scan(uint64_t mine, uint64_t* slot, uint32_t ranks, uint64_t& total) {
   if (ranks == 1) {
@@ -76,7 +82,7 @@ __device__ __forceinline__ uint64_t cluster_scan(uint64_t mine, uint64_t* slot, 
     return 0;
   }
   if (threadIdx.x == 0) *slot = mine;
-  ptx::cluster_sync();
+  cluster_sync();
   const uint32_t rank = ptx::cluster_ctarank();
   uint64_t before = 0;
   total = 0;
@@ -91,7 +97,7 @@ __device__ __forceinline__ uint64_t cluster_scan(uint64_t mine, uint64_t* slot, 
 
 __device__ __forceinline__ void sync_all(uint32_t ranks) {
   if (ranks == 1) __syncthreads();
-  else ptx::cluster_sync();  // (its release and acquire cover global memory too)
+  else cluster_sync();  // (its release and acquire cover global memory too)
 }
 
 // the sum over the block's warps before this one, and of all, from one value a warp
@@ -353,7 +359,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const Reserv
       if (dcheck(r < a.rows && s < (int64_t)a.pages * a.block, a.err)) a.slots[t] = s;
     }
   }
-  if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's slot
+  if (ranks > 1) cluster_sync();  // the others have read this CTA's slot
 }
 
 // ------------------------------------------------------------------ fork
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
       a.refs[src] = 0;
     }
   }
-  if (ranks > 1) ptx::cluster_sync();  // the others have read this CTA's slots
+  if (ranks > 1) cluster_sync();  // the others have read this CTA's slots
 }
 
 // ------------------------------------------------------------------ contents

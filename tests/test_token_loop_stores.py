@@ -2,7 +2,7 @@
 every store to memory of the caller's or to the workspace stands in a statement or
 block whose own condition checks its place (``dcheck``), or behind one in the same
 block that leaves it, and the check says more than the loop or branch around it.
-CPU only: the sources are read."""
+And of their cluster barriers.  CPU only: the sources are read."""
 import os
 import re
 
@@ -87,3 +87,10 @@ def test_each_store_has_a_check_of_its_own(name):
         assert clauses, (name, statement, heads[-2:])
         around = " ".join(around)
         assert any(c not in around for c in clauses), (name, statement, clauses)
+
+
+@pytest.mark.parametrize("name", ["pages.cu", "sample.cu", "sample.cuh", "sample_exact.cu", "rotary.cu"])
+def test_cluster_barriers_ask_for_no_converged_warp(name):
+    # the lanes of a warp come to them from branches and loops of their own: an aligned barrier would be undefined there
+    text = source(name)
+    assert "ptx::cluster_sync" not in text and not re.search(r"barrier\.cluster\.\w+(\.\w+)?\.aligned", text)
