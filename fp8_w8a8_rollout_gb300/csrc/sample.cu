@@ -33,7 +33,7 @@
 // 10 instructions an element: 1024 x 151936 bf16 takes 70 us (4.4 TB/s), and the
 // exact kernel 28 for the 40 or so draws of so many that fall among the lightest tokens; with
 // top-50 and top-p 104 us.  Pieces come through a ring in shared memory, two
-// rounds ahead of each lane (without: 127 us for both kernels, 120 so).  16 rows: 11 us
+// rounds ahead of each lane (when both kernels took 127 us without, 120 so; 98 now).  16 rows: 11 us
 // where nothing is cut off, 16 with top-50, 14 with min-p.
 #include <algorithm>
 
@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(T) sample_kernel(const SampleArgs a) {
   const bool by_rank = CUT && draw.k > 0 && draw.k <= kCap;
   if (CUT) {
     // Each CTA gives the first ceil(k / CTAs) of its threads' maxima; the least of these bounds is one of the
-    // k-th largest element.  The upper half of the ordered number: a lower bound.
+    // k-th largest element.  The upper half of the ordered number: a lower bound.  (More than a maximum a thread: no
+    // bound, the row is the exact kernel's.)
     float bound = -INFINITY;
     if (by_rank) {
       const int want = (int)((draw.k + ranks - 1) / ranks);

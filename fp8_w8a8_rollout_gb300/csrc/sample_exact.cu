@@ -13,7 +13,7 @@
 // 151936 bf16 takes 14 us where nothing is cut off (one pass, whose weights are 4 us of
 // fp32 arithmetic), 33 with top-p: counting the values 5, their sums and weights 4, the
 // cut 4, the kept ones' mass by place 9.  Where nothing is cut off four CTAs share an SM
-// (64 registers: 1024 x 151936 136 us for both kernels, 199 with one of 512 threads).
+// (64 registers: 1024 x 151936 136 us for both kernels when that came, 199 with one of 512 threads; 98 now).
 #include <algorithm>
 
 #include "sample.cuh"
@@ -723,8 +723,9 @@ struct Team {
 
 // The next row for this cluster: from `start` on, the first one still undecided that it gets hold of (a row is
 // taken by writing kTaken over its mark), -1: none within the next `cover`.  All of the cluster call it; `cursor` is
-// rank 0's place.  Rows are few and fall where they fall: with each cluster keeping to rows of its own, the 128 or
-// so of 1024 x 151936 took 50 us, five rows one behind the other somewhere.
+// rank 0's place.  Rows are few and fall where they fall: with each cluster keeping to rows of its own, 128 of
+// 1024 x 151936 (as many as the pass's wider margin left then; 40 or so now) took 50 us, five rows one behind the other
+// somewhere.
 constexpr int32_t kTaken = -3;
 template <int T>
 __device__ int64_t next_row(const SampleArgs& a, Shared<T>& sh, uint32_t rank, uint32_t ranks, int32_t start, int32_t cover, int32_t& cursor) {
